@@ -370,6 +370,111 @@ pisa_status pisa_attend_decode(const pisa_params* p, const void* q,
  * launches in flight; never needed outside tests. */
 void pisa_test_inject_leaf_timeout(uint64_t wait_limit_ns, int32_t drop_first_key_tile);
 
+/* ------------------------------------------------------------------------
+ * A serving layer's cache and its attention.  Keys and values live in two
+ * pools of pages of C positions, [num_pages, H_kv, C, d] each, behind one
+ * page table int32 [B, ceil(N / C)] (page j of a sequence holds its positions
+ * [C j, C j + C)), the layout of pisa_build_pyramid_paged and
+ * pisa_select_decode_paged.  p->N is the capacity of a sequence; p->K is read
+ * by pisa_attend_decode_paged alone; scorer and summaries play no part.
+ * seq_lens int32 [B] counts a sequence's positions with its new tokens: the
+ * last of them sits at seq_lens[b] - 1, as for pisa_select_decode.  Where a
+ * call takes n new tokens per sequence, new_lens int32 [B] (nullable: n for
+ * every sequence) says how many of them are there; new token i of sequence b
+ * sits at position seq_lens[b] - new_lens[b] + i, and rows of outputs at or
+ * behind new_lens[b] are left as they were.
+ *
+ * Workspace of all four calls: pisa_paged_workspace_bytes(p, n) bytes (n = 1
+ * for the decode calls); it may be used by any number of calls that do not
+ * overlap.  Faults in device data end in its status word: a length that does
+ * not fit (PISA_DEV_BAD_SEQ_LEN) or a page index outside the pool
+ * (PISA_DEV_BAD_INDEX, never read or written).  The part of the output that
+ * they touch is stated per call; everything else is computed.
+ *
+ * Page table entries behind a sequence's last position are never read, nor
+ * are the positions of its last page behind its length: they may hold
+ * anything, NaN included. */
+
+/* Appends n new tokens per sequence to the pages.  k and v [B, H_kv, n, d]
+ * and (nullable) q [B, H_q, n, d] may be strided views: k_strides points at
+ * three element counts (sequence, head, token), each a multiple of 16 bytes,
+ * with the d elements of a row adjacent (null: contiguous; q_strides and
+ * v_strides likewise).  Keys and queries are rotated on the way: with
+ * h = rot_dim / 2 and rope fp32 [N, rot_dim] (cosines of a position's h
+ * angles, then their sines), the pair (x_i, x_{i+h}), or with interleaved != 0
+ * the pair (x_{2i}, x_{2i+1}), becomes (a cos - b sin, b cos + a sin); dims
+ * from rot_dim on stay.  rope null (rot_dim 0): no rotation.  rot_dim must be
+ * a multiple of 16 and at most d.  The rotated keys and the values go to
+ * their pages; q_out [B, H_q, n, d] takes the rotated queries (not null when
+ * q is given; it may be q itself when q is contiguous), k_out (nullable) [B,
+ * H_kv, n, d] a contiguous copy of the rotated keys (likewise k).  bf16 and
+ * fp32; products in fp32, one rounding to the dtype.
+ * A sequence whose lengths do not fit (0 <= new_lens[b] <= min(n,
+ * seq_lens[b]), seq_lens[b] <= N) is skipped whole; a token whose page is
+ * outside the pool reaches q_out and k_out but no page. */
+pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, const int64_t* q_strides,
+                              const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                              const int32_t* seq_lens, const int32_t* new_lens, const float* rope, int32_t rot_dim,
+                              int32_t interleaved, void* k_pages, void* v_pages, int64_t num_pages,
+                              const int32_t* page_table, void* ws, size_t ws_bytes, void* q_out, void* k_out,
+                              void* stream);
+
+/* What a dense attention call does to a score x = scale * q . k of a query
+ * at position t and a key at position j, and which keys it sees:
+ *   softcap > 0       x becomes softcap * tanh(x / softcap)
+ *   slopes            fp32 [H_q] on the device: x += slopes[h] * (j - t)
+ *   window > 0        only keys j > t - window
+ *   first_key         int32 [B, n] on the device: only keys j >= first_key[b, i]
+ *                     (packed documents: the start of the token's document)
+ *   prefix_lens       int32 [B] on the device: only keys j <= max(t,
+ *                     prefix_lens[b] - 1) (tokens of the prefix see each
+ *                     other); without it, only keys j <= t
+ * A query that sees no key gets zeros.  A null pisa_mask* is plain causal
+ * attention. */
+typedef struct {
+  uint32_t struct_size;        /* sizeof(pisa_mask) */
+  float softcap;               /* 0: none */
+  int64_t window;              /* 0: none */
+  const float* slopes;         /* nullable */
+  const int32_t* first_key;    /* nullable */
+  const int32_t* prefix_lens;  /* nullable */
+} pisa_mask;
+
+/* Dense attention of one new token per sequence: q and out bf16 [B, H_q, d],
+ * over positions 0 .. seq_lens[b] - 1 of the pages (first_key is [B, 1];
+ * prefix_lens has no key to add and is not read).  The work is split evenly
+ * over the GPU along the sequences' lengths and joined in the same launch; the
+ * order of every sum follows from the lengths alone.  A sequence whose length
+ * lies outside [1, N] gets zeros; keys of a page outside the pool count as
+ * not seen. */
+pisa_status pisa_dense_decode_paged(const pisa_params* p, const pisa_mask* mask, const void* q, const void* k_pages,
+                                    const void* v_pages, int64_t num_pages, const int32_t* page_table,
+                                    const int32_t* seq_lens, void* ws, size_t ws_bytes, void* out, void* stream);
+
+/* pisa_attend_decode over the pages: attention of one new token per sequence
+ * over the blocks of idx [B, H_kv, K+3] (for instance out_idx of
+ * pisa_select_decode_paged); an entry that is negative, repeated or past the
+ * query's own block counts for nothing.  Faults as for
+ * pisa_dense_decode_paged. */
+pisa_status pisa_attend_decode_paged(const pisa_params* p, const void* q, const void* k_pages, const void* v_pages,
+                                     int64_t num_pages, const int32_t* page_table, const int32_t* seq_lens,
+                                     const int32_t* idx, void* ws, size_t ws_bytes, void* out, void* stream);
+
+/* Dense attention of n new tokens per sequence (a prompt, or a chunk of one
+ * behind a cached part) over the pages, which hold the new tokens' keys and
+ * values already (pisa_append_paged): q and out bf16 [B, H_q, n, d].  A
+ * sequence whose lengths do not fit (as for pisa_append_paged) gets zeros in
+ * its rows before min(n, new_lens[b]); keys of a page outside the pool count
+ * as not seen. */
+pisa_status pisa_dense_prefill_paged(const pisa_params* p, const pisa_mask* mask, int64_t n, const void* q,
+                                     const void* k_pages, const void* v_pages, int64_t num_pages,
+                                     const int32_t* page_table, const int32_t* seq_lens, const int32_t* new_lens,
+                                     void* ws, size_t ws_bytes, void* out, void* stream);
+
+/* Workspace of the four calls above for n new tokens per sequence (0 for an
+ * unsupported problem or n < 0). */
+size_t pisa_paged_workspace_bytes(const pisa_params* p, int64_t n);
+
 /* Synchronises `stream`, then copies the workspace status word into
  * *device_code (PISA_DEV_*).  Returns PISA_ERR_DEVICE when it is non-zero. */
 pisa_status pisa_read_device_status(const void* ws, int32_t* device_code,

@@ -34,8 +34,6 @@ bool make_pyr(int64_t N, int32_t C, Pyr* s) {
   return true;
 }
 
-static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 PrefillWs prefill_ws_layout(const Prob& pr, const Pyr& s) {
   PrefillWs w{};
   const int64_t nq = pr.B * pr.Hkv * pr.N;
@@ -102,7 +100,7 @@ int sm_count(int device) {
 }
 
 // Shared validation of the problem description.
-static pisa_status check_params(const pisa_params* p, Prob* pr, Pyr* s) {
+pisa_status check_params(const pisa_params* p, Prob* pr, Pyr* s) {
   if (!p || p->struct_size < sizeof(pisa_params)) return PISA_ERR_INVALID_ARG;
   if (p->B < 0 || p->N < 0 || p->H_q < 1 || p->H_kv < 1 || p->d < 1 || p->C < 1 || p->g < 1 ||
       p->K < 1 || p->qtile < 1)
@@ -125,10 +123,6 @@ static pisa_status check_params(const pisa_params* p, Prob* pr, Pyr* s) {
   pr->scale2 = sc * kLog2e;
   return PISA_OK;
 }
-
-static bool aligned16(const void* x) { return ((uintptr_t)x & 15u) == 0; }
-
-static pisa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PISA_OK : PISA_ERR_CUDA; }
 
 static std::atomic<unsigned long long> g_launches{0};
 

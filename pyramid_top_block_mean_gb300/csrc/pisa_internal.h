@@ -75,6 +75,12 @@ size_t flat_ws_bytes(const Prob& pr, const Pyr& s);
 
 int sm_count(int device);
 
+// Validation of a problem description shared by every entry point.
+pisa_status check_params(const pisa_params* p, Prob* pr, Pyr* s);
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned16(const void* x) { return ((uintptr_t)x & 15u) == 0; }
+inline pisa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PISA_OK : PISA_ERR_CUDA; }
+
 // Counts one kernel launch (process-wide, relaxed atomic); called before every launch.
 void note_launch();
 

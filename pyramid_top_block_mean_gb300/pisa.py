@@ -38,7 +38,9 @@ EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pi
             "pisa_prefill_route", "pisa_prefill_leaves", "pisa_select_decode", "pisa_select_flat",
             "pisa_read_device_status", "pisa_select_prefill_static", "pisa_kernel_launches",
             "pisa_attend_prefill", "pisa_build_pyramid_paged", "pisa_select_decode_paged", "pisa_attend_decode",
-            "pisa_read_static_status", "pisa_test_inject_leaf_timeout"]
+            "pisa_read_static_status", "pisa_test_inject_leaf_timeout", "pisa_append_paged",
+            "pisa_dense_decode_paged", "pisa_attend_decode_paged", "pisa_dense_prefill_paged",
+            "pisa_paged_workspace_bytes"]
 
 
 class Params(ctypes.Structure):
@@ -50,7 +52,14 @@ class Params(ctypes.Structure):
                 ("summaries", ctypes.c_int32)]
 
 
+class Mask(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("softcap", ctypes.c_float), ("window", ctypes.c_int64),
+                ("slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
+
+
 _P = ctypes.POINTER(Params)
+_M = ctypes.POINTER(Mask)
+_strides_t = ctypes.c_int64 * 3
 _vp = ctypes.c_void_p
 _lib.pisa_abi_version.restype = ctypes.c_int
 _lib.pisa_kernel_launches.restype = ctypes.c_uint64
@@ -85,6 +94,20 @@ _lib.pisa_attend_decode.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_s
 _lib.pisa_attend_decode.restype = ctypes.c_int
 _lib.pisa_attend_prefill.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_attend_prefill.restype = ctypes.c_int
+_lib.pisa_append_paged.argtypes = [_P, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int32,
+                                   ctypes.c_int32, _vp, _vp, ctypes.c_int64, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
+_lib.pisa_append_paged.restype = ctypes.c_int
+_lib.pisa_dense_decode_paged.argtypes = [_P, _M, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_size_t, _vp,
+                                         _vp]
+_lib.pisa_dense_decode_paged.restype = ctypes.c_int
+_lib.pisa_attend_decode_paged.argtypes = [_P, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp,
+                                          _vp]
+_lib.pisa_attend_decode_paged.restype = ctypes.c_int
+_lib.pisa_dense_prefill_paged.argtypes = [_P, _M, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, _vp,
+                                          ctypes.c_size_t, _vp, _vp]
+_lib.pisa_dense_prefill_paged.restype = ctypes.c_int
+_lib.pisa_paged_workspace_bytes.argtypes = [_P, ctypes.c_int64]
+_lib.pisa_paged_workspace_bytes.restype = ctypes.c_size_t
 _lib.pisa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32), _vp]
 _lib.pisa_read_device_status.restype = ctypes.c_int
 _lib.pisa_select_prefill_static.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -255,6 +278,169 @@ def attend_decode(p: Params, q, k_cache, v_cache, seq_lens, idx, ws, out, stream
     return rc
 
 
+def paged_workspace_bytes(p: Params, n: int = 1) -> int:
+    return _lib.pisa_paged_workspace_bytes(ctypes.byref(p), n)
+
+
+# What the paged calls ask of their tensors (the C side sees only addresses):
+# dtype, shape, one device, and adjacent elements.
+def _want(t, name: str, shape, dtype, dev, strided: bool = False):
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not (t.stride(-1) == 1 or shape[-1] <= 1 if strided else t.is_contiguous()):
+        raise ValueError(f"{name}: " + ("the last dimension must be contiguous" if strided else "must be contiguous"))
+
+
+def _want_pools(p: Params, k_pages, v_pages, page_table, seq_lens, ws, dtype, dev):
+    shape = (k_pages.shape[0], p.H_kv, p.C, p.d)
+    _want(k_pages, "k_pages", shape, dtype, dev)
+    _want(v_pages, "v_pages", shape, dtype, dev)
+    _want(page_table, "page_table", (p.B, -(-p.N // p.C) if p.C > 0 else 0), torch.int32, dev)
+    _want(seq_lens, "seq_lens", (p.B,), torch.int32, dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: must be contiguous on {dev}")
+
+
+def _dtype(p: Params) -> torch.dtype:
+    return torch.bfloat16 if p.dtype == BF16 else torch.float32
+
+
+class _on:
+    """Makes `dev` the current device around a call and gives the stream to
+    launch on: the given one, or the device's current one."""
+
+    def __init__(self, dev: torch.device, stream):
+        if dev.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {dev}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream: expected one on {dev}, got {stream.device}")
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _row_strides(t):
+    """(sequence, head, token) strides of a [B, H, n, d] view; null when contiguous.
+    A dimension of one entry has no stride of its own."""
+    if t is None or t.is_contiguous():
+        return None
+    st = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
+    return _strides_t(*st)
+
+
+class AttentionMask:
+    """What a dense paged attention call does to its scores and which keys it
+    sees (pisa_mask): a tanh cap, a window, per-head distance slopes [H_q]
+    fp32, first visible keys [B, n] int32, prefix lengths [B] int32."""
+
+    def __init__(self, softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
+                 first_key: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None):
+        self.slopes, self.first_key, self.prefix_lens = slopes, first_key, prefix_lens
+        self.c = Mask(ctypes.sizeof(Mask), softcap, window, None if slopes is None else slopes.data_ptr(),
+                      None if first_key is None else first_key.data_ptr(),
+                      None if prefix_lens is None else prefix_lens.data_ptr())
+
+
+def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, dev):
+    if mask is None:
+        return None
+    if mask.slopes is not None:
+        _want(mask.slopes, "slopes", (p.H_q,), torch.float32, dev)
+    if mask.first_key is not None:
+        _want(mask.first_key, "first_key", (p.B, n), torch.int32, dev)
+    if mask.prefix_lens is not None:
+        _want(mask.prefix_lens, "prefix_lens", (p.B,), torch.int32, dev)
+    return ctypes.byref(mask.c)
+
+
+def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, rope=None, interleaved: bool = False,
+                 q=None, q_out=None, k_out=None, new_lens=None, stream=None, check: bool = True) -> int:
+    """k, v [B, H_kv, n, d] and q [B, H_q, n, d], strided views allowed; rope
+    fp32 [N, rot_dim] (cosines, then sines); seq_lens counts the new tokens."""
+    dev, dt, n = k.device, _dtype(p), k.shape[2]
+    _want(k, "k", (p.B, p.H_kv, n, p.d), dt, dev, strided=True)
+    _want(v, "v", (p.B, p.H_kv, n, p.d), dt, dev, strided=True)
+    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
+    if q is not None:
+        _want(q, "q", (p.B, p.H_q, n, p.d), dt, dev, strided=True)
+    if q_out is not None:
+        _want(q_out, "q_out", (p.B, p.H_q, n, p.d), dt, dev)
+    if k_out is not None:
+        _want(k_out, "k_out", (p.B, p.H_kv, n, p.d), dt, dev)
+    if new_lens is not None:
+        _want(new_lens, "new_lens", (p.B,), torch.int32, dev)
+    if rope is not None:
+        _want(rope, "rope", (p.N, rope.shape[-1]), torch.float32, dev)
+    with _on(dev, stream) as st:
+        rc = _lib.pisa_append_paged(ctypes.byref(p), n, _ptr(q), _row_strides(q), _ptr(k), _row_strides(k), _ptr(v),
+                                    _row_strides(v), _ptr(seq_lens), _ptr(new_lens), _ptr(rope),
+                                    0 if rope is None else rope.shape[1], int(interleaved), _ptr(k_pages),
+                                    _ptr(v_pages), k_pages.shape[0], _ptr(page_table), _ptr(ws),
+                                    ws.numel() * ws.element_size(), _ptr(q_out), _ptr(k_out), st)
+    if check:
+        _check(rc, "pisa_append_paged")
+    return rc
+
+
+def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out,
+                       mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
+    """q and out [B, H_q, d]: attention of one new token per sequence over its whole cache."""
+    dev, dt = q.device, _dtype(p)
+    _want(q, "q", (p.B, p.H_q, p.d), dt, dev)
+    _want(out, "out", (p.B, p.H_q, p.d), dt, dev)
+    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
+    with _on(dev, stream) as st:
+        rc = _lib.pisa_dense_decode_paged(ctypes.byref(p), _mask_arg(mask, p, 1, dev), _ptr(q), _ptr(k_pages),
+                                          _ptr(v_pages), k_pages.shape[0], _ptr(page_table), _ptr(seq_lens),
+                                          _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), st)
+    if check:
+        _check(rc, "pisa_dense_decode_paged")
+    return rc
+
+
+def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, idx, ws, out, stream=None,
+                        check: bool = True) -> int:
+    """attend_decode over a paged cache; idx int32 [B, H_kv, K+3]."""
+    dev, dt = q.device, _dtype(p)
+    _want(q, "q", (p.B, p.H_q, p.d), dt, dev)
+    _want(out, "out", (p.B, p.H_q, p.d), dt, dev)
+    _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, dev)
+    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
+    with _on(dev, stream) as st:
+        rc = _lib.pisa_attend_decode_paged(ctypes.byref(p), _ptr(q), _ptr(k_pages), _ptr(v_pages), k_pages.shape[0],
+                                           _ptr(page_table), _ptr(seq_lens), _ptr(idx), _ptr(ws),
+                                           ws.numel() * ws.element_size(), _ptr(out), st)
+    if check:
+        _check(rc, "pisa_attend_decode_paged")
+    return rc
+
+
+def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out, new_lens=None,
+                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
+    """q and out [B, H_q, n, d]: attention of n new tokens per sequence over the pages that hold them already."""
+    dev, dt, n = q.device, _dtype(p), q.shape[2]
+    _want(q, "q", (p.B, p.H_q, n, p.d), dt, dev)
+    _want(out, "out", (p.B, p.H_q, n, p.d), dt, dev)
+    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
+    if new_lens is not None:
+        _want(new_lens, "new_lens", (p.B,), torch.int32, dev)
+    with _on(dev, stream) as st:
+        rc = _lib.pisa_dense_prefill_paged(ctypes.byref(p), _mask_arg(mask, p, n, dev), n, _ptr(q), _ptr(k_pages),
+                                           _ptr(v_pages), k_pages.shape[0], _ptr(page_table), _ptr(seq_lens),
+                                           _ptr(new_lens), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), st)
+    if check:
+        _check(rc, "pisa_dense_prefill_paged")
+    return rc
+
+
 def read_device_status(ws: torch.Tensor, stream=None) -> int:
     code = ctypes.c_int32(0)
     rc = _lib.pisa_read_device_status(_ptr(ws), ctypes.byref(code), _stream(stream))
@@ -336,6 +522,59 @@ class Attention:
     def decode(self, q, k_cache, v_cache, seq_lens, idx, stream=None):
         attend_decode(self.p, q, k_cache, v_cache, seq_lens, idx, self.ws, self.out, stream)
         return self.out
+
+    def device_status(self, stream=None) -> int:
+        return read_device_status(self.ws, stream)
+
+
+class PagedAttention:
+    """A serving layer's calls over a paged cache for one problem shape, with
+    up to n new tokens per sequence in a call: appending rotated keys and
+    values, dense attention of one token or of a prompt, and attention over
+    the selector's blocks.  Owns the workspace and one output buffer per kind
+    of call, zeroed once and written again by the next call of its kind; rows
+    behind a sequence's new tokens are not written.
+    rope: fp32 [N, rot_dim] as append_paged takes it, or None."""
+
+    def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 device="cuda"):
+        self.p, self.n, self.rope, self.interleaved = p, n, rope, interleaved
+        self.device = torch.device(device)
+        nbytes = max(paged_workspace_bytes(p, n), paged_workspace_bytes(p, min(n, 1)))
+        if nbytes == 0:
+            raise ValueError("unsupported problem shape, or n outside [0, N]")
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        rows = p.B * p.H_q * p.d
+        self._out = {kind: torch.zeros(rows * m, dtype=_dtype(p), device=self.device)
+                     for kind, m in (("q", n), ("prefill", n), ("dense", 1), ("selected", 1))}
+
+    def _buffer(self, kind: str, like):
+        flat = self._out[kind]
+        if like.numel() > flat.numel():
+            raise ValueError(f"{tuple(like.shape)}: more than the {self.n} new tokens per sequence asked for")
+        return flat[:like.numel()].view(like.shape)
+
+    def append(self, q, k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_out=None, stream=None):
+        """Rotates and appends k and v; returns the rotated queries [B, H_q, n, d] (None when q is None)."""
+        q_out = None if q is None else self._buffer("q", q)
+        append_paged(self.p, k, v, k_pages, v_pages, page_table, seq_lens, self.ws, self.rope, self.interleaved, q,
+                     q_out, k_out, new_lens, stream)
+        return q_out
+
+    def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None):
+        out = self._buffer("dense", q)
+        dense_decode_paged(self.p, q, k_pages, v_pages, page_table, seq_lens, self.ws, out, mask, stream)
+        return out
+
+    def selected_decode(self, q, k_pages, v_pages, page_table, seq_lens, idx, stream=None):
+        out = self._buffer("selected", q)
+        attend_decode_paged(self.p, q, k_pages, v_pages, page_table, seq_lens, idx, self.ws, out, stream)
+        return out
+
+    def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None):
+        out = self._buffer("prefill", q)
+        dense_prefill_paged(self.p, q, k_pages, v_pages, page_table, seq_lens, self.ws, out, new_lens, mask, stream)
+        return out
 
     def device_status(self, stream=None) -> int:
         return read_device_status(self.ws, stream)
