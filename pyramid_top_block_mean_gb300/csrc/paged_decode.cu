@@ -1,89 +1,621 @@
-// paged_decode.cu -- attention of one new token per sequence over the paged cache.
+// paged_decode.cu -- attention of one new token per sequence over the paged
+// cache: all of it (pisa_dense_decode_paged) or the blocks that the selector
+// chose (pisa_attend_decode_paged).
+//
+// For each query head, o = sum_j p_j v_j / sum_j p_j with p_j = 2^(x_j - m),
+// x_j the key's score in log2 units and m their running maximum; parts over
+// disjoint keys join by (m, l, o) -> (M, sum l 2^(m - M), sum o 2^(m - M)).
+// Bound by HBM: the G heads of a group share every key and value, so a page
+// costs 256 d bytes and G / 2 multiply-adds per byte.
+//
+// The unit of work is one page (64 keys and values) of one (sequence, key
+// head).  All units of a call are numbered sequence by sequence, head by head
+// and cut into equal runs, one per CTA, so a long sequence spreads over the
+// GPU and short ones share a CTA; every CTA derives the cut from the lengths
+// on the device.  A producer warp brings the run's pages by TMA (128-byte
+// swizzle, so that every ldmatrix below is free of bank conflicts) into a
+// ring of stages; four warps take 16 of a page's 64 keys each and hold their
+// own (m, l, o): S = K q by m16n8k16 MMAs with the heads as the 8 columns,
+// O^T += V^T P with P turned in registers by movmatrix.  At the end of its
+// part of a (sequence, head) the warps merge in shared memory.  A part that
+// is not the whole goes to the workspace in fp32, and the CTA that brings the
+// last one joins them in the order of the CTAs, so results do not depend on
+// timing.
+#include <algorithm>
+
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace pisa {
 
 namespace {
 
-// One warp per (sequence, query head, new token): lane l holds dims l + 32 j.
+constexpr int kWarps = 4;               // consumer warps, 16 keys each
+constexpr int kCons = 32 * kWarps;      // consumer threads
+constexpr int kThreads = kCons + 32;    // and the producer warp
+constexpr int kPage = 64;
+constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
+constexpr uint64_t kWaitNs = 4000000000ull;
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_decode_kernel(Prob pr, MaskArgs m, int64_t n, const uint16_t* __restrict__ q, Pools pools,
-                                               const int32_t* __restrict__ seq_lens,
-                                               const int32_t* __restrict__ new_lens,
-                                               const int32_t* __restrict__ idx, int32_t* __restrict__ status,
-                                               uint16_t* __restrict__ out) {
-  constexpr int J = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / 32;
-  if (w >= pr.B * pr.Hq * n) return;
-  const int64_t i = w % n, b = w / n / pr.Hq;
-  const int hq = (int)(w / n % pr.Hq), h = hq / pr.G;
-  int64_t len, cnt;
-  bool ok = new_span(seq_lens, new_lens, b, n, pr.N, &len, &cnt);
-  if (1 && len < 1) { ok = false; cnt = 1; }
-  if (!ok && lane == 0) set_status(status, PISA_DEV_BAD_SEQ_LEN);
-  if (i >= cnt) return;
-  uint16_t* o = out + w * D;
-  float acc[J], x[J], mx = -INFINITY, l = 0.0f;
-  for (int j = 0; j < J; ++j) acc[j] = 0.0f;
-  if (ok) {
-    for (int j = 0; j < J; ++j) x[j] = bf16_to_f(q[w * D + lane + 32 * j]);
-    const int64_t t = len - cnt + i;
-    int64_t lo, hi;
-    key_span(m, b, n, i, t, len, &lo, &hi);
-    const float sl = m.slopes ? m.slopes[hq] * kLog2e : 0.0f;
-    const int W = pr.K + 3;
-    const int32_t* row = idx ? idx + (b * pr.Hkv + h) * W : nullptr;
-    const int64_t nslot = row ? W : (lo <= hi ? hi / pr.C - lo / pr.C + 1 : 0);
-    for (int64_t e = 0; e < nslot; ++e) {
-      int64_t blk = lo / pr.C + e;
-      if (row) {
-        blk = row[e];
-        if (blk < 0 || blk > hi / pr.C) continue;
-        bool dup = false;
-        for (int f = 0; f < e; ++f) dup |= row[f] == blk;
-        if (dup) continue;
-      }
-      const int64_t page = pools.table[b * pools.nb + blk];
-      if (page < 0 || page >= pools.num_pages) {
-        if (lane == 0) set_status(status, PISA_DEV_BAD_INDEX);
-        continue;
-      }
-      const int64_t j0 = blk * pr.C < lo ? lo : blk * pr.C, j1 = blk * pr.C + 63 < hi ? blk * pr.C + 63 : hi;
-      for (int64_t key = j0; key <= j1; ++key) {
-        const int64_t at = ((page * pr.Hkv + h) * pr.C + key % pr.C) * D + lane;
-        float s = 0.0f;
-        for (int j = 0; j < J; ++j) s = fmaf(x[j], bf16_to_f(((const uint16_t*)pools.k)[at + 32 * j]), s);
-        s = warp_sum(s);
-        s = m.cap2 > 0.0f ? m.cap2 * tanhf(s * m.pre) : s * pr.scale2;
-        s = fmaf(sl, (float)(key - t), s);
-        const float nm = fmaxf(mx, s);
-        if (nm == -INFINITY) continue;
-        const float f = exp2f(mx - nm), p = exp2f(s - nm);
-        l = l * f + p;
-        for (int j = 0; j < J; ++j) acc[j] = fmaf(p, bf16_to_f(((const uint16_t*)pools.v)[at + 32 * j]), acc[j] * f);
-        mx = nm;
+struct Shape {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr uint32_t kTile = kPage * D * 2;  // bytes of a page's keys
+};
+
+// What a stage holds and what to do with it.
+struct Meta {
+  int32_t item;      // b * Hkv + h
+  int32_t rel;       // position of the page's first key minus the query's
+  int32_t klo, khi;  // keys klo .. khi of the page are seen
+  int32_t first, last;    // of this CTA's part of the item
+  int32_t cfirst, parts;  // with last: the item's first CTA and how many share it
+  int32_t slot;           // with last and parts > 1: where this part goes
+  int32_t slot0;          // and where the first CTA's part goes
+};
+
+template <int D, int G>
+struct Smem {
+  uint8_t kv[Shape<D>::kStages][2][Shape<D>::kTile];
+  uint16_t q[Shape<D>::kStages][G * D];
+  float o[kWarps][G][D / 2];
+  float m[kWarps][8], l[kWarps][8];
+  Meta meta[Shape<D>::kStages];
+  uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages];
+  int32_t abort, zero, last_part;
+};
+
+// Parts: fp32 m[G], l[G], o[G][D] per slot; counters of arrived parts per item.
+struct Parts {
+  int32_t* counter;
+  float* ml;
+  float* o;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void cons_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory"); }
+
+// Keys that the query of sequence b sees, and the pages that hold them; a
+// query that sees none has one page, dead.
+struct Span {
+  int64_t t, lo;
+  int32_t j0, np;
+  bool dead, bad;
+};
+__device__ __forceinline__ Span seq_span(const MaskArgs& m, const int32_t* seq_lens, int64_t b, int64_t N) {
+  Span s;
+  const int64_t len = seq_lens[b];
+  s.bad = len < 1 || len > N;
+  s.t = len - 1;
+  int64_t hi = 0;
+  s.lo = 0;
+  if (!s.bad) key_span(m, b, 1, 0, s.t, len, &s.lo, &hi);
+  s.dead = s.bad || s.lo > s.t;
+  s.j0 = s.dead ? 0 : (int32_t)(s.lo / kPage);
+  s.np = s.dead ? 1 : (int32_t)(s.t / kPage) - s.j0 + 1;
+  return s;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_decode_kernel(Prob pr, MaskArgs mk, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, const uint16_t* __restrict__ q,
+                        const int32_t* __restrict__ table, int64_t nb, int64_t num_pages,
+                        const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ idx, Parts parts,
+                        int32_t min_run, int32_t* __restrict__ status, uint16_t* __restrict__ out) {
+  constexpr int kStages = Shape<D>::kStages;
+  constexpr uint32_t kTile = Shape<D>::kTile;
+  constexpr int kHalf = kPage * 128;  // bytes of a tile's 64-column half
+  extern __shared__ unsigned char smem_raw[];
+  Smem<D, G>& sm = *reinterpret_cast<Smem<D, G>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int32_t* abort = &sm.abort;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), kWarps);
+    }
+    sm.abort = 0;
+    sm.zero = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  // The cut: T units in runs of `run`, this CTA's is [u0, u1).  Every warp
+  // derives it for itself.
+  const int W = pr.K + 3;
+  int64_t T;
+  if (idx) {
+    T = pr.B * pr.Hkv * W;
+  } else {
+    int64_t n = 0;
+    for (int64_t b = lane; b < pr.B; b += 32) n += seq_span(mk, seq_lens, b, pr.N).np;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    T = n * pr.Hkv;
+  }
+  const int64_t run = max((int64_t)min_run, ceil_div64(T, gridDim.x));
+  const int64_t u0 = blockIdx.x * run, u1 = min(T, u0 + run);
+  __syncthreads();
+  if (u0 >= T) return;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    // the sequence, head and page of u0
+    int64_t b = 0, i0 = 0;
+    if (idx) {
+      b = u0 / (pr.Hkv * W);
+      i0 = b * pr.Hkv * W;
+    } else {
+      for (int64_t c = 0; c < pr.B; c += 32) {
+        const int64_t x0 = c + lane < pr.B ? (int64_t)seq_span(mk, seq_lens, c + lane, pr.N).np * pr.Hkv : 0;
+        int64_t x = x0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, i0 + x > u0);
+        if (over) {
+          const int at = __ffs(over) - 1;
+          i0 += __shfl_sync(0xffffffffu, x - x0, at);
+          b = c + at;
+          break;
+        }
+        i0 += __shfl_sync(0xffffffffu, x, 31);
       }
     }
+    Span sp = seq_span(mk, seq_lens, b, pr.N);
+    int32_t np = idx ? W : sp.np;
+    int32_t h = (int32_t)((u0 - i0) / np);
+    i0 += (int64_t)h * np;  // first unit of the item
+    int it = 0;
+    bool ok = true;
+    // one stage; page < 0: none to load
+    auto emit = [&](const Meta& meta, int64_t page, int32_t head, int64_t seq) -> bool {
+      const int st = it % kStages;
+      const bool got = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      if (lane == 0) {
+        sm.meta[st] = meta;
+        const uint32_t full = ptx::smem_u32(&sm.full[st]);
+        const uint32_t bytes = (page >= 0 ? 2 * kTile : 0u) + (meta.first ? (uint32_t)(G * D * 2) : 0u);
+        ptx::mbar_arrive_expect_tx(full, bytes);
+        if (page >= 0) {
+          const int32_t y = (int32_t)((page * pr.Hkv + head) * kPage);
+#pragma unroll
+          for (int hh = 0; hh < D / 64; ++hh) {
+            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][0]) + hh * kHalf, &kmap, 64 * hh, y, full);
+            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][1]) + hh * kHalf, &vmap, 64 * hh, y, full);
+          }
+        }
+        if (meta.first)
+          ptx::bulk_g2s(ptx::smem_u32(sm.q[st]), q + (seq * pr.Hq + head * G) * D, G * D * 2, full);
+      }
+      __syncwarp();
+      ++it;
+      return true;
+    };
+    for (int64_t u = u0; u < u1 && ok;) {
+      if (lane == 0 && sp.bad) set_status(status, PISA_DEV_BAD_SEQ_LEN);
+      const int32_t s0 = (int32_t)(u - i0), s1 = (int32_t)min((int64_t)np, u1 - i0);
+      Meta meta;
+      meta.item = (int32_t)(b * pr.Hkv + h);
+      meta.first = 1;
+      meta.last = 0;
+      meta.rel = 0;
+      meta.klo = kPage;
+      meta.khi = -1;
+      const int64_t c0 = i0 / run, c1 = (i0 + np - 1) / run;
+      meta.cfirst = (int32_t)c0;
+      meta.parts = (int32_t)(c1 - c0 + 1);
+      meta.slot0 = (int32_t)(2 * c0 + (c0 * run < i0 ? 1 : 0));
+      meta.slot = blockIdx.x == c0 ? meta.slot0 : 2 * (int32_t)blockIdx.x;
+      const int32_t* trow = table + b * nb;
+      if (sp.dead) {
+        meta.last = 1;
+        ok = emit(meta, -1, h, b);
+      } else {
+        // the entries of this part, 32 at a time: lane l looks after entry s + l
+        int32_t r0 = -1, r1 = -1;
+        if (idx) {
+          const int32_t* row = idx + (b * pr.Hkv + h) * W;
+          if (lane < W) r0 = row[lane];
+          if (lane + 32 < W) r1 = row[lane + 32];
+        }
+        const int32_t qb = (int32_t)(sp.t / kPage);
+        int32_t left = 0;  // entries of the part that hold a page, not yet emitted
+        uint64_t keep = 0;
+        if (idx) {
+          const bool k0 = r0 >= 0 && r0 <= qb, k1 = r1 >= 0 && r1 <= qb;
+          const unsigned below = (1u << lane) - 1u;
+          const unsigned m0 = __match_any_sync(0xffffffffu, k0 ? r0 : -1 - lane);  // others match nothing
+          const unsigned m1 = __match_any_sync(0xffffffffu, k1 ? r1 : -1 - lane);
+          bool dup1 = (m1 & below) != 0u;
+          for (int x = 0; x < 32; ++x) {
+            const int32_t o = __shfl_sync(0xffffffffu, k0 ? r0 : -1, x);
+            dup1 |= k1 && o == r1;
+          }
+          const unsigned b0 = __ballot_sync(0xffffffffu, k0 && (m0 & below) == 0u);
+          const unsigned b1 = __ballot_sync(0xffffffffu, k1 && !dup1);
+          keep = ((uint64_t)b1 << 32 | b0) >> s0 << s0;  // this part's entries
+          if (s1 < 64) keep &= ((uint64_t)1 << s1) - 1;
+          left = __popcll(keep);
+        } else {
+          left = s1 - s0;
+        }
+        if (left == 0) {
+          meta.last = 1;
+          ok = emit(meta, -1, h, b);
+        }
+        for (int32_t s = s0 & ~31; s < s1 && ok; s += 32) {
+          // lane l: block and page of entry s + l
+          int32_t blk = idx ? (s == 0 ? r0 : r1) : sp.j0 + s + lane;
+          bool mine = idx ? ((keep >> (s + lane)) & 1) != 0 : s + lane >= s0 && s + lane < s1;
+          int32_t page = -1;
+          if (mine) {
+            page = trow[blk];
+            if (page < 0 || page >= num_pages) {
+              page = -1;
+              set_status(status, PISA_DEV_BAD_INDEX);
+            }
+          }
+          unsigned todo = __ballot_sync(0xffffffffu, mine);
+          while (todo && ok) {
+            const int x = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int32_t bx = __shfl_sync(0xffffffffu, blk, x), px = __shfl_sync(0xffffffffu, page, x);
+            const int64_t key0 = (int64_t)bx * kPage;
+            meta.rel = (int32_t)(key0 - sp.t);
+            meta.klo = px < 0 ? kPage : (int32_t)max((int64_t)0, min((int64_t)kPage, sp.lo - key0));
+            meta.khi = (int32_t)min((int64_t)(kPage - 1), sp.t - key0);
+            meta.last = --left == 0;
+            ok = emit(meta, px, h, b);
+            meta.first = 0;
+          }
+        }
+      }
+      u = i0 + s1;
+      if (s1 == np) {
+        i0 += np;
+        if (++h == pr.Hkv) {
+          h = 0;
+          if (++b < pr.B) {
+            sp = seq_span(mk, seq_lens, b, pr.N);
+            if (!idx) np = sp.np;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) *abort = 1;
+    // a stage without an item ends the consumers
+    bool closed = false;
+    if (ok) {
+      const int st = it % kStages;
+      closed = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
+      if (closed && lane == 0) {
+        sm.meta[st].item = -1;
+        ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
+      }
+    }
+    // every copy lands before the CTA ends (the closing stage's own last one has, since it was free again)
+    if (lane == 0)
+      for (int k = max(0, it - kStages + (closed ? 1 : 0)); k < it; ++k)
+        ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero, kWaitNs);
+    if (lane == 0 && sm.abort) set_status(status, PISA_DEV_TIMEOUT);
+    return;
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  for (int j = 0; j < J; ++j) o[lane + 32 * j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
+
+  // ------------------------------------------------------------- consumers
+  const int grp = lane >> 2, tig = lane & 3;
+  const int r16 = 16 * warp;
+  // ldmatrix rows: lane l addresses row l % 8 of matrix l / 8
+  const int krow = r16 + (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
+  const int vrow = r16 + (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
+  uint32_t bq[D / 16][2];
+  float oacc[D / 16][4];
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
+  float sl0 = 0.0f, sl1 = 0.0f;
+  for (int it = 0;; ++it) {
+    const int st = it % kStages;
+    const bool okw = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[st]), (it / kStages) & 1, abort, kWaitNs);
+    if (!__all_sync(0xffffffffu, okw)) {
+      *abort = 1;
+      break;
+    }
+    const Meta meta = sm.meta[st];
+    if (meta.item < 0) break;
+    if (meta.first) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t* qr = reinterpret_cast<const uint32_t*>(sm.q[st] + (grp < G ? grp : 0) * D + 16 * ks);
+        bq[ks][0] = grp < G ? qr[tig] : 0u;
+        bq[ks][1] = grp < G ? qr[tig + 4] : 0u;
+        oacc[ks][0] = oacc[ks][1] = oacc[ks][2] = oacc[ks][3] = 0.0f;
+      }
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.0f;
+      if (mk.slopes) {
+        const float* sl = mk.slopes + (int64_t)(meta.item % pr.Hkv) * G;
+        sl0 = 2 * tig < G ? sl[2 * tig] * kLog2e : 0.0f;
+        sl1 = 2 * tig + 1 < G ? sl[2 * tig + 1] * kLog2e : 0.0f;
+      }
+    }
+    if (meta.klo <= meta.khi && r16 <= meta.khi && r16 + 15 >= meta.klo) {
+      const uint32_t kb = ptx::smem_u32(sm.kv[st][0]), vb = ptx::smem_u32(sm.kv[st][1]);
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t a[4];
+        const int ch = 2 * ks + kch;
+        ldsm4(kb + (ch >> 3) * kHalf + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a);
+        if (ks & 1) mma16816(e, a, bq[ks][0], bq[ks][1]);
+        else mma16816(d, a, bq[ks][0], bq[ks][1]);
+      }
+      // keys grp and grp + 8 of this warp's 16, heads 2 tig and 2 tig + 1
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = d[j] + e[j];
+        if (mk.cap2 > 0.0f) {
+          // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
+          const float w = ptx::ex2(x[j] * mk.pre * (2.0f * kLog2e));
+          x[j] = fmaf(-2.0f * mk.cap2, __frcp_rn(1.0f + w), mk.cap2);
+        } else {
+          x[j] *= pr.scale2;
+        }
+      }
+      const int ka = r16 + grp;
+      if (mk.slopes) {
+        const float ra = (float)(meta.rel + ka), rb = (float)(meta.rel + ka + 8);
+        x[0] = fmaf(sl0, ra, x[0]); x[1] = fmaf(sl1, ra, x[1]);
+        x[2] = fmaf(sl0, rb, x[2]); x[3] = fmaf(sl1, rb, x[3]);
+      }
+      const bool part = r16 < meta.klo || r16 + 15 > meta.khi;  // some of the 16 keys are not seen
+      uint32_t va = 0xffffffffu, vz = 0xffffffffu;              // masks of the value pairs below
+      if (part) {
+        if (ka < meta.klo || ka > meta.khi) x[0] = x[1] = -INFINITY;
+        if (ka + 8 < meta.klo || ka + 8 > meta.khi) x[2] = x[3] = -INFINITY;
+        const int k2 = r16 + 2 * tig;
+        auto seen = [&](int k) { return k >= meta.klo && k <= meta.khi; };
+        va = (seen(k2) ? 0xffffu : 0u) | (seen(k2 + 1) ? 0xffff0000u : 0u);
+        vz = (seen(k2 + 8) ? 0xffffu : 0u) | (seen(k2 + 9) ? 0xffff0000u : 0u);
+      }
+      float c0 = fmaxf(x[0], x[2]), c1 = fmaxf(x[1], x[3]);
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) {
+        c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
+        c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
+      }
+      const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
+      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+        const float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - n0);
+        const float f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          oacc[mt][0] *= f0; oacc[mt][2] *= f0;
+          oacc[mt][1] *= f1; oacc[mt][3] *= f1;
+        }
+      }
+      // a key without weight: its score is -inf (m is, only if all were)
+      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+      const float p0 = ptx::ex2(x[0] - z0), p1 = ptx::ex2(x[1] - z1);
+      const float p2 = ptx::ex2(x[2] - z0), p3 = ptx::ex2(x[3] - z1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step)
+      const uint32_t b0 = transpose8(pack_bf16(p0, p1)), b1 = transpose8(pack_bf16(p2, p3));
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        uint32_t a[4];
+        const int ch = 2 * mt + vch;
+        ldsm4_t(vb + (ch >> 3) * kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), a);
+        if (part) {  // a value that is not seen may be anything
+          a[0] &= va; a[1] &= va;
+          a[2] &= vz; a[3] &= vz;
+        }
+        mma16816(oacc[mt], a, b0, b1);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
+    if (!meta.last) continue;
+
+    // ------------------------------------------- end of a part: merge warps
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if (grp == 0) {
+      sm.m[warp][2 * tig] = m0; sm.m[warp][2 * tig + 1] = m1;
+      sm.l[warp][2 * tig] = l0; sm.l[warp][2 * tig + 1] = l1;
+    }
+    cons_sync();
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      M0 = fmaxf(M0, sm.m[w][2 * tig]);
+      M1 = fmaxf(M1, sm.m[w][2 * tig + 1]);
+    }
+    const float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - M1);
+    const int64_t orow = (int64_t)meta.item * G * D;  // item's G rows of out are adjacent
+    float* po = parts.o + (int64_t)meta.slot * G * D;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half) cons_sync();  // the first half has been read
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const int mt = half * (D / 32) + k;
+        if (2 * tig < G) {
+          sm.o[warp][2 * tig][16 * k + grp] = oacc[mt][0] * f0;
+          sm.o[warp][2 * tig][16 * k + grp + 8] = oacc[mt][2] * f0;
+        }
+        if (2 * tig + 1 < G) {
+          sm.o[warp][2 * tig + 1][16 * k + grp] = oacc[mt][1] * f1;
+          sm.o[warp][2 * tig + 1][16 * k + grp + 8] = oacc[mt][3] * f1;
+        }
+      }
+      cons_sync();
+      for (int e = threadIdx.x; e < G * D / 4; e += kCons) {
+        const int g = e / (D / 4), c = 2 * (e % (D / 4));
+        float a = 0.0f, z = 0.0f, L = 0.0f, M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][g]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          a += sm.o[w][g][c];
+          z += sm.o[w][g][c + 1];
+          L += sm.m[w][g] == -INFINITY ? sm.l[w][g] : sm.l[w][g] * ptx::ex2(sm.m[w][g] - M);
+        }
+        const int dim = half * (D / 2) + c;
+        if (meta.parts == 1) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          *reinterpret_cast<uint32_t*>(out + orow + g * D + dim) = pack_bf16(a * inv, z * inv);
+        } else {
+          *reinterpret_cast<float2*>(po + g * D + dim) = make_float2(a, z);
+          if (dim == 0) {
+            parts.ml[(int64_t)meta.slot * 2 * G + 2 * g] = M;
+            parts.ml[(int64_t)meta.slot * 2 * G + 2 * g + 1] = L;
+          }
+        }
+      }
+    }
+    if (meta.parts > 1) {
+      __threadfence();
+      cons_sync();
+      if (threadIdx.x == 0) sm.last_part = atomicAdd(parts.counter + meta.item, 1) == meta.parts - 1;
+      cons_sync();
+      if (sm.last_part) {
+        __threadfence();
+        for (int e = threadIdx.x; e < G * D / 2; e += kCons) {
+          const int g = e / (D / 2), c = 2 * (e % (D / 2));
+          float M = -INFINITY, L = 0.0f, a = 0.0f, z = 0.0f;
+          constexpr int kBatch = 8;  // parts in flight
+          for (int p0 = 0; p0 < meta.parts; p0 += kBatch) {
+            float2 ml[kBatch], o[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int p = p0 + k;
+              const int64_t slot = p == 0 ? meta.slot0 : 2 * (int64_t)(meta.cfirst + p);
+              ml[k] = make_float2(-INFINITY, 0.0f);
+              o[k] = make_float2(0.0f, 0.0f);
+              if (p < meta.parts) {
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(parts.ml + slot * 2 * G + 2 * g));
+                o[k] = __ldcg(reinterpret_cast<const float2*>(parts.o + slot * G * D + g * D + c));
+              }
+            }
+            float bm = M;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
+            if (bm > M) {
+              const float f = M == -INFINITY ? 0.0f : ptx::ex2(M - bm);
+              L *= f; a *= f; z *= f;
+              M = bm;
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.0f ? 0.0f : 1.0f) : ptx::ex2(ml[k].x - M);
+              L = fmaf(ml[k].y, f, L);
+              a = fmaf(o[k].x, f, a);
+              z = fmaf(o[k].y, f, z);
+            }
+          }
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          *reinterpret_cast<uint32_t*>(out + orow + g * D + c) = pack_bf16(a * inv, z * inv);
+        }
+      }
+    }
+    cons_sync();  // the merge buffers are free again
+  }
+}
+
+constexpr int kMinRun = 4;  // pages a CTA takes at least: below, joining costs more than a page
+
+struct Ws {
+  size_t counter, ml, o, total;
+};
+Ws ws_layout(const Prob& pr) {
+  Ws w;
+  size_t o = 256;  // the status word's; the counters follow, so that one memset clears both
+  w.counter = o; o = align_up(o + (size_t)pr.B * pr.Hkv * 4, 256);
+  w.ml = o; o = align_up(o + (size_t)2 * kMaxCtas * 2 * pr.G * 4, 256);
+  w.o = o; o = align_up(o + (size_t)2 * kMaxCtas * pr.G * pr.d * 4, 256);
+  w.total = o;
+  return w;
+}
+
+template <int D, int G>
+cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Pools& pools, const int32_t* seq_lens,
+                     const int32_t* idx, char* ws, void* out, cudaStream_t st) {
+  const Ws w = ws_layout(pr);
+  CUtensorMap kmap, vmap;
+  const int64_t rows = pools.num_pages * pr.Hkv * kPage;
+  if (!make_tmap_rows(&kmap, pools.k, rows, D, kPage) || !make_tmap_rows(&vmap, pools.v, rows, D, kPage))
+    return cudaErrorInvalidValue;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(Smem<D, G>) + 1024;
+  auto kern = paged_decode_kernel<D, G>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(ws, 0, w.counter + (size_t)pr.B * pr.Hkv * 4, st);
+  if (e != cudaSuccess) return e;
+  // two CTAs share an SM; fewer where the capacity has fewer units
+  const int64_t units = pr.B * pr.Hkv * (idx ? pr.K + 3 : pools.nb);
+  const int64_t grid = std::min<int64_t>(std::min(2 * sm_count(dev), kMaxCtas), ceil_div64(units, kMinRun));
+  Parts parts{(int32_t*)(ws + w.counter), (float*)(ws + w.ml), (float*)(ws + w.o)};
+  note_launch();
+  kern<<<(unsigned)grid, kThreads, smem, st>>>(pr, m, kmap, vmap, (const uint16_t*)q, pools.table, pools.nb,
+                                               pools.num_pages, seq_lens, idx, parts, kMinRun, (int32_t*)ws,
+                                               (uint16_t*)out);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t paged_decode_ws_bytes(const Prob&) { return 256; }
+size_t paged_decode_ws_bytes(const Prob& pr) { return ws_layout(pr).total; }
 
 cudaError_t launch_paged_decode(const Prob& pr, const MaskArgs& m, const void* q, const Pools& pools,
                                 const int32_t* seq_lens, const int32_t* idx, char* ws, void* out, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  const unsigned grid = (unsigned)ceil_div64(pr.B * pr.Hq, 4);
-  auto kern = pr.d == 128 ? paged_decode_kernel<128> : paged_decode_kernel<64>;
-  kern<<<grid, 128, 0, st>>>(pr, m, 1, (const uint16_t*)q, pools, seq_lens, nullptr, idx, (int32_t*)ws,
-                             (uint16_t*)out);
-  return cudaGetLastError();
+#define PISA_PD_CASE(DD, GG) \
+  if (pr.d == DD && pr.G == GG) return launch_t<DD, GG>(pr, m, q, pools, seq_lens, idx, ws, out, st);
+  PISA_PD_CASE(128, 1) PISA_PD_CASE(128, 2) PISA_PD_CASE(128, 4) PISA_PD_CASE(128, 8)
+  PISA_PD_CASE(64, 1) PISA_PD_CASE(64, 2) PISA_PD_CASE(64, 4) PISA_PD_CASE(64, 8)
+#undef PISA_PD_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pisa
