@@ -1,90 +1,707 @@
-// paged_prefill.cu -- attention of a prompt over the paged cache.
+// paged_prefill.cu -- dense attention of new tokens (a prompt, or a chunk of
+// one behind a cached part) over the paged cache, on the tcgen05 tensor cores.
+//
+// For every row (token, query head): o = sum_j p_j v_j / sum_j p_j over the
+// keys that it sees, p_j = 2^(x_j - m), in one pass over the keys.  The
+// reference m only follows the running maximum when that has grown by more
+// than 2^8: until then the weights stay below 2^8, which neither fp32 sums nor
+// bf16 weights mind, and the output tile needs no rescaling.
+//
+// One CTA takes 256 rows -- 256 / G tokens of the G heads that share a key
+// head -- as two tiles of 128, against tiles of 128 keys (two pages):
+//   - a loader warp brings the query tiles once, then keys and values through
+//     one ring of stages by TMA (128-byte swizzle); a page is found through
+//     the table, so a tile is four boxes;
+//   - one thread issues S = Q K^T into TMEM and, when its weights P are there,
+//     O += P V with P read from TMEM (over the columns of S, which the warps
+//     have read by then) and V in its natural key-major layout.  The two
+//     tiles alternate: while one's softmax runs, the other's MMAs do;
+//   - two groups of four warps do the softmax, one thread per row, so that a
+//     row's maximum and sum need no exchange.
+// Work: 4 d flops for each (row, key); S and O take 2 x 512 cycles of the
+// tensor pipe per tile pair of d = 128 and the softmax 128 exponentials a row.
+//
+// Rows with few tokens and a long cache: the keys of a CTA's rows are split
+// over several CTAs, whose parts a second kernel joins.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace pisa {
 
 namespace {
 
-// One warp per (sequence, query head, new token): lane l holds dims l + 32 j.
+constexpr int kRows = 128;  // rows of a tile
+constexpr int kKeys = 128;  // keys of a tile
+constexpr int kPage = 64;
+constexpr int kMmaWarp = 8;   // warps 0-3 and 4-7: softmax of tile 0 and 1
+constexpr int kLoadWarp = 9;
+constexpr int kThreads = 384;  // warps 10 and 11 only make up the third warpgroup
+// Registers a thread: the softmax warpgroups hold a row of S each, the third
+// gives up what they need (2 x 216 + 72 = 3 x 168, the launch's share).
+#define PISA_SOFTMAX_REGS "216"
+#define PISA_OTHER_REGS "72"
+constexpr uint64_t kWaitNs = 4000000000ull;
+constexpr float kSlack = 8.0f;  // log2 of how far weights may exceed 1
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_prefill_kernel(Prob pr, MaskArgs m, int64_t n, const uint16_t* __restrict__ q, Pools pools,
-                                               const int32_t* __restrict__ seq_lens,
-                                               const int32_t* __restrict__ new_lens,
-                                               const int32_t* __restrict__ idx, int32_t* __restrict__ status,
-                                               uint16_t* __restrict__ out) {
-  constexpr int J = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / 32;
-  if (w >= pr.B * pr.Hq * n) return;
-  const int64_t i = w % n, b = w / n / pr.Hq;
-  const int hq = (int)(w / n % pr.Hq), h = hq / pr.G;
+struct Cfg {
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t kTile = kKeys * D * 2;  // bytes of a key or value tile, and of a query tile
+};
+
+template <int D>
+struct Smem {
+  uint8_t q[2][Cfg<D>::kTile];
+  uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTile];
+  uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
+  uint64_t qfull, scrub, sfull[2], pfull[2], odone[2], done;
+  int32_t lo[2], hi[2];  // keys that a tile's rows see
+  uint32_t tmem;
+  int32_t abort, zero, bad_page;
+};
+
+struct Args {
+  int64_t n, nb, num_pages;
+  const int32_t *seq_lens, *new_lens, *table;
+  int32_t* status;
+  uint16_t* out;
+  float *part_o, *part_ml;  // [split][cta][256][D] and [..][2] (m in log2 units, l)
+  int32_t tiles, splits, lg_tokens;  // CTAs per (sequence, key head), splits, log2 of a tile's tokens
+};
+
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;  // next 64 MN elements
+  d |= (uint64_t)(1024u >> 4) << 32;            // next 8 K rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T
+__device__ __forceinline__ void mma_ts_bf16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            int32_t w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// MODE 0: scores are scale * q . k; 1: with a cap and / or a distance bias.
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prefill_kernel(Prob pr, MaskArgs mk, const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Args a) {
+  constexpr int kStages = Cfg<D>::kStages;
+  constexpr uint32_t kTile = Cfg<D>::kTile;
+  constexpr uint32_t kHalf = kKeys * 128;      // bytes of a tile's 64-column half
+  constexpr uint32_t kPageHalf = kPage * 128;  // and of a page's
+  constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRows, kKeys);
+  constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);  // values MN-major
+  extern __shared__ unsigned char smem_raw[];
+  Smem<D>& sm =
+      *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int32_t* abort = &sm.abort;
+
+  // which rows: the last tokens' CTAs, which see the most keys, come first
+  int64_t x = blockIdx.x;
+  const int split = (int)(x % a.splits);
+  x /= a.splits;
+  const int64_t bh = x % (pr.B * pr.Hkv);
+  const int tile = a.tiles - 1 - (int)(x / (pr.B * pr.Hkv));
+  const int64_t b = bh / pr.Hkv;
+  const int h = (int)(bh % pr.Hkv);
+  const int tokens = 1 << a.lg_tokens;  // of one tile
   int64_t len, cnt;
-  bool ok = new_span(seq_lens, new_lens, b, n, pr.N, &len, &cnt);
-  if (0 && len < 1) { ok = false; cnt = 1; }
-  if (!ok && lane == 0) set_status(status, PISA_DEV_BAD_SEQ_LEN);
-  if (i >= cnt) return;
-  uint16_t* o = out + w * D;
-  float acc[J], x[J], mx = -INFINITY, l = 0.0f;
-  for (int j = 0; j < J; ++j) acc[j] = 0.0f;
-  if (ok) {
-    for (int j = 0; j < J; ++j) x[j] = bf16_to_f(q[w * D + lane + 32 * j]);
-    const int64_t t = len - cnt + i;
-    int64_t lo, hi;
-    key_span(m, b, n, i, t, len, &lo, &hi);
-    const float sl = m.slopes ? m.slopes[hq] * kLog2e : 0.0f;
-    const int W = pr.K + 3;
-    const int32_t* row = idx ? idx + (b * pr.Hkv + h) * W : nullptr;
-    const int64_t nslot = row ? W : (lo <= hi ? hi / pr.C - lo / pr.C + 1 : 0);
-    for (int64_t e = 0; e < nslot; ++e) {
-      int64_t blk = lo / pr.C + e;
-      if (row) {
-        blk = row[e];
-        if (blk < 0 || blk > hi / pr.C) continue;
-        bool dup = false;
-        for (int f = 0; f < e; ++f) dup |= row[f] == blk;
-        if (dup) continue;
+  const bool fits = new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
+  const int64_t i0 = (int64_t)tile * 2 * tokens;
+  if (!fits && threadIdx.x == 0) set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
+  if (i0 >= cnt) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(&sm.qfull), 1);
+    ptx::mbar_init(ptx::smem_u32(&sm.scrub), 1);
+    ptx::mbar_init(ptx::smem_u32(&sm.done), 1);
+    for (int w = 0; w < 2; ++w) {
+      ptx::mbar_init(ptx::smem_u32(&sm.sfull[w]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.pfull[w]), 4);
+      ptx::mbar_init(ptx::smem_u32(&sm.odone[w]), 1);
+      sm.lo[w] = 0x7fffffff;
+      sm.hi[w] = -1;
+    }
+    sm.abort = 0;
+    sm.zero = 0;
+    sm.bad_page = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(&sm.tmem), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  // this thread's row (softmax warps) and the keys that it sees
+  const int w = warp >> 2, r = threadIdx.x & 127;
+  const int64_t i = i0 + (int64_t)w * tokens + (r & (tokens - 1));
+  const int g = r >> a.lg_tokens;
+  const bool row = warp < 8 && i < cnt;
+  const int64_t t = len - cnt + i;
+  int32_t lo = 0x7fffffff, hi = -1;
+  if (row && fits) {
+    int64_t l, u;
+    key_span(mk, b, a.n, i, t, len, &l, &u);
+    if (l <= u) {
+      lo = (int32_t)l;
+      hi = (int32_t)u;
+    }
+  }
+  if (warp < 8) {
+    const int32_t wlo = __reduce_min_sync(0xffffffffu, lo), whi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      atomicMin(&sm.lo[w], wlo);
+      atomicMax(&sm.hi[w], whi);
+    }
+  }
+  __syncthreads();
+  // key tiles: this split's share [ja, jb) of the CTA's, and each tile's own part of it
+  const int32_t klo = min(sm.lo[0], sm.lo[1]), khi = max(sm.hi[0], sm.hi[1]);
+  int ja = 0, jb = 0, wa[2], wb[2];
+  if (khi >= 0) {
+    const int a0 = klo / kKeys, cntj = khi / kKeys + 1 - a0;
+    ja = a0 + (int)((int64_t)cntj * split / a.splits);
+    jb = a0 + (int)((int64_t)cntj * (split + 1) / a.splits);
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    wa[v] = sm.hi[v] < 0 ? jb : max(ja, sm.lo[v] / kKeys);
+    wb[v] = sm.hi[v] < 0 ? jb : min(jb, sm.hi[v] / kKeys + 1);
+    if (wb[v] < wa[v]) wb[v] = wa[v];
+  }
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_OTHER_REGS ";");
+  if (warp == kLoadWarp) {
+    // -------------------------------------------------------------- loader
+    bool ok = true;
+    int fills = 0, scrubs = 0;
+    const bool act0 = wa[0] < wb[0], act1 = wa[1] < wb[1];
+    if (lane == 0 && (act0 || act1)) {
+      const uint32_t bar = ptx::smem_u32(&sm.qfull);
+      ptx::mbar_arrive_expect_tx(bar, kTile * ((act0 ? 1 : 0) + (act1 ? 1 : 0)));
+      for (int v = 0; v < 2; ++v) {
+        if (!(v ? act1 : act0)) continue;
+#pragma unroll
+        for (int hh = 0; hh < D / 64; ++hh)
+          tma_load_4d(ptx::smem_u32(sm.q[v]) + hh * kHalf, &qmap, 64 * hh, (int32_t)(i0 + (int64_t)v * tokens),
+                      h * pr.G, (int32_t)b, bar);
       }
-      const int64_t page = pools.table[b * pools.nb + blk];
-      if (page < 0 || page >= pools.num_pages) {
-        if (lane == 0) set_status(status, PISA_DEV_BAD_INDEX);
-        continue;
+    }
+    const int32_t* trow = a.table + b * a.nb;
+    int32_t entry = -1;  // lane l: the page of block 2 jc + l, -1: none of its keys is seen, -2: outside the pool
+    auto wait_empty = [&](int f) {
+      const bool got = ptx::mbar_wait_bounded_hint(ptx::smem_u32(&sm.empty[f % kStages]), ((f / kStages) & 1) ^ 1,
+                                                   abort, kWaitNs, 1000);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    for (int j = ja; j < jb; ++j) {
+      const int at = (j - ja) & 15;
+      if (at == 0) {
+        const int32_t blk = 2 * j + lane;
+        entry = -1;
+        if ((int64_t)blk * kPage <= khi && (int64_t)blk * kPage + kPage > klo && blk < 2 * jb) {
+          entry = trow[blk];
+          if (entry < 0 || entry >= a.num_pages) {
+            entry = -2;
+            set_status(a.status, PISA_DEV_BAD_INDEX);
+            *(volatile int32_t*)&sm.bad_page = 1;
+          }
+        }
+        __syncwarp();
       }
-      const int64_t j0 = blk * pr.C < lo ? lo : blk * pr.C, j1 = blk * pr.C + 63 < hi ? blk * pr.C + 63 : hi;
-      for (int64_t key = j0; key <= j1; ++key) {
-        const int64_t at = ((page * pr.Hkv + h) * pr.C + key % pr.C) * D + lane;
-        float s = 0.0f;
-        for (int j = 0; j < J; ++j) s = fmaf(x[j], bf16_to_f(((const uint16_t*)pools.k)[at + 32 * j]), s);
-        s = warp_sum(s);
-        s = m.cap2 > 0.0f ? m.cap2 * tanhf(s * m.pre) : s * pr.scale2;
-        s = fmaf(sl, (float)(key - t), s);
-        const float nm = fmaxf(mx, s);
-        if (nm == -INFINITY) continue;
-        const float f = exp2f(mx - nm), p = exp2f(s - nm);
-        l = l * f + p;
-        for (int j = 0; j < J; ++j) acc[j] = fmaf(p, bf16_to_f(((const uint16_t*)pools.v)[at + 32 * j]), acc[j] * f);
-        mx = nm;
+      const int32_t pg[2] = {__shfl_sync(0xffffffffu, entry, 2 * at), __shfl_sync(0xffffffffu, entry, 2 * at + 1)};
+      const int pages = (pg[0] >= 0) + (pg[1] >= 0);
+      // values that no row of the CTA sees (behind the sequence's end among
+      // them) may be anything, and a weight of zero does not undo a NaN: they
+      // are cleared before the MMA reads the tile
+      const int32_t key0 = j * kKeys;
+      const bool clear = key0 < klo || key0 + kKeys - 1 > khi || pages < 2;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!(ok = wait_empty(fills))) break;
+        const int st = fills % kStages;
+        const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
+        const bool scrub = kv == 1 && clear;
+        const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
+        if (lane == 0) {
+          if (pages) ptx::mbar_arrive_expect_tx(bar, pages * (kTile / 2));
+          else if (!scrub) ptx::mbar_arrive(bar);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            if (pg[p] < 0) continue;
+            const int32_t y = (int32_t)(((int64_t)pg[p] * pr.Hkv + h) * kPage);
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh)
+              ptx::tma_load_2d(dst + hh * kHalf + p * kPageHalf, kv ? &vmap : &kmap, 64 * hh, y, bar);
+          }
+        }
+        if (scrub) {
+          if (pages) {
+            const bool got = ptx::mbar_wait_bounded(bar, scrubs & 1, &sm.zero, kWaitNs);
+            ++scrubs;
+            if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
+          }
+          for (int e = lane; e < kKeys * 8; e += 32) {
+            const int rr = e >> 3;
+            const int32_t key = key0 + rr;
+            if (key < klo || key > khi || pg[rr >> 6] < 0) {
+#pragma unroll
+              for (int hh = 0; hh < D / 64; ++hh)
+                *reinterpret_cast<uint4*>(sm.kv[st] + hh * kHalf + rr * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(full);
+        }
+        ++fills;
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) *abort = 1;
+    // every issued load lands before the CTA can end, whoever gave up
+    if (lane == 0) {
+      if (act0 || act1) ptx::mbar_wait_bounded(ptx::smem_u32(&sm.qfull), 0, &sm.zero, kWaitNs);
+      for (int f = max(0, fills - kStages); f < fills; ++f)
+        ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero, kWaitNs);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0 && (wa[0] < wb[0] || wa[1] < wb[1])) {
+      bool ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.qfull), 0, abort, kWaitNs);
+      auto wait_full = [&](int f) {
+        return ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, abort, kWaitNs);
+      };
+      // step j: O of key tile j, then S of key tile j + 1, for each row tile
+      for (int j = ja - 1; j < jb && ok; ++j) {
+        const int fv = 2 * (j - ja) + 1, fk = 2 * (j + 1 - ja);  // fills of V(j) and K(j + 1)
+        if (j + 1 < jb && !(ok = wait_full(fk))) break;
+        if (j >= ja && !(ok = wait_full(fv))) break;
+        const uint32_t kb = ptx::smem_u32(sm.kv[fk % kStages]);
+        const uint32_t vb = ptx::smem_u32(sm.kv[j >= ja ? fv % kStages : 0]);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (j >= wa[v] && j < wb[v]) {
+            ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.pfull[v]), (j - wa[v]) & 1, abort, kWaitNs);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t o = tmem + 256 + v * D, p = tmem + v * 128;
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts_bf16(o, p + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, (j > wa[v] || k > 0) ? 1u : 0u);
+            if (j + 1 == wb[v]) ptx::mma_commit(ptx::smem_u32(&sm.odone[v]));
+          }
+          if (j + 1 >= wa[v] && j + 1 < wb[v]) {
+            // over P of key tile j, which the MMAs above have read: they run in order
+            const uint32_t qb = ptx::smem_u32(sm.q[v]);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+              ptx::mma_bf16(tmem + v * 128, ptx::desc_sw128(qb + off), ptx::desc_sw128(kb + off), kIdescS,
+                            k > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(ptx::smem_u32(&sm.sfull[v]));
+          }
+        }
+        if (!ok) break;
+        if (j >= ja) ptx::mma_commit(ptx::smem_u32(&sm.empty[fv % kStages]));
+        if (j + 1 < jb) ptx::mma_commit(ptx::smem_u32(&sm.empty[fk % kStages]));
+      }
+      if (!ok) *abort = 1;
+      ptx::mma_commit(ptx::smem_u32(&sm.done));
+      ptx::mbar_wait_bounded(ptx::smem_u32(&sm.done), 0, &sm.zero, kWaitNs);
+    }
+    __syncwarp();
+  }
+  } else {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 " PISA_SOFTMAX_REGS ";");
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * D;
+    // MODE 0 keeps the dots and scales them inside the exponent
+    const float sc = MODE == 0 ? pr.scale2 : 1.0f;
+    const float slack = kSlack / sc;
+    const float slope = MODE == 1 && mk.slopes && row ? mk.slopes[h * pr.G + g] * kLog2e : 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int j = wa[w]; j < wb[w]; ++j) {
+      ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.sfull[w]), (j - wa[w]) & 1, abort, kWaitNs);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      ptx::tc_fence_after();
+      float s[kKeys];
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
+      ptx::tmem_ld_wait();
+      const int32_t key0 = j * kKeys;
+      if (MODE == 1) {
+        if (mk.cap2 > 0.0f) {
+          // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
+          const float pre = mk.pre * (2.0f * kLog2e);
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            s[c] = fmaf(-2.0f * mk.cap2, rcp_approx(1.0f + ptx::ex2(s[c] * pre)), mk.cap2);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] *= pr.scale2;
+        }
+        if (mk.slopes) {
+          const float base = slope * (float)(int32_t)(key0 - t);
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] += fmaf(slope, (float)c, base);
+        }
+      }
+      // keys clo .. chi of the tile are seen
+      const int32_t clo = max(lo, key0) - key0, chi = min(hi, key0 + kKeys - 1) - key0;
+      if (__any_sync(0xffffffffu, clo > 0 || chi < kKeys - 1)) {
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          if (c < clo || c > chi) s[c] = -INFINITY;
+      }
+      if (*(volatile int32_t*)&sm.bad_page) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int64_t blk = 2 * (int64_t)j + p;
+          if (blk * kPage > khi) continue;
+          const int32_t pg = a.table[b * a.nb + blk];
+          if (pg >= 0 && pg < a.num_pages) continue;
+#pragma unroll
+          for (int c = 0; c < kPage; ++c) s[p * kPage + c] = -INFINITY;
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mx[k] = fmaxf(s[32 * k], s[32 * k + 1]);
+#pragma unroll
+        for (int c = 2; c < 32; c += 2) mx[k] = ptx::max3(mx[k], s[32 * k + c], s[32 * k + c + 1]);
+      }
+      const float top = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
+      const bool grow = top > m + slack || (m == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow && m > -INFINITY ? ptx::ex2((m - top) * sc) : 1.0f;
+        if (grow) m = top;
+        l *= f;
+        if (j > wa[w] && __any_sync(0xffffffffu, f != 1.0f)) {
+          // the MMAs into O so far are done: S of this tile was issued after them
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld32(o_at + c, o);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(o_at + c, o);
+          }
+        }
+      }
+      const float neg = m == -INFINITY ? 0.0f : -m * sc;
+      const uint64_t sc2 = ptx::pack2(sc, sc), neg2 = ptx::pack2(neg, neg);
+      uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float p0, p1;
+          ptx::unpack2(ptx::fma2(ptx::pack2(s[c + k], s[c + k + 1]), sc2, neg2), p0, p1);
+          p0 = ptx::ex2(p0);
+          p1 = ptx::ex2(p1);
+          sum[(k >> 1) & 1] = ptx::add2(sum[(k >> 1) & 1], ptx::pack2(p0, p1));
+          // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step); l is not
+          pk[k / 2] = pack_bf16(p0, p1);
+        }
+        tmem_st16(s_at + c / 2, pk);
+      }
+      tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w]));
+      float s0, s1;
+      ptx::unpack2(ptx::add2(sum[0], sum[1]), s0, s1);
+      l += s0 + s1;
+    }
+    const bool any = wa[w] < wb[w];
+    if (ok && any) {
+      ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.odone[w]), 0, abort, kWaitNs);
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      ptx::tc_fence_after();
+    }
+    if (!ok) *abort = 1;
+    if (a.splits > 1) {
+      // this part of the row: m in log2 units, l, and O as it is
+      const int64_t at = (((int64_t)split * a.tiles + tile) * pr.B * pr.Hkv + bh) * (2 * kRows) + w * kRows + r;
+      if (row) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(any ? m * sc : -INFINITY, any ? l : 0.0f);
+      if (any && ok) {
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld32(o_at + c, o);
+          ptx::tmem_ld_wait();
+          if (row)
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(a.part_o + at * D + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+    } else {
+      // rows through this warp's part of the query tile (its MMAs are done),
+      // so that the stores cover whole lines
+      const float inv = any && l != 0.0f ? 1.0f / l : 0.0f;
+      const bool none = !any || l == 0.0f;
+      uint16_t* dst = row ? a.out + (((b * pr.Hq + (int64_t)h * pr.G + g) * a.n + i) * D) : nullptr;
+      const uint32_t srow = ptx::smem_u32(sm.q[w]) + (warp & 3) * 32 * 128;
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        if (half > 0) __syncwarp();
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece) {
+          uint32_t o[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+          if (any && ok) {
+            ptx::tmem_ld32(o_at + half * 64 + piece * 32, o);
+            ptx::tmem_ld_wait();
+          }
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pk[k] = none ? 0u : pack_bf16(__uint_as_float(o[8 * c4 + 2 * k]) * inv,
+                                            __uint_as_float(o[8 * c4 + 2 * k + 1]) * inv);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(srow + lane * 128 +
+                                                                          (((piece * 4 + c4) ^ (lane & 7)) << 4)),
+                         "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                         : "memory");
+          }
+        }
+        __syncwarp();
+        const int c = lane & 7;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + (lane >> 3);
+          const uint64_t dp = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), rr);
+          uint32_t a0, a1, a2, a3;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                       : "r"(srow + rr * 128 + ((c ^ (rr & 7)) << 4))
+                       : "memory");
+          if (dp) reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dp) + half * 64)[c] = make_uint4(a0, a1, a2, a3);
+        }
       }
     }
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  for (int j = 0; j < J; ++j) o[lane + 32 * j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && sm.abort) set_status(a.status, PISA_DEV_TIMEOUT);
+}
+
+// Joins the parts of a row: one thread per (row, 8 dims).
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(Prob pr, Args a) {
+  pdl_wait();
+  constexpr int CH = D / 8;
+  const int64_t rows = (int64_t)a.tiles * pr.B * pr.Hkv * (2 * kRows);
+  const int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int ch = (int)(e % CH);
+  const int64_t at = e / CH;
+  if (at >= rows) return;
+  const int r = (int)(at & 127), w = (int)(at >> 7 & 1);
+  const int64_t bh = (at >> 8) % (pr.B * pr.Hkv);
+  const int64_t tile = (at >> 8) / (pr.B * pr.Hkv);
+  const int64_t b = bh / pr.Hkv;
+  const int tokens = 1 << a.lg_tokens;
+  const int64_t i = tile * 2 * tokens + (int64_t)w * tokens + (r & (tokens - 1));
+  int64_t len, cnt;
+  new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
+  if (i >= cnt) return;
+  float M = -INFINITY, L = 0.0f, acc[8] = {};
+  constexpr int kBatch = 4;
+  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+    float2 ml[kBatch];
+    float4 o[kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      o[k][0] = o[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (s0 + k < a.splits) {
+        const int64_t p = (int64_t)(s0 + k) * rows + at;
+        ml[k] = *reinterpret_cast<const float2*>(a.part_ml + 2 * p);
+        if (ml[k].y != 0.0f) {  // a part that saw no key wrote no output
+          o[k][0] = *reinterpret_cast<const float4*>(a.part_o + p * D + 8 * ch);
+          o[k][1] = *reinterpret_cast<const float4*>(a.part_o + p * D + 8 * ch + 4);
+        }
+      }
+    }
+    float bm = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
+    if (bm > M) {
+      const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - bm);
+      L *= f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) acc[d] *= f;
+      M = bm;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
+      L = fmaf(ml[k].y, f, L);
+      const float ov[8] = {o[k][0].x, o[k][0].y, o[k][0].z, o[k][0].w, o[k][1].x, o[k][1].y, o[k][1].z, o[k][1].w};
+#pragma unroll
+      for (int d = 0; d < 8; ++d) acc[d] = fmaf(ov[d], f, acc[d]);
+    }
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int64_t hq = (bh % pr.Hkv) * pr.G + (r >> a.lg_tokens);
+  uint4 v;
+  v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+  v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+  v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
+  v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
+  *reinterpret_cast<uint4*>(a.out + ((b * pr.Hq + hq) * a.n + i) * D + 8 * ch) = v;
+}
+
+// Grid of a call.  A GPU that has fewer CTAs than SMs gets the rows' keys
+// split so that about one CTA per SM runs, each with four key tiles at least;
+// the lengths are on the device, so the capacity stands for them.
+constexpr int kSms = 152;
+struct Plan {
+  int32_t tiles, splits, lg_tokens;
+  int64_t ctas;  // without the splits
+  size_t ml, o, total;
+};
+Plan make_plan(const Prob& pr, int64_t n) {
+  Plan p;
+  p.lg_tokens = pr.G == 1 ? 7 : (pr.G == 2 ? 6 : (pr.G == 4 ? 5 : 4));
+  p.tiles = (int32_t)ceil_div64(n, (int64_t)2 << p.lg_tokens);
+  p.ctas = p.tiles * pr.B * pr.Hkv;
+  p.splits = 1;
+  if (p.ctas > 0 && 2 * p.ctas <= kSms)
+    p.splits = (int32_t)std::max<int64_t>(1, std::min(kSms / p.ctas, ceil_div64(pr.N, kKeys) / 4));
+  const size_t rows = p.splits > 1 ? (size_t)p.splits * p.ctas * 2 * kRows : 0;
+  size_t o = 256;
+  p.ml = o; o = align_up(o + rows * 2 * 4, 256);
+  p.o = o; o = align_up(o + rows * pr.d * 4, 256);
+  p.total = o;
+  return p;
+}
+
+template <int D, int MODE>
+cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const Plan& pl, const CUtensorMap& qmap,
+                     const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& a, cudaStream_t st) {
+  const size_t smem = sizeof(Smem<D>) + 1024;
+  auto kern = paged_prefill_kernel<D, MODE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  kern<<<(unsigned)(pl.ctas * pl.splits), kThreads, smem, st>>>(pr, m, qmap, kmap, vmap, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || pl.splits == 1) return e;
+  note_launch();
+  return launch_pdl(true, prefill_join_kernel<D>, dim3((unsigned)ceil_div64(pl.ctas * 2 * kRows * (D / 8), 256)),
+                    dim3(256), 0, st, pr, a);
 }
 
 }  // namespace
 
-size_t paged_prefill_ws_bytes(const Prob&, int64_t) { return 256; }
+size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) { return make_plan(pr, n).total; }
 
 cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, const void* q, const Pools& pools,
                                  const int32_t* seq_lens, const int32_t* new_lens, char* ws, void* out,
                                  cudaStream_t st) {
+  const Plan pl = make_plan(pr, n);
+  if (pl.ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
+  CUtensorMap qmap, kmap, vmap;
+  const int64_t rows = pools.num_pages * pr.Hkv * kPage;
+  if (!make_tmap_rows(&kmap, pools.k, rows, pr.d, kPage) || !make_tmap_rows(&vmap, pools.v, rows, pr.d, kPage) ||
+      !make_tmap_q(&qmap, q, pr.B, pr.Hq, n, pr.d, pr.G, 1 << pl.lg_tokens))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
   if (e != cudaSuccess) return e;
-  note_launch();
-  const unsigned grid = (unsigned)ceil_div64(pr.B * pr.Hq * n, 4);
-  auto kern = pr.d == 128 ? paged_prefill_kernel<128> : paged_prefill_kernel<64>;
-  kern<<<grid, 128, 0, st>>>(pr, m, n, (const uint16_t*)q, pools, seq_lens, new_lens, nullptr, (int32_t*)ws,
-                             (uint16_t*)out);
-  return cudaGetLastError();
+  Args a{};
+  a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages;
+  a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = pools.table;
+  a.status = (int32_t*)ws;
+  a.out = (uint16_t*)out;
+  a.part_ml = (float*)(ws + pl.ml);
+  a.part_o = (float*)(ws + pl.o);
+  a.tiles = pl.tiles; a.splits = pl.splits; a.lg_tokens = pl.lg_tokens;
+  const bool shaped = m.cap2 > 0.0f || m.slopes;
+  if (pr.d == 128)
+    return shaped ? launch_t<128, 1>(pr, m, pl, qmap, kmap, vmap, a, st)
+                  : launch_t<128, 0>(pr, m, pl, qmap, kmap, vmap, a, st);
+  return shaped ? launch_t<64, 1>(pr, m, pl, qmap, kmap, vmap, a, st)
+                : launch_t<64, 0>(pr, m, pl, qmap, kmap, vmap, a, st);
 }
 
 }  // namespace pisa
