@@ -283,57 +283,70 @@ def paged_workspace_bytes(p: Params, n: int = 1) -> int:
 
 
 # What the paged calls ask of their tensors (the C side sees only addresses):
-# dtype, shape, one device, and adjacent elements.
-def _want(t, name: str, shape, dtype, dev, strided: bool = False):
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} {shape} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not (t.stride(-1) == 1 or shape[-1] <= 1 if strided else t.is_contiguous()):
-        raise ValueError(f"{name}: " + ("the last dimension must be contiguous" if strided else "must be contiguous"))
+# dtype, shape, one device, and adjacent elements.  These run before every
+# decode step, so they only touch attributes that cost a fraction of a
+# microsecond.
+def _refuse(t, name: str, shape, dtype, index: int, layout: str):
+    raise ValueError(f"{name}: expected {layout} {dtype} {tuple(shape)} on cuda:{index}, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _want_pools(p: Params, k_pages, v_pages, page_table, seq_lens, ws, dtype, dev):
-    shape = (k_pages.shape[0], p.H_kv, p.C, p.d)
-    _want(k_pages, "k_pages", shape, dtype, dev)
-    _want(v_pages, "v_pages", shape, dtype, dev)
-    _want(page_table, "page_table", (p.B, -(-p.N // p.C) if p.C > 0 else 0), torch.int32, dev)
-    _want(seq_lens, "seq_lens", (p.B,), torch.int32, dev)
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: must be contiguous on {dev}")
+def _want(t, name: str, shape, dtype, index: int) -> int:
+    """Address of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, index, "contiguous")
+    return t.data_ptr()
+
+
+def _want_rows(t, name: str, shape, dtype, index: int):
+    """Address and (sequence, head, token) strides of a [B, H, n, d] view with
+    adjacent elements in a row; no strides when it is contiguous.  A dimension
+    of one entry has no stride of its own."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, name, shape, dtype, index, "a")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    st = t.stride()
+    if st[3] != 1:
+        _refuse(t, name, shape, dtype, index, "row-contiguous")
+    return t.data_ptr(), _strides_t(*[0 if shape[i] == 1 else st[i] for i in range(3)])
+
+
+def _want_cache(p: Params, k_pages, v_pages, page_table, seq_lens, ws, dtype, index: int):
+    """(k_pages, v_pages, number of pages, page_table, seq_lens) and the workspace's address and size."""
+    num = k_pages.shape[0]
+    shape = (num, p.H_kv, p.C, p.d)
+    if ws.get_device() != index or not ws.is_contiguous():
+        _refuse(ws, "ws", ws.shape, ws.dtype, index, "contiguous")
+    return ((_want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index), num,
+             _want(page_table, "page_table", (p.B, -(-p.N // 64)), torch.int32, index),
+             _want(seq_lens, "seq_lens", (p.B,), torch.int32, index)),
+            (ws.data_ptr(), ws.numel() * ws.element_size()))
 
 
 def _dtype(p: Params) -> torch.dtype:
     return torch.bfloat16 if p.dtype == BF16 else torch.float32
 
 
-class _on:
-    """Makes `dev` the current device around a call and gives the stream to
-    launch on: the given one, or the device's current one."""
-
-    def __init__(self, dev: torch.device, stream):
-        if dev.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {dev}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream: expected one on {dev}, got {stream.device}")
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _row_strides(t):
-    """(sequence, head, token) strides of a [B, H, n, d] view; null when contiguous.
-    A dimension of one entry has no stride of its own."""
-    if t is None or t.is_contiguous():
-        return None
-    st = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
-    return _strides_t(*st)
+def _launch(index: int, stream, what: str, check: bool, fn, *args) -> int:
+    """Calls fn(*args, stream) with the tensors' device current, on the given
+    stream or the device's current one."""
+    if index < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{index}")
+    else:
+        st = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, st)
+    if check and rc != PISA_OK:
+        raise PisaError(rc, what)
+    return rc
 
 
 class AttentionMask:
@@ -349,15 +362,15 @@ class AttentionMask:
                       None if prefix_lens is None else prefix_lens.data_ptr())
 
 
-def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, dev):
+def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, index: int):
     if mask is None:
         return None
     if mask.slopes is not None:
-        _want(mask.slopes, "slopes", (p.H_q,), torch.float32, dev)
+        _want(mask.slopes, "slopes", (p.H_q,), torch.float32, index)
     if mask.first_key is not None:
-        _want(mask.first_key, "first_key", (p.B, n), torch.int32, dev)
+        _want(mask.first_key, "first_key", (p.B, n), torch.int32, index)
     if mask.prefix_lens is not None:
-        _want(mask.prefix_lens, "prefix_lens", (p.B,), torch.int32, dev)
+        _want(mask.prefix_lens, "prefix_lens", (p.B,), torch.int32, index)
     return ctypes.byref(mask.c)
 
 
@@ -365,80 +378,51 @@ def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, ro
                  q=None, q_out=None, k_out=None, new_lens=None, stream=None, check: bool = True) -> int:
     """k, v [B, H_kv, n, d] and q [B, H_q, n, d], strided views allowed; rope
     fp32 [N, rot_dim] (cosines, then sines); seq_lens counts the new tokens."""
-    dev, dt, n = k.device, _dtype(p), k.shape[2]
-    _want(k, "k", (p.B, p.H_kv, n, p.d), dt, dev, strided=True)
-    _want(v, "v", (p.B, p.H_kv, n, p.d), dt, dev, strided=True)
-    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
-    if q is not None:
-        _want(q, "q", (p.B, p.H_q, n, p.d), dt, dev, strided=True)
-    if q_out is not None:
-        _want(q_out, "q_out", (p.B, p.H_q, n, p.d), dt, dev)
-    if k_out is not None:
-        _want(k_out, "k_out", (p.B, p.H_kv, n, p.d), dt, dev)
-    if new_lens is not None:
-        _want(new_lens, "new_lens", (p.B,), torch.int32, dev)
-    if rope is not None:
-        _want(rope, "rope", (p.N, rope.shape[-1]), torch.float32, dev)
-    with _on(dev, stream) as st:
-        rc = _lib.pisa_append_paged(ctypes.byref(p), n, _ptr(q), _row_strides(q), _ptr(k), _row_strides(k), _ptr(v),
-                                    _row_strides(v), _ptr(seq_lens), _ptr(new_lens), _ptr(rope),
-                                    0 if rope is None else rope.shape[1], int(interleaved), _ptr(k_pages),
-                                    _ptr(v_pages), k_pages.shape[0], _ptr(page_table), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _ptr(q_out), _ptr(k_out), st)
-    if check:
-        _check(rc, "pisa_append_paged")
-    return rc
+    index, dt, n = k.get_device(), _dtype(p), k.shape[2]
+    kv_shape, q_shape = (p.B, p.H_kv, n, p.d), (p.B, p.H_q, n, p.d)
+    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
+    return _launch(
+        index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n,
+        *((None, None) if q is None else _want_rows(q, "q", q_shape, dt, index)),
+        *_want_rows(k, "k", kv_shape, dt, index), *_want_rows(v, "v", kv_shape, dt, index), cache[4],
+        None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index),
+        None if rope is None else _want(rope, "rope", (p.N, rope.shape[-1]), torch.float32, index),
+        0 if rope is None else rope.shape[-1], interleaved, *cache[:4], *space,
+        None if q_out is None else _want(q_out, "q_out", q_shape, dt, index),
+        None if k_out is None else _want(k_out, "k_out", kv_shape, dt, index))
 
 
 def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out,
                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
     """q and out [B, H_q, d]: attention of one new token per sequence over its whole cache."""
-    dev, dt = q.device, _dtype(p)
-    _want(q, "q", (p.B, p.H_q, p.d), dt, dev)
-    _want(out, "out", (p.B, p.H_q, p.d), dt, dev)
-    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
-    with _on(dev, stream) as st:
-        rc = _lib.pisa_dense_decode_paged(ctypes.byref(p), _mask_arg(mask, p, 1, dev), _ptr(q), _ptr(k_pages),
-                                          _ptr(v_pages), k_pages.shape[0], _ptr(page_table), _ptr(seq_lens),
-                                          _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), st)
-    if check:
-        _check(rc, "pisa_dense_decode_paged")
-    return rc
+    index, dt, shape = q.get_device(), _dtype(p), (p.B, p.H_q, p.d)
+    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
+    return _launch(index, stream, "pisa_dense_decode_paged", check, _lib.pisa_dense_decode_paged, ctypes.byref(p),
+                   _mask_arg(mask, p, 1, index), _want(q, "q", shape, dt, index), *cache, *space,
+                   _want(out, "out", shape, dt, index))
 
 
 def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, idx, ws, out, stream=None,
                         check: bool = True) -> int:
     """attend_decode over a paged cache; idx int32 [B, H_kv, K+3]."""
-    dev, dt = q.device, _dtype(p)
-    _want(q, "q", (p.B, p.H_q, p.d), dt, dev)
-    _want(out, "out", (p.B, p.H_q, p.d), dt, dev)
-    _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, dev)
-    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
-    with _on(dev, stream) as st:
-        rc = _lib.pisa_attend_decode_paged(ctypes.byref(p), _ptr(q), _ptr(k_pages), _ptr(v_pages), k_pages.shape[0],
-                                           _ptr(page_table), _ptr(seq_lens), _ptr(idx), _ptr(ws),
-                                           ws.numel() * ws.element_size(), _ptr(out), st)
-    if check:
-        _check(rc, "pisa_attend_decode_paged")
-    return rc
+    index, dt, shape = q.get_device(), _dtype(p), (p.B, p.H_q, p.d)
+    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
+    return _launch(index, stream, "pisa_attend_decode_paged", check, _lib.pisa_attend_decode_paged, ctypes.byref(p),
+                   _want(q, "q", shape, dt, index), *cache,
+                   _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space,
+                   _want(out, "out", shape, dt, index))
 
 
 def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out, new_lens=None,
                         mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
     """q and out [B, H_q, n, d]: attention of n new tokens per sequence over the pages that hold them already."""
-    dev, dt, n = q.device, _dtype(p), q.shape[2]
-    _want(q, "q", (p.B, p.H_q, n, p.d), dt, dev)
-    _want(out, "out", (p.B, p.H_q, n, p.d), dt, dev)
-    _want_pools(p, k_pages, v_pages, page_table, seq_lens, ws, dt, dev)
-    if new_lens is not None:
-        _want(new_lens, "new_lens", (p.B,), torch.int32, dev)
-    with _on(dev, stream) as st:
-        rc = _lib.pisa_dense_prefill_paged(ctypes.byref(p), _mask_arg(mask, p, n, dev), n, _ptr(q), _ptr(k_pages),
-                                           _ptr(v_pages), k_pages.shape[0], _ptr(page_table), _ptr(seq_lens),
-                                           _ptr(new_lens), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), st)
-    if check:
-        _check(rc, "pisa_dense_prefill_paged")
-    return rc
+    index, dt, n = q.get_device(), _dtype(p), q.shape[2]
+    shape = (p.B, p.H_q, n, p.d)
+    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
+    return _launch(index, stream, "pisa_dense_prefill_paged", check, _lib.pisa_dense_prefill_paged, ctypes.byref(p),
+                   _mask_arg(mask, p, n, index), n, _want(q, "q", shape, dt, index), *cache,
+                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space,
+                   _want(out, "out", shape, dt, index))
 
 
 def read_device_status(ws: torch.Tensor, stream=None) -> int:
@@ -544,15 +528,19 @@ class PagedAttention:
         if nbytes == 0:
             raise ValueError("unsupported problem shape, or n outside [0, N]")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        rows = p.B * p.H_q * p.d
-        self._out = {kind: torch.zeros(rows * m, dtype=_dtype(p), device=self.device)
-                     for kind, m in (("q", n), ("prefill", n), ("dense", 1), ("selected", 1))}
+        dt = _dtype(p)
+        self._out = {"dense": torch.zeros(p.B, p.H_q, p.d, dtype=dt, device=self.device),
+                     "selected": torch.zeros(p.B, p.H_q, p.d, dtype=dt, device=self.device),
+                     "q": torch.zeros(p.B, p.H_q, n, p.d, dtype=dt, device=self.device),
+                     "prefill": torch.zeros(p.B, p.H_q, n, p.d, dtype=dt, device=self.device)}
 
     def _buffer(self, kind: str, like):
-        flat = self._out[kind]
-        if like.numel() > flat.numel():
+        out = self._out[kind]
+        if out.shape == like.shape:
+            return out
+        if like.numel() > out.numel():
             raise ValueError(f"{tuple(like.shape)}: more than the {self.n} new tokens per sequence asked for")
-        return flat[:like.numel()].view(like.shape)
+        return out.view(-1)[:like.numel()].view(like.shape)
 
     def append(self, q, k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_out=None, stream=None):
         """Rotates and appends k and v; returns the rotated queries [B, H_q, n, d] (None when q is None)."""
