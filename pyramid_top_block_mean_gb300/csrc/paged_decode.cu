@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // one stage; page < 0: none to load
     auto emit = [&](const Meta& meta, int64_t page, int32_t head, int64_t seq) -> bool {
       const int st = it % kStages;
-      const bool got = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
+      const bool got = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
       if (!__all_sync(0xffffffffu, got)) return false;
       if (lane == 0) {
         sm.meta[st] = meta;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool closed = false;
     if (ok) {
       const int st = it % kStages;
-      closed = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
+      closed = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
       if (closed && lane == 0) {
         sm.meta[st].item = -1;
         ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // every copy lands before the CTA ends (the closing stage's own last one has, since it was free again)
     if (lane == 0)
       for (int k = max(0, it - kStages + (closed ? 1 : 0)); k < it; ++k)
-        ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero, kWaitNs);
+        ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero, kWaitNs);
     if (lane == 0 && sm.abort) set_status(status, PISA_DEV_TIMEOUT);
     return;
   }
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float sl0 = 0.0f, sl1 = 0.0f;
   for (int it = 0;; ++it) {
     const int st = it % kStages;
-    const bool okw = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[st]), (it / kStages) & 1, abort, kWaitNs);
+    const bool okw = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), (it / kStages) & 1, abort, kWaitNs);
     if (!__all_sync(0xffffffffu, okw)) {
       *abort = 1;
       break;

@@ -12,7 +12,7 @@
 //   - a loader warp brings the query tiles once, then keys and values through
 //     one ring of stages by TMA (128-byte swizzle); a page is found through
 //     the table, so a tile is four boxes;
-//   - one thread issues S = Q K^T into TMEM and, when its weights P are there,
+//   - a warp per row tile issues S = Q K^T into TMEM and, when its weights P are there,
 //     O += P V with P read from TMEM (over the columns of S, which the warps
 //     have read by then) and V in its natural key-major layout.  The two
 //     tiles alternate: while one's softmax runs, the other's MMAs do;
@@ -37,9 +37,9 @@ namespace {
 constexpr int kRows = 128;  // rows of a tile
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kPage = 64;
-constexpr int kMmaWarp = 8;   // warps 0-3 and 4-7: softmax of tile 0 and 1
-constexpr int kLoadWarp = 9;
-constexpr int kThreads = 384;  // warps 10 and 11 only make up the third warpgroup
+constexpr int kMmaWarp = 8;   // warps 0-3 and 4-7: softmax of tile 0 and 1; 8 and 9: their MMAs
+constexpr int kLoadWarp = 10;
+constexpr int kThreads = 384;  // warp 11 only makes up the third warpgroup
 // Registers a thread: the softmax warpgroups hold a row of S each, the third
 // gives up what they need (2 x 216 + 72 = 3 x 168, the launch's share).
 #define PISA_SOFTMAX_REGS "216"
@@ -58,7 +58,7 @@ struct Smem {
   uint8_t q[2][Cfg<D>::kTile];
   uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTile];
   uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
-  uint64_t qfull, scrub, sfull[2], pfull[2], odone[2], done;
+  uint64_t qfull, scrub, sfull[2], pfull[2][2], odone[2], done[2];
   int32_t lo[2], hi[2];  // keys that a tile's rows see
   uint32_t tmem;
   int32_t abort, zero, bad_page;
@@ -124,6 +124,20 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(x));
+  return x != 0;
+}
+
+// The two MMA warps' turns: warp v waits for its own, and hands over to the other.
+__device__ __forceinline__ void turn_wait(int v) { asm volatile("bar.sync %0, 64;" ::"r"(1 + v) : "memory"); }
+__device__ __forceinline__ void turn_pass(int v) { asm volatile("bar.arrive %0, 64;" ::"r"(2 - v) : "memory"); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -148,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   Smem<D>& sm =
       *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
 
   // which rows: the last tokens' CTAs, which see the most keys, come first
@@ -169,15 +183,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 2);
     }
     ptx::mbar_init(ptx::smem_u32(&sm.qfull), 1);
     ptx::mbar_init(ptx::smem_u32(&sm.scrub), 1);
-    ptx::mbar_init(ptx::smem_u32(&sm.done), 1);
     for (int w = 0; w < 2; ++w) {
       ptx::mbar_init(ptx::smem_u32(&sm.sfull[w]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.pfull[w]), 4);
+      ptx::mbar_init(ptx::smem_u32(&sm.pfull[w][0]), 4);
+      ptx::mbar_init(ptx::smem_u32(&sm.pfull[w][1]), 4);
       ptx::mbar_init(ptx::smem_u32(&sm.odone[w]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.done[w]), 1);
       sm.lo[w] = 0x7fffffff;
       sm.hi[w] = -1;
     }
@@ -255,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* trow = a.table + b * a.nb;
     int32_t entry = -1;  // lane l: the page of block 2 jc + l, -1: none of its keys is seen, -2: outside the pool
     auto wait_empty = [&](int f) {
-      const bool got = ptx::mbar_wait_bounded_hint(ptx::smem_u32(&sm.empty[f % kStages]), ((f / kStages) & 1) ^ 1,
-                                                   abort, kWaitNs, 1000);
+      const bool got = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[f % kStages]), ((f / kStages) & 1) ^ 1, abort,
+                                              kWaitNs);
       return __all_sync(0xffffffffu, got) != 0;
     };
     for (int j = ja; j < jb; ++j) {
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (scrub) {
           if (pages) {
-            const bool got = ptx::mbar_wait_bounded(bar, scrubs & 1, &sm.zero, kWaitNs);
+            const bool got = ptx::mbar_wait_fast(bar, scrubs & 1, &sm.zero, kWaitNs);
             ++scrubs;
             if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
           }
@@ -326,56 +341,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) *abort = 1;
     // every issued load lands before the CTA can end, whoever gave up
     if (lane == 0) {
-      if (act0 || act1) ptx::mbar_wait_bounded(ptx::smem_u32(&sm.qfull), 0, &sm.zero, kWaitNs);
+      if (act0 || act1) ptx::mbar_wait_fast(ptx::smem_u32(&sm.qfull), 0, &sm.zero, kWaitNs);
       for (int f = max(0, fills - kStages); f < fills; ++f)
-        ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero, kWaitNs);
+        ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero, kWaitNs);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ----------------------------------------------------------------- MMA
-    if (lane == 0 && (wa[0] < wb[0] || wa[1] < wb[1])) {
-      bool ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.qfull), 0, abort, kWaitNs);
-      auto wait_full = [&](int f) {
-        return ptx::mbar_wait_bounded(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, abort, kWaitNs);
+  } else if (warp < kLoadWarp) {
+    // ----------------------------------------------- the MMAs of row tile v
+    // The tensor pipe takes few MMAs ahead and a wait on an mbarrier costs some
+    // 300 cycles while the MMAs occupy shared memory, so each row tile has a
+    // warp of its own: one waits while the other's MMAs run.  They take turns
+    // (named barriers, which need no shared memory): a group -- O of key tile
+    // j, then S of key tile j + 1 -- goes in whole, so that the other tile's
+    // softmax runs beside it.  The softmax warps have seen V(j) and K(j + 1)
+    // land before they hand over weights, so that only pfull is waited for.
+    // All lanes run the loop, and what it branches on is broadcast, so that
+    // the descriptors stay in uniform registers; one elected lane issues.
+    const int v = warp - kMmaWarp;
+    const int av = __shfl_sync(0xffffffffu, v ? wa[1] : wa[0], 0), bv = __shfl_sync(0xffffffffu, v ? wb[1] : wb[0], 0);
+    const int uja = __shfl_sync(0xffffffffu, ja, 0), ujb = __shfl_sync(0xffffffffu, jb, 0);
+    const uint32_t ut = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t o = ut + 256 + v * D, sp = ut + v * 128, qb = ptx::smem_u32(sm.q[v]);
+    if (uja < ujb) {
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
       };
-      // step j: O of key tile j, then S of key tile j + 1, for each row tile
-      for (int j = ja - 1; j < jb && ok; ++j) {
-        const int fv = 2 * (j - ja) + 1, fk = 2 * (j + 1 - ja);  // fills of V(j) and K(j + 1)
-        if (j + 1 < jb && !(ok = wait_full(fk))) break;
-        if (j >= ja && !(ok = wait_full(fv))) break;
-        const uint32_t kb = ptx::smem_u32(sm.kv[fk % kStages]);
-        const uint32_t vb = ptx::smem_u32(sm.kv[j >= ja ? fv % kStages : 0]);
+      if (av < bv) wait(&sm.qfull, 0);
+      int st = 0, ph = 0;  // stage and phase of the next fill to release
+      // a warp that gave up keeps taking its turns, so that the other one ends
+      for (int j = uja - 1; j < ujb; ++j) {
+        const bool has_o = j >= av && j < bv, has_s = j + 1 >= av && j + 1 < bv;
+        const int sv = st, pv = ph;  // V(j)
+        if (j >= uja && ++st == kStages) { st = 0; ph ^= 1; }
+        const int sk = st, pk = ph;  // K(j + 1)
+        if (j + 1 < ujb && ++st == kStages) { st = 0; ph ^= 1; }
+        const uint32_t vb = ptx::smem_u32(sm.kv[sv]), kb = ptx::smem_u32(sm.kv[sk]);
+        if (has_o) {
+          wait(&sm.pfull[v][0], j - av);
+        } else {
+          if (j >= uja) wait(&sm.full[sv], pv);
+          if (j + 1 < ujb) wait(&sm.full[sk], pk);
+        }
+        if (v == 1 || j >= uja) turn_wait(v);
+        if (has_o) {
+          ptx::tc_fence_after();
+          if (ok && elect_one()) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          if (j >= wa[v] && j < wb[v]) {
-            ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.pfull[v]), (j - wa[v]) & 1, abort, kWaitNs);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const uint32_t o = tmem + 256 + v * D, p = tmem + v * 128;
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts_bf16(o, p + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, (j > wa[v] || k > 0) ? 1u : 0u);
-            if (j + 1 == wb[v]) ptx::mma_commit(ptx::smem_u32(&sm.odone[v]));
+            for (int k = 0; k < 4; ++k)
+              mma_ts_bf16(o, sp + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, (j > av || k > 0) ? 1u : 0u);
           }
-          if (j + 1 >= wa[v] && j + 1 < wb[v]) {
-            // over P of key tile j, which the MMAs above have read: they run in order
-            const uint32_t qb = ptx::smem_u32(sm.q[v]);
+          wait(&sm.pfull[v][1], j - av);
+          ptx::tc_fence_after();
+          if (ok && elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-              ptx::mma_bf16(tmem + v * 128, ptx::desc_sw128(qb + off), ptx::desc_sw128(kb + off), kIdescS,
-                            k > 0 ? 1u : 0u);
-            }
-            ptx::mma_commit(ptx::smem_u32(&sm.sfull[v]));
+            for (int k = 4; k < 8; ++k)
+              mma_ts_bf16(o, sp + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, 1u);
           }
         }
-        if (!ok) break;
-        if (j >= ja) ptx::mma_commit(ptx::smem_u32(&sm.empty[fv % kStages]));
-        if (j + 1 < jb) ptx::mma_commit(ptx::smem_u32(&sm.empty[fk % kStages]));
+        if (has_s && ok && elect_one()) {
+          // over P of key tile j, which the MMAs above read: they run in order
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+            ptx::mma_bf16(sp, ptx::desc_sw128(qb + off), ptx::desc_sw128(kb + off), kIdescS, k > 0 ? 1u : 0u);
+          }
+          ptx::mma_commit(ptx::smem_u32(&sm.sfull[v]));
+        }
+        __syncwarp();
+        if (v == 0 || j + 1 < ujb) turn_pass(v);
+        if (ok && elect_one()) {
+          if (has_o && j + 1 == bv) ptx::mma_commit(ptx::smem_u32(&sm.odone[v]));
+          if (j >= uja) ptx::mma_commit(ptx::smem_u32(&sm.empty[sv]));
+          if (j + 1 < ujb) ptx::mma_commit(ptx::smem_u32(&sm.empty[sk]));
+        }
+        __syncwarp();
+        if (!ok && lane == 0) *abort = 1;
       }
-      if (!ok) *abort = 1;
-      ptx::mma_commit(ptx::smem_u32(&sm.done));
-      ptx::mbar_wait_bounded(ptx::smem_u32(&sm.done), 0, &sm.zero, kWaitNs);
+      if (elect_one()) ptx::mma_commit(ptx::smem_u32(&sm.done[v]));
+      __syncwarp();
+      ptx::mbar_wait_fast(ptx::smem_u32(&sm.done[v]), 0, &sm.zero, kWaitNs);
     }
     __syncwarp();
   }
@@ -390,8 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float slope = MODE == 1 && mk.slopes && row ? mk.slopes[h * pr.G + g] * kLog2e : 0.0f;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    int st = (2 * (wa[w] - ja) + 1) % kStages, ph = ((2 * (wa[w] - ja) + 1) / kStages) & 1;  // of V(j)
     for (int j = wa[w]; j < wb[w]; ++j) {
-      ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.sfull[w]), (j - wa[w]) & 1, abort, kWaitNs);
+      ok = true;
+      if ((warp & 3) == 0) {
+        // for the MMA thread: V(j) and K(j + 1) are there (as a rule they are by now)
+        ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+        if (++st == kStages) { st = 0; ph ^= 1; }
+        if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+        if (++st == kStages) { st = 0; ph ^= 1; }
+      }
+      ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.sfull[w]), (j - wa[w]) & 1, abort, kWaitNs);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       ptx::tc_fence_after();
       float s[kKeys];
@@ -477,18 +531,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[k / 2] = pack_bf16(p0, p1);
         }
         tmem_st16(s_at + c / 2, pk);
+        if (c & 32) {  // half of the weights: the MMAs may start on them
+          tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w][c >> 6]));
+        }
       }
-      tmem_st_wait();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w]));
       float s0, s1;
       ptx::unpack2(ptx::add2(sum[0], sum[1]), s0, s1);
       l += s0 + s1;
     }
     const bool any = wa[w] < wb[w];
     if (ok && any) {
-      ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sm.odone[w]), 0, abort, kWaitNs);
+      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.odone[w]), 0, abort, kWaitNs);
       ok = __all_sync(0xffffffffu, ok) != 0;
       ptx::tc_fence_after();
     }

@@ -113,6 +113,18 @@ __device__ __forceinline__ bool mbar_wait_bounded_hint(uint32_t bar, uint32_t pa
   }
 }
 
+// As mbar_wait_bounded, for waits on the critical path of a pipeline: reading
+// the timer costs about 700 cycles, which a wait that ends sooner would pay
+// in full, so the clock only starts after a number of polls (each of which
+// may sleep in the barrier unit by itself).
+__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile int32_t* abort,
+                                               uint64_t limit_ns) {
+#pragma unroll 1
+  for (int it = 0; it < 256; ++it)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, abort, limit_ns);
+}
+
 // ------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
                                             uint32_t bar) {
