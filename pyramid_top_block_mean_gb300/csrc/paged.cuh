@@ -24,6 +24,9 @@ struct Pools {
 struct MaskArgs {
   float cap2;                  // softcap * log2(e), 0: none
   float pre;                   // with a cap: scale / softcap, the argument of tanh per unit of q . k
+  // cap2 tanh(pre x) = x (tk[0] + x^2 (tk[1] + x^2 (tk[2] + x^2 tk[3]))) for |x| <= tlim, off by less than 2^-22 cap2:
+  // the odd polynomial of degree 7 whose largest error over |pre x| <= 1/2 is least
+  float tk[4], tlim;
   int64_t window;              // 0: none
   const float* slopes;         // null: none
   const int32_t* first_key;    // null: none; [B, n]

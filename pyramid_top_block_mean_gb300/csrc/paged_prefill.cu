@@ -142,6 +142,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// The factor that caps two small scores (MaskArgs::tk).
+__device__ __forceinline__ uint64_t cap_factor(const MaskArgs& m, uint64_t x2) {
+  const uint64_t w2 = mul2(x2, x2);
+  uint64_t f = ptx::fma2(w2, ptx::pack2(m.tk[3], m.tk[3]), ptx::pack2(m.tk[2], m.tk[2]));
+  f = ptx::fma2(w2, f, ptx::pack2(m.tk[1], m.tk[1]));
+  return ptx::fma2(w2, f, ptx::pack2(m.tk[0], m.tk[0]));
+}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -453,31 +465,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
       ptx::tmem_ld_wait();
       const int32_t key0 = j * kKeys;
-      if (MODE == 1) {
-        if (mk.cap2 > 0.0f) {
-          // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
-          const float pre = mk.pre * (2.0f * kLog2e);
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            s[c] = fmaf(-2.0f * mk.cap2, rcp_approx(1.0f + ptx::ex2(s[c] * pre)), mk.cap2);
-        } else {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] *= pr.scale2;
-        }
-        if (mk.slopes) {
-          const float base = slope * (float)(int32_t)(key0 - t);
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] += fmaf(slope, (float)c, base);
-        }
-      }
       // keys clo .. chi of the tile are seen
       const int32_t clo = max(lo, key0) - key0, chi = min(hi, key0 + kKeys - 1) - key0;
-      if (__any_sync(0xffffffffu, clo > 0 || chi < kKeys - 1)) {
+      const bool bad = *(volatile int32_t*)&sm.bad_page != 0;
+      const bool part = __any_sync(0xffffffffu, clo > 0 || chi < kKeys - 1) || bad;
+      bool late = false;  // the cap is applied on the way to the exponential
+      if (MODE == 1) {
+        if (mk.cap2 > 0.0f) {
+          float big[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            big[k] = fmaxf(fabsf(s[32 * k]), fabsf(s[32 * k + 1]));
+#pragma unroll
+            for (int c = 2; c < 32; c += 2) big[k] = ptx::max3(big[k], fabsf(s[32 * k + c]), fabsf(s[32 * k + c + 1]));
+          }
+          // small scores: a polynomial on the FMA pipe, two at a time (the
+          // exponential and the reciprocal of the other way take 12 cycles of
+          // the SFU a warp, three times what the softmax takes itself)
+          if (__all_sync(0xffffffffu, fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) <= mk.tlim)) {
+            late = !part && !mk.slopes;  // the cap is monotone: the largest score stays the largest
+            if (!late) {
+#pragma unroll
+              for (int c = 0; c < kKeys; c += 2)
+                ptx::unpack2(mul2(ptx::pack2(s[c], s[c + 1]), cap_factor(mk, ptx::pack2(s[c], s[c + 1]))), s[c],
+                             s[c + 1]);
+            }
+          } else {
+            // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
+            const float pre = mk.pre * (2.0f * kLog2e);
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              s[c] = fmaf(-2.0f * mk.cap2, rcp_approx(1.0f + ptx::ex2(s[c] * pre)), mk.cap2);
+          }
+        }
+        if (mk.slopes) {
+          // bias slope (j - t), j - t exact up to the fp32 product
+          const float rel = (float)(int32_t)(key0 - t);
+          const float by = mk.cap2 > 0.0f ? 1.0f : pr.scale2;
+          const uint64_t by2 = ptx::pack2(by, by), slope2 = ptx::pack2(slope, slope), two = ptx::pack2(2.0f, 2.0f);
+          uint64_t j2 = ptx::pack2(rel, rel + 1.0f);
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 2) {
+            ptx::unpack2(ptx::fma2(ptx::pack2(s[c], s[c + 1]), by2, mul2(slope2, j2)), s[c], s[c + 1]);
+            j2 = ptx::add2(j2, two);
+          }
+        }
+      }
+      if (part) {
 #pragma unroll
         for (int c = 0; c < kKeys; ++c)
           if (c < clo || c > chi) s[c] = -INFINITY;
       }
-      if (*(volatile int32_t*)&sm.bad_page) {
+      if (bad) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const int64_t blk = 2 * (int64_t)j + p;
@@ -495,7 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 2; c < 32; c += 2) mx[k] = ptx::max3(mx[k], s[32 * k + c], s[32 * k + c + 1]);
       }
-      const float top = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
+      float top = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
+      if (MODE == 1 && late) {
+        float unused;
+        ptx::unpack2(mul2(ptx::pack2(top, top), cap_factor(mk, ptx::pack2(top, top))), top, unused);
+      }
       const bool grow = top > m + slack || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow && m > -INFINITY ? ptx::ex2((m - top) * sc) : 1.0f;
@@ -517,27 +560,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float neg = m == -INFINITY ? 0.0f : -m * sc;
       const uint64_t sc2 = ptx::pack2(sc, sc), neg2 = ptx::pack2(neg, neg);
       uint64_t sum[2] = {0ull, 0ull};
+      // weights of the row, 32 at a time, from the exponents of two scores
+      auto weights = [&](auto exponents) {
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) {
-        uint32_t pk[16];
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float p0, p1;
-          ptx::unpack2(ptx::fma2(ptx::pack2(s[c + k], s[c + k + 1]), sc2, neg2), p0, p1);
-          p0 = ptx::ex2(p0);
-          p1 = ptx::ex2(p1);
-          sum[(k >> 1) & 1] = ptx::add2(sum[(k >> 1) & 1], ptx::pack2(p0, p1));
-          // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step); l is not
-          pk[k / 2] = pack_bf16(p0, p1);
+          for (int k = 0; k < 32; k += 2) {
+            float p0, p1;
+            ptx::unpack2(exponents(ptx::pack2(s[c + k], s[c + k + 1])), p0, p1);
+            p0 = ptx::ex2(p0);
+            p1 = ptx::ex2(p1);
+            sum[(k >> 1) & 1] = ptx::add2(sum[(k >> 1) & 1], ptx::pack2(p0, p1));
+            // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step); l is not
+            pk[k / 2] = pack_bf16(p0, p1);
+          }
+          tmem_st16(s_at + c / 2, pk);
+          if (c & 32) {  // half of the weights: the MMAs may start on them
+            tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w][c >> 6]));
+          }
         }
-        tmem_st16(s_at + c / 2, pk);
-        if (c & 32) {  // half of the weights: the MMAs may start on them
-          tmem_st_wait();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w][c >> 6]));
-        }
-      }
+      };
+      if (MODE == 1 && late) weights([&](uint64_t x2) { return ptx::fma2(x2, cap_factor(mk, x2), neg2); });
+      else weights([&](uint64_t x2) { return ptx::fma2(x2, sc2, neg2); });
       float s0, s1;
       ptx::unpack2(ptx::add2(sum[0], sum[1]), s0, s1);
       l += s0 + s1;
@@ -621,16 +669,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && sm.abort) set_status(a.status, PISA_DEV_TIMEOUT);
 }
 
-// Joins the parts of a row: one thread per (row, 8 dims).
+// Joins the parts of a row: one CTA per row, 8 dims x every 16th part a
+// thread, so that all loads of a row are in flight at once.
 template <int D>
-__global__ void __launch_bounds__(256) prefill_join_kernel(Prob pr, Args a) {
-  pdl_wait();
-  constexpr int CH = D / 8;
+__global__ void __launch_bounds__(D * 2) prefill_join_kernel(Prob pr, Args a) {
+  constexpr int CH = D / 8, PL = 16;
+  __shared__ float sm_m[PL], sm_l[PL];
+  __shared__ float sm_o[PL][D];
   const int64_t rows = (int64_t)a.tiles * pr.B * pr.Hkv * (2 * kRows);
-  const int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int ch = (int)(e % CH);
-  const int64_t at = e / CH;
-  if (at >= rows) return;
+  const int64_t at = blockIdx.x;
+  const int ch = threadIdx.x % CH, pl = threadIdx.x / CH;
   const int r = (int)(at & 127), w = (int)(at >> 7 & 1);
   const int64_t bh = (at >> 8) % (pr.B * pr.Hkv);
   const int64_t tile = (at >> 8) / (pr.B * pr.Hkv);
@@ -640,22 +688,21 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(Prob pr, Args a) {
   int64_t len, cnt;
   new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
   if (i >= cnt) return;
+  pdl_wait();  // the lengths are the caller's, the parts the kernel's before
   float M = -INFINITY, L = 0.0f, acc[8] = {};
   constexpr int kBatch = 4;
-  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+  for (int s0 = pl; s0 < a.splits; s0 += PL * kBatch) {
     float2 ml[kBatch];
     float4 o[kBatch][2];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       ml[k] = make_float2(-INFINITY, 0.0f);
       o[k][0] = o[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (s0 + k < a.splits) {
-        const int64_t p = (int64_t)(s0 + k) * rows + at;
+      if (s0 + PL * k < a.splits) {
+        const int64_t p = (int64_t)(s0 + PL * k) * rows + at;
         ml[k] = *reinterpret_cast<const float2*>(a.part_ml + 2 * p);
-        if (ml[k].y != 0.0f) {  // a part that saw no key wrote no output
-          o[k][0] = *reinterpret_cast<const float4*>(a.part_o + p * D + 8 * ch);
-          o[k][1] = *reinterpret_cast<const float4*>(a.part_o + p * D + 8 * ch + 4);
-        }
+        o[k][0] = *reinterpret_cast<const float4*>(a.part_o + p * D + 8 * ch);
+        o[k][1] = *reinterpret_cast<const float4*>(a.part_o + p * D + 8 * ch + 4);
       }
     }
     float bm = M;
@@ -670,6 +717,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(Prob pr, Args a) {
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
+      if (ml[k].y == 0.0f) continue;  // a part that saw no key wrote no output
       const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
       L = fmaf(ml[k].y, f, L);
       const float ov[8] = {o[k][0].x, o[k][0].y, o[k][0].z, o[k][0].w, o[k][1].x, o[k][1].y, o[k][1].z, o[k][1].w};
@@ -677,14 +725,29 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(Prob pr, Args a) {
       for (int d = 0; d < 8; ++d) acc[d] = fmaf(ov[d], f, acc[d]);
     }
   }
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  if (ch == 0) {
+    sm_m[pl] = M;
+    sm_l[pl] = L;
+  }
+#pragma unroll
+  for (int d = 0; d < 8; ++d) sm_o[pl][8 * ch + d] = acc[d];
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  const int d = 2 * threadIdx.x;
+  float top = -INFINITY, total = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+  for (int k = 0; k < PL; ++k) top = fmaxf(top, sm_m[k]);
+#pragma unroll
+  for (int k = 0; k < PL; ++k) {
+    if (sm_l[k] == 0.0f) continue;
+    const float f = sm_m[k] == -INFINITY ? 1.0f : ptx::ex2(sm_m[k] - top);
+    total = fmaf(sm_l[k], f, total);
+    x = fmaf(sm_o[k][d], f, x);
+    y = fmaf(sm_o[k][d + 1], f, y);
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t hq = (bh % pr.Hkv) * pr.G + (r >> a.lg_tokens);
-  uint4 v;
-  v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
-  v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-  v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
-  v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4*>(a.out + ((b * pr.Hq + hq) * a.n + i) * D + 8 * ch) = v;
+  *reinterpret_cast<uint32_t*>(a.out + ((b * pr.Hq + hq) * a.n + i) * D + d) = pack_bf16(x * inv, y * inv);
 }
 
 // Grid of a call.  A GPU that has fewer CTAs than SMs gets the rows' keys
@@ -724,8 +787,7 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const Plan& pl, const CU
   e = cudaGetLastError();
   if (e != cudaSuccess || pl.splits == 1) return e;
   note_launch();
-  return launch_pdl(true, prefill_join_kernel<D>, dim3((unsigned)ceil_div64(pl.ctas * 2 * kRows * (D / 8), 256)),
-                    dim3(256), 0, st, pr, a);
+  return launch_pdl(true, prefill_join_kernel<D>, dim3((unsigned)(pl.ctas * 2 * kRows)), dim3(D * 2), 0, st, pr, a);
 }
 
 }  // namespace
@@ -752,7 +814,7 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   a.part_ml = (float*)(ws + pl.ml);
   a.part_o = (float*)(ws + pl.o);
   a.tiles = pl.tiles; a.splits = pl.splits; a.lg_tokens = pl.lg_tokens;
-  const bool shaped = m.cap2 > 0.0f || m.slopes;
+  const bool shaped = m.cap2 > 0.0f || m.slopes;  // scores that are more than scaled dots
   if (pr.d == 128)
     return shaped ? launch_t<128, 1>(pr, m, pl, qmap, kmap, vmap, a, st)
                   : launch_t<128, 0>(pr, m, pl, qmap, kmap, vmap, a, st);
