@@ -168,6 +168,8 @@ pisa_status pisa_dense_prefill_paged(const pisa_params* p, const pisa_mask* mask
   rc = pool_checks(pr, s, k_pages, v_pages, num_pages, page_table, seq_lens, ws, &pools);
   if (rc != PISA_OK) return rc;
   if (!aligned16(q) || !aligned16(out) || !aligned4(new_lens)) return PISA_ERR_MISALIGNED;
+  // groups of rows (16 tokens and more of a key head) are numbered in 32 bits
+  if (pr.B * pr.Hkv * ceil_div64(n, 32) >= ((int64_t)1 << 31)) return PISA_ERR_UNSUPPORTED;
   if (ws_bytes < paged_prefill_ws_bytes(pr, n)) return PISA_ERR_WORKSPACE;
   return cuda_status(launch_paged_prefill(pr, m, n, q, pools, seq_lens, new_lens, (char*)ws, out,
                                           (cudaStream_t)stream));

@@ -53,13 +53,28 @@ struct Cfg {
   static constexpr uint32_t kTile = kKeys * D * 2;  // bytes of a key or value tile, and of a query tile
 };
 
+constexpr int kItems = 2;  // items in flight: the loader is at most one ahead
+
+// What the loader tells the other warps about an item: 256 rows against a run
+// of key tiles.
+struct Item {
+  int32_t bh, tile, split;  // bh < 0: no more items
+  int32_t len, cnt;         // of the sequence; cnt rows before it are new
+  int32_t fits;             // its lengths do
+  int32_t ja, jb;           // key tiles
+  int32_t wa[2], wb[2];     // and those that each row tile takes part in
+  int32_t khi;              // last key that any row sees
+  int32_t fill;             // fills of the ring before the item's first
+};
+
 template <int D>
 struct Smem {
   uint8_t q[2][Cfg<D>::kTile];
   uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTile];
   uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
-  uint64_t qfull, scrub, sfull[2], pfull[2][2], odone[2], done[2];
-  int32_t lo[2], hi[2];  // keys that a tile's rows see
+  uint64_t ifull[kItems], iempty[kItems];
+  uint64_t qfull[2], qempty[2], scrub, sfull[2], pfull[2][2], odone[2], done[2];
+  Item item[kItems];
   uint32_t tmem;
   int32_t abort, zero, bad_page;
 };
@@ -67,10 +82,12 @@ struct Smem {
 struct Args {
   int64_t n, nb, num_pages;
   const int32_t *seq_lens, *new_lens, *table;
-  int32_t* status;
+  int32_t *status, *claimed;  // claimed: items taken beyond each CTA's first
   uint16_t* out;
-  float *part_o, *part_ml;  // [split][cta][256][D] and [..][2] (m in log2 units, l)
-  int32_t tiles, splits, lg_tokens;  // CTAs per (sequence, key head), splits, log2 of a tile's tokens
+  float *part_o, *part_ml;  // [split][256-row group][256][D] and [..][2] (m in log2 units, l)
+  // 256-row groups per (sequence, key head), parts of the keys, log2 of a tile's tokens, items in all
+  int32_t tiles, splits, lg_tokens, items;
+  int32_t wide;  // outputs and parts start on 32-byte boundaries
 };
 
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
@@ -102,15 +119,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -131,6 +146,36 @@ __device__ __forceinline__ bool elect_one() {
       "elect.sync _|p, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(x));
+  return x != 0;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// 32 bytes, in one store where the address allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], int wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+// Both MMA warps meet; true for both if both say so.
+__device__ __forceinline__ bool both_ok(bool ok) {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 3, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(x)
+      : "r"((uint32_t)ok)
+      : "memory");
   return x != 0;
 }
 
@@ -177,36 +222,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
 
-  // which rows: the last tokens' CTAs, which see the most keys, come first
-  int64_t x = blockIdx.x;
-  const int split = (int)(x % a.splits);
-  x /= a.splits;
-  const int64_t bh = x % (pr.B * pr.Hkv);
-  const int tile = a.tiles - 1 - (int)(x / (pr.B * pr.Hkv));
-  const int64_t b = bh / pr.Hkv;
-  const int h = (int)(bh % pr.Hkv);
-  const int tokens = 1 << a.lg_tokens;  // of one tile
-  int64_t len, cnt;
-  const bool fits = new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
-  const int64_t i0 = (int64_t)tile * 2 * tokens;
-  if (!fits && threadIdx.x == 0) set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
-  if (i0 >= cnt) return;
-
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 2);
+    for (int k = 0; k < kStages; ++k) {
+      ptx::mbar_init(ptx::smem_u32(&sm.full[k]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[k]), 2);
     }
-    ptx::mbar_init(ptx::smem_u32(&sm.qfull), 1);
+    for (int k = 0; k < kItems; ++k) {
+      ptx::mbar_init(ptx::smem_u32(&sm.ifull[k]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.iempty[k]), 10);
+    }
     ptx::mbar_init(ptx::smem_u32(&sm.scrub), 1);
-    for (int w = 0; w < 2; ++w) {
-      ptx::mbar_init(ptx::smem_u32(&sm.sfull[w]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.pfull[w][0]), 4);
-      ptx::mbar_init(ptx::smem_u32(&sm.pfull[w][1]), 4);
-      ptx::mbar_init(ptx::smem_u32(&sm.odone[w]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.done[w]), 1);
-      sm.lo[w] = 0x7fffffff;
-      sm.hi[w] = -1;
+    for (int v = 0; v < 2; ++v) {
+      ptx::mbar_init(ptx::smem_u32(&sm.qfull[v]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.qempty[v]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.sfull[v]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.pfull[v][0]), 4);
+      ptx::mbar_init(ptx::smem_u32(&sm.pfull[v][1]), 4);
+      ptx::mbar_init(ptx::smem_u32(&sm.odone[v]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.done[v]), 1);
     }
     sm.abort = 0;
     sm.zero = 0;
@@ -214,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
+  if (warp == kLoadWarp && lane < 3) prefetch_map(lane == 0 ? &qmap : (lane == 1 ? &kmap : &vmap));
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&sm.tmem), 512);
     ptx::tmem_relinquish();
@@ -222,444 +256,513 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem;
-
-  // this thread's row (softmax warps) and the keys that it sees
-  const int w = warp >> 2, r = threadIdx.x & 127;
-  const int64_t i = i0 + (int64_t)w * tokens + (r & (tokens - 1));
-  const int g = r >> a.lg_tokens;
-  const bool row = warp < 8 && i < cnt;
-  const int64_t t = len - cnt + i;
-  int32_t lo = 0x7fffffff, hi = -1;
-  if (row && fits) {
-    int64_t l, u;
-    key_span(mk, b, a.n, i, t, len, &l, &u);
-    if (l <= u) {
-      lo = (int32_t)l;
-      hi = (int32_t)u;
-    }
-  }
-  if (warp < 8) {
-    const int32_t wlo = __reduce_min_sync(0xffffffffu, lo), whi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      atomicMin(&sm.lo[w], wlo);
-      atomicMax(&sm.hi[w], whi);
-    }
-  }
-  __syncthreads();
-  // key tiles: this split's share [ja, jb) of the CTA's, and each tile's own part of it
-  const int32_t klo = min(sm.lo[0], sm.lo[1]), khi = max(sm.hi[0], sm.hi[1]);
-  int ja = 0, jb = 0, wa[2], wb[2];
-  if (khi >= 0) {
-    const int a0 = klo / kKeys, cntj = khi / kKeys + 1 - a0;
-    ja = a0 + (int)((int64_t)cntj * split / a.splits);
-    jb = a0 + (int)((int64_t)cntj * (split + 1) / a.splits);
-  }
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    wa[v] = sm.hi[v] < 0 ? jb : max(ja, sm.lo[v] / kKeys);
-    wb[v] = sm.hi[v] < 0 ? jb : min(jb, sm.hi[v] / kKeys + 1);
-    if (wb[v] < wa[v]) wb[v] = wa[v];
-  }
+  const int tokens = 1 << a.lg_tokens;  // of one row tile
+  const uint32_t heads = (uint32_t)(pr.B * pr.Hkv);
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_OTHER_REGS ";");
-  if (warp == kLoadWarp) {
-    // -------------------------------------------------------------- loader
-    bool ok = true;
-    int fills = 0, scrubs = 0;
-    const bool act0 = wa[0] < wb[0], act1 = wa[1] < wb[1];
-    if (lane == 0 && (act0 || act1)) {
-      const uint32_t bar = ptx::smem_u32(&sm.qfull);
-      ptx::mbar_arrive_expect_tx(bar, kTile * ((act0 ? 1 : 0) + (act1 ? 1 : 0)));
-      for (int v = 0; v < 2; ++v) {
-        if (!(v ? act1 : act0)) continue;
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------ loader
+      bool ok = true;
+      int fills = 0, scrubs = 0, items = 0, qfills[2] = {0, 0};
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
+        return ok;
+      };
+      auto claim = [&] {
+        int32_t k = 0;
+        if (lane == 0) k = (int32_t)gridDim.x + atomicAdd(a.claimed, 1);
+        return __shfl_sync(0xffffffffu, k, 0);
+      };
+      // the last tokens' items, which see the most keys, come first; a CTA
+      // that has loaded what its item needs claims the next one
+      for (int32_t now = blockIdx.x; ok && now < a.items; now = claim()) {
+        uint32_t x = (uint32_t)now;
+        Item it;
+        it.split = (int32_t)(x % (uint32_t)a.splits);
+        x /= (uint32_t)a.splits;
+        it.bh = (int32_t)(x % heads);
+        it.tile = a.tiles - 1 - (int32_t)(x / heads);
+        const int64_t b = (uint32_t)it.bh / (uint32_t)pr.Hkv;
+        const int h = it.bh - (int)b * pr.Hkv;
+        const int64_t i0 = (int64_t)it.tile * 2 * tokens;
+        int64_t len, cnt;
+        it.fits = new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
+        if (!it.fits && lane == 0) set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
+        if (i0 >= cnt) continue;
+        it.len = (int32_t)len;
+        it.cnt = (int32_t)cnt;
+        // keys that each row tile sees
+        int32_t lo[2], hi[2];
 #pragma unroll
-        for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_4d(ptx::smem_u32(sm.q[v]) + hh * kHalf, &qmap, 64 * hh, (int32_t)(i0 + (int64_t)v * tokens),
-                      h * pr.G, (int32_t)b, bar);
-      }
-    }
-    const int32_t* trow = a.table + b * a.nb;
-    int32_t entry = -1;  // lane l: the page of block 2 jc + l, -1: none of its keys is seen, -2: outside the pool
-    auto wait_empty = [&](int f) {
-      const bool got = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[f % kStages]), ((f / kStages) & 1) ^ 1, abort,
-                                              kWaitNs);
-      return __all_sync(0xffffffffu, got) != 0;
-    };
-    for (int j = ja; j < jb; ++j) {
-      const int at = (j - ja) & 15;
-      if (at == 0) {
-        const int32_t blk = 2 * j + lane;
-        entry = -1;
-        if ((int64_t)blk * kPage <= khi && (int64_t)blk * kPage + kPage > klo && blk < 2 * jb) {
-          entry = trow[blk];
-          if (entry < 0 || entry >= a.num_pages) {
-            entry = -2;
-            set_status(a.status, PISA_DEV_BAD_INDEX);
-            *(volatile int32_t*)&sm.bad_page = 1;
+        for (int v = 0; v < 2; ++v) {
+          lo[v] = 0x7fffffff;
+          hi[v] = -1;
+          for (int k = lane; k < tokens && it.fits; k += 32) {
+            const int64_t i = i0 + (int64_t)v * tokens + k;
+            if (i >= cnt) break;
+            int64_t l, u;
+            key_span(mk, b, a.n, i, len - cnt + i, len, &l, &u);
+            if (l > u) continue;
+            lo[v] = min(lo[v], (int32_t)l);
+            hi[v] = max(hi[v], (int32_t)u);
           }
+          lo[v] = __reduce_min_sync(0xffffffffu, lo[v]);
+          hi[v] = __reduce_max_sync(0xffffffffu, hi[v]);
+        }
+        const int32_t klo = min(lo[0], lo[1]), khi = max(hi[0], hi[1]);
+        it.ja = it.jb = 0;
+        if (khi >= 0) {
+          const int j0 = klo / kKeys;
+          const uint32_t cntj = (uint32_t)(khi / kKeys + 1 - j0);
+          it.ja = j0 + (int)(a.splits == 1 ? 0 : (uint64_t)cntj * it.split / (uint32_t)a.splits);
+          it.jb = j0 + (int)(a.splits == 1 ? cntj : (uint64_t)cntj * (it.split + 1) / (uint32_t)a.splits);
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          it.wa[v] = hi[v] < 0 ? it.jb : max(it.ja, lo[v] / kKeys);
+          it.wb[v] = hi[v] < 0 ? it.jb : min(it.jb, hi[v] / kKeys + 1);
+          if (it.wb[v] < it.wa[v]) it.wb[v] = it.wa[v];
+        }
+        it.khi = khi;
+        it.fill = fills;
+        const int is = items % kItems;
+        if (!wait(&sm.iempty[is], (items / kItems) + 1)) break;
+        if (lane == 0) {
+          sm.item[is] = it;
+          ptx::mbar_arrive(ptx::smem_u32(&sm.ifull[is]));
         }
         __syncwarp();
-      }
-      const int32_t pg[2] = {__shfl_sync(0xffffffffu, entry, 2 * at), __shfl_sync(0xffffffffu, entry, 2 * at + 1)};
-      const int pages = (pg[0] >= 0) + (pg[1] >= 0);
-      // values that no row of the CTA sees (behind the sequence's end among
-      // them) may be anything, and a weight of zero does not undo a NaN: they
-      // are cleared before the MMA reads the tile
-      const int32_t key0 = j * kKeys;
-      const bool clear = key0 < klo || key0 + kKeys - 1 > khi || pages < 2;
+        ++items;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!(ok = wait_empty(fills))) break;
-        const int st = fills % kStages;
-        const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
-        const bool scrub = kv == 1 && clear;
-        const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
-        if (lane == 0) {
-          if (pages) ptx::mbar_arrive_expect_tx(bar, pages * (kTile / 2));
-          else if (!scrub) ptx::mbar_arrive(bar);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            if (pg[p] < 0) continue;
-            const int32_t y = (int32_t)(((int64_t)pg[p] * pr.Hkv + h) * kPage);
+        for (int v = 0; v < 2; ++v) {
+          if (it.wa[v] >= it.wb[v]) continue;
+          if (!wait(&sm.qempty[v], qfills[v] + 1)) break;
+          ++qfills[v];
+          if (lane == 0) {
+            const uint32_t bar = ptx::smem_u32(&sm.qfull[v]);
+            ptx::mbar_arrive_expect_tx(bar, kTile);
 #pragma unroll
             for (int hh = 0; hh < D / 64; ++hh)
-              ptx::tma_load_2d(dst + hh * kHalf + p * kPageHalf, kv ? &vmap : &kmap, 64 * hh, y, bar);
+              tma_load_4d(ptx::smem_u32(sm.q[v]) + hh * kHalf, &qmap, 64 * hh, (int32_t)i0 + v * tokens, h * pr.G,
+                          (int32_t)b, bar);
           }
-        }
-        if (scrub) {
-          if (pages) {
-            const bool got = ptx::mbar_wait_fast(bar, scrubs & 1, &sm.zero, kWaitNs);
-            ++scrubs;
-            if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
-          }
-          for (int e = lane; e < kKeys * 8; e += 32) {
-            const int rr = e >> 3;
-            const int32_t key = key0 + rr;
-            if (key < klo || key > khi || pg[rr >> 6] < 0) {
-#pragma unroll
-              for (int hh = 0; hh < D / 64; ++hh)
-                *reinterpret_cast<uint4*>(sm.kv[st] + hh * kHalf + rr * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(full);
         }
-        ++fills;
+        const int32_t* trow = a.table + b * a.nb;
+        int32_t entry = -1;  // lane l: the page of block 2 jc + l, -1: none of its keys is seen, -2: outside the pool
+        for (int j = it.ja; j < it.jb && ok; ++j) {
+          const int at = (j - it.ja) & 15;
+          if (at == 0) {
+            const int32_t blk = 2 * j + lane;
+            entry = -1;
+            if ((int64_t)blk * kPage <= khi && (int64_t)blk * kPage + kPage > klo && blk < 2 * it.jb) {
+              entry = trow[blk];
+              if (entry < 0 || entry >= a.num_pages) {
+                entry = -2;
+                set_status(a.status, PISA_DEV_BAD_INDEX);
+                *(volatile int32_t*)&sm.bad_page = 1;
+              }
+            }
+            __syncwarp();
+          }
+          const int32_t pg[2] = {__shfl_sync(0xffffffffu, entry, 2 * at), __shfl_sync(0xffffffffu, entry, 2 * at + 1)};
+          const int pages = (pg[0] >= 0) + (pg[1] >= 0);
+          // values that no row of the item sees (behind the sequence's end among
+          // them) may be anything, and a weight of zero does not undo a NaN:
+          // they are cleared before the MMA reads the tile
+          const int32_t key0 = j * kKeys;
+          const bool clear = key0 < klo || key0 + kKeys - 1 > khi || pages < 2;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = fills % kStages;
+            if (!wait(&sm.empty[st], fills / kStages + 1)) break;
+            const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
+            const bool scrub = kv == 1 && clear;
+            const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
+            if (lane == 0) {
+              if (pages) ptx::mbar_arrive_expect_tx(bar, pages * (kTile / 2));
+              else if (!scrub) ptx::mbar_arrive(bar);
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                if (pg[p] < 0) continue;
+                const int32_t y = (int32_t)(((int64_t)pg[p] * pr.Hkv + h) * kPage);
+#pragma unroll
+                for (int hh = 0; hh < D / 64; ++hh)
+                  ptx::tma_load_2d(dst + hh * kHalf + p * kPageHalf, kv ? &vmap : &kmap, 64 * hh, y, bar);
+              }
+            }
+            __syncwarp();
+            if (scrub) {
+              if (pages) {
+                const bool got = ptx::mbar_wait_fast(bar, scrubs & 1, &sm.zero, kWaitNs);
+                ++scrubs;
+                if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
+              }
+              for (int e = lane; e < kKeys * 8; e += 32) {
+                const int rr = e >> 3;
+                const int32_t key = key0 + rr;
+                if (key < klo || key > khi || (rr < kPage ? pg[0] : pg[1]) < 0) {
+#pragma unroll
+                  for (int hh = 0; hh < D / 64; ++hh)
+                    *reinterpret_cast<uint4*>(sm.kv[st] + hh * kHalf + rr * 128 + (e & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+              }
+              ptx::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(full);
+            }
+            ++fills;
+          }
+        }
       }
-      if (!ok) break;
-    }
-    if (!ok && lane == 0) *abort = 1;
-    // every issued load lands before the CTA can end, whoever gave up
-    if (lane == 0) {
-      if (act0 || act1) ptx::mbar_wait_fast(ptx::smem_u32(&sm.qfull), 0, &sm.zero, kWaitNs);
-      for (int f = max(0, fills - kStages); f < fills; ++f)
-        ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero, kWaitNs);
-    }
-    __syncwarp();
-  } else if (warp < kLoadWarp) {
-    // ----------------------------------------------- the MMAs of row tile v
-    // The tensor pipe takes few MMAs ahead and a wait on an mbarrier costs some
-    // 300 cycles while the MMAs occupy shared memory, so each row tile has a
-    // warp of its own: one waits while the other's MMAs run.  They take turns
-    // (named barriers, which need no shared memory): a group -- O of key tile
-    // j, then S of key tile j + 1 -- goes in whole, so that the other tile's
-    // softmax runs beside it.  The softmax warps have seen V(j) and K(j + 1)
-    // land before they hand over weights, so that only pfull is waited for.
-    // All lanes run the loop, and what it branches on is broadcast, so that
-    // the descriptors stay in uniform registers; one elected lane issues.
-    const int v = warp - kMmaWarp;
-    const int av = __shfl_sync(0xffffffffu, v ? wa[1] : wa[0], 0), bv = __shfl_sync(0xffffffffu, v ? wb[1] : wb[0], 0);
-    const int uja = __shfl_sync(0xffffffffu, ja, 0), ujb = __shfl_sync(0xffffffffu, jb, 0);
-    const uint32_t ut = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t o = ut + 256 + v * D, sp = ut + v * 128, qb = ptx::smem_u32(sm.q[v]);
-    if (uja < ujb) {
+      if (wait(&sm.iempty[items % kItems], (items / kItems) + 1) && lane == 0) {
+        sm.item[items % kItems].bh = -1;
+        ptx::mbar_arrive(ptx::smem_u32(&sm.ifull[items % kItems]));
+      }
+      if (!ok && lane == 0) *abort = 1;
+      // every issued load lands before the CTA can end, whoever gave up
+      if (lane == 0) {
+        for (int v = 0; v < 2; ++v)
+          if (qfills[v]) ptx::mbar_wait_fast(ptx::smem_u32(&sm.qfull[v]), (qfills[v] - 1) & 1, &sm.zero, kWaitNs);
+        for (int f = max(0, fills - kStages); f < fills; ++f)
+          ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero, kWaitNs);
+      }
+      __syncwarp();
+    } else if (warp < kLoadWarp) {
+      // --------------------------------------------- the MMAs of row tile v
+      // The tensor pipe takes few MMAs ahead and a wait on an mbarrier costs
+      // some 300 cycles while the MMAs occupy shared memory, so each row tile
+      // has a warp of its own: one waits while the other's MMAs run.  They
+      // take turns (named barriers, which need no shared memory): a group -- O
+      // of key tile j, then S of key tile j + 1 -- goes in whole, so that the
+      // other tile's softmax runs beside it.  The softmax warps have seen V(j)
+      // and K(j + 1) land before they hand over weights, so that only pfull is
+      // waited for.  All lanes run the loop, and what it branches on is
+      // broadcast, so that the descriptors stay in uniform registers (an MMA
+      // then takes about 70 cycles to issue, not 100); one elected lane issues.
+      const int v = warp - kMmaWarp;
+      const uint32_t ut = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t o = ut + 256 + v * D, sp = ut + v * 128, qb = ptx::smem_u32(sm.q[v]);
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
         ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
       };
-      if (av < bv) wait(&sm.qfull, 0);
-      int st = 0, ph = 0;  // stage and phase of the next fill to release
-      // a warp that gave up keeps taking its turns, so that the other one ends
-      for (int j = uja - 1; j < ujb; ++j) {
-        const bool has_o = j >= av && j < bv, has_s = j + 1 >= av && j + 1 < bv;
-        const int sv = st, pv = ph;  // V(j)
-        if (j >= uja && ++st == kStages) { st = 0; ph ^= 1; }
-        const int sk = st, pk = ph;  // K(j + 1)
-        if (j + 1 < ujb && ++st == kStages) { st = 0; ph ^= 1; }
-        const uint32_t vb = ptx::smem_u32(sm.kv[sv]), kb = ptx::smem_u32(sm.kv[sk]);
-        if (has_o) {
-          wait(&sm.pfull[v][0], j - av);
-        } else {
-          if (j >= uja) wait(&sm.full[sv], pv);
-          if (j + 1 < ujb) wait(&sm.full[sk], pk);
-        }
-        if (v == 1 || j >= uja) turn_wait(v);
-        if (has_o) {
-          ptx::tc_fence_after();
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts_bf16(o, sp + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, (j > av || k > 0) ? 1u : 0u);
-          }
-          wait(&sm.pfull[v][1], j - av);
-          ptx::tc_fence_after();
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 4; k < 8; ++k)
-              mma_ts_bf16(o, sp + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, 1u);
-          }
-        }
-        if (has_s && ok && elect_one()) {
-          // over P of key tile j, which the MMAs above read: they run in order
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-            ptx::mma_bf16(sp, ptx::desc_sw128(qb + off), ptx::desc_sw128(kb + off), kIdescS, k > 0 ? 1u : 0u);
-          }
-          ptx::mma_commit(ptx::smem_u32(&sm.sfull[v]));
-        }
+      int st = 0, ph = 0;             // stage and phase of the next fill to release
+      int tiles_done = 0, qfills = 0;  // key tiles of this row tile so far; query tiles
+      for (int items = 0;; ++items) {
+        const Item* ip = &sm.item[items % kItems];
+        wait(&sm.ifull[items % kItems], items / kItems);
+        // both warps go on, or neither: a turn is never waited for in vain
+        if (!both_ok(ok)) break;
+        if (__shfl_sync(0xffffffffu, ip->bh, 0) < 0) break;
+        const int av = __shfl_sync(0xffffffffu, ip->wa[v], 0), bv = __shfl_sync(0xffffffffu, ip->wb[v], 0);
+        const int uja = __shfl_sync(0xffffffffu, ip->ja, 0), ujb = __shfl_sync(0xffffffffu, ip->jb, 0);
         __syncwarp();
-        if (v == 0 || j + 1 < ujb) turn_pass(v);
-        if (ok && elect_one()) {
-          if (has_o && j + 1 == bv) ptx::mma_commit(ptx::smem_u32(&sm.odone[v]));
-          if (j >= uja) ptx::mma_commit(ptx::smem_u32(&sm.empty[sv]));
-          if (j + 1 < ujb) ptx::mma_commit(ptx::smem_u32(&sm.empty[sk]));
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
+        if (uja >= ujb) continue;
+        if (av < bv) wait(&sm.qfull[v], qfills++);
+        for (int j = uja - 1; j < ujb; ++j) {
+          const bool has_o = j >= av && j < bv, has_s = j + 1 >= av && j + 1 < bv;
+          const int sv = st, pv = ph;  // V(j)
+          if (j >= uja && ++st == kStages) { st = 0; ph ^= 1; }
+          const int sk = st, pk = ph;  // K(j + 1)
+          if (j + 1 < ujb && ++st == kStages) { st = 0; ph ^= 1; }
+          const uint32_t vb = ptx::smem_u32(sm.kv[sv]), kb = ptx::smem_u32(sm.kv[sk]);
+          if (has_o) {
+            wait(&sm.pfull[v][0], tiles_done);
+          } else {
+            if (j >= uja) wait(&sm.full[sv], pv);
+            if (j + 1 < ujb) wait(&sm.full[sk], pk);
+          }
+          if (v == 1 || j >= uja) turn_wait(v);
+          if (has_o) {
+            ptx::tc_fence_after();
+            if (ok && elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts_bf16(o, sp + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, (j > av || k > 0) ? 1u : 0u);
+            }
+            wait(&sm.pfull[v][1], tiles_done);
+            ptx::tc_fence_after();
+            if (ok && elect_one()) {
+#pragma unroll
+              for (int k = 4; k < 8; ++k)
+                mma_ts_bf16(o, sp + 8 * k, desc_mn_sw128(vb + k * 2048, kHalf), kIdescO, 1u);
+            }
+            ++tiles_done;
+          }
+          if (has_s && ok && elect_one()) {
+            // over P of key tile j, which the MMAs above read: they run in order
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+              ptx::mma_bf16(sp, ptx::desc_sw128(qb + off), ptx::desc_sw128(kb + off), kIdescS, k > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(ptx::smem_u32(&sm.sfull[v]));
+          }
+          __syncwarp();
+          if (v == 0 || j + 1 < ujb) turn_pass(v);
+          if (ok && elect_one()) {
+            if (has_o && j + 1 == bv) ptx::mma_commit(ptx::smem_u32(&sm.odone[v]));
+            if (has_s && j + 2 == bv) ptx::mma_commit(ptx::smem_u32(&sm.qempty[v]));
+            if (j >= uja) ptx::mma_commit(ptx::smem_u32(&sm.empty[sv]));
+            if (j + 1 < ujb) ptx::mma_commit(ptx::smem_u32(&sm.empty[sk]));
+          }
+          __syncwarp();
+          if (!ok && lane == 0) *abort = 1;
         }
-        __syncwarp();
-        if (!ok && lane == 0) *abort = 1;
       }
       if (elect_one()) ptx::mma_commit(ptx::smem_u32(&sm.done[v]));
       __syncwarp();
       ptx::mbar_wait_fast(ptx::smem_u32(&sm.done[v]), 0, &sm.zero, kWaitNs);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 " PISA_SOFTMAX_REGS ";");
+    const int w = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * D;
     // MODE 0 keeps the dots and scales them inside the exponent
     const float sc = MODE == 0 ? pr.scale2 : 1.0f;
     const float slack = kSlack / sc;
-    const float slope = MODE == 1 && mk.slopes && row ? mk.slopes[h * pr.G + g] * kLog2e : 0.0f;
-    float m = -INFINITY, l = 0.0f;
     bool ok = true;
-    int st = (2 * (wa[w] - ja) + 1) % kStages, ph = ((2 * (wa[w] - ja) + 1) / kStages) & 1;  // of V(j)
-    for (int j = wa[w]; j < wb[w]; ++j) {
-      ok = true;
-      if ((warp & 3) == 0) {
-        // for the MMA thread: V(j) and K(j + 1) are there (as a rule they are by now)
-        ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
-        if (++st == kStages) { st = 0; ph ^= 1; }
-        if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
-        if (++st == kStages) { st = 0; ph ^= 1; }
-      }
-      ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.sfull[w]), (j - wa[w]) & 1, abort, kWaitNs);
+    int tiles_done = 0, outs_done = 0;
+    for (int items = 0;; ++items) {
+      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.ifull[items % kItems]), (items / kItems) & 1, abort, kWaitNs);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      ptx::tc_fence_after();
-      float s[kKeys];
+      const Item* ip = &sm.item[items % kItems];
+      if (ip->bh < 0) break;
+      const int wa = ip->wa[w], wb = ip->wb[w], jb = ip->jb;
+      // this thread's row and the keys that it sees; rows behind the new
+      // tokens are computed as if they saw all, and not written
+      int32_t lo = 0, hi = 0x7fffffff, t;
+      float slope = 0.0f;
+      {
+        const int32_t b = (uint32_t)ip->bh / (uint32_t)pr.Hkv;
+        const int32_t i = ip->tile * 2 * tokens + w * tokens + (r & (tokens - 1));
+        t = ip->len - ip->cnt + i;
+        if (i < ip->cnt && ip->fits) {
+          int64_t l, u;
+          key_span(mk, b, a.n, i, t, ip->len, &l, &u);
+          lo = l <= u ? (int32_t)l : 0x7fffffff;
+          hi = l <= u ? (int32_t)u : -1;
+        }
+        if (MODE == 1 && mk.slopes)
+          slope = mk.slopes[(ip->bh - b * pr.Hkv) * pr.G + (r >> a.lg_tokens)] * kLog2e;
+      }
+      const int f0 = ip->fill + 2 * (wa - ip->ja) + 1;  // the fill of the first V
+      float m = -INFINITY, l = 0.0f;
+      int st = f0 % kStages, ph = (f0 / kStages) & 1;
+      for (int j = wa; j < wb; ++j) {
+        ok = true;
+        if ((warp & 3) == 0) {
+          // for the MMA thread: V(j) and K(j + 1) are there (as a rule they are by now)
+          ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+          if (++st == kStages) { st = 0; ph ^= 1; }
+          if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+          if (++st == kStages) { st = 0; ph ^= 1; }
+        }
+        ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.sfull[w]), tiles_done & 1, abort, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        ptx::tc_fence_after();
+        float s[kKeys];
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
-      ptx::tmem_ld_wait();
-      const int32_t key0 = j * kKeys;
-      // keys clo .. chi of the tile are seen
-      const int32_t clo = max(lo, key0) - key0, chi = min(hi, key0 + kKeys - 1) - key0;
-      const bool bad = *(volatile int32_t*)&sm.bad_page != 0;
-      const bool part = __any_sync(0xffffffffu, clo > 0 || chi < kKeys - 1) || bad;
-      bool late = false;  // the cap is applied on the way to the exponential
-      if (MODE == 1) {
-        if (mk.cap2 > 0.0f) {
-          float big[4];
+        for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
+        ptx::tmem_ld_wait();
+        const int32_t key0 = j * kKeys;
+        // keys clo .. chi of the tile are seen
+        const int32_t clo = max(lo, key0) - key0, chi = min(hi, key0 + kKeys - 1) - key0;
+        const bool bad = *(volatile int32_t*)&sm.bad_page != 0;
+        const bool part = __any_sync(0xffffffffu, clo > 0 || chi < kKeys - 1) || bad;
+        bool late = false;  // the cap is applied on the way to the exponential
+        if (MODE == 1) {
+          if (mk.cap2 > 0.0f) {
+            float big[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            big[k] = fmaxf(fabsf(s[32 * k]), fabsf(s[32 * k + 1]));
+            for (int k = 0; k < 4; ++k) {
+              big[k] = fmaxf(fabsf(s[32 * k]), fabsf(s[32 * k + 1]));
 #pragma unroll
-            for (int c = 2; c < 32; c += 2) big[k] = ptx::max3(big[k], fabsf(s[32 * k + c]), fabsf(s[32 * k + c + 1]));
-          }
-          // small scores: a polynomial on the FMA pipe, two at a time (the
-          // exponential and the reciprocal of the other way take 12 cycles of
-          // the SFU a warp, three times what the softmax takes itself)
-          if (__all_sync(0xffffffffu, fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) <= mk.tlim)) {
-            late = !part && !mk.slopes;  // the cap is monotone: the largest score stays the largest
-            if (!late) {
-#pragma unroll
-              for (int c = 0; c < kKeys; c += 2)
-                ptx::unpack2(mul2(ptx::pack2(s[c], s[c + 1]), cap_factor(mk, ptx::pack2(s[c], s[c + 1]))), s[c],
-                             s[c + 1]);
+              for (int c = 2; c < 32; c += 2) big[k] = ptx::max3(big[k], fabsf(s[32 * k + c]), fabsf(s[32 * k + c + 1]));
             }
-          } else {
-            // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
-            const float pre = mk.pre * (2.0f * kLog2e);
+            // small scores: a polynomial on the FMA pipe, two at a time (the
+            // exponential and the reciprocal of the other way take 12 cycles of
+            // the SFU a warp, three times what the softmax takes itself)
+            if (__all_sync(0xffffffffu, fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) <= mk.tlim)) {
+              late = !part && !mk.slopes;  // the cap is monotone: the largest score stays the largest
+              if (!late) {
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 2)
+                  ptx::unpack2(mul2(ptx::pack2(s[c], s[c + 1]), cap_factor(mk, ptx::pack2(s[c], s[c + 1]))), s[c],
+                               s[c + 1]);
+              }
+            } else {
+              // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
+              const float pre = mk.pre * (2.0f * kLog2e);
+#pragma unroll
+              for (int c = 0; c < kKeys; ++c)
+                s[c] = fmaf(-2.0f * mk.cap2, rcp_approx(1.0f + ptx::ex2(s[c] * pre)), mk.cap2);
+            }
+          }
+          if (mk.slopes) {
+            // bias slope (j - t), j - t exact up to the fp32 product
+            const float rel = (float)(int32_t)(key0 - t);
+            const float by = mk.cap2 > 0.0f ? 1.0f : pr.scale2;
+            const uint64_t by2 = ptx::pack2(by, by), slope2 = ptx::pack2(slope, slope), two = ptx::pack2(2.0f, 2.0f);
+            uint64_t j2 = ptx::pack2(rel, rel + 1.0f);
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+              ptx::unpack2(ptx::fma2(ptx::pack2(s[c], s[c + 1]), by2, mul2(slope2, j2)), s[c], s[c + 1]);
+              j2 = ptx::add2(j2, two);
+            }
+          }
+        }
+        if (part) {
+          // one comparison where no row starts inside the tile
+          if (__any_sync(0xffffffffu, clo > 0)) {
 #pragma unroll
             for (int c = 0; c < kKeys; ++c)
-              s[c] = fmaf(-2.0f * mk.cap2, rcp_approx(1.0f + ptx::ex2(s[c] * pre)), mk.cap2);
+              if (c < clo) s[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (c > chi) s[c] = -INFINITY;
+        }
+        if (bad) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int64_t blk = 2 * (int64_t)j + p;
+            if (blk * kPage > ip->khi) continue;
+            const int32_t pg = a.table[(int64_t)((uint32_t)ip->bh / (uint32_t)pr.Hkv) * a.nb + blk];
+            if (pg >= 0 && pg < a.num_pages) continue;
+#pragma unroll
+            for (int c = 0; c < kPage; ++c) s[p * kPage + c] = -INFINITY;
           }
         }
-        if (mk.slopes) {
-          // bias slope (j - t), j - t exact up to the fp32 product
-          const float rel = (float)(int32_t)(key0 - t);
-          const float by = mk.cap2 > 0.0f ? 1.0f : pr.scale2;
-          const uint64_t by2 = ptx::pack2(by, by), slope2 = ptx::pack2(slope, slope), two = ptx::pack2(2.0f, 2.0f);
-          uint64_t j2 = ptx::pack2(rel, rel + 1.0f);
+        float mx[4];
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 2) {
-            ptx::unpack2(ptx::fma2(ptx::pack2(s[c], s[c + 1]), by2, mul2(slope2, j2)), s[c], s[c + 1]);
-            j2 = ptx::add2(j2, two);
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = fmaxf(s[32 * k], s[32 * k + 1]);
+#pragma unroll
+          for (int c = 2; c < 32; c += 2) mx[k] = ptx::max3(mx[k], s[32 * k + c], s[32 * k + c + 1]);
+        }
+        float top = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
+        if (MODE == 1 && late) {
+          float unused;
+          ptx::unpack2(mul2(ptx::pack2(top, top), cap_factor(mk, ptx::pack2(top, top))), top, unused);
+        }
+        const bool grow = top > m + slack || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow && m > -INFINITY ? ptx::ex2((m - top) * sc) : 1.0f;
+          if (grow) m = top;
+          l *= f;
+          if (j > wa && __any_sync(0xffffffffu, f != 1.0f)) {
+            // the MMAs into O so far are done: S of this tile was issued after them
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + c, o);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(o_at + c, o);
+            }
           }
         }
-      }
-      if (part) {
+        const float neg = m == -INFINITY ? 0.0f : -m * sc;
+        const uint64_t sc2 = ptx::pack2(sc, sc), neg2 = ptx::pack2(neg, neg);
+        uint64_t sum[2] = {0ull, 0ull};
+        // weights of the row, 32 at a time, from the exponents of two scores
+        auto weights = [&](auto exponents) {
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c < clo || c > chi) s[c] = -INFINITY;
-      }
-      if (bad) {
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t pk[16];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int64_t blk = 2 * (int64_t)j + p;
-          if (blk * kPage > khi) continue;
-          const int32_t pg = a.table[b * a.nb + blk];
-          if (pg >= 0 && pg < a.num_pages) continue;
-#pragma unroll
-          for (int c = 0; c < kPage; ++c) s[p * kPage + c] = -INFINITY;
-        }
+            for (int k = 0; k < 32; k += 2) {
+              float p0, p1;
+              ptx::unpack2(exponents(ptx::pack2(s[c + k], s[c + k + 1])), p0, p1);
+              p0 = ptx::ex2(p0);
+              p1 = ptx::ex2(p1);
+              sum[(k >> 1) & 1] = ptx::add2(sum[(k >> 1) & 1], ptx::pack2(p0, p1));
+              // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step); l is not
+              pk[k / 2] = pack_bf16(p0, p1);
+            }
+            tmem_st16(s_at + c / 2, pk);
+            if (c & 32) {  // half of the weights: the MMAs may start on them
+              tmem_st_wait();
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w][c >> 6]));
+            }
+          }
+        };
+        if (MODE == 1 && late) weights([&](uint64_t x2) { return ptx::fma2(x2, cap_factor(mk, x2), neg2); });
+        else weights([&](uint64_t x2) { return ptx::fma2(x2, sc2, neg2); });
+        float s0, s1;
+        ptx::unpack2(ptx::add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        ++tiles_done;
       }
-      float mx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        mx[k] = fmaxf(s[32 * k], s[32 * k + 1]);
-#pragma unroll
-        for (int c = 2; c < 32; c += 2) mx[k] = ptx::max3(mx[k], s[32 * k + c], s[32 * k + c + 1]);
+      if (!ok) break;
+      const bool any = wa < wb;
+      if (any) {
+        ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.odone[w]), outs_done & 1, abort, kWaitNs);
+        ++outs_done;
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        ptx::tc_fence_after();
       }
-      float top = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
-      if (MODE == 1 && late) {
-        float unused;
-        ptx::unpack2(mul2(ptx::pack2(top, top), cap_factor(mk, ptx::pack2(top, top))), top, unused);
-      }
-      const bool grow = top > m + slack || (m == -INFINITY && top > -INFINITY);
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow && m > -INFINITY ? ptx::ex2((m - top) * sc) : 1.0f;
-        if (grow) m = top;
-        l *= f;
-        if (j > wa[w] && __any_sync(0xffffffffu, f != 1.0f)) {
-          // the MMAs into O so far are done: S of this tile was issued after them
+      const int64_t b = (uint32_t)ip->bh / (uint32_t)pr.Hkv;
+      const int32_t hq = (ip->bh - (int32_t)b * pr.Hkv) * pr.G + (r >> a.lg_tokens);
+      const int32_t i = ip->tile * 2 * tokens + w * tokens + (r & (tokens - 1));
+      const bool row = i < ip->cnt;
+      const int64_t at =
+          (((int64_t)ip->split * a.tiles + ip->tile) * heads + (uint32_t)ip->bh) * (2 * kRows) + w * kRows + r;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
+      // rows go out in whole 32-byte sectors, straight from registers: the
+      // next item's queries may be in the tile that these rows came from
+      if (a.splits > 1) {
+        // this part of the row: m in log2 units, l, and O as it is
+        if (row) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(any ? m * sc : -INFINITY, any ? l : 0.0f);
+        if (any) {
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             ptx::tmem_ld32(o_at + c, o);
             ptx::tmem_ld_wait();
+            if (row) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(o_at + c, o);
+              for (int k = 0; k < 32; k += 8)
+                store32(a.part_o + at * D + c + k, *reinterpret_cast<uint32_t(*)[8]>(&o[k]), a.wide);
+            }
           }
         }
-      }
-      const float neg = m == -INFINITY ? 0.0f : -m * sc;
-      const uint64_t sc2 = ptx::pack2(sc, sc), neg2 = ptx::pack2(neg, neg);
-      uint64_t sum[2] = {0ull, 0ull};
-      // weights of the row, 32 at a time, from the exponents of two scores
-      auto weights = [&](auto exponents) {
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float p0, p1;
-            ptx::unpack2(exponents(ptx::pack2(s[c + k], s[c + k + 1])), p0, p1);
-            p0 = ptx::ex2(p0);
-            p1 = ptx::ex2(p1);
-            sum[(k >> 1) & 1] = ptx::add2(sum[(k >> 1) & 1], ptx::pack2(p0, p1));
-            // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step); l is not
-            pk[k / 2] = pack_bf16(p0, p1);
-          }
-          tmem_st16(s_at + c / 2, pk);
-          if (c & 32) {  // half of the weights: the MMAs may start on them
-            tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.pfull[w][c >> 6]));
-          }
-        }
-      };
-      if (MODE == 1 && late) weights([&](uint64_t x2) { return ptx::fma2(x2, cap_factor(mk, x2), neg2); });
-      else weights([&](uint64_t x2) { return ptx::fma2(x2, sc2, neg2); });
-      float s0, s1;
-      ptx::unpack2(ptx::add2(sum[0], sum[1]), s0, s1);
-      l += s0 + s1;
-    }
-    const bool any = wa[w] < wb[w];
-    if (ok && any) {
-      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.odone[w]), 0, abort, kWaitNs);
-      ok = __all_sync(0xffffffffu, ok) != 0;
-      ptx::tc_fence_after();
-    }
-    if (!ok) *abort = 1;
-    if (a.splits > 1) {
-      // this part of the row: m in log2 units, l, and O as it is
-      const int64_t at = (((int64_t)split * a.tiles + tile) * pr.B * pr.Hkv + bh) * (2 * kRows) + w * kRows + r;
-      if (row) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(any ? m * sc : -INFINITY, any ? l : 0.0f);
-      if (any && ok) {
+      } else {
+        const float inv = 1.0f / l;
+        const bool none = !any || l == 0.0f;
+        uint16_t* dst = a.out + ((b * pr.Hq + hq) * a.n + i) * D;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          ptx::tmem_ld32(o_at + c, o);
-          ptx::tmem_ld_wait();
-          if (row)
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(a.part_o + at * D + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        }
-      }
-    } else {
-      // rows through this warp's part of the query tile (its MMAs are done),
-      // so that the stores cover whole lines
-      const float inv = any && l != 0.0f ? 1.0f / l : 0.0f;
-      const bool none = !any || l == 0.0f;
-      uint16_t* dst = row ? a.out + (((b * pr.Hq + (int64_t)h * pr.G + g) * a.n + i) * D) : nullptr;
-      const uint32_t srow = ptx::smem_u32(sm.q[w]) + (warp & 3) * 32 * 128;
-#pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        if (half > 0) __syncwarp();
-#pragma unroll
-        for (int piece = 0; piece < 2; ++piece) {
-          uint32_t o[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-          if (any && ok) {
-            ptx::tmem_ld32(o_at + half * 64 + piece * 32, o);
+          if (any) {
+            ptx::tmem_ld32(o_at + c, o);
             ptx::tmem_ld_wait();
           }
+          uint32_t pk[16];
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pk[k] = none ? 0u : pack_bf16(__uint_as_float(o[8 * c4 + 2 * k]) * inv,
-                                            __uint_as_float(o[8 * c4 + 2 * k + 1]) * inv);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(srow + lane * 128 +
-                                                                          (((piece * 4 + c4) ^ (lane & 7)) << 4)),
-                         "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
-                         : "memory");
+          for (int k = 0; k < 16; ++k)
+            pk[k] = none ? 0u : pack_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          if (row) {
+            store32(dst + c, *reinterpret_cast<uint32_t(*)[8]>(&pk[0]), a.wide);
+            store32(dst + c + 16, *reinterpret_cast<uint32_t(*)[8]>(&pk[8]), a.wide);
           }
         }
-        __syncwarp();
-        const int c = lane & 7;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = 4 * k + (lane >> 3);
-          const uint64_t dp = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), rr);
-          uint32_t a0, a1, a2, a3;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
-                       : "r"(srow + rr * 128 + ((c ^ (rr & 7)) << 4))
-                       : "memory");
-          if (dp) reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dp) + half * 64)[c] = make_uint4(a0, a1, a2, a3);
-        }
       }
+      ptx::tc_fence_before();  // the next item's weights, and so its first MMA into O, come after these reads
     }
+    if (!ok) *abort = 1;
   }
 
   ptx::tc_fence_before();
@@ -777,13 +880,13 @@ Plan make_plan(const Prob& pr, int64_t n) {
 
 template <int D, int MODE>
 cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const Plan& pl, const CUtensorMap& qmap,
-                     const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& a, cudaStream_t st) {
+                     const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& a, int num_sms, cudaStream_t st) {
   const size_t smem = sizeof(Smem<D>) + 1024;
   auto kern = paged_prefill_kernel<D, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   note_launch();
-  kern<<<(unsigned)(pl.ctas * pl.splits), kThreads, smem, st>>>(pr, m, qmap, kmap, vmap, a);
+  kern<<<(unsigned)std::min<int64_t>(a.items, num_sms), kThreads, smem, st>>>(pr, m, qmap, kmap, vmap, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || pl.splits == 1) return e;
   note_launch();
@@ -798,7 +901,6 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
                                  const int32_t* seq_lens, const int32_t* new_lens, char* ws, void* out,
                                  cudaStream_t st) {
   const Plan pl = make_plan(pr, n);
-  if (pl.ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
   CUtensorMap qmap, kmap, vmap;
   const int64_t rows = pools.num_pages * pr.Hkv * kPage;
   if (!make_tmap_rows(&kmap, pools.k, rows, pr.d, kPage) || !make_tmap_rows(&vmap, pools.v, rows, pr.d, kPage) ||
@@ -810,16 +912,24 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages;
   a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = pools.table;
   a.status = (int32_t*)ws;
+  a.claimed = (int32_t*)ws + 32;  // cleared with the status word
   a.out = (uint16_t*)out;
   a.part_ml = (float*)(ws + pl.ml);
   a.part_o = (float*)(ws + pl.o);
+  a.wide = ((uintptr_t)out & 31) == 0 && ((uintptr_t)ws & 31) == 0;
+  a.items = (int32_t)(pl.ctas * pl.splits);
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count(dev);
+  if (sms < 1) return cudaErrorInvalidDevice;
   a.tiles = pl.tiles; a.splits = pl.splits; a.lg_tokens = pl.lg_tokens;
   const bool shaped = m.cap2 > 0.0f || m.slopes;  // scores that are more than scaled dots
   if (pr.d == 128)
-    return shaped ? launch_t<128, 1>(pr, m, pl, qmap, kmap, vmap, a, st)
-                  : launch_t<128, 0>(pr, m, pl, qmap, kmap, vmap, a, st);
-  return shaped ? launch_t<64, 1>(pr, m, pl, qmap, kmap, vmap, a, st)
-                : launch_t<64, 0>(pr, m, pl, qmap, kmap, vmap, a, st);
+    return shaped ? launch_t<128, 1>(pr, m, pl, qmap, kmap, vmap, a, sms, st)
+                  : launch_t<128, 0>(pr, m, pl, qmap, kmap, vmap, a, sms, st);
+  return shaped ? launch_t<64, 1>(pr, m, pl, qmap, kmap, vmap, a, sms, st)
+                : launch_t<64, 0>(pr, m, pl, qmap, kmap, vmap, a, sms, st);
 }
 
 }  // namespace pisa
