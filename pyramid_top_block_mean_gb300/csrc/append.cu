@@ -78,7 +78,10 @@ __device__ __forceinline__ void append_unit(const Prob& pr, const AppendArgs& a,
   if (i >= a.n) return;
   int64_t len, cnt;
   if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt)) {
-    if (x == 0) set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
+    if (x == 0) {
+      pdl_wait();
+      set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
+    }
     return;
   }
   if (i >= cnt) return;
@@ -133,7 +136,10 @@ __device__ __forceinline__ void append_unit(const Prob& pr, const AppendArgs& a,
   }
   const int64_t page = a.table[b * a.nb + pos / pr.C];
   if (page < 0 || page >= a.num_pages) {
-    if (u == 0) set_status(a.status, PISA_DEV_BAD_INDEX);
+    if (u == 0) {
+      pdl_wait();
+      set_status(a.status, PISA_DEV_BAD_INDEX);
+    }
     return;
   }
   T* dst = (T*)(is_k ? a.k_pages : a.v_pages) + ((page * pr.Hkv + h) * pr.C + pos % pr.C) * pr.d;
@@ -144,6 +150,7 @@ __device__ __forceinline__ void append_unit(const Prob& pr, const AppendArgs& a,
 template <typename T>
 __global__ void __launch_bounds__(256) append_kernel(Prob pr, AppendArgs a) {
   for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_unit<T>(pr, a, b);
+  pdl_wait();
 }
 
 }  // namespace
@@ -164,9 +171,8 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   const int64_t threads = n * ((q ? pr.Hq : 0) + 2 * pr.Hkv) * (pr.d / (2 * E));
   const dim3 grid((unsigned)ceil_div64(threads, 256), (unsigned)std::min<int64_t>(pr.B, 65535));
   note_launch();
-  if (pr.dtype == PISA_BF16) append_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(pr, a);
-  else append_kernel<float><<<grid, 256, 0, st>>>(pr, a);
-  return cudaGetLastError();
+  return launch_pdl(true, pr.dtype == PISA_BF16 ? append_kernel<__nv_bfloat16> : append_kernel<float>, grid, dim3(256),
+                    0, st, pr, a);
 }
 
 }  // namespace pisa

@@ -71,6 +71,11 @@ cudaError_t launch_paged_decode(const Prob& pr, const MaskArgs& m, const void* q
 cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, const void* q, const Pools& pools,
                                  const int32_t* seq_lens, const int32_t* new_lens, char* ws, void* out,
                                  cudaStream_t st);
+// Clears the first `bytes` (a multiple of 4) of a workspace in a kernel that
+// lets the next one of its call start at once: that one, launched with
+// launch_pdl, may read the caller's inputs before pdl_wait() and the cleared
+// words only behind it.  (A memset in its place costs a call 2 us.)
+cudaError_t launch_clear(void* ws, size_t bytes, cudaStream_t st);
 // Workspace bytes of the two launchers, the status word's 256 included.
 size_t paged_decode_ws_bytes(const Prob& pr);
 size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n);

@@ -9,6 +9,27 @@
 
 using namespace pisa;
 
+namespace pisa {
+
+namespace {
+
+__global__ void __launch_bounds__(256) clear_kernel(int32_t* p, int64_t n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  if (i < n) p[i] = 0;
+}
+
+}  // namespace
+
+cudaError_t launch_clear(void* ws, size_t bytes, cudaStream_t st) {
+  const int64_t n = (int64_t)(bytes / 4);
+  note_launch();
+  clear_kernel<<<(unsigned)ceil_div64(n, 256), 256, 0, st>>>((int32_t*)ws, n);
+  return cudaGetLastError();
+}
+
+}  // namespace pisa
+
 namespace {
 
 bool aligned4(const void* x) { return ((uintptr_t)x & 3u) == 0; }
@@ -115,7 +136,7 @@ pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, co
   if (rc != PISA_OK) return rc;
   if (ws_bytes < pisa_paged_workspace_bytes(p, n)) return PISA_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
-  if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return PISA_ERR_CUDA;
+  if (launch_clear(ws, 256, st) != cudaSuccess) return PISA_ERR_CUDA;
   return cuda_status(launch_append_paged(pr, n, q, qs, k, ks, v, vs, seq_lens, new_lens, rope, rot_dim, interleaved,
                                          k_pages, v_pages, page_table, s.nb, num_pages, (int32_t*)ws, q_out, k_out,
                                          st));

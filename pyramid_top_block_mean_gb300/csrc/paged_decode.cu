@@ -138,6 +138,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
+  if (threadIdx.x == kCons) {
+    ptx::prefetch_map(&kmap);
+    ptx::prefetch_map(&vmap);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t run = max((int64_t)min_run, ceil_div64(T, gridDim.x));
   const int64_t u0 = blockIdx.x * run, u1 = min(T, u0 + run);
   __syncthreads();
+  pdl_wait();  // from here on the status word and the counters are clear
   if (u0 >= T) return;
 
   if (warp == kWarps) {
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const unsigned m0 = __match_any_sync(0xffffffffu, k0 ? r0 : -1 - lane);  // others match nothing
           const unsigned m1 = __match_any_sync(0xffffffffu, k1 ? r1 : -1 - lane);
           bool dup1 = (m1 & below) != 0u;
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < 32 && W > 32; ++x) {
             const int32_t o = __shfl_sync(0xffffffffu, k0 ? r0 : -1, x);
             dup1 |= k1 && o == r1;
           }
@@ -591,17 +596,16 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Poo
   auto kern = paged_decode_kernel<D, G>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = cudaMemsetAsync(ws, 0, w.counter + (size_t)pr.B * pr.Hkv * 4, st);
+  e = launch_clear(ws, w.counter + (size_t)pr.B * pr.Hkv * 4, st);
   if (e != cudaSuccess) return e;
   // two CTAs share an SM; fewer where the capacity has fewer units
   const int64_t units = pr.B * pr.Hkv * (idx ? pr.K + 3 : pools.nb);
   const int64_t grid = std::min<int64_t>(std::min(2 * sm_count(dev), kMaxCtas), ceil_div64(units, kMinRun));
   Parts parts{(int32_t*)(ws + w.counter), (float*)(ws + w.ml), (float*)(ws + w.o)};
   note_launch();
-  kern<<<(unsigned)grid, kThreads, smem, st>>>(pr, m, kmap, vmap, (const uint16_t*)q, pools.table, pools.nb,
-                                               pools.num_pages, seq_lens, idx, parts, kMinRun, (int32_t*)ws,
-                                               (uint16_t*)out);
-  return cudaGetLastError();
+  return launch_pdl(true, kern, dim3((unsigned)grid), dim3(kThreads), smem, st, pr, m, kmap, vmap,
+                    (const uint16_t*)q, pools.table, pools.nb, pools.num_pages, seq_lens, idx, parts, kMinRun,
+                    (int32_t*)ws, (uint16_t*)out);
 }
 
 }  // namespace

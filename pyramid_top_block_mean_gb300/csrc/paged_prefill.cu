@@ -149,9 +149,7 @@ __device__ __forceinline__ bool elect_one() {
   return x != 0;
 }
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-}
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // 32 bytes, in one store where the address allows it.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], int wide) {
@@ -222,6 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
 
+  if (warp == kLoadWarp && lane == 3) {  // the first item's lengths
+    const int64_t b0 = (uint32_t)(blockIdx.x / a.splits) % (uint32_t)(pr.B * pr.Hkv) / (uint32_t)pr.Hkv;
+    prefetch_l1(a.seq_lens + b0);
+    if (a.new_lens) prefetch_l1(a.new_lens + b0);
+  }
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
       ptx::mbar_init(ptx::smem_u32(&sm.full[k]), 1);
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  if (warp == kLoadWarp && lane < 3) prefetch_map(lane == 0 ? &qmap : (lane == 1 ? &kmap : &vmap));
+  if (warp == kLoadWarp && lane < 3) ptx::prefetch_map(lane == 0 ? &qmap : (lane == 1 ? &kmap : &vmap));
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&sm.tmem), 512);
     ptx::tmem_relinquish();
@@ -255,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  pdl_wait();  // from here on the status word and the claims are clear
   const uint32_t tmem = sm.tmem;
   const int tokens = 1 << a.lg_tokens;  // of one row tile
   const uint32_t heads = (uint32_t)(pr.B * pr.Hkv);
@@ -265,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ loader
       bool ok = true;
       int fills = 0, scrubs = 0, items = 0, qfills[2] = {0, 0};
+      int st = 0, ph = 0;  // stage and phase of the next fill
       auto wait = [&](uint64_t* bar, int phase) {
         ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
         return ok;
@@ -298,17 +303,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int v = 0; v < 2; ++v) {
           lo[v] = 0x7fffffff;
           hi[v] = -1;
-          for (int k = lane; k < tokens && it.fits; k += 32) {
-            const int64_t i = i0 + (int64_t)v * tokens + k;
-            if (i >= cnt) break;
+          const int64_t r0 = i0 + v * tokens, r1 = min(cnt, r0 + tokens);  // its tokens
+          if (!it.fits || r0 >= r1) continue;
+          if (!mk.first_key) {  // both ends grow with the position
             int64_t l, u;
-            key_span(mk, b, a.n, i, len - cnt + i, len, &l, &u);
-            if (l > u) continue;
-            lo[v] = min(lo[v], (int32_t)l);
-            hi[v] = max(hi[v], (int32_t)u);
+            key_span(mk, b, a.n, r0, len - cnt + r0, len, &l, &u);
+            lo[v] = (int32_t)l;
+            key_span(mk, b, a.n, r1 - 1, len - cnt + r1 - 1, len, &l, &u);
+            hi[v] = (int32_t)u;
+          } else {
+            for (int64_t i = r0 + lane; i < r1; i += 32) {
+              int64_t l, u;
+              key_span(mk, b, a.n, i, len - cnt + i, len, &l, &u);
+              if (l > u) continue;
+              lo[v] = min(lo[v], (int32_t)l);
+              hi[v] = max(hi[v], (int32_t)u);
+            }
+            lo[v] = __reduce_min_sync(0xffffffffu, lo[v]);
+            hi[v] = __reduce_max_sync(0xffffffffu, hi[v]);
           }
-          lo[v] = __reduce_min_sync(0xffffffffu, lo[v]);
-          hi[v] = __reduce_max_sync(0xffffffffu, hi[v]);
         }
         const int32_t klo = min(lo[0], lo[1]), khi = max(hi[0], hi[1]);
         it.ja = it.jb = 0;
@@ -326,8 +339,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         it.khi = khi;
         it.fill = fills;
+        // lane l: the page of block 2 j + l, -1: none of its keys is seen, -2: outside the pool
+        const int32_t* trow = a.table + b * a.nb;
+        auto look_up = [&](int j) {
+          const int32_t blk = 2 * j + lane;
+          int32_t e = -1;
+          if ((int64_t)blk * kPage <= khi && (int64_t)blk * kPage + kPage > klo && blk < 2 * it.jb) {
+            e = trow[blk];
+            if (e < 0 || e >= a.num_pages) e = -2;
+          }
+          return e;
+        };
+        int32_t entry = look_up(it.ja);  // under way while the item is handed out
         const int is = items % kItems;
-        if (!wait(&sm.iempty[is], (items / kItems) + 1)) break;
+        if (items >= kItems && !wait(&sm.iempty[is], (items / kItems) + 1)) break;
         if (lane == 0) {
           sm.item[is] = it;
           ptx::mbar_arrive(ptx::smem_u32(&sm.ifull[is]));
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           if (it.wa[v] >= it.wb[v]) continue;
-          if (!wait(&sm.qempty[v], qfills[v] + 1)) break;
+          if (qfills[v] && !wait(&sm.qempty[v], qfills[v] + 1)) break;
           ++qfills[v];
           if (lane == 0) {
             const uint32_t bar = ptx::smem_u32(&sm.qfull[v]);
@@ -349,20 +374,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        const int32_t* trow = a.table + b * a.nb;
-        int32_t entry = -1;  // lane l: the page of block 2 jc + l, -1: none of its keys is seen, -2: outside the pool
         for (int j = it.ja; j < it.jb && ok; ++j) {
           const int at = (j - it.ja) & 15;
           if (at == 0) {
-            const int32_t blk = 2 * j + lane;
-            entry = -1;
-            if ((int64_t)blk * kPage <= khi && (int64_t)blk * kPage + kPage > klo && blk < 2 * it.jb) {
-              entry = trow[blk];
-              if (entry < 0 || entry >= a.num_pages) {
-                entry = -2;
-                set_status(a.status, PISA_DEV_BAD_INDEX);
-                *(volatile int32_t*)&sm.bad_page = 1;
-              }
+            if (j > it.ja) entry = look_up(j);
+            if (entry == -2) {
+              set_status(a.status, PISA_DEV_BAD_INDEX);
+              *(volatile int32_t*)&sm.bad_page = 1;
             }
             __syncwarp();
           }
@@ -375,8 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool clear = key0 < klo || key0 + kKeys - 1 > khi || pages < 2;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int st = fills % kStages;
-            if (!wait(&sm.empty[st], fills / kStages + 1)) break;
+            if (fills >= kStages && !wait(&sm.empty[st], ph ^ 1)) break;  // the first round finds them empty
             const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
             const bool scrub = kv == 1 && clear;
             const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
@@ -414,10 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) ptx::mbar_arrive(full);
             }
             ++fills;
+            if (++st == kStages) { st = 0; ph ^= 1; }
           }
         }
       }
-      if (wait(&sm.iempty[items % kItems], (items / kItems) + 1) && lane == 0) {
+      if ((items < kItems || wait(&sm.iempty[items % kItems], (items / kItems) + 1)) && ok && lane == 0) {
         sm.item[items % kItems].bh = -1;
         ptx::mbar_arrive(ptx::smem_u32(&sm.ifull[items % kItems]));
       }
@@ -559,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = wa; j < wb; ++j) {
         ok = true;
         if ((warp & 3) == 0) {
-          // for the MMA thread: V(j) and K(j + 1) are there (as a rule they are by now)
+          // for the MMA warp: V(j) and K(j + 1) are there (as a rule they are by now)
           ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
           if (++st == kStages) { st = 0; ph ^= 1; }
           if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
@@ -775,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of a row: one CTA per row, 8 dims x every 16th part a
 // thread, so that all loads of a row are in flight at once.
 template <int D>
-__global__ void __launch_bounds__(D * 2) prefill_join_kernel(Prob pr, Args a) {
+__global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(Prob pr, Args a) {
   constexpr int CH = D / 8, PL = 16;
   __shared__ float sm_m[PL], sm_l[PL];
   __shared__ float sm_o[PL][D];
@@ -793,7 +811,7 @@ __global__ void __launch_bounds__(D * 2) prefill_join_kernel(Prob pr, Args a) {
   if (i >= cnt) return;
   pdl_wait();  // the lengths are the caller's, the parts the kernel's before
   float M = -INFINITY, L = 0.0f, acc[8] = {};
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 2;
   for (int s0 = pl; s0 < a.splits; s0 += PL * kBatch) {
     float2 ml[kBatch];
     float4 o[kBatch][2];
@@ -886,8 +904,8 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const Plan& pl, const CU
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   note_launch();
-  kern<<<(unsigned)std::min<int64_t>(a.items, num_sms), kThreads, smem, st>>>(pr, m, qmap, kmap, vmap, a);
-  e = cudaGetLastError();
+  e = launch_pdl(true, kern, dim3((unsigned)std::min<int64_t>(a.items, num_sms)), dim3(kThreads), smem, st, pr, m,
+                 qmap, kmap, vmap, a);
   if (e != cudaSuccess || pl.splits == 1) return e;
   note_launch();
   return launch_pdl(true, prefill_join_kernel<D>, dim3((unsigned)(pl.ctas * 2 * kRows)), dim3(D * 2), 0, st, pr, a);
@@ -906,7 +924,7 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   if (!make_tmap_rows(&kmap, pools.k, rows, pr.d, kPage) || !make_tmap_rows(&vmap, pools.v, rows, pr.d, kPage) ||
       !make_tmap_q(&qmap, q, pr.B, pr.Hq, n, pr.d, pr.G, 1 << pl.lg_tokens))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  cudaError_t e = launch_clear(ws, 256, st);
   if (e != cudaSuccess) return e;
   Args a{};
   a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages;
