@@ -398,8 +398,8 @@ void pisa_test_inject_leaf_timeout(uint64_t wait_limit_ns, int32_t drop_first_ke
 /* Appends n new tokens per sequence to the pages.  k and v [B, H_kv, n, d]
  * and (nullable) q [B, H_q, n, d] may be strided views: k_strides points at
  * three element counts (sequence, head, token), each a multiple of 16 bytes,
- * with the d elements of a row adjacent (null: contiguous; q_strides and
- * v_strides likewise).  Keys and queries are rotated on the way: with
+ * with the d elements of a row adjacent (null: contiguous; the stride of a
+ * dimension of one entry is not read; q_strides and v_strides likewise).  Keys and queries are rotated on the way: with
  * h = rot_dim / 2 and rope fp32 [N, rot_dim] (cosines of a position's h
  * angles, then their sines), the pair (x_i, x_{i+h}), or with interleaved != 0
  * the pair (x_{2i}, x_{2i+1}), becomes (a cos - b sin, b cos + a sin); dims

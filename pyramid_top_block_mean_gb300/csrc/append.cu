@@ -64,21 +64,23 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// One thread: one 32-byte unit of one row (q, k or v head) of one token.
-template <typename T>
-__device__ __forceinline__ void append_unit(const Prob& pr, const AppendArgs& a, int64_t b) {
+// One thread: one 32-byte unit of R rows (q, k and v heads, every groups-th)
+// of one token, all of whose loads are in flight together; the token's
+// cosines and sines are read once for them.
+template <typename T, int R>
+__device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a, int64_t b) {
   constexpr int E = Vec<T>::E;
-  const int units = pr.d / (2 * E);
-  const int rows = (a.q ? pr.Hq : 0) + 2 * pr.Hkv;
-  const int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int u = (int)(x % units);
-  const int64_t y = x / units;
-  const int r = (int)(y % rows);
-  const int64_t i = y / rows;
+  const uint32_t units = pr.d / (2 * E);
+  const uint32_t kv0 = a.q ? pr.Hq : 0, rows = kv0 + 2 * pr.Hkv, groups = (rows + R - 1) / R;
+  const uint32_t per = blockDim.x / units;  // (token, group) pairs of a block
+  const uint32_t u = threadIdx.x % units;
+  const int64_t y = (int64_t)blockIdx.x * per + threadIdx.x / units;
+  const int64_t i = y < (int64_t)0xffffffff ? (int64_t)((uint32_t)y / groups) : y / groups;
+  const uint32_t r0 = (uint32_t)(y - i * groups);
   if (i >= a.n) return;
   int64_t len, cnt;
   if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt)) {
-    if (x == 0) {
+    if (y == 0 && u == 0) {
       pdl_wait();
       set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
     }
@@ -86,70 +88,87 @@ __device__ __forceinline__ void append_unit(const Prob& pr, const AppendArgs& a,
   }
   if (i >= cnt) return;
   const int64_t pos = len - cnt + i;
-  const int kv0 = a.q ? pr.Hq : 0;
-  const bool is_q = r < kv0, is_k = !is_q && r < kv0 + pr.Hkv;
-  const int h = is_q ? r : (is_k ? r - kv0 : r - kv0 - pr.Hkv);
+  const uint32_t page = (uint32_t)a.table[b * a.nb + pos / pr.C];  // a negative entry is past any pool
+  const bool in_pool = page < a.num_pages;
+  if (!in_pool && r0 == 0 && u == 0) {
+    pdl_wait();
+    set_status(a.status, PISA_DEV_BAD_INDEX);
+  }
   const int half = a.rot / 2;
+  const bool turns = (int)(2 * E * u) < a.rot;  // this unit's dims are among the rotated ones
+  float cs[E], sn[E];
+  if (turns) {
+    const float* at = a.rope + pos * a.rot + E * u;
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(at + j), s = *reinterpret_cast<const float4*>(at + half + j);
+      cs[j] = c.x; cs[j + 1] = c.y; cs[j + 2] = c.z; cs[j + 3] = c.w;
+      sn[j] = s.x; sn[j + 1] = s.y; sn[j + 2] = s.z; sn[j + 3] = s.w;
+    }
+  }
   // the unit's two vectors: partners in the rotated dims, neighbours elsewhere
-  int e0 = 2 * E * u, e1 = e0 + E;
-  const bool rotated = (is_q || is_k) && 2 * E * u < a.rot;
-  if (rotated && !a.interleaved) {
-    e0 = E * u;
-    e1 = e0 + half;
+  auto place = [&](bool rotated, int* e0, int* e1) {
+    const bool split = rotated && !a.interleaved;
+    *e0 = split ? E * u : 2 * E * u;
+    *e1 = split ? E * u + half : 2 * E * u + E;
+  };
+  uint4 w[R][2];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const uint32_t r = r0 + k * groups;
+    if (r >= rows) break;
+    const bool is_q = r < kv0, is_v = r >= kv0 + pr.Hkv;
+    const int64_t* sd = is_q ? a.qs : (is_v ? a.vs : a.ks);
+    const int64_t h = is_q ? r : (is_v ? r - kv0 - pr.Hkv : r - kv0);
+    const T* src = (const T*)(is_q ? a.q : (is_v ? a.v : a.k)) + b * sd[0] + h * sd[1] + i * sd[2];
+    int e0, e1;
+    place(turns && !is_v, &e0, &e1);
+    w[k][0] = *reinterpret_cast<const uint4*>(src + e0);
+    w[k][1] = *reinterpret_cast<const uint4*>(src + e1);
   }
-  const int64_t* sd = is_q ? a.qs : (is_k ? a.ks : a.vs);
-  const T* src = (const T*)(is_q ? a.q : (is_k ? a.k : a.v)) + b * sd[0] + h * sd[1] + i * sd[2];
-  uint4 w0 = *reinterpret_cast<const uint4*>(src + e0), w1 = *reinterpret_cast<const uint4*>(src + e1);
-  if (rotated) {
-    float p[2 * E], o[2 * E];
-    Vec<T>::load(w0, p);
-    Vec<T>::load(w1, p + E);
-    const float* cs = a.rope + pos * a.rot + E * u;
-    if (a.interleaved) {
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const uint32_t r = r0 + k * groups;
+    if (r >= rows) break;
+    const bool is_q = r < kv0, is_v = r >= kv0 + pr.Hkv;
+    const int64_t h = is_q ? r : (is_v ? r - kv0 - pr.Hkv : r - kv0);
+    int e0, e1;
+    place(turns && !is_v, &e0, &e1);
+    if (turns && !is_v) {
+      float p[2 * E], o[2 * E];
+      Vec<T>::load(w[k][0], p);
+      Vec<T>::load(w[k][1], p + E);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float c = cs[j], sn = cs[half + j];
-        o[2 * j] = p[2 * j] * c - p[2 * j + 1] * sn;
-        o[2 * j + 1] = p[2 * j + 1] * c + p[2 * j] * sn;
+        const float x = a.interleaved ? p[2 * j] : p[j], z = a.interleaved ? p[2 * j + 1] : p[E + j];
+        const float xr = x * cs[j] - z * sn[j], zr = z * cs[j] + x * sn[j];
+        if (a.interleaved) {
+          o[2 * j] = xr;
+          o[2 * j + 1] = zr;
+        } else {
+          o[j] = xr;
+          o[E + j] = zr;
+        }
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const float c = cs[j], sn = cs[half + j];
-        o[j] = p[j] * c - p[E + j] * sn;
-        o[E + j] = p[E + j] * c + p[j] * sn;
-      }
+      w[k][0] = Vec<T>::store(o);
+      w[k][1] = Vec<T>::store(o + E);
     }
-    w0 = Vec<T>::store(o);
-    w1 = Vec<T>::store(o + E);
-  }
-  if (is_q) {
-    T* dst = (T*)a.q_out + ((b * pr.Hq + h) * a.n + i) * pr.d;
-    *reinterpret_cast<uint4*>(dst + e0) = w0;
-    *reinterpret_cast<uint4*>(dst + e1) = w1;
-    return;
-  }
-  if (is_k && a.k_out) {
-    T* dst = (T*)a.k_out + ((b * pr.Hkv + h) * a.n + i) * pr.d;
-    *reinterpret_cast<uint4*>(dst + e0) = w0;
-    *reinterpret_cast<uint4*>(dst + e1) = w1;
-  }
-  const int64_t page = a.table[b * a.nb + pos / pr.C];
-  if (page < 0 || page >= a.num_pages) {
-    if (u == 0) {
-      pdl_wait();
-      set_status(a.status, PISA_DEV_BAD_INDEX);
+    if (is_q || (!is_v && a.k_out)) {
+      T* dst = (T*)(is_q ? a.q_out : a.k_out) + ((b * (is_q ? pr.Hq : pr.Hkv) + h) * a.n + i) * pr.d;
+      *reinterpret_cast<uint4*>(dst + e0) = w[k][0];
+      *reinterpret_cast<uint4*>(dst + e1) = w[k][1];
     }
-    return;
+    if (!is_q && in_pool) {
+      T* dst = (T*)(is_v ? a.v_pages : a.k_pages) + (((int64_t)page * pr.Hkv + h) * pr.C + pos % pr.C) * pr.d;
+      *reinterpret_cast<uint4*>(dst + e0) = w[k][0];
+      *reinterpret_cast<uint4*>(dst + e1) = w[k][1];
+    }
   }
-  T* dst = (T*)(is_k ? a.k_pages : a.v_pages) + ((page * pr.Hkv + h) * pr.C + pos % pr.C) * pr.d;
-  *reinterpret_cast<uint4*>(dst + e0) = w0;
-  *reinterpret_cast<uint4*>(dst + e1) = w1;
 }
 
-template <typename T>
+template <typename T, int R>
 __global__ void __launch_bounds__(256) append_kernel(Prob pr, AppendArgs a) {
-  for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_unit<T>(pr, a, b);
+  for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_units<T, R>(pr, a, b);
   pdl_wait();
 }
 
@@ -167,12 +186,16 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   a.rope = rope; a.rot = rot_dim; a.interleaved = interleaved != 0;
   a.k_pages = k_pages; a.v_pages = v_pages; a.q_out = q_out; a.k_out = k_out;
   a.n = n; a.nb = nb; a.num_pages = num_pages; a.status = status;
-  const int E = pr.dtype == PISA_BF16 ? 8 : 4;
-  const int64_t threads = n * ((q ? pr.Hq : 0) + 2 * pr.Hkv) * (pr.d / (2 * E));
-  const dim3 grid((unsigned)ceil_div64(threads, 256), (unsigned)std::min<int64_t>(pr.B, 65535));
+  const int per = 256 / (pr.d / (pr.dtype == PISA_BF16 ? 16 : 8));
+  const int64_t rows = (q ? pr.Hq : 0) + 2 * pr.Hkv;
+  // four rows a thread once there are threads enough to fill the GPU with that
+  const bool many = pr.B * n * rows * (256 / per) >= 4 * 152 * 2048;
+  const dim3 grid((unsigned)ceil_div64(n * ceil_div64(rows, many ? 4 : 1), per),
+                  (unsigned)std::min<int64_t>(pr.B, 65535));
+  auto kern = pr.dtype == PISA_BF16 ? (many ? append_kernel<__nv_bfloat16, 4> : append_kernel<__nv_bfloat16, 1>)
+                                    : (many ? append_kernel<float, 4> : append_kernel<float, 1>);
   note_launch();
-  return launch_pdl(true, pr.dtype == PISA_BF16 ? append_kernel<__nv_bfloat16> : append_kernel<float>, grid, dim3(256),
-                    0, st, pr, a);
+  return launch_pdl(true, kern, grid, dim3(256), 0, st, pr, a);
 }
 
 }  // namespace pisa

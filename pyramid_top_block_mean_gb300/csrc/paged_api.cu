@@ -87,13 +87,17 @@ pisa_status mask_checks(const Prob& pr, const pisa_mask* mask, MaskArgs* m) {
 }
 
 // Strides (sequence, head, token) of a [B, H, n, d] view in elements: each a
-// multiple of 16 bytes, so that every row takes 16-byte accesses.
-pisa_status stride_checks(const int64_t* given, int64_t H, int64_t n, int64_t d, int64_t per16, int64_t* out) {
+// multiple of 16 bytes, so that every row takes 16-byte accesses.  A dimension
+// of one entry has no stride.
+pisa_status stride_checks(const int64_t* given, int64_t B, int64_t H, int64_t n, int64_t d, int64_t per16,
+                          int64_t* out) {
+  const int64_t size[3] = {B, H, n};
   out[0] = H * n * d;
   out[1] = n * d;
   out[2] = d;
   if (!given) return PISA_OK;
   for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
     if (given[i] < 0) return PISA_ERR_INVALID_ARG;
     if (given[i] % per16 != 0) return PISA_ERR_MISALIGNED;
     out[i] = given[i];
@@ -130,9 +134,9 @@ pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, co
     return PISA_ERR_MISALIGNED;
   const int64_t per16 = pr.dtype == PISA_BF16 ? 8 : 4;
   int64_t qs[3], ks[3], vs[3];
-  rc = stride_checks(q_strides, pr.Hq, n, pr.d, per16, qs);
-  if (rc == PISA_OK) rc = stride_checks(k_strides, pr.Hkv, n, pr.d, per16, ks);
-  if (rc == PISA_OK) rc = stride_checks(v_strides, pr.Hkv, n, pr.d, per16, vs);
+  rc = stride_checks(q_strides, pr.B, pr.Hq, n, pr.d, per16, qs);
+  if (rc == PISA_OK) rc = stride_checks(k_strides, pr.B, pr.Hkv, n, pr.d, per16, ks);
+  if (rc == PISA_OK) rc = stride_checks(v_strides, pr.B, pr.Hkv, n, pr.d, per16, vs);
   if (rc != PISA_OK) return rc;
   if (ws_bytes < pisa_paged_workspace_bytes(p, n)) return PISA_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;

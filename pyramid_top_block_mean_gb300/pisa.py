@@ -59,7 +59,7 @@ class Mask(ctypes.Structure):
 
 _P = ctypes.POINTER(Params)
 _M = ctypes.POINTER(Mask)
-_strides_t = ctypes.c_int64 * 3
+_strides_t = ctypes.c_int64 * 9
 _vp = ctypes.c_void_p
 _lib.pisa_abi_version.restype = ctypes.c_int
 _lib.pisa_kernel_launches.restype = ctypes.c_uint64
@@ -299,17 +299,11 @@ def _want(t, name: str, shape, dtype, index: int) -> int:
 
 
 def _want_rows(t, name: str, shape, dtype, index: int):
-    """Address and (sequence, head, token) strides of a [B, H, n, d] view with
-    adjacent elements in a row; no strides when it is contiguous.  A dimension
-    of one entry has no stride of its own."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
-        _refuse(t, name, shape, dtype, index, "a")
-    if t.is_contiguous():
-        return t.data_ptr(), None
+    """Address and strides of a [B, H, n, d] view with adjacent elements in a row."""
     st = t.stride()
-    if st[3] != 1:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or st[3] != 1:
         _refuse(t, name, shape, dtype, index, "row-contiguous")
-    return t.data_ptr(), _strides_t(*[0 if shape[i] == 1 else st[i] for i in range(3)])
+    return t.data_ptr(), st
 
 
 def _want_cache(p: Params, k_pages, v_pages, page_table, seq_lens, ws, dtype, index: int):
@@ -381,11 +375,14 @@ def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, ro
     index, dt, n = k.get_device(), _dtype(p), k.shape[2]
     kv_shape, q_shape = (p.B, p.H_kv, n, p.d), (p.B, p.H_q, n, p.d)
     cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
+    kp, ks = _want_rows(k, "k", kv_shape, dt, index)
+    vp, vs = _want_rows(v, "v", kv_shape, dt, index)
+    qp, qs = (None, ks) if q is None else _want_rows(q, "q", q_shape, dt, index)
+    strides = _strides_t(*qs[:3], *ks[:3], *vs[:3])
+    at = ctypes.addressof(strides)
     return _launch(
-        index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n,
-        *((None, None) if q is None else _want_rows(q, "q", q_shape, dt, index)),
-        *_want_rows(k, "k", kv_shape, dt, index), *_want_rows(v, "v", kv_shape, dt, index), cache[4],
-        None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index),
+        index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, at, kp, at + 24, vp,
+        at + 48, cache[4], None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index),
         None if rope is None else _want(rope, "rope", (p.N, rope.shape[-1]), torch.float32, index),
         0 if rope is None else rope.shape[-1], interleaved, *cache[:4], *space,
         None if q_out is None else _want(q_out, "q_out", q_shape, dt, index),
