@@ -30,38 +30,48 @@ namespace pisa {
 
 namespace {
 
-constexpr int kWarps = 4;               // consumer warps, 16 keys each
+constexpr int kWarps = 8;               // consumer warps, 16 keys each: two groups, which take turns at the pages
 constexpr int kCons = 32 * kWarps;      // consumer threads
 constexpr int kThreads = kCons + 32;    // and the producer warp
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
 constexpr uint64_t kWaitNs = 4000000000ull;
 
-template <int D>
+template <int D, int G>
 struct Shape {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  // as many as fit beside the merge buffer
+  static constexpr int kStages = D == 128 ? (G == 8 ? 5 : 6) : (G == 8 ? 11 : 12);
   static constexpr uint32_t kTile = kPage * D * 2;  // bytes of a page's keys
 };
 
 // What a stage holds and what to do with it.
-struct Meta {
-  int32_t item;      // b * Hkv + h
+struct __align__(16) Meta {
+  int32_t item;      // b * Hkv + h, -1: the end
   int32_t rel;       // position of the page's first key minus the query's
-  int32_t klo, khi;  // keys klo .. khi of the page are seen
-  int32_t first, last;    // of this CTA's part of the item
+  int16_t klo, khi;  // keys klo .. khi of the page are seen
+  int16_t first, last;    // of what a group gets of this CTA's part of the item
   int32_t cfirst, parts;  // with last: the item's first CTA and how many share it
   int32_t slot;           // with last and parts > 1: where this part goes
   int32_t slot0;          // and where the first CTA's part goes
 };
 
+// The join of an item's parts: 4 dims a thread; what threads are left over
+// take every kLanes-th part.
+template <int D, int G>
+struct Join {
+  static constexpr int kCols = G * D / 4;
+  static constexpr int kLanes = kCols >= kCons ? 1 : kCons / kCols;
+};
+
 template <int D, int G>
 struct Smem {
-  uint8_t kv[Shape<D>::kStages][2][Shape<D>::kTile];
-  uint16_t q[Shape<D>::kStages][G * D];
-  float o[kWarps][G][D / 2];
-  float m[kWarps][8], l[kWarps][8];
-  Meta meta[Shape<D>::kStages];
-  uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages];
+  uint8_t kv[Shape<D, G>::kStages][2][Shape<D, G>::kTile];
+  uint16_t q[Shape<D, G>::kStages][G * D];
+  float o[kWarps][G * D];                  // a part's merge
+  float m[2][kWarps][8], l[2][kWarps][8];  // by turns
+  float jo[Join<D, G>::kLanes > 1 ? kCons : 1][4], jm[kCons], jl[kCons];
+  Meta meta[Shape<D, G>::kStages];
+  uint64_t full[Shape<D, G>::kStages], empty[Shape<D, G>::kStages];
   int32_t abort, zero, last_part;
 };
 
@@ -124,14 +134,14 @@ __device__ __forceinline__ Span seq_span(const MaskArgs& m, const int32_t* seq_l
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(Prob pr, MaskArgs mk, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const uint16_t* __restrict__ q,
                         const int32_t* __restrict__ table, int64_t nb, int64_t num_pages,
                         const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ idx, Parts parts,
                         int32_t min_run, int32_t* __restrict__ status, uint16_t* __restrict__ out) {
-  constexpr int kStages = Shape<D>::kStages;
-  constexpr uint32_t kTile = Shape<D>::kTile;
+  constexpr int kStages = Shape<D, G>::kStages;
+  constexpr uint32_t kTile = Shape<D, G>::kTile;
   constexpr int kHalf = kPage * 128;  // bytes of a tile's 64-column half
   extern __shared__ unsigned char smem_raw[];
   Smem<D, G>& sm = *reinterpret_cast<Smem<D, G>*>(
@@ -145,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), kWarps);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), kWarps / 2);
     }
     sm.abort = 0;
     sm.zero = 0;
@@ -201,31 +211,34 @@ __global__ void __launch_bounds__(kThreads, 2)
     int32_t np = idx ? W : sp.np;
     int32_t h = (int32_t)((u0 - i0) / np);
     i0 += (int64_t)h * np;  // first unit of the item
-    int it = 0;
+    // (64-bit divisions take a hundred cycles and more)
+    auto over_run = [&](int64_t x) { return T < (int64_t)1 << 32 ? (int64_t)((uint32_t)x / (uint32_t)run) : x / run; };
+    int it = 0, st = 0, ph = 0;  // stages filled; the next one and its phase
     bool ok = true;
     // one stage; page < 0: none to load
-    auto emit = [&](const Meta& meta, int64_t page, int32_t head, int64_t seq) -> bool {
-      const int st = it % kStages;
-      const bool got = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
-      if (!__all_sync(0xffffffffu, got)) return false;
+    auto emit = [&](const Meta& meta, int32_t page, int32_t head, int64_t seq) -> bool {
+      if (it >= kStages &&
+          !__all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ph ^ 1, abort, kWaitNs)))
+        return false;
       if (lane == 0) {
         sm.meta[st] = meta;
         const uint32_t full = ptx::smem_u32(&sm.full[st]);
         const uint32_t bytes = (page >= 0 ? 2 * kTile : 0u) + (meta.first ? (uint32_t)(G * D * 2) : 0u);
         ptx::mbar_arrive_expect_tx(full, bytes);
         if (page >= 0) {
-          const int32_t y = (int32_t)((page * pr.Hkv + head) * kPage);
-#pragma unroll
-          for (int hh = 0; hh < D / 64; ++hh) {
-            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][0]) + hh * kHalf, &kmap, 64 * hh, y, full);
-            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][1]) + hh * kHalf, &vmap, 64 * hh, y, full);
-          }
+          const int32_t y = (int32_t)(((int64_t)page * pr.Hkv + head) * kPage);
+          ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][0]), &kmap, 0, y, 0, full);
+          ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][1]), &vmap, 0, y, 0, full);
         }
         if (meta.first)
           ptx::bulk_g2s(ptx::smem_u32(sm.q[st]), q + (seq * pr.Hq + head * G) * D, G * D * 2, full);
       }
       __syncwarp();
       ++it;
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
+      }
       return true;
     };
     for (int64_t u = u0; u < u1 && ok;) {
@@ -238,16 +251,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       meta.rel = 0;
       meta.klo = kPage;
       meta.khi = -1;
-      const int64_t c0 = i0 / run, c1 = (i0 + np - 1) / run;
+      const int64_t c0 = over_run(i0), c1 = over_run(i0 + np - 1);
       meta.cfirst = (int32_t)c0;
       meta.parts = (int32_t)(c1 - c0 + 1);
       meta.slot0 = (int32_t)(2 * c0 + (c0 * run < i0 ? 1 : 0));
       meta.slot = blockIdx.x == c0 ? meta.slot0 : 2 * (int32_t)blockIdx.x;
       const int32_t* trow = table + b * nb;
-      if (sp.dead) {
-        meta.last = 1;
-        ok = emit(meta, -1, h, b);
-      } else {
+      int32_t count = 0;  // stages of this part so far
+      if (!sp.dead) {
         // the entries of this part, 32 at a time: lane l looks after entry s + l
         int32_t r0 = -1, r1 = -1;
         if (idx) {
@@ -256,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (lane + 32 < W) r1 = row[lane + 32];
         }
         const int32_t qb = (int32_t)(sp.t / kPage);
-        int32_t left = 0;  // entries of the part that hold a page, not yet emitted
+        int32_t left = 0;  // entries of the part that hold a page, not yet emitted; the last two are the groups' last
         uint64_t keep = 0;
         if (idx) {
           const bool k0 = r0 >= 0 && r0 <= qb, k1 = r1 >= 0 && r1 <= qb;
@@ -275,10 +286,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           left = __popcll(keep);
         } else {
           left = s1 - s0;
-        }
-        if (left == 0) {
-          meta.last = 1;
-          ok = emit(meta, -1, h, b);
         }
         for (int32_t s = s0 & ~31; s < s1 && ok; s += 32) {
           // lane l: block and page of entry s + l
@@ -299,13 +306,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int32_t bx = __shfl_sync(0xffffffffu, blk, x), px = __shfl_sync(0xffffffffu, page, x);
             const int64_t key0 = (int64_t)bx * kPage;
             meta.rel = (int32_t)(key0 - sp.t);
-            meta.klo = px < 0 ? kPage : (int32_t)max((int64_t)0, min((int64_t)kPage, sp.lo - key0));
-            meta.khi = (int32_t)min((int64_t)(kPage - 1), sp.t - key0);
-            meta.last = --left == 0;
+            meta.klo = px < 0 ? kPage : (int16_t)max((int64_t)0, min((int64_t)kPage, sp.lo - key0));
+            meta.khi = (int16_t)min((int64_t)(kPage - 1), sp.t - key0);
+            meta.last = --left < 2;
+            meta.first = ++count <= 2;
             ok = emit(meta, px, h, b);
-            meta.first = 0;
           }
         }
+      }
+      // each group has a stage of every part, if an empty one
+      for (; count < 2 && ok; ++count) {
+        meta.klo = kPage;
+        meta.first = meta.last = 1;
+        ok = emit(meta, -1, h, b);
       }
       u = i0 + s1;
       if (s1 == np) {
@@ -319,28 +332,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    if (!ok && lane == 0) *abort = 1;
-    // a stage without an item ends the consumers
-    bool closed = false;
+    // a stage without an item ends a group
     if (ok) {
-      const int st = it % kStages;
-      closed = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ((it / kStages) & 1) ^ 1, abort, kWaitNs);
-      if (closed && lane == 0) {
-        sm.meta[st].item = -1;
-        ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
-      }
+      Meta meta;
+      meta.item = -1;
+      meta.first = 0;
+      ok = emit(meta, -1, 0, 0) && emit(meta, -1, 0, 0);
     }
-    // every copy lands before the CTA ends (the closing stage's own last one has, since it was free again)
+    // every copy lands before the CTA ends
     if (lane == 0)
-      for (int k = max(0, it - kStages + (closed ? 1 : 0)); k < it; ++k)
+      for (int k = max(0, it - kStages); k < it; ++k)
         ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero, kWaitNs);
+    if (!ok && lane == 0) *abort = 1;
     if (lane == 0 && sm.abort) set_status(status, PISA_DEV_TIMEOUT);
     return;
   }
 
   // ------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
-  const int r16 = 16 * warp;
+  const int r16 = 16 * (warp & 3);
   // ldmatrix rows: lane l addresses row l % 8 of matrix l / 8
   const int krow = r16 + (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
   const int vrow = r16 + (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
@@ -348,9 +358,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   float oacc[D / 16][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
   float sl0 = 0.0f, sl1 = 0.0f;
-  for (int it = 0;; ++it) {
-    const int st = it % kStages;
-    const bool okw = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), (it / kStages) & 1, abort, kWaitNs);
+  // group warp / 4 takes every other stage
+  int st = (warp >> 2) - 2, ph = 0, turn = 0;
+  for (;;) {
+    if ((st += 2) >= kStages) {
+      st -= kStages;
+      ph ^= 1;
+    }
+    const bool okw = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
     if (!__all_sync(0xffffffffu, okw)) {
       *abort = 1;
       break;
@@ -376,13 +391,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (meta.klo <= meta.khi && r16 <= meta.khi && r16 + 15 >= meta.klo) {
       const uint32_t kb = ptx::smem_u32(sm.kv[st][0]), vb = ptx::smem_u32(sm.kv[st][1]);
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains
+      {
+        uint32_t a[D / 16][4];
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[4];
-        const int ch = 2 * ks + kch;
-        ldsm4(kb + (ch >> 3) * kHalf + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a);
-        if (ks & 1) mma16816(e, a, bq[ks][0], bq[ks][1]);
-        else mma16816(d, a, bq[ks][0], bq[ks][1]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int ch = 2 * ks + kch;
+          ldsm4(kb + (ch >> 3) * kHalf + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a[ks]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          mma16816(d, a[ks], bq[ks][0], bq[ks][1]);
+          mma16816(e, a[ks + 1], bq[ks + 1][0], bq[ks + 1][1]);
+        }
+      }
+      uint32_t av[D / 16][4];  // the values' fragments, on their way during the softmax
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        const int ch = 2 * mt + vch;
+        ldsm4_t(vb + (ch >> 3) * kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), av[mt]);
       }
       // keys grp and grp + 8 of this warp's 16, heads 2 tig and 2 tig + 1
       float x[4];
@@ -443,80 +469,79 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t b0 = transpose8(pack_bf16(p0, p1)), b1 = transpose8(pack_bf16(p2, p3));
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        uint32_t a[4];
-        const int ch = 2 * mt + vch;
-        ldsm4_t(vb + (ch >> 3) * kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), a);
         if (part) {  // a value that is not seen may be anything
-          a[0] &= va; a[1] &= va;
-          a[2] &= vz; a[3] &= vz;
+          av[mt][0] &= va; av[mt][1] &= va;
+          av[mt][2] &= vz; av[mt][3] &= vz;
         }
-        mma16816(oacc[mt], a, b0, b1);
+        mma16816(oacc[mt], av[mt], b0, b1);
       }
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
     if (!meta.last) continue;
 
-    // ------------------------------------------- end of a part: merge warps
+    // ----------------------------- end of a part: merge the warps of both groups
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    if (grp == 0) {
-      sm.m[warp][2 * tig] = m0; sm.m[warp][2 * tig + 1] = m1;
-      sm.l[warp][2 * tig] = l0; sm.l[warp][2 * tig + 1] = l1;
-    }
+    if (grp == 0) *reinterpret_cast<float2*>(&sm.m[turn][warp][2 * tig]) = make_float2(m0, m1);
     cons_sync();
     float M0 = -INFINITY, M1 = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      M0 = fmaxf(M0, sm.m[w][2 * tig]);
-      M1 = fmaxf(M1, sm.m[w][2 * tig + 1]);
+      const float2 mw = *reinterpret_cast<const float2*>(&sm.m[turn][w][2 * tig]);
+      M0 = fmaxf(M0, mw.x);
+      M1 = fmaxf(M1, mw.y);
     }
-    const float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - M1);
-    const int64_t orow = (int64_t)meta.item * G * D;  // item's G rows of out are adjacent
-    float* po = parts.o + (int64_t)meta.slot * G * D;
+    // without a maximum a warp saw no key (or nothing but NaN scores)
+    const float f0 = m0 == -INFINITY ? 1.0f : ptx::ex2(m0 - M0), f1 = m1 == -INFINITY ? 1.0f : ptx::ex2(m1 - M1);
+    if (grp == 0) *reinterpret_cast<float2*>(&sm.l[turn][warp][2 * tig]) = make_float2(l0 * f0, l1 * f1);
+    // o[warp][head][dim]; the dims of a head are permuted by 8 (head / 2), which spreads tig over the banks
+    {
+      float* ow = sm.o[warp];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half) cons_sync();  // the first half has been read
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const int mt = half * (D / 32) + k;
+      for (int mt = 0; mt < D / 16; ++mt) {
+        const int c0 = (16 * mt + grp) ^ (8 * tig), c1 = (16 * mt + grp + 8) ^ (8 * tig);
         if (2 * tig < G) {
-          sm.o[warp][2 * tig][16 * k + grp] = oacc[mt][0] * f0;
-          sm.o[warp][2 * tig][16 * k + grp + 8] = oacc[mt][2] * f0;
+          ow[2 * tig * D + c0] = oacc[mt][0] * f0;
+          ow[2 * tig * D + c1] = oacc[mt][2] * f0;
         }
         if (2 * tig + 1 < G) {
-          sm.o[warp][2 * tig + 1][16 * k + grp] = oacc[mt][1] * f1;
-          sm.o[warp][2 * tig + 1][16 * k + grp + 8] = oacc[mt][3] * f1;
-        }
-      }
-      cons_sync();
-      for (int e = threadIdx.x; e < G * D / 4; e += kCons) {
-        const int g = e / (D / 4), c = 2 * (e % (D / 4));
-        float a = 0.0f, z = 0.0f, L = 0.0f, M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][g]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          a += sm.o[w][g][c];
-          z += sm.o[w][g][c + 1];
-          L += sm.m[w][g] == -INFINITY ? sm.l[w][g] : sm.l[w][g] * ptx::ex2(sm.m[w][g] - M);
-        }
-        const int dim = half * (D / 2) + c;
-        if (meta.parts == 1) {
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          *reinterpret_cast<uint32_t*>(out + orow + g * D + dim) = pack_bf16(a * inv, z * inv);
-        } else {
-          *reinterpret_cast<float2*>(po + g * D + dim) = make_float2(a, z);
-          if (dim == 0) {
-            parts.ml[(int64_t)meta.slot * 2 * G + 2 * g] = M;
-            parts.ml[(int64_t)meta.slot * 2 * G + 2 * g + 1] = L;
-          }
+          ow[(2 * tig + 1) * D + c0] = oacc[mt][1] * f1;
+          ow[(2 * tig + 1) * D + c1] = oacc[mt][3] * f1;
         }
       }
     }
+    cons_sync();
+    const int64_t orow = (int64_t)meta.item * G * D;  // item's G rows of out are adjacent
+    float* po = parts.o + (int64_t)meta.slot * G * D;
+    for (int e = threadIdx.x; e < G * D / 2; e += kCons) {
+      const int g = e / (D / 2), c = 2 * (e % (D / 2));
+      const float* at = sm.o[0] + g * D + (c ^ (8 * (g >> 1)));
+      float a = 0.0f, z = 0.0f, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = *reinterpret_cast<const float2*>(at + w * (G * D));
+        a += x.x;
+        z += x.y;
+        L += sm.l[turn][w][g];
+      }
+      if (meta.parts == 1) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        *reinterpret_cast<uint32_t*>(out + orow + g * D + c) = pack_bf16(a * inv, z * inv);
+      } else {
+        *reinterpret_cast<float2*>(po + g * D + c) = make_float2(a, z);
+        if (c == 0) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[turn][w][g]);
+          *reinterpret_cast<float2*>(parts.ml + ((int64_t)meta.slot * G + g) * 2) = make_float2(M, L);
+        }
+      }
+    }
+    turn ^= 1;
     if (meta.parts > 1) {
       __threadfence();
       cons_sync();
@@ -524,49 +549,77 @@ __global__ void __launch_bounds__(kThreads, 2)
       cons_sync();
       if (sm.last_part) {
         __threadfence();
-        for (int e = threadIdx.x; e < G * D / 2; e += kCons) {
-          const int g = e / (D / 2), c = 2 * (e % (D / 2));
-          float M = -INFINITY, L = 0.0f, a = 0.0f, z = 0.0f;
+        constexpr int kCols = Join<D, G>::kCols, kLanes = Join<D, G>::kLanes;
+        for (int e = threadIdx.x % (kCols < kCons ? kCols : kCons); e < kCols; e += kCons) {
+          const int g = e / (D / 4), c = 4 * (e % (D / 4)), pl = threadIdx.x / (kCols < kCons ? kCols : kCons);
+          float M = -INFINITY, L = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           constexpr int kBatch = 8;  // parts in flight
-          for (int p0 = 0; p0 < meta.parts; p0 += kBatch) {
-            float2 ml[kBatch], o[kBatch];
+          for (int p0 = pl; p0 < meta.parts; p0 += kBatch * kLanes) {
+            float2 ml[kBatch];
+            float4 o[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-              const int p = p0 + k;
+              const int p = p0 + k * kLanes;
               const int64_t slot = p == 0 ? meta.slot0 : 2 * (int64_t)(meta.cfirst + p);
               ml[k] = make_float2(-INFINITY, 0.0f);
-              o[k] = make_float2(0.0f, 0.0f);
+              o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               if (p < meta.parts) {
                 ml[k] = __ldcg(reinterpret_cast<const float2*>(parts.ml + slot * 2 * G + 2 * g));
-                o[k] = __ldcg(reinterpret_cast<const float2*>(parts.o + slot * G * D + g * D + c));
+                o[k] = __ldcg(reinterpret_cast<const float4*>(parts.o + slot * G * D + g * D + c));
               }
             }
             float bm = M;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
             if (bm > M) {
-              const float f = M == -INFINITY ? 0.0f : ptx::ex2(M - bm);
-              L *= f; a *= f; z *= f;
+              const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - bm);
+              L *= f;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) acc[d] *= f;
               M = bm;
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-              const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.0f ? 0.0f : 1.0f) : ptx::ex2(ml[k].x - M);
+              // a part without a maximum saw no key (or nothing but NaN scores)
+              const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
               L = fmaf(ml[k].y, f, L);
-              a = fmaf(o[k].x, f, a);
-              z = fmaf(o[k].y, f, z);
+              acc[0] = fmaf(o[k].x, f, acc[0]);
+              acc[1] = fmaf(o[k].y, f, acc[1]);
+              acc[2] = fmaf(o[k].z, f, acc[2]);
+              acc[3] = fmaf(o[k].w, f, acc[3]);
             }
           }
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          *reinterpret_cast<uint32_t*>(out + orow + g * D + c) = pack_bf16(a * inv, z * inv);
+          if (kLanes > 1) {
+            sm.jm[threadIdx.x] = M;
+            sm.jl[threadIdx.x] = L;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) sm.jo[threadIdx.x][d] = acc[d];
+            cons_sync();
+            if (pl == 0) {
+#pragma unroll
+              for (int k = 1; k < kLanes; ++k) {
+                const float m2 = sm.jm[e + k * kCols], top = fmaxf(M, m2);
+                const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - top);
+                const float f2 = m2 == -INFINITY ? 1.0f : ptx::ex2(m2 - top);
+                L = L * f + sm.jl[e + k * kCols] * f2;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) acc[d] = acc[d] * f + sm.jo[e + k * kCols][d] * f2;
+                M = top;
+              }
+            }
+          }
+          if (pl == 0) {
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            *reinterpret_cast<uint2*>(out + orow + g * D + c) =
+                make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+          }
         }
       }
     }
-    cons_sync();  // the merge buffers are free again
   }
 }
 
-constexpr int kMinRun = 4;  // pages a CTA takes at least: below, joining costs more than a page
+constexpr int kMinRun = 4;  // pages a CTA takes at least
 
 struct Ws {
   size_t counter, ml, o, total;
@@ -587,7 +640,7 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Poo
   const Ws w = ws_layout(pr);
   CUtensorMap kmap, vmap;
   const int64_t rows = pools.num_pages * pr.Hkv * kPage;
-  if (!make_tmap_rows(&kmap, pools.k, rows, D, kPage) || !make_tmap_rows(&vmap, pools.v, rows, D, kPage))
+  if (!make_tmap_page(&kmap, pools.k, rows, D) || !make_tmap_page(&vmap, pools.v, rows, D))
     return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -598,9 +651,9 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Poo
   if (e != cudaSuccess) return e;
   e = launch_clear(ws, w.counter + (size_t)pr.B * pr.Hkv * 4, st);
   if (e != cudaSuccess) return e;
-  // two CTAs share an SM; fewer where the capacity has fewer units
+  // a CTA per SM; fewer where the capacity has fewer units
   const int64_t units = pr.B * pr.Hkv * (idx ? pr.K + 3 : pools.nb);
-  const int64_t grid = std::min<int64_t>(std::min(2 * sm_count(dev), kMaxCtas), ceil_div64(units, kMinRun));
+  const int64_t grid = std::min<int64_t>(std::min(sm_count(dev), kMaxCtas), ceil_div64(units, kMinRun));
   Parts parts{(int32_t*)(ws + w.counter), (float*)(ws + w.ml), (float*)(ws + w.o)};
   note_launch();
   return launch_pdl(true, kern, dim3((unsigned)grid), dim3(kThreads), smem, st, pr, m, kmap, vmap,

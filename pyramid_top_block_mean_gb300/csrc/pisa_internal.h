@@ -113,6 +113,10 @@ cudaError_t launch_pdl(bool pdl, void (*kern)(KArgs...), dim3 grid, dim3 block, 
 // 128-byte swizzle (the K-major operand layout of the tcgen05 MMAs).
 bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int d, int box_rows);
 
+// 3D TMA view [64 columns, rows, d / 64] of a bf16 tensor [rows, d]: one box
+// is 64 rows whole, its 64-column parts one after the other (128-byte swizzle).
+bool make_tmap_page(CUtensorMap* m, const void* base, int64_t rows, int d);
+
 // 4D TMA view of bf16 queries [B, Hq, n, d]: box of 64 columns x `tokens`
 // tokens x the G heads of a group, 128-byte swizzle; tokens past n read as zeros.
 bool make_tmap_q(CUtensorMap* m, const void* base, int64_t B, int64_t Hq, int64_t n, int d, int G, int tokens);
