@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kWarps = 8;               // consumer warps, 16 keys each: two groups, which take turns at the pages
 constexpr int kCons = 32 * kWarps;      // consumer threads
-constexpr int kThreads = kCons + 32;    // and the producer warp
+constexpr int kMerge = 96;              // threads that merge a part while the consumers are at the next one
+constexpr int kThreads = kCons + 32 + kMerge;  // and the producer warp
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
 constexpr uint64_t kWaitNs = 4000000000ull;
@@ -55,12 +56,13 @@ struct __align__(16) Meta {
   int32_t slot0;          // and where the first CTA's part goes
 };
 
-// The join of an item's parts: 4 dims a thread; what threads are left over
-// take every kLanes-th part.
+// The join of an item's parts: 8 dims a thread; where that leaves threads
+// over, they take every kLanes-th part.
 template <int D, int G>
 struct Join {
-  static constexpr int kCols = G * D / 4;
-  static constexpr int kLanes = kCols >= kCons ? 1 : kCons / kCols;
+  static constexpr int kCols = G * D / 8;
+  static constexpr int kLanes = kCols * 2 <= kMerge ? kMerge / kCols : 1;
+  static constexpr int kStep = kLanes > 1 ? kCols : kMerge;
 };
 
 template <int D, int G>
@@ -68,10 +70,10 @@ struct Smem {
   uint8_t kv[Shape<D, G>::kStages][2][Shape<D, G>::kTile];
   uint16_t q[Shape<D, G>::kStages][G * D];
   float o[kWarps][G * D];                  // a part's merge
-  float m[2][kWarps][8], l[2][kWarps][8];  // by turns
-  float jo[Join<D, G>::kLanes > 1 ? kCons : 1][4], jm[kCons], jl[kCons];
-  Meta meta[Shape<D, G>::kStages];
-  uint64_t full[Shape<D, G>::kStages], empty[Shape<D, G>::kStages];
+  float m[kWarps][8], l[kWarps][8];
+  float jo[kMerge][8], jm[kMerge], jl[kMerge];
+  Meta meta[Shape<D, G>::kStages], part;
+  uint64_t full[Shape<D, G>::kStages], empty[Shape<D, G>::kStages], mfull, mempty;
   int32_t abort, zero, last_part;
 };
 
@@ -110,7 +112,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void cons_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory"); }
+__device__ __forceinline__ bool merge_all(bool ok) {  // true for all merging threads if for all
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 2, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(x)
+      : "r"((uint32_t)ok), "n"(kMerge)
+      : "memory");
+  return x != 0;
+}
+__device__ __forceinline__ void merge_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMerge) : "memory"); }
 
 // Keys that the query of sequence b sees, and the pages that hold them; a
 // query that sees none has one page, dead.
@@ -148,6 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
+  auto give_up = [&] {  // a wait ran out
+    *abort = 1;
+    if (lane == 0) set_status(status, PISA_DEV_TIMEOUT);
+  };
   if (threadIdx.x == kCons) {
     ptx::prefetch_map(&kmap);
     ptx::prefetch_map(&vmap);
@@ -157,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), kWarps / 2);
     }
+    ptx::mbar_init(ptx::smem_u32(&sm.mfull), kWarps);
+    ptx::mbar_init(ptx::smem_u32(&sm.mempty), kMerge / 32);
     sm.abort = 0;
     sm.zero = 0;
     ptx::fence_mbar_init();
@@ -343,8 +363,127 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0)
       for (int k = max(0, it - kStages); k < it; ++k)
         ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero, kWaitNs);
-    if (!ok && lane == 0) *abort = 1;
-    if (lane == 0 && sm.abort) set_status(status, PISA_DEV_TIMEOUT);
+    if (!ok) give_up();
+    return;
+  }
+
+  if (warp > kWarps) {
+    // ------------------------------------------------- merging a part's warps
+    const int mt = threadIdx.x - (kCons + 32);
+    for (int n = 0;; ++n) {
+      const bool ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.mfull), n & 1, abort, kWaitNs);
+      // all of the merging warps go on, or none
+      if (!merge_all(ok)) {
+        give_up();
+        break;
+      }
+      const Meta part = sm.part;
+      if (part.item < 0) break;
+      const int64_t orow = (int64_t)part.item * G * D;  // an item's G rows of out are adjacent
+      float* po = parts.o + (int64_t)part.slot * G * D;
+      for (int e = mt; e < G * D / 2; e += kMerge) {
+        const int g = e / (D / 2), c = 2 * (e % (D / 2));
+        const float* at = sm.o[0] + g * D + (c ^ (8 * (g >> 1)));
+        float a = 0.0f, z = 0.0f, L = 0.0f, M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][g]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          // without a maximum a warp saw no key (or nothing but NaN scores)
+          const float f = sm.m[w][g] == -INFINITY ? 1.0f : ptx::ex2(sm.m[w][g] - M);
+          const float2 x = *reinterpret_cast<const float2*>(at + w * (G * D));
+          a = fmaf(x.x, f, a);
+          z = fmaf(x.y, f, z);
+          L = fmaf(sm.l[w][g], f, L);
+        }
+        if (part.parts == 1) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          *reinterpret_cast<uint32_t*>(out + orow + g * D + c) = pack_bf16(a * inv, z * inv);
+        } else {
+          *reinterpret_cast<float2*>(po + g * D + c) = make_float2(a, z);
+          if (c == 0) *reinterpret_cast<float2*>(parts.ml + ((int64_t)part.slot * G + g) * 2) = make_float2(M, L);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.mempty));
+      if (part.parts == 1) continue;
+      __threadfence();
+      merge_sync();
+      if (mt == 0) sm.last_part = atomicAdd(parts.counter + part.item, 1) == part.parts - 1;
+      merge_sync();
+      if (!sm.last_part) continue;
+      __threadfence();
+      constexpr int kCols = Join<D, G>::kCols, kLanes = Join<D, G>::kLanes, kStep = Join<D, G>::kStep;
+      const int pl = kLanes > 1 ? mt / kCols : 0;
+      static_assert(kLanes == 1 || kCols * kLanes == kMerge, "every merging thread has a column");
+      for (int e = kLanes > 1 ? mt % kCols : mt; e < kCols; e += kStep) {
+        const int g = e / (D / 8), c = 8 * (e % (D / 8));
+        float M = -INFINITY, L = 0.0f, acc[8] = {};
+        constexpr int kBatch = 8;  // parts in flight
+        for (int p0 = pl; p0 < part.parts; p0 += kBatch * kLanes) {
+          float2 ml[kBatch];
+          float4 o[kBatch][2];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int p = p0 + k * kLanes;
+            const int64_t slot = p == 0 ? part.slot0 : 2 * (int64_t)(part.cfirst + p);
+            ml[k] = make_float2(-INFINITY, 0.0f);
+            o[k][0] = o[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p < part.parts) {
+              const float4* po = reinterpret_cast<const float4*>(parts.o + slot * G * D + g * D + c);
+              ml[k] = __ldcg(reinterpret_cast<const float2*>(parts.ml + (slot * G + g) * 2));
+              o[k][0] = __ldcg(po);
+              o[k][1] = __ldcg(po + 1);
+            }
+          }
+          float bm = M;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
+          if (bm > M) {
+            const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - bm);
+            L *= f;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) acc[d] *= f;
+            M = bm;
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
+            L = fmaf(ml[k].y, f, L);
+            const float ov[8] = {o[k][0].x, o[k][0].y, o[k][0].z, o[k][0].w,
+                                 o[k][1].x, o[k][1].y, o[k][1].z, o[k][1].w};
+#pragma unroll
+            for (int d = 0; d < 8; ++d) acc[d] = fmaf(ov[d], f, acc[d]);
+          }
+        }
+        if (kLanes > 1) {  // (one round of the loop, for all threads)
+          sm.jm[mt] = M;
+          sm.jl[mt] = L;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) sm.jo[mt][d] = acc[d];
+          merge_sync();
+          if (pl == 0) {
+#pragma unroll
+            for (int k = 1; k < kLanes; ++k) {
+              const float m2 = sm.jm[e + k * kCols], top = fmaxf(M, m2);
+              const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - top);
+              const float f2 = m2 == -INFINITY ? 1.0f : ptx::ex2(m2 - top);
+              L = L * f + sm.jl[e + k * kCols] * f2;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) acc[d] = acc[d] * f + sm.jo[e + k * kCols][d] * f2;
+              M = top;
+            }
+          }
+          merge_sync();
+        }
+        if (pl == 0) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          *reinterpret_cast<uint4*>(out + orow + g * D + c) =
+              make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
+                         pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+        }
+      }
+    }
     return;
   }
 
@@ -359,7 +498,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
   float sl0 = 0.0f, sl1 = 0.0f;
   // group warp / 4 takes every other stage
-  int st = (warp >> 2) - 2, ph = 0, turn = 0;
+  int st = (warp >> 2) - 2, ph = 0, merges = 0;
+  auto wait_merged = [&] {  // the merge buffer is free
+    const bool ok = merges == 0 || ptx::mbar_wait_fast(ptx::smem_u32(&sm.mempty), (merges - 1) & 1, abort, kWaitNs);
+    if (!__all_sync(0xffffffffu, ok)) {
+      give_up();
+      return false;
+    }
+    return true;
+  };
   for (;;) {
     if ((st += 2) >= kStages) {
       st -= kStages;
@@ -367,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const bool okw = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
     if (!__all_sync(0xffffffffu, okw)) {
-      *abort = 1;
+      give_up();
       break;
     }
     const Meta meta = sm.meta[st];
@@ -480,142 +627,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
     if (!meta.last) continue;
 
-    // ----------------------------- end of a part: merge the warps of both groups
+    // ------------------ end of a part: hand (m, l, o) to the merging warps
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    if (grp == 0) *reinterpret_cast<float2*>(&sm.m[turn][warp][2 * tig]) = make_float2(m0, m1);
-    cons_sync();
-    float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 mw = *reinterpret_cast<const float2*>(&sm.m[turn][w][2 * tig]);
-      M0 = fmaxf(M0, mw.x);
-      M1 = fmaxf(M1, mw.y);
+    if (!wait_merged()) break;
+    if (warp == 0 && lane == 0) sm.part = meta;
+    if (grp == 0) {
+      *reinterpret_cast<float2*>(&sm.m[warp][2 * tig]) = make_float2(m0, m1);
+      *reinterpret_cast<float2*>(&sm.l[warp][2 * tig]) = make_float2(l0, l1);
     }
-    // without a maximum a warp saw no key (or nothing but NaN scores)
-    const float f0 = m0 == -INFINITY ? 1.0f : ptx::ex2(m0 - M0), f1 = m1 == -INFINITY ? 1.0f : ptx::ex2(m1 - M1);
-    if (grp == 0) *reinterpret_cast<float2*>(&sm.l[turn][warp][2 * tig]) = make_float2(l0 * f0, l1 * f1);
     // o[warp][head][dim]; the dims of a head are permuted by 8 (head / 2), which spreads tig over the banks
-    {
-      float* ow = sm.o[warp];
+    float* ow = sm.o[warp];
 #pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        const int c0 = (16 * mt + grp) ^ (8 * tig), c1 = (16 * mt + grp + 8) ^ (8 * tig);
-        if (2 * tig < G) {
-          ow[2 * tig * D + c0] = oacc[mt][0] * f0;
-          ow[2 * tig * D + c1] = oacc[mt][2] * f0;
-        }
-        if (2 * tig + 1 < G) {
-          ow[(2 * tig + 1) * D + c0] = oacc[mt][1] * f1;
-          ow[(2 * tig + 1) * D + c1] = oacc[mt][3] * f1;
-        }
+    for (int mt = 0; mt < D / 16; ++mt) {
+      const int c0 = (16 * mt + grp) ^ (8 * tig), c1 = (16 * mt + grp + 8) ^ (8 * tig);
+      if (2 * tig < G) {
+        ow[2 * tig * D + c0] = oacc[mt][0];
+        ow[2 * tig * D + c1] = oacc[mt][2];
+      }
+      if (2 * tig + 1 < G) {
+        ow[(2 * tig + 1) * D + c0] = oacc[mt][1];
+        ow[(2 * tig + 1) * D + c1] = oacc[mt][3];
       }
     }
-    cons_sync();
-    const int64_t orow = (int64_t)meta.item * G * D;  // item's G rows of out are adjacent
-    float* po = parts.o + (int64_t)meta.slot * G * D;
-    for (int e = threadIdx.x; e < G * D / 2; e += kCons) {
-      const int g = e / (D / 2), c = 2 * (e % (D / 2));
-      const float* at = sm.o[0] + g * D + (c ^ (8 * (g >> 1)));
-      float a = 0.0f, z = 0.0f, L = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 x = *reinterpret_cast<const float2*>(at + w * (G * D));
-        a += x.x;
-        z += x.y;
-        L += sm.l[turn][w][g];
-      }
-      if (meta.parts == 1) {
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        *reinterpret_cast<uint32_t*>(out + orow + g * D + c) = pack_bf16(a * inv, z * inv);
-      } else {
-        *reinterpret_cast<float2*>(po + g * D + c) = make_float2(a, z);
-        if (c == 0) {
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[turn][w][g]);
-          *reinterpret_cast<float2*>(parts.ml + ((int64_t)meta.slot * G + g) * 2) = make_float2(M, L);
-        }
-      }
-    }
-    turn ^= 1;
-    if (meta.parts > 1) {
-      __threadfence();
-      cons_sync();
-      if (threadIdx.x == 0) sm.last_part = atomicAdd(parts.counter + meta.item, 1) == meta.parts - 1;
-      cons_sync();
-      if (sm.last_part) {
-        __threadfence();
-        constexpr int kCols = Join<D, G>::kCols, kLanes = Join<D, G>::kLanes;
-        for (int e = threadIdx.x % (kCols < kCons ? kCols : kCons); e < kCols; e += kCons) {
-          const int g = e / (D / 4), c = 4 * (e % (D / 4)), pl = threadIdx.x / (kCols < kCons ? kCols : kCons);
-          float M = -INFINITY, L = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          constexpr int kBatch = 8;  // parts in flight
-          for (int p0 = pl; p0 < meta.parts; p0 += kBatch * kLanes) {
-            float2 ml[kBatch];
-            float4 o[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int p = p0 + k * kLanes;
-              const int64_t slot = p == 0 ? meta.slot0 : 2 * (int64_t)(meta.cfirst + p);
-              ml[k] = make_float2(-INFINITY, 0.0f);
-              o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (p < meta.parts) {
-                ml[k] = __ldcg(reinterpret_cast<const float2*>(parts.ml + slot * 2 * G + 2 * g));
-                o[k] = __ldcg(reinterpret_cast<const float4*>(parts.o + slot * G * D + g * D + c));
-              }
-            }
-            float bm = M;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
-            if (bm > M) {
-              const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - bm);
-              L *= f;
-#pragma unroll
-              for (int d = 0; d < 4; ++d) acc[d] *= f;
-              M = bm;
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              // a part without a maximum saw no key (or nothing but NaN scores)
-              const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
-              L = fmaf(ml[k].y, f, L);
-              acc[0] = fmaf(o[k].x, f, acc[0]);
-              acc[1] = fmaf(o[k].y, f, acc[1]);
-              acc[2] = fmaf(o[k].z, f, acc[2]);
-              acc[3] = fmaf(o[k].w, f, acc[3]);
-            }
-          }
-          if (kLanes > 1) {
-            sm.jm[threadIdx.x] = M;
-            sm.jl[threadIdx.x] = L;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) sm.jo[threadIdx.x][d] = acc[d];
-            cons_sync();
-            if (pl == 0) {
-#pragma unroll
-              for (int k = 1; k < kLanes; ++k) {
-                const float m2 = sm.jm[e + k * kCols], top = fmaxf(M, m2);
-                const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - top);
-                const float f2 = m2 == -INFINITY ? 1.0f : ptx::ex2(m2 - top);
-                L = L * f + sm.jl[e + k * kCols] * f2;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) acc[d] = acc[d] * f + sm.jo[e + k * kCols][d] * f2;
-                M = top;
-              }
-            }
-          }
-          if (pl == 0) {
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            *reinterpret_cast<uint2*>(out + orow + g * D + c) =
-                make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-          }
-        }
-      }
-    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.mfull));
+    ++merges;
+  }
+  // no more parts
+  if (wait_merged()) {
+    if (warp == 0 && lane == 0) sm.part.item = -1;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.mfull));
   }
 }
 
