@@ -40,8 +40,10 @@ constexpr uint64_t kWaitNs = 4000000000ull;
 
 template <int D, int G>
 struct Shape {
-  // as many as fit beside the merge buffer
-  static constexpr int kStages = D == 128 ? (G == 8 ? 5 : 6) : (G == 8 ? 11 : 12);
+  // as many as fit beside the merge buffer; even, so that a stage always goes
+  // to the same group, which then sees each of its phases
+  static constexpr int kStages = D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);
+  static_assert(kStages % 2 == 0, "a group must see every phase of its stages");
   static constexpr uint32_t kTile = kPage * D * 2;  // bytes of a page's keys
 };
 

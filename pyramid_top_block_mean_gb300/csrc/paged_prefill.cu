@@ -73,7 +73,7 @@ struct Smem {
   uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTile];
   uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
   uint64_t ifull[kItems], iempty[kItems];
-  uint64_t qfull[2], qempty[2], scrub, sfull[2], pfull[2][2], odone[2], done[2];
+  uint64_t qfull[2], qempty[2], scrub, sfull[2], pfull[2][2], odone[2], done[2], lent, rows_out;
   Item item[kItems];
   uint32_t tmem;
   int32_t abort, zero, bad_page;
@@ -87,7 +87,6 @@ struct Args {
   float *part_o, *part_ml;  // [split][256-row group][256][D] and [..][2] (m in log2 units, l)
   // 256-row groups per (sequence, key head), parts of the keys, log2 of a tile's tokens, items in all
   int32_t tiles, splits, lg_tokens, items;
-  int32_t wide;  // outputs and parts start on 32-byte boundaries
 };
 
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
@@ -150,18 +149,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
-
-// 32 bytes, in one store where the address allows it.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], int wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-  }
-}
 
 // Both MMA warps meet; true for both if both say so.
 __device__ __forceinline__ bool both_ok(bool ok) {
@@ -235,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&sm.iempty[k]), 10);
     }
     ptx::mbar_init(ptx::smem_u32(&sm.scrub), 1);
+    ptx::mbar_init(ptx::smem_u32(&sm.lent), 1);
+    ptx::mbar_init(ptx::smem_u32(&sm.rows_out), 8);
     for (int v = 0; v < 2; ++v) {
       ptx::mbar_init(ptx::smem_u32(&sm.qfull[v]), 1);
       ptx::mbar_init(ptx::smem_u32(&sm.qempty[v]), 1);
@@ -270,8 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int fills = 0, scrubs = 0, items = 0, qfills[2] = {0, 0};
       int st = 0, ph = 0;  // stage and phase of the next fill
+      auto advance = [&] {
+        ++fills;
+        if (++st == kStages) { st = 0; ph ^= 1; }
+      };
       auto wait = [&](uint64_t* bar, int phase) {
         ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
+        return ok;
+      };
+      // the stage that an item's rows go out through, until they have
+      int lent = -1, lendings = 0;
+      auto take_back = [&] {
+        if (lent >= 0) wait(&sm.rows_out, lendings++);
+        lent = -1;
         return ok;
       };
       auto claim = [&] {
@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (fills >= kStages && !wait(&sm.empty[st], ph ^ 1)) break;  // the first round finds them empty
+            if (lent == st && !take_back()) break;
             const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
             const bool scrub = kv == 1 && clear;
             const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
@@ -430,10 +431,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (lane == 0) ptx::mbar_arrive(full);
             }
-            ++fills;
-            if (++st == kStages) { st = 0; ph ^= 1; }
+            advance();
           }
         }
+        // one more stage, empty: the item's rows go out through it
+        if (!take_back() || (fills >= kStages && !wait(&sm.empty[st], ph ^ 1))) break;
+        lent = st;
+        if (lane == 0) {
+          ptx::mbar_arrive(ptx::smem_u32(&sm.lent));
+          // nobody else sees it filled or releases it: rows_out says when it is free
+          ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
+          ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
+          ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
+        }
+        __syncwarp();
+        advance();
       }
       if ((items < kItems || wait(&sm.iempty[items % kItems], (items / kItems) + 1)) && ok && lane == 0) {
         sm.item[items % kItems].bh = -1;
@@ -479,21 +491,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int uja = __shfl_sync(0xffffffffu, ip->ja, 0), ujb = __shfl_sync(0xffffffffu, ip->jb, 0);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
-        if (uja >= ujb) continue;
-        if (av < bv) wait(&sm.qfull[v], qfills++);
-        for (int j = uja - 1; j < ujb; ++j) {
+        if (uja < ujb && av < bv) wait(&sm.qfull[v], qfills++);
+        for (int j = uja - 1; j < ujb && uja < ujb; ++j) {
           const bool has_o = j >= av && j < bv, has_s = j + 1 >= av && j + 1 < bv;
           const int sv = st, pv = ph;  // V(j)
           if (j >= uja && ++st == kStages) { st = 0; ph ^= 1; }
           const int sk = st, pk = ph;  // K(j + 1)
           if (j + 1 < ujb && ++st == kStages) { st = 0; ph ^= 1; }
           const uint32_t vb = ptx::smem_u32(sm.kv[sv]), kb = ptx::smem_u32(sm.kv[sk]);
-          if (has_o) {
-            wait(&sm.pfull[v][0], tiles_done);
-          } else {
+          if (!has_o || j == av) {  // (else a softmax warp has)
             if (j >= uja) wait(&sm.full[sv], pv);
             if (j + 1 < ujb) wait(&sm.full[sk], pk);
           }
+          if (has_o) wait(&sm.pfull[v][0], tiles_done);
           if (v == 1 || j >= uja) turn_wait(v);
           if (has_o) {
             ptx::tc_fence_after();
@@ -531,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (!ok && lane == 0) *abort = 1;
         }
+        if (++st == kStages) { st = 0; ph ^= 1; }  // the stage that the rows go out through
       }
       if (elect_one()) ptx::mma_commit(ptx::smem_u32(&sm.done[v]));
       __syncwarp();
@@ -571,13 +582,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MODE == 1 && mk.slopes)
           slope = mk.slopes[(ip->bh - b * pr.Hkv) * pr.G + (r >> a.lg_tokens)] * kLog2e;
       }
-      const int f0 = ip->fill + 2 * (wa - ip->ja) + 1;  // the fill of the first V
+      const int f0 = ip->fill + 2 * (wa - ip->ja) + 3;  // the fill of the second V
       float m = -INFINITY, l = 0.0f;
       int st = f0 % kStages, ph = (f0 / kStages) & 1;
       for (int j = wa; j < wb; ++j) {
         ok = true;
-        if ((warp & 3) == 0) {
-          // for the MMA warp: V(j) and K(j + 1) are there (as a rule they are by now)
+        if ((warp & 3) == 0 && j > wa) {
+          // for the MMA warp: V(j) and K(j + 1) are there (as a rule they are by
+          // now).  Not at an item's first tile: this warp has not followed the
+          // ring up to it, and could take a phase for the one two fills earlier.
           ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
           if (++st == kStages) { st = 0; ph ^= 1; }
           if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
@@ -638,15 +651,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (part) {
-          // one comparison where no row starts inside the tile
+          // each side by itself: a tile rarely needs both
           if (__any_sync(0xffffffffu, clo > 0)) {
 #pragma unroll
             for (int c = 0; c < kKeys; ++c)
               if (c < clo) s[c] = -INFINITY;
           }
+          if (__any_sync(0xffffffffu, chi < kKeys - 1)) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c > chi) s[c] = -INFINITY;
+            for (int c = 0; c < kKeys; ++c)
+              if (c > chi) s[c] = -INFINITY;
+          }
         }
         if (bad) {
 #pragma unroll
@@ -731,6 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         ptx::tc_fence_after();
       }
+      const int est = (ip->fill + 2 * (jb - ip->ja)) % kStages;  // the stage lent for the rows
+      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.lent), items & 1, abort, kWaitNs);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       const int64_t b = (uint32_t)ip->bh / (uint32_t)pr.Hkv;
       const int32_t hq = (ip->bh - (int32_t)b * pr.Hkv) * pr.G + (r >> a.lg_tokens);
       const int32_t i = ip->tile * 2 * tokens + w * tokens + (r & (tokens - 1));
@@ -739,45 +757,73 @@ __global__ void __launch_bounds__(kThreads, 1)
           (((int64_t)ip->split * a.tiles + ip->tile) * heads + (uint32_t)ip->bh) * (2 * kRows) + w * kRows + r;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
-      // rows go out in whole 32-byte sectors, straight from registers: the
-      // next item's queries may be in the tile that these rows came from
+      // Rows go out through shared memory, a part of each at a time, so that
+      // the stores cover whole lines (a row per thread would occupy the LSU,
+      // and with it every barrier, for 4000 cycles).
+      constexpr int kPart = D == 128 ? 128 : 64;  // bytes of a row at a time
+      constexpr int kLines = kPart / 16;          // 16-byte pieces of that
+      const uint32_t buf = ptx::smem_u32(sm.kv[est]) + w * (kTile / 2) + (warp & 3) * (32 * kPart);
+      const int swz = kLines == 8 ? (lane & 7) : ((lane >> 1) & 3);
+      auto pass = [&](const uint32_t (&x)[kPart / 4], char* dst) {
+#pragma unroll
+        for (int c = 0; c < kLines; ++c)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * kPart + ((c ^ swz) << 4)),
+                       "r"(x[4 * c]), "r"(x[4 * c + 1]), "r"(x[4 * c + 2]), "r"(x[4 * c + 3])
+                       : "memory");
+        __syncwarp();
+        const int c = lane % kLines;
+#pragma unroll
+        for (int k = 0; k < kLines; ++k) {
+          const int rr = (32 / kLines) * k + lane / kLines;
+          const uint64_t dp = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), rr);
+          uint32_t a0, a1, a2, a3;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                       : "r"(buf + rr * kPart + ((c ^ (kLines == 8 ? (rr & 7) : ((rr >> 1) & 3))) << 4))
+                       : "memory");
+          if (dp) reinterpret_cast<uint4*>(dp)[c] = make_uint4(a0, a1, a2, a3);
+        }
+        __syncwarp();
+      };
       if (a.splits > 1) {
         // this part of the row: m in log2 units, l, and O as it is
         if (row) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(any ? m * sc : -INFINITY, any ? l : 0.0f);
         if (any) {
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            ptx::tmem_ld32(o_at + c, o);
+          for (int c = 0; c < D; c += kPart / 4) {
+            uint32_t o[kPart / 4];
+            if constexpr (kPart == 128) ptx::tmem_ld32(o_at + c, o);
+            else tmem_ld16(o_at + c, o);
             ptx::tmem_ld_wait();
-            if (row) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 8)
-                store32(a.part_o + at * D + c + k, *reinterpret_cast<uint32_t(*)[8]>(&o[k]), a.wide);
-            }
+            pass(o, row ? reinterpret_cast<char*>(a.part_o + at * D + c) : nullptr);
           }
         }
       } else {
         const float inv = 1.0f / l;
         const bool none = !any || l == 0.0f;
-        uint16_t* dst = a.out + ((b * pr.Hq + hq) * a.n + i) * D;
+        char* dst = row ? reinterpret_cast<char*>(a.out + ((b * pr.Hq + hq) * a.n + i) * D) : nullptr;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (any) {
-            ptx::tmem_ld32(o_at + c, o);
-            ptx::tmem_ld_wait();
-          }
-          uint32_t pk[16];
+        for (int c = 0; c < D; c += kPart / 2) {
+          uint32_t pk[kPart / 4];
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            pk[k] = none ? 0u : pack_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-          if (row) {
-            store32(dst + c, *reinterpret_cast<uint32_t(*)[8]>(&pk[0]), a.wide);
-            store32(dst + c + 16, *reinterpret_cast<uint32_t(*)[8]>(&pk[8]), a.wide);
+          for (int c2 = 0; c2 < kPart / 2; c2 += 32) {
+            uint32_t o[32];
+            if (any) {
+              ptx::tmem_ld32(o_at + c + c2, o);
+              ptx::tmem_ld_wait();
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              pk[c2 / 2 + k] =
+                  none ? 0u : pack_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
           }
+          pass(pk, dst ? dst + 2 * c : nullptr);
         }
       }
+      // the copy that fills the stage next comes after these accesses
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.rows_out));
       ptx::tc_fence_before();  // the next item's weights, and so its first MMA into O, come after these reads
     }
     if (!ok) *abort = 1;
@@ -934,7 +980,6 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   a.out = (uint16_t*)out;
   a.part_ml = (float*)(ws + pl.ml);
   a.part_o = (float*)(ws + pl.o);
-  a.wide = ((uintptr_t)out & 31) == 0 && ((uintptr_t)ws & 31) == 0;
   a.items = (int32_t)(pl.ctas * pl.splits);
   int dev = 0;
   e = cudaGetDevice(&dev);

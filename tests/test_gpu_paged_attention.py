@@ -73,10 +73,12 @@ def test_decode_masks_and_scores(pisa, kw):
     assert run_decode(pisa, 6, 8, 2, 128, 777, [1, 64, 65, 300, 777, 641], seed=3, **kw) == 0
 
 
-@pytest.mark.parametrize("B,N,Hq,Hkv", [(1, 40000, 8, 1), (2, 20011, 16, 8), (1, 5, 1, 1), (300, 130, 4, 2)])
-def test_decode_split_over_the_gpu(pisa, B, N, Hq, Hkv):
+@pytest.mark.parametrize("B,N,Hq,Hkv", [(1, 40000, 8, 1), (2, 20011, 16, 8), (1, 5, 1, 1), (300, 130, 4, 2),
+                                        (12, 4000, 16, 2)])
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_split_over_the_gpu(pisa, B, N, Hq, Hkv, d):
     lens = [max(1, N - 37 * b) for b in range(B)]
-    assert run_decode(pisa, B, Hq, Hkv, 128, N, lens, seed=B) == 0
+    assert run_decode(pisa, B, Hq, Hkv, d, N, lens, seed=B) == 0
 
 
 def test_decode_uneven_batch(pisa):
@@ -243,6 +245,19 @@ def test_prefill_few_rows_behind_a_long_cache(pisa, n, past, B):
     run_prefill(pisa, 8, 2, 128, past + n, n, [past + n - 100 * b for b in range(B)], [n] * B, seed=n)
     run_prefill(pisa, 8, 2, 128, past + n, n, [past + n - 100 * b for b in range(B)], [n] * B, seed=n, softcap=20.0,
                 window=past // 2)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 2, 128), (8, 2, 128), (8, 1, 64)])
+def test_prefill_row_tiles_with_distant_spans(pisa, Hq, Hkv, d):
+    # neighbouring tokens that see far apart parts of the cache, or short ones
+    n = 300
+    first = torch.zeros(3, n, dtype=torch.int32)
+    first[0, 20:] = 2700
+    first[0, 128:] = 0
+    first[1, :128] = 2500
+    first[2] = (torch.arange(n) % 7) * 450
+    for prefix in (None, [0, 2990, 100]):
+        run_prefill(pisa, Hq, Hkv, d, 3000, n, [3000, 2900, 2999], [n, n, 290], seed=8, first=first.cuda(), prefix=prefix)
 
 
 def test_prefill_many_sequences(pisa):
