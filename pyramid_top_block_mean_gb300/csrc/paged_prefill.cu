@@ -63,7 +63,7 @@ struct Item {
   int32_t fits;             // its lengths do
   int32_t ja, jb;           // key tiles
   int32_t wa[2], wb[2];     // and those that each row tile takes part in
-  int32_t khi;              // last key that any row sees
+  int32_t klo, khi;         // first and last key that any row sees
   int32_t fill;             // fills of the ring before the item's first
 };
 
@@ -81,6 +81,7 @@ struct Smem {
 
 struct Args {
   int64_t n, nb, num_pages;
+  const uint16_t *q, *k, *v;
   const int32_t *seq_lens, *new_lens, *table;
   int32_t *status, *claimed;  // claimed: items taken beyond each CTA's first
   uint16_t* out;
@@ -190,6 +191,74 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// A weight of zero does not undo a value that is not finite: the MMA takes the
+// values of all keys of a tile into all of its rows.  When a row came out
+// without being finite, a warp looks through the values that the row does not
+// see but that its tiles held; if one of them is to blame, it computes the row
+// anew from the keys that the row sees, one after the other.  (Slow, and only
+// there for that case; it is not inlined to keep the kernel's code small.)
+// Row: token i at position t, head g of key head bh % Hkv, keys lo .. hi; its
+// tiles held the keys ka .. kb; `at` is its place among the parts.
+template <int D, int MODE>
+__device__ __noinline__ void mend_row(const Prob& pr, const MaskArgs& mk, const Args& a, int32_t bh, int32_t i,
+                                      int32_t g, int32_t t, int32_t lo, int32_t hi, int32_t ka, int32_t kb,
+                                      int64_t at) {
+  constexpr int J = D / 32;  // dims lane + 32 j
+  const int lane = threadIdx.x & 31;
+  const int64_t b = (uint32_t)bh / (uint32_t)pr.Hkv;
+  const int h = bh - (int)b * pr.Hkv;
+  const int32_t* trow = a.table + b * a.nb;
+  auto row_of = [&](int32_t key) -> int64_t {  // of the pools; negative: page outside
+    const int32_t page = trow[key / kPage];
+    return page < 0 || page >= a.num_pages ? -1 : (((int64_t)page * pr.Hkv + h) * kPage + key % kPage) * D + lane;
+  };
+  const int32_t s0 = max(lo, ka), s1 = min(hi, kb);
+  bool found = false;
+  for (int32_t key = ka; key <= kb && !found; ++key) {
+    if (key == s0 && s0 <= s1) {
+      key = s1;
+      continue;
+    }
+    const int64_t v = row_of(key);
+    bool odd = false;
+    if (v >= 0)
+      for (int j = 0; j < J; ++j) odd |= !(fabsf(bf16_to_f(a.v[v + 32 * j])) < INFINITY);
+    found = __any_sync(0xffffffffu, odd);
+  }
+  if (!found) return;
+  const int64_t hq = (int64_t)h * pr.G + g, orow = ((b * pr.Hq + hq) * a.n + i) * D;
+  const float slope = MODE == 1 && mk.slopes ? mk.slopes[hq] * kLog2e : 0.0f;
+  float x[J], acc[J], m = -INFINITY, l = 0.0f;
+  for (int j = 0; j < J; ++j) {
+    x[j] = bf16_to_f(a.q[orow + lane + 32 * j]);
+    acc[j] = 0.0f;
+  }
+  for (int32_t key = s0; key <= s1; ++key) {
+    const int64_t r = row_of(key);
+    if (r < 0) continue;
+    float s = 0.0f;
+    for (int j = 0; j < J; ++j) s = fmaf(x[j], bf16_to_f(a.k[r + 32 * j]), s);
+    s = warp_sum(s);
+    if (MODE == 1 && mk.cap2 > 0.0f)
+      s = fmaf(-2.0f * mk.cap2, 1.0f / (1.0f + exp2f(s * mk.pre * (2.0f * kLog2e))), mk.cap2);
+    else
+      s *= pr.scale2;
+    s = fmaf(slope, (float)(key - t), s);
+    const float top = fmaxf(m, s);
+    const float f = m == -INFINITY ? 1.0f : exp2f(m - top), p = exp2f(s - (top == -INFINITY ? 0.0f : top));
+    l = fmaf(l, f, p);
+    for (int j = 0; j < J; ++j) acc[j] = fmaf(p, bf16_to_f(a.v[r + 32 * j]), acc[j] * f);
+    m = top;
+  }
+  if (a.splits > 1) {
+    if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, l);
+    for (int j = 0; j < J; ++j) a.part_o[at * D + lane + 32 * j] = acc[j];
+  } else {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    for (int j = 0; j < J; ++j) a.out[orow + lane + 32 * j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
+  }
+}
+
 // MODE 0: scores are scale * q . k; 1: with a cap and / or a distance bias.
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -248,6 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   pdl_wait();  // from here on the status word and the claims are clear
+  // the joining kernel, where there is one, may be set up as CTAs of this one end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = sm.tmem;
   const int tokens = 1 << a.lg_tokens;  // of one row tile
   const uint32_t heads = (uint32_t)(pr.B * pr.Hkv);
@@ -337,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.wb[v] = hi[v] < 0 ? it.jb : min(it.jb, hi[v] / kKeys + 1);
           if (it.wb[v] < it.wa[v]) it.wb[v] = it.wa[v];
         }
+        it.klo = klo;
         it.khi = khi;
         it.fill = fills;
         // lane l: the page of block 2 j + l, -1: none of its keys is seen, -2: outside the pool
@@ -755,8 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row = i < ip->cnt;
       const int64_t at =
           (((int64_t)ip->split * a.tiles + ip->tile) * heads + (uint32_t)ip->bh) * (2 * kRows) + w * kRows + r;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
       // Rows go out through shared memory, a part of each at a time, so that
       // the stores cover whole lines (a row per thread would occupy the LSU,
       // and with it every barrier, for 4000 cycles).
@@ -785,16 +855,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
+      float finite = 0.0f;  // NaN once one of the row's outputs is not
       if (a.splits > 1) {
         // this part of the row: m in log2 units, l, and O as it is
         if (row) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(any ? m * sc : -INFINITY, any ? l : 0.0f);
         if (any) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += kPart / 4) {
             uint32_t o[kPart / 4];
             if constexpr (kPart == 128) ptx::tmem_ld32(o_at + c, o);
             else tmem_ld16(o_at + c, o);
             ptx::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < kPart / 4; ++k) finite = fmaf(__uint_as_float(o[k]), 0.0f, finite);
             pass(o, row ? reinterpret_cast<char*>(a.part_o + at * D + c) : nullptr);
           }
         }
@@ -802,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = 1.0f / l;
         const bool none = !any || l == 0.0f;
         char* dst = row ? reinterpret_cast<char*>(a.out + ((b * pr.Hq + hq) * a.n + i) * D) : nullptr;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += kPart / 2) {
           uint32_t pk[kPart / 4];
 #pragma unroll
@@ -811,6 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (any) {
               ptx::tmem_ld32(o_at + c + c2, o);
               ptx::tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) finite = fmaf(__uint_as_float(o[k]), 0.0f, finite);
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -820,6 +895,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           pass(pk, dst ? dst + 2 * c : nullptr);
         }
       }
+      if (unsigned todo = __ballot_sync(0xffffffffu, row && finite != 0.0f)) {
+        const int32_t ka = max(ip->klo, wa * kKeys), kb = min(ip->khi, wb * kKeys - 1);
+        __syncwarp();  // the rows' stores come before those that replace them
+        for (; todo; todo &= todo - 1) {
+          const int x = __ffs(todo) - 1;
+          mend_row<D, MODE>(pr, mk, a, ip->bh, __shfl_sync(0xffffffffu, i, x),
+                            __shfl_sync(0xffffffffu, r >> a.lg_tokens, x), __shfl_sync(0xffffffffu, t, x),
+                            __shfl_sync(0xffffffffu, lo, x), __shfl_sync(0xffffffffu, hi, x), ka, kb,
+                            __shfl_sync(0xffffffffu, at, x));
+        }
+      }
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
       // the copy that fills the stage next comes after these accesses
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -974,6 +1061,7 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   if (e != cudaSuccess) return e;
   Args a{};
   a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages;
+  a.q = (const uint16_t*)q; a.k = (const uint16_t*)pools.k; a.v = (const uint16_t*)pools.v;
   a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = pools.table;
   a.status = (int32_t*)ws;
   a.claimed = (int32_t*)ws + 32;  // cleared with the status word

@@ -351,21 +351,18 @@ class AttentionMask:
     def __init__(self, softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
                  first_key: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None):
         self.slopes, self.first_key, self.prefix_lens = slopes, first_key, prefix_lens
-        self.c = Mask(ctypes.sizeof(Mask), softcap, window, None if slopes is None else slopes.data_ptr(),
-                      None if first_key is None else first_key.data_ptr(),
-                      None if prefix_lens is None else prefix_lens.data_ptr())
+        self.c = Mask(ctypes.sizeof(Mask), softcap, window, None, None, None)  # addresses: at each call
 
 
 def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, index: int):
     if mask is None:
         return None
-    if mask.slopes is not None:
-        _want(mask.slopes, "slopes", (p.H_q,), torch.float32, index)
-    if mask.first_key is not None:
-        _want(mask.first_key, "first_key", (p.B, n), torch.int32, index)
-    if mask.prefix_lens is not None:
-        _want(mask.prefix_lens, "prefix_lens", (p.B,), torch.int32, index)
-    return ctypes.byref(mask.c)
+    c = mask.c
+    c.slopes = None if mask.slopes is None else _want(mask.slopes, "slopes", (p.H_q,), torch.float32, index)
+    c.first_key = None if mask.first_key is None else _want(mask.first_key, "first_key", (p.B, n), torch.int32, index)
+    c.prefix_lens = (None if mask.prefix_lens is None else
+                     _want(mask.prefix_lens, "prefix_lens", (p.B,), torch.int32, index))
+    return ctypes.byref(c)
 
 
 def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, rope=None, interleaved: bool = False,

@@ -294,5 +294,31 @@ def test_prefill_non_finite_values_behind_the_window(pisa):
     run_prefill(pisa, 4, 2, 64, 900, 70, [900], [70], seed=6, window=300, poke=poke)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0, slopes=True), dict(window=40)])
+@pytest.mark.parametrize("n,lens", [(280, [600]), (280, [280]), (30, [3000])])
+def test_prefill_non_finite_values_among_unseen_keys_of_a_tile(pisa, n, lens, kw):
+    # a value reaches the rows that see its key, and no other; the last case is split over the keys
+    Hq, Hkv, d, N = 4, 2, 64, lens[0]
+    k, v, kp, vp, table = cache(1, Hkv, N, d, lens, 6)
+    late = N - n // 2  # seen by the later half of the new tokens alone
+    for j, x in ((late, float("inf")), (late + 3, R.NAN)):
+        vp[int(table[0, j // 64]), :, j % 64, ::5] = x
+    q = (torch.randn(1, Hq, n, d, generator=torch.Generator().manual_seed(7)) * 2).to(torch.bfloat16).cuda()
+    sl = slopes_of(Hq) if kw.get("slopes") else None
+    mask = pisa.AttentionMask(kw.get("softcap", 0.0), kw.get("window", 0), sl)
+    layer = pisa.PagedAttention(pisa.make_params(1, N, Hq, Hkv, d), n=n)
+    out = layer.dense_prefill(q, kp, vp, table, i32(lens), mask=mask)[0]
+    assert layer.device_status() == 0
+    pos = torch.arange(N - n, N, device="cuda")
+    want, tol = R.dense(q[0], k[0], v[0], N, pos, 0.125, kw.get("softcap", 0.0), kw.get("window", 0), sl)
+    lo, _ = R.spans(pos, N, kw.get("window", 0))
+    clean = ~(((pos >= late) & (lo <= late)) | ((pos >= late + 3) & (lo <= late + 3)))
+    assert int(clean.sum()) >= n // 2 and int((~clean).sum()) > 0
+    R.within(out[:, clean], want[:, clean], tol[:, clean], "rows that see finite values")
+    other = torch.arange(d, device="cuda") % 5 != 0
+    R.within(out[:, ~clean][..., other], want[:, ~clean][..., other], tol[:, ~clean][..., other], "finite dims")
+    assert not bool(torch.isfinite(out[:, ~clean][..., ~other]).any())
+
+
 def test_prefill_long_prompt(pisa):
     run_prefill(pisa, 4, 1, 128, 3000, 2500, [3000, 2500], [2500, 2400], seed=7)
