@@ -262,8 +262,9 @@ __device__ __noinline__ void mend_row(const Prob& pr, const MaskArgs& mk, const 
 // MODE 0: scores are scale * q . k; 1: with a cap and / or a distance bias.
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_prefill_kernel(Prob pr, MaskArgs mk, const __grid_constant__ CUtensorMap qmap,
-                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Args a) {
+    paged_prefill_kernel(const __grid_constant__ Prob pr, const __grid_constant__ MaskArgs mk,
+                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
   constexpr int kStages = Cfg<D>::kStages;
   constexpr uint32_t kTile = Cfg<D>::kTile;
   constexpr uint32_t kHalf = kKeys * 128;      // bytes of a tile's 64-column half
