@@ -391,9 +391,10 @@ void pisa_test_inject_leaf_timeout(uint64_t wait_limit_ns, int32_t drop_first_ke
  * (PISA_DEV_BAD_INDEX, never read or written).  The part of the output that
  * they touch is stated per call; everything else is computed.
  *
- * Page table entries behind a sequence's last position are never read, nor
- * are the positions of its last page behind its length: they may hold
- * anything, NaN included. */
+ * Page table entries behind a sequence's last position are never read, and
+ * the positions of its last page behind its length may hold anything, NaN
+ * included.  A value that is not finite reaches the queries that see its key
+ * and no other. */
 
 /* Appends n new tokens per sequence to the pages.  k and v [B, H_kv, n, d]
  * and (nullable) q [B, H_q, n, d] may be strided views: k_strides points at

@@ -10,17 +10,24 @@
 //
 // The unit of work is one page (64 keys and values) of one (sequence, key
 // head).  All units of a call are numbered sequence by sequence, head by head
-// and cut into equal runs, one per CTA, so a long sequence spreads over the
-// GPU and short ones share a CTA; every CTA derives the cut from the lengths
-// on the device.  A producer warp brings the run's pages by TMA (128-byte
-// swizzle, so that every ldmatrix below is free of bank conflicts) into a
-// ring of stages; four warps take 16 of a page's 64 keys each and hold their
-// own (m, l, o): S = K q by m16n8k16 MMAs with the heads as the 8 columns,
-// O^T += V^T P with P turned in registers by movmatrix.  At the end of its
-// part of a (sequence, head) the warps merge in shared memory.  A part that
-// is not the whole goes to the workspace in fp32, and the CTA that brings the
-// last one joins them in the order of the CTAs, so results do not depend on
-// timing.
+// and cut into equal runs, one per CTA and SM, so a long sequence spreads over
+// the GPU and short ones share a CTA; every CTA derives the cut from the
+// lengths on the device.  A producer warp brings the run's pages by TMA
+// (128-byte swizzle, so that every ldmatrix below is free of bank conflicts)
+// into a ring of stages (192 KB in flight on an SM); two groups of four warps
+// take alternate pages, a warp 16 of a page's 64 keys, and hold their own (m,
+// l, o): S = K q by m16n8k16 MMAs with the heads as the 8 columns, O^T += V^T P
+// with P turned in registers by movmatrix.  A page takes a group about 1300
+// cycles, nearly all latency, which is what the second group hides.  At the
+// end of its part of a (sequence, head) three more warps merge the eight while
+// the stream goes on.  A part that is not the whole goes to the workspace in
+// fp32, and the CTA that brings the last one joins them in the order of the
+// CTAs, so results do not depend on timing.
+//
+// Measured (GB300): 64 ragged sequences of up to 8192 tokens, 32 / 8 heads, d
+// = 128: 233 us, 6.7 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
+// tokens 150 us (6.5 TB/s); 64 sequences' 35 selected blocks 95 us (6.1 TB/s);
+// one sequence of 197 tokens 6.8 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -667,7 +674,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-constexpr int kMinRun = 4;  // pages a CTA takes at least
+// Pages a CTA takes at least.  Joining costs 2 us and a page 0.4: 197 tokens of 4
+// heads 6.8 us with 4 (one CTA a head), 8.2 with 2, 9.2 with 8; 4096 tokens 10.0,
+// 10.8 and 10.6.
+constexpr int kMinRun = 4;
 
 struct Ws {
   size_t counter, ml, o, total;

@@ -18,8 +18,17 @@
 //     tiles alternate: while one's softmax runs, the other's MMAs do;
 //   - two groups of four warps do the softmax, one thread per row, so that a
 //     row's maximum and sum need no exchange.
-// Work: 4 d flops for each (row, key); S and O take 2 x 512 cycles of the
-// tensor pipe per tile pair of d = 128 and the softmax 128 exponentials a row.
+// Work: 4 d flops for each (row, key).  For d = 128 the two tiles' MMAs of a
+// step take about 2300 cycles (2048 at the nominal rate; both operands of S
+// come from shared memory, which they saturate) and one tile's chain -- S,
+// softmax, P V, the next S -- about 2800, which is what a step takes.
+// CTAs are persistent: the loader claims the next 256 rows when it has loaded
+// what the current ones need.
+//
+// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 670 us (1640 TFLOP/s of
+// the seen pairs, 85 % of cuBLAS's measured rate), 65536 tokens 10.5 ms (1670),
+// 16384 with a tanh cap 947 us, 2 x 4096 tokens (ragged) 90 us, 61 tokens behind
+// 65536 cached ones 49 us.
 //
 // Rows with few tokens and a long cache: the keys of a CTA's rows are split
 // over several CTAs, whose parts a second kernel joins.
