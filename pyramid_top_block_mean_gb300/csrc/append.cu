@@ -79,21 +79,10 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
   const uint32_t r0 = (uint32_t)(y - i * groups);
   if (i >= a.n) return;
   int64_t len, cnt;
-  if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt)) {
-    if (y == 0 && u == 0) {
-      pdl_wait();
-      set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
-    }
-    return;
-  }
-  if (i >= cnt) return;
+  if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt) || i >= cnt) return;
   const int64_t pos = len - cnt + i;
   const uint32_t page = (uint32_t)a.table[b * a.nb + pos / pr.C];  // a negative entry is past any pool
   const bool in_pool = page < a.num_pages;
-  if (!in_pool && r0 == 0 && u == 0) {
-    pdl_wait();
-    set_status(a.status, PISA_DEV_BAD_INDEX);
-  }
   const int half = a.rot / 2;
   const bool turns = (int)(2 * E * u) < a.rot;  // this unit's dims are among the rotated ones
   float cs[E], sn[E];
@@ -171,7 +160,22 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
 template <typename T, int R>
 __global__ void __launch_bounds__(256, 3) append_kernel(Prob pr, AppendArgs a) {
   for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_units<T, R>(pr, a, b);
-  pdl_wait();
+  // One CTA looks at every length and page for faults and writes the status
+  // word, so that nothing has to clear it before the call.
+  if (blockIdx.x != 0 || blockIdx.y != 0) return;
+  int bad_len = 0, bad_page = 0;
+  for (int64_t b = threadIdx.x; b < pr.B; b += blockDim.x) {
+    int64_t len, cnt;
+    if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt)) {
+      bad_len = 1;
+    } else if (cnt > 0) {
+      for (int64_t j = (len - cnt) / pr.C; j <= (len - 1) / pr.C; ++j)
+        bad_page |= (uint32_t)a.table[b * a.nb + j] >= a.num_pages;
+    }
+  }
+  bad_len = __syncthreads_or(bad_len);
+  bad_page = __syncthreads_or(bad_page);
+  if (threadIdx.x == 0) *a.status = bad_len ? PISA_DEV_BAD_SEQ_LEN : (bad_page ? PISA_DEV_BAD_INDEX : PISA_DEV_OK);
 }
 
 }  // namespace
@@ -199,7 +203,8 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   auto kern = pr.dtype == PISA_BF16 ? (many ? append_kernel<__nv_bfloat16, 4> : append_kernel<__nv_bfloat16, 1>)
                                     : (many ? append_kernel<float, 4> : append_kernel<float, 1>);
   note_launch();
-  return launch_pdl(true, kern, grid, dim3(256), 0, st, pr, a);
+  kern<<<grid, 256, 0, st>>>(pr, a);
+  return cudaGetLastError();
 }
 
 }  // namespace pisa

@@ -140,7 +140,6 @@ pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, co
   if (rc != PISA_OK) return rc;
   if (ws_bytes < pisa_paged_workspace_bytes(p, n)) return PISA_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
-  if (launch_clear(ws, 256, st) != cudaSuccess) return PISA_ERR_CUDA;
   return cuda_status(launch_append_paged(pr, n, q, qs, k, ks, v, vs, seq_lens, new_lens, rope, rot_dim, interleaved,
                                          k_pages, v_pages, page_table, s.nb, num_pages, (int32_t*)ws, q_out, k_out,
                                          st));

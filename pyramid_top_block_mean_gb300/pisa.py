@@ -306,16 +306,21 @@ def _want_rows(t, name: str, shape, dtype, index: int):
     return t.data_ptr(), st
 
 
-def _want_cache(p: Params, k_pages, v_pages, page_table, seq_lens, ws, dtype, index: int):
-    """(k_pages, v_pages, number of pages, page_table, seq_lens) and the workspace's address and size."""
+def _want_cache(p: Params, k_pages, v_pages, page_table, seq_lens, dtype, index: int):
+    """(k_pages, v_pages, number of pages, page_table, seq_lens) as the calls take them."""
     num = k_pages.shape[0]
     shape = (num, p.H_kv, p.C, p.d)
+    B = p.B
+    return (_want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index), num,
+            _want(page_table, "page_table", (B, -(-p.N // 64)), torch.int32, index),
+            _want(seq_lens, "seq_lens", (B,), torch.int32, index))
+
+
+def _want_space(ws, index: int):
+    """Address and bytes of a workspace."""
     if ws.get_device() != index or not ws.is_contiguous():
         _refuse(ws, "ws", ws.shape, ws.dtype, index, "contiguous")
-    return ((_want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index), num,
-             _want(page_table, "page_table", (p.B, -(-p.N // 64)), torch.int32, index),
-             _want(seq_lens, "seq_lens", (p.B,), torch.int32, index)),
-            (ws.data_ptr(), ws.numel() * ws.element_size()))
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _dtype(p: Params) -> torch.dtype:
@@ -365,58 +370,85 @@ def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, index: int):
     return ctypes.byref(c)
 
 
+# The calls proper, with a workspace, outputs and angles (addresses) that their
+# callers have looked at already: the functions below at each call,
+# PagedAttention when it makes them.
+def _append(p, k, v, k_pages, v_pages, page_table, seq_lens, space, rope, rot, interleaved, q, q_out, k_out, new_lens,
+            stream, check) -> int:
+    index, dt = k.get_device(), _dtype(p)
+    n = k.shape[2]
+    kv_shape = (p.B, p.H_kv, n, p.d)
+    kp, ks = _want_rows(k, "k", kv_shape, dt, index)
+    vp, vs = _want_rows(v, "v", kv_shape, dt, index)
+    qp, qs = (None, ks) if q is None else _want_rows(q, "q", (p.B, p.H_q, n, p.d), dt, index)
+    strides = _strides_t(*qs[:3], *ks[:3], *vs[:3])
+    at = ctypes.addressof(strides)
+    kpp, vpp, num, table, lens = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+    return _launch(index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, at, kp,
+                   at + 24, vp, at + 48, lens,
+                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), rope, rot,
+                   interleaved, kpp, vpp, num, table, *space, q_out,
+                   None if k_out is None else _want(k_out, "k_out", kv_shape, dt, index))
+
+
+def _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, space, out, mask, stream, check) -> int:
+    index, dt = q.get_device(), _dtype(p)
+    cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+    return _launch(index, stream, "pisa_dense_decode_paged", check, _lib.pisa_dense_decode_paged, ctypes.byref(p),
+                   _mask_arg(mask, p, 1, index), _want(q, "q", (p.B, p.H_q, p.d), dt, index), *cache, *space, out)
+
+
+def _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, space, out, stream, check) -> int:
+    index, dt = q.get_device(), _dtype(p)
+    cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+    return _launch(index, stream, "pisa_attend_decode_paged", check, _lib.pisa_attend_decode_paged, ctypes.byref(p),
+                   _want(q, "q", (p.B, p.H_q, p.d), dt, index), *cache,
+                   _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space, out)
+
+
+def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, stream, check) -> int:
+    index, dt, n = q.get_device(), _dtype(p), q.shape[2]
+    cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+    return _launch(index, stream, "pisa_dense_prefill_paged", check, _lib.pisa_dense_prefill_paged, ctypes.byref(p),
+                   _mask_arg(mask, p, n, index), n, _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), *cache,
+                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space, out)
+
+
 def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, rope=None, interleaved: bool = False,
                  q=None, q_out=None, k_out=None, new_lens=None, stream=None, check: bool = True) -> int:
     """k, v [B, H_kv, n, d] and q [B, H_q, n, d], strided views allowed; rope
     fp32 [N, rot_dim] (cosines, then sines); seq_lens counts the new tokens."""
-    index, dt, n = k.get_device(), _dtype(p), k.shape[2]
-    kv_shape, q_shape = (p.B, p.H_kv, n, p.d), (p.B, p.H_q, n, p.d)
-    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
-    kp, ks = _want_rows(k, "k", kv_shape, dt, index)
-    vp, vs = _want_rows(v, "v", kv_shape, dt, index)
-    qp, qs = (None, ks) if q is None else _want_rows(q, "q", q_shape, dt, index)
-    strides = _strides_t(*qs[:3], *ks[:3], *vs[:3])
-    at = ctypes.addressof(strides)
-    return _launch(
-        index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, at, kp, at + 24, vp,
-        at + 48, cache[4], None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index),
-        None if rope is None else _want(rope, "rope", (p.N, rope.shape[-1]), torch.float32, index),
-        0 if rope is None else rope.shape[-1], interleaved, *cache[:4], *space,
-        None if q_out is None else _want(q_out, "q_out", q_shape, dt, index),
-        None if k_out is None else _want(k_out, "k_out", kv_shape, dt, index))
+    index, rot = k.get_device(), 0 if rope is None else rope.shape[-1]
+    if q_out is not None:
+        q_out = _want(q_out, "q_out", (p.B, p.H_q, k.shape[2], p.d), _dtype(p), index)
+    if rope is not None:
+        rope = _want(rope, "rope", (p.N, rot), torch.float32, index)
+    return _append(p, k, v, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), rope, rot, interleaved, q,
+                   q_out, k_out, new_lens, stream, check)
 
 
 def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out,
                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
     """q and out [B, H_q, d]: attention of one new token per sequence over its whole cache."""
-    index, dt, shape = q.get_device(), _dtype(p), (p.B, p.H_q, p.d)
-    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
-    return _launch(index, stream, "pisa_dense_decode_paged", check, _lib.pisa_dense_decode_paged, ctypes.byref(p),
-                   _mask_arg(mask, p, 1, index), _want(q, "q", shape, dt, index), *cache, *space,
-                   _want(out, "out", shape, dt, index))
+    index = q.get_device()
+    return _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index),
+                         _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), mask, stream, check)
 
 
 def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, idx, ws, out, stream=None,
                         check: bool = True) -> int:
     """attend_decode over a paged cache; idx int32 [B, H_kv, K+3]."""
-    index, dt, shape = q.get_device(), _dtype(p), (p.B, p.H_q, p.d)
-    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
-    return _launch(index, stream, "pisa_attend_decode_paged", check, _lib.pisa_attend_decode_paged, ctypes.byref(p),
-                   _want(q, "q", shape, dt, index), *cache,
-                   _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space,
-                   _want(out, "out", shape, dt, index))
+    index = q.get_device()
+    return _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, _want_space(ws, index),
+                            _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), stream, check)
 
 
 def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out, new_lens=None,
                         mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
     """q and out [B, H_q, n, d]: attention of n new tokens per sequence over the pages that hold them already."""
-    index, dt, n = q.get_device(), _dtype(p), q.shape[2]
-    shape = (p.B, p.H_q, n, p.d)
-    cache, space = _want_cache(p, k_pages, v_pages, page_table, seq_lens, ws, dt, index)
-    return _launch(index, stream, "pisa_dense_prefill_paged", check, _lib.pisa_dense_prefill_paged, ctypes.byref(p),
-                   _mask_arg(mask, p, n, index), n, _want(q, "q", shape, dt, index), *cache,
-                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space,
-                   _want(out, "out", shape, dt, index))
+    index = q.get_device()
+    return _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, _want_space(ws, index),
+                          _want(out, "out", (p.B, p.H_q, q.shape[2], p.d), _dtype(p), index), mask, stream, check)
 
 
 def read_device_status(ws: torch.Tensor, stream=None) -> int:
@@ -516,12 +548,19 @@ class PagedAttention:
 
     def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
                  device="cuda"):
+        p = Params.from_buffer_copy(p)  # the buffers below are made for these numbers
         self.p, self.n, self.rope, self.interleaved = p, n, rope, interleaved
         self.device = torch.device(device)
-        nbytes = max(paged_workspace_bytes(p, n), paged_workspace_bytes(p, min(n, 1)))
+        nbytes = paged_workspace_bytes(p, n)
         if nbytes == 0:
             raise ValueError("unsupported problem shape, or n outside [0, N]")
+        nbytes = max(nbytes, paged_workspace_bytes(p, min(p.N, 1)))
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.device = self.ws.device
+        self._index = self.ws.get_device()
+        self._space = _want_space(self.ws, self._index)
+        self._rot = 0 if rope is None else rope.shape[-1]
+        self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
         dt = _dtype(p)
         self._out = {"dense": torch.zeros(p.B, p.H_q, p.d, dtype=dt, device=self.device),
                      "selected": torch.zeros(p.B, p.H_q, p.d, dtype=dt, device=self.device),
@@ -530,32 +569,37 @@ class PagedAttention:
 
     def _buffer(self, kind: str, like):
         out = self._out[kind]
+        if like.get_device() != self._index:
+            raise ValueError(f"expected tensors on {self.device}, got {like.device}")
         if out.shape == like.shape:
             return out
-        if like.numel() > out.numel():
+        if like.dim() != out.dim() or like.numel() > out.numel():
             raise ValueError(f"{tuple(like.shape)}: more than the {self.n} new tokens per sequence asked for")
         return out.view(-1)[:like.numel()].view(like.shape)
 
     def append(self, q, k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_out=None, stream=None):
         """Rotates and appends k and v; returns the rotated queries [B, H_q, n, d] (None when q is None)."""
-        q_out = None if q is None else self._buffer("q", q)
-        append_paged(self.p, k, v, k_pages, v_pages, page_table, seq_lens, self.ws, self.rope, self.interleaved, q,
-                     q_out, k_out, new_lens, stream)
-        return q_out
+        q_out = self._buffer("q", q if q is not None else k)  # (without queries: the check alone)
+        _append(self.p, k, v, k_pages, v_pages, page_table, seq_lens, self._space, self._rope, self._rot,
+                self.interleaved, q, None if q is None else q_out.data_ptr(), k_out, new_lens, stream, True)
+        return None if q is None else q_out
 
     def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None):
         out = self._buffer("dense", q)
-        dense_decode_paged(self.p, q, k_pages, v_pages, page_table, seq_lens, self.ws, out, mask, stream)
+        _dense_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, self._space, out.data_ptr(), mask, stream,
+                      True)
         return out
 
     def selected_decode(self, q, k_pages, v_pages, page_table, seq_lens, idx, stream=None):
         out = self._buffer("selected", q)
-        attend_decode_paged(self.p, q, k_pages, v_pages, page_table, seq_lens, idx, self.ws, out, stream)
+        _selected_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, idx, self._space, out.data_ptr(), stream,
+                         True)
         return out
 
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None):
         out = self._buffer("prefill", q)
-        dense_prefill_paged(self.p, q, k_pages, v_pages, page_table, seq_lens, self.ws, out, new_lens, mask, stream)
+        _dense_prefill(self.p, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space, out.data_ptr(), mask,
+                       stream, True)
         return out
 
     def device_status(self, stream=None) -> int:

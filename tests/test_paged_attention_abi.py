@@ -129,6 +129,23 @@ def test_binding_checks_tensors(pisa):
             call(**bad)
 
 
+def test_layer_checks_its_tensors(pisa):
+    p = pisa.make_params(2, 128, 4, 2, 64)
+    for bad in (dict(n=129), dict(n=-1), dict(rope=torch.zeros(100, 64)), dict(rope=torch.zeros(128, 64).double())):
+        with pytest.raises((ValueError, RuntimeError)):
+            pisa.PagedAttention(p, **(dict(n=3, device="cpu") | bad))
+    layer = pisa.PagedAttention(p, n=3, rope=torch.zeros(128, 64), device="cpu")
+    q, k = (torch.zeros(2, h, 3, 64, dtype=torch.bfloat16) for h in (4, 2))
+    pool = torch.zeros(4, 2, 64, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: layer.append(q, k, k, pool, pool, table, lens),  # not on a GPU
+                 lambda: layer.append(None, k, k, pool, pool, table, lens),
+                 lambda: layer.dense_prefill(q.repeat(1, 1, 2, 1), pool, pool, table, lens),  # six new tokens
+                 lambda: layer.dense_decode(q, pool, pool, table, lens)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_reference_attention_against_a_library_routine():
     g = torch.Generator().manual_seed(0)
     q, k, v = (torch.randn(n, 16, generator=g, dtype=torch.float64) for n in (5, 9, 9))
