@@ -89,6 +89,18 @@ def test_in_place_and_contiguous_inputs(pisa, dtype, inter):
     check(p, q0, k0, v0, pools, table, lens, new, rope, inter, q1, k1, marked=None)
 
 
+def test_broadcast_inputs(pisa):
+    # one row for all heads, one for all tokens: strides of zero
+    p, q, k, v, pools, table, ws = setup(pisa, 2, 150, 40, 8, 2, 64, "bf16", seed=11)
+    rope = rope_table(150, 64).cuda()
+    q, k, v = q[:, :1].expand(-1, 8, -1, -1), k[:, :, :1].expand(-1, -1, 40, -1), v[:1].expand(2, -1, -1, -1)
+    q_out = torch.full((2, 8, 40, 64), MARK, dtype=q.dtype, device="cuda")
+    lt = torch.tensor([150, 40], dtype=torch.int32).cuda()
+    pisa.append_paged(p, k, v, *pools, table, lt, ws, rope, False, q, q_out)
+    assert pisa.read_device_status(ws) == 0
+    check(p, q, k, v, pools, table, [150, 40], [40, 40], rope, False, q_out, None)
+
+
 def test_without_queries(pisa):
     p, _, k, v, pools, table, ws = setup(pisa, 2, 150, 40, 8, 2, 64, "bf16", seed=6)
     rope = rope_table(150, 64).cuda()

@@ -286,6 +286,37 @@ def test_prefill_bad_page_counts_as_unseen(pisa):
             R.within(out[0, h], o, t)
 
 
+def test_pages_before_the_window_may_be_gone(pisa):
+    # a serving program gives pages that a window has left back: their entries are never read
+    def poke(kp, vp, table):
+        table[0, :(900 - 70 - 299) // 64] = -7
+    run_prefill(pisa, 4, 2, 64, 900, 70, [900], [70], seed=6, window=300, poke=poke)
+    k, v, kp, vp, table = cache(1, 2, 5000, 128, [5000], 7)
+    table[0, :(5000 - 1000) // 64] = 2 ** 31 - 1
+    q = torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(1, 5000, 8, 2, 128))
+    out = layer.dense_decode(q, kp, vp, table, i32([5000]), mask=pisa.AttentionMask(window=1000))
+    assert layer.device_status() == 0
+    want, tol = R.dense(q[0][:, None], k[0], v[0], 5000, torch.tensor([4999], device="cuda"), 128 ** -0.5, window=1000)
+    R.within(out[0], want[:, 0], tol[:, 0])
+
+
+def test_sequences_that_share_pages(pisa):
+    # a common prefix of two pages, own pages behind it
+    k, v, kp, vp, table = cache(2, 2, 300, 64, [300, 300], 8, fill=0.0)
+    table[1, :2] = table[0, :2]
+    k[1, :, :128], v[1, :, :128] = k[0, :, :128], v[0, :, :128]
+    layer = pisa.PagedAttention(pisa.make_params(2, 300, 4, 2, 64), n=100)
+    q = torch.randn(2, 4, 100, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    out = layer.dense_prefill(q, kp, vp, table, i32([300, 250]))
+    one = layer.dense_decode(q[:, :, 0].contiguous(), kp, vp, table, i32([300, 250]))
+    for b, n in enumerate([300, 250]):
+        want, tol = R.dense(q[b], k[b], v[b], n, torch.arange(n - 100, n, device="cuda"), 0.125)
+        R.within(out[b], want, tol)
+        want, tol = R.dense(q[b][:, :1], k[b], v[b], n, torch.tensor([n - 1], device="cuda"), 0.125)
+        R.within(one[b], want[:, 0], tol[:, 0])
+
+
 def test_prefill_non_finite_values_behind_the_window(pisa):
     # whole tiles that no row sees are never read
     def poke(kp, vp, table):
