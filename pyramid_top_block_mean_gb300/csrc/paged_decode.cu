@@ -43,7 +43,6 @@ constexpr int kMerge = 96;              // threads that merge a part while the c
 constexpr int kThreads = kCons + 32 + kMerge;  // and the producer warp
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
-constexpr uint64_t kWaitNs = 4000000000ull;
 
 template <int D, int G>
 struct Shape {
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one stage; page < 0: none to load
     auto emit = [&](const Meta& meta, int32_t page, int32_t head, int64_t seq) -> bool {
       if (it >= kStages &&
-          !__all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ph ^ 1, abort, kWaitNs)))
+          !__all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ph ^ 1, abort)))
         return false;
       if (lane == 0) {
         sm.meta[st] = meta;
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every copy lands before the CTA ends
     if (lane == 0)
       for (int k = max(0, it - kStages); k < it; ++k)
-        ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero, kWaitNs);
+        ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[k % kStages]), (k / kStages) & 1, &sm.zero);
     if (!ok) give_up();
     return;
   }
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- merging a part's warps
     const int mt = threadIdx.x - (kCons + 32);
     for (int n = 0;; ++n) {
-      const bool ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.mfull), n & 1, abort, kWaitNs);
+      const bool ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.mfull), n & 1, abort);
       // all of the merging warps go on, or none
       if (!merge_all(ok)) {
         give_up();
@@ -509,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // group warp / 4 takes every other stage
   int st = (warp >> 2) - 2, ph = 0, merges = 0;
   auto wait_merged = [&] {  // the merge buffer is free
-    const bool ok = merges == 0 || ptx::mbar_wait_fast(ptx::smem_u32(&sm.mempty), (merges - 1) & 1, abort, kWaitNs);
+    const bool ok = merges == 0 || ptx::mbar_wait_fast(ptx::smem_u32(&sm.mempty), (merges - 1) & 1, abort);
     if (!__all_sync(0xffffffffu, ok)) {
       give_up();
       return false;
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       st -= kStages;
       ph ^= 1;
     }
-    const bool okw = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+    const bool okw = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort);
     if (!__all_sync(0xffffffffu, okw)) {
       give_up();
       break;

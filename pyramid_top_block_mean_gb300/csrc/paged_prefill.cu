@@ -53,7 +53,6 @@ constexpr int kThreads = 384;  // warp 11 only makes up the third warpgroup
 // gives up what they need (2 x 216 + 72 = 3 x 168, the launch's share).
 #define PISA_SOFTMAX_REGS "216"
 #define PISA_OTHER_REGS "72"
-constexpr uint64_t kWaitNs = 4000000000ull;
 constexpr float kSlack = 8.0f;  // log2 of how far weights may exceed 1
 
 template <int D>
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++st == kStages) { st = 0; ph ^= 1; }
       };
       auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort)) != 0;
         return ok;
       };
       // the stage that an item's rows go out through, until they have
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (scrub) {
               if (pages) {
-                const bool got = ptx::mbar_wait_fast(bar, scrubs & 1, &sm.zero, kWaitNs);
+                const bool got = ptx::mbar_wait_fast(bar, scrubs & 1, &sm.zero);
                 ++scrubs;
                 if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
               }
@@ -537,9 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every issued load lands before the CTA can end, whoever gave up
       if (lane == 0) {
         for (int v = 0; v < 2; ++v)
-          if (qfills[v]) ptx::mbar_wait_fast(ptx::smem_u32(&sm.qfull[v]), (qfills[v] - 1) & 1, &sm.zero, kWaitNs);
+          if (qfills[v]) ptx::mbar_wait_fast(ptx::smem_u32(&sm.qfull[v]), (qfills[v] - 1) & 1, &sm.zero);
         for (int f = max(0, fills - kStages); f < fills; ++f)
-          ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero, kWaitNs);
+          ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero);
       }
       __syncwarp();
     } else if (warp < kLoadWarp) {
@@ -559,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t o = ut + 256 + v * D, sp = ut + v * 128, qb = ptx::smem_u32(sm.q[v]);
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort, kWaitNs)) != 0;
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(bar), phase & 1, abort)) != 0;
       };
       int st = 0, ph = 0;             // stage and phase of the next fill to release
       int tiles_done = 0, qfills = 0;  // key tiles of this row tile so far; query tiles
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (elect_one()) ptx::mma_commit(ptx::smem_u32(&sm.done[v]));
       __syncwarp();
-      ptx::mbar_wait_fast(ptx::smem_u32(&sm.done[v]), 0, &sm.zero, kWaitNs);
+      ptx::mbar_wait_fast(ptx::smem_u32(&sm.done[v]), 0, &sm.zero);
       __syncwarp();
     }
   } else {
@@ -642,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int tiles_done = 0, outs_done = 0;
     for (int items = 0;; ++items) {
-      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.ifull[items % kItems]), (items / kItems) & 1, abort, kWaitNs);
+      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.ifull[items % kItems]), (items / kItems) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       const Item* ip = &sm.item[items % kItems];
       if (ip->bh < 0) break;
@@ -673,12 +672,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           // for the MMA warp: V(j) and K(j + 1) are there (as a rule they are by
           // now).  Not at an item's first tile: this warp has not followed the
           // ring up to it, and could take a phase for the one two fills earlier.
-          ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+          ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort);
           if (++st == kStages) { st = 0; ph ^= 1; }
-          if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort, kWaitNs);
+          if (j + 1 < jb) ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[st]), ph, abort);
           if (++st == kStages) { st = 0; ph ^= 1; }
         }
-        ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.sfull[w]), tiles_done & 1, abort, kWaitNs);
+        ok = ok && ptx::mbar_wait_fast(ptx::smem_u32(&sm.sfull[w]), tiles_done & 1, abort);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         ptx::tc_fence_after();
         float s[kKeys];
@@ -823,13 +822,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const bool any = wa < wb;
       if (any) {
-        ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.odone[w]), outs_done & 1, abort, kWaitNs);
+        ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.odone[w]), outs_done & 1, abort);
         ++outs_done;
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         ptx::tc_fence_after();
       }
       const int est = (ip->fill + 2 * (jb - ip->ja)) % kStages;  // the stage lent for the rows
-      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.lent), items & 1, abort, kWaitNs);
+      ok = ptx::mbar_wait_fast(ptx::smem_u32(&sm.lent), items & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       const int64_t b = (uint32_t)ip->bh / (uint32_t)pr.Hkv;
       const int32_t hq = (ip->bh - (int32_t)b * pr.Hkv) * pr.G + (r >> a.lg_tokens);

@@ -113,16 +113,19 @@ __device__ __forceinline__ bool mbar_wait_bounded_hint(uint32_t bar, uint32_t pa
   }
 }
 
-// As mbar_wait_bounded, for waits on the critical path of a pipeline: reading
-// the timer costs about 700 cycles, which a wait that ends sooner would pay
-// in full, so the clock only starts after a number of polls (each of which
-// may sleep in the barrier unit by itself).
-__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile int32_t* abort,
-                                               uint64_t limit_ns) {
+// As mbar_wait_bounded, for waits on the critical path of a pipeline and for
+// kernels with dozens of them: bounded by a number of polls instead of a time
+// (reading the timer costs about 700 cycles and its code is four times as
+// long).  A poll may sleep in the barrier unit for up to the hint, so the limit
+// lies between a tenth of a second and some seconds.
+constexpr uint32_t kMaxPolls = 1u << 22;
+__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile int32_t* abort) {
 #pragma unroll 1
-  for (int it = 0; it < 256; ++it)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity, abort, limit_ns);
+  for (uint32_t it = 0; it < kMaxPolls; ++it) {
+    if (mbar_try_wait_hint(bar, parity, 1000)) return true;
+    if ((it & 255u) == 255u && *abort) return false;
+  }
+  return false;
 }
 
 // ------------------------------------------------------------------- TMA
