@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // they are cleared before the MMA reads the tile
           const int32_t key0 = j * kKeys;
           const bool clear = key0 < klo || key0 + kKeys - 1 > khi || pages < 2;
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             if (fills >= kStages && !wait(&sm.empty[st], ph ^ 1)) break;  // the first round finds them empty
             if (lent == st && !take_back()) break;
