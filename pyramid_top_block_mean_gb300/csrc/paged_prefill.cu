@@ -12,10 +12,10 @@
 //   - a loader warp brings the query tiles once, then keys and values through
 //     one ring of stages by TMA (128-byte swizzle); a page is found through
 //     the table, so a tile is four boxes;
-//   - a warp per row tile issues S = Q K^T into TMEM and, when its weights P are there,
-//     O += P V with P read from TMEM (over the columns of S, which the warps
-//     have read by then) and V in its natural key-major layout.  The two
-//     tiles alternate: while one's softmax runs, the other's MMAs do;
+//   - a warp per row tile issues S = Q K^T into TMEM and, when its weights P
+//     are there, O += P V with P read from TMEM (over the columns of S, which
+//     the warps have read by then) and V in its natural key-major layout.  The
+//     two tiles alternate: while one's softmax runs, the other's MMAs do;
 //   - two groups of four warps do the softmax, one thread per row, so that a
 //     row's maximum and sum need no exchange.
 // Work: 4 d flops for each (row, key).  For d = 128 the two tiles' MMAs of a
@@ -25,10 +25,10 @@
 // CTAs are persistent: the loader claims the next 256 rows when it has loaded
 // what the current ones need.
 //
-// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 670 us (1640 TFLOP/s of
-// the seen pairs, 85 % of cuBLAS's measured rate), 65536 tokens 10.5 ms (1670),
-// 16384 with a tanh cap 947 us, 2 x 4096 tokens (ragged) 90 us, 61 tokens behind
-// 65536 cached ones 49 us.
+// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 660 us (1660 TFLOP/s of
+// the seen pairs, 86 % of cuBLAS's measured rate), 65536 tokens 10.5 ms (1670),
+// 16384 with a tanh cap 945 us, 2 x 4096 tokens (ragged) 87 us, 61 tokens behind
+// 65536 cached ones 48 us.
 //
 // Rows with few tokens and a long cache: the keys of a CTA's rows are split
 // over several CTAs, whose parts a second kernel joins.
