@@ -154,6 +154,7 @@ pisa_status pisa_dense_decode_paged(const pisa_params* p, const pisa_mask* mask,
   if (pr.dtype != PISA_BF16) return PISA_ERR_UNSUPPORTED;  // built for bf16 inputs
   rc = mask_checks(pr, mask, &m);
   if (rc != PISA_OK) return rc;
+  m.prefix_lens = nullptr;  // the last token sees every key already
   if (!q || !out) return PISA_ERR_INVALID_ARG;
   rc = pool_checks(pr, s, k_pages, v_pages, num_pages, page_table, seq_lens, ws, &pools);
   if (rc != PISA_OK) return rc;

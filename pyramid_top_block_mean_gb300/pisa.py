@@ -561,11 +561,11 @@ class PagedAttention:
         self._space = _want_space(self.ws, self._index)
         self._rot = 0 if rope is None else rope.shape[-1]
         self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
-        dt = _dtype(p)
-        self._out = {"dense": torch.zeros(p.B, p.H_q, p.d, dtype=dt, device=self.device),
-                     "selected": torch.zeros(p.B, p.H_q, p.d, dtype=dt, device=self.device),
-                     "q": torch.zeros(p.B, p.H_q, n, p.d, dtype=dt, device=self.device),
-                     "prefill": torch.zeros(p.B, p.H_q, n, p.d, dtype=dt, device=self.device)}
+        one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
+        rows = p.B * p.H_q * p.d
+        flat = torch.zeros(rows * (2 + 2 * n), dtype=_dtype(p), device=self.device)
+        self._out = {"dense": flat[:rows].view(one), "selected": flat[rows:2 * rows].view(one),
+                     "q": flat[2 * rows:(2 + n) * rows].view(many), "prefill": flat[(2 + n) * rows:].view(many)}
 
     def _buffer(self, kind: str, like):
         out = self._out[kind]
