@@ -683,12 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s[kKeys];
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
-        ptx::tmem_ld_wait();
         const int32_t key0 = j * kKeys;
         // keys clo .. chi of the tile are seen
         const int32_t clo = max(lo, key0) - key0, chi = min(hi, key0 + kKeys - 1) - key0;
         const bool bad = *(volatile int32_t*)&sm.bad_page != 0;
         const bool part = __any_sync(0xffffffffu, clo > 0 || chi < kKeys - 1) || bad;
+        ptx::tmem_ld_wait();  // (all of the above in its shadow)
         bool late = false;  // the cap is applied on the way to the exponential
         if (MODE == 1) {
           if (mk.cap2 > 0.0f) {
