@@ -384,9 +384,9 @@ void pisa_test_inject_leaf_timeout(uint64_t wait_limit_ns, int32_t drop_first_ke
  * sits at position seq_lens[b] - new_lens[b] + i, and rows of outputs at or
  * behind new_lens[b] are left as they were.
  *
- * Workspace of all four calls: pisa_paged_workspace_bytes(p, n) bytes (n = 1
- * for the decode calls); it may be used by any number of calls that do not
- * overlap.  Faults in device data end in its status word: a length that does
+ * Workspace of all four calls: pisa_paged_workspace_bytes(p, n) bytes for
+ * calls of up to n new tokens (n = 1 for the decode calls); it may be used by
+ * any number of calls that do not overlap.  Faults in device data end in its status word: a length that does
  * not fit (PISA_DEV_BAD_SEQ_LEN) or a page index outside the pool
  * (PISA_DEV_BAD_INDEX, never read or written).  The part of the output that
  * they touch is stated per call; everything else is computed.
@@ -472,8 +472,8 @@ pisa_status pisa_dense_prefill_paged(const pisa_params* p, const pisa_mask* mask
                                      const int32_t* page_table, const int32_t* seq_lens, const int32_t* new_lens,
                                      void* ws, size_t ws_bytes, void* out, void* stream);
 
-/* Workspace of the four calls above for n new tokens per sequence (0 for an
- * unsupported problem or n < 0). */
+/* Workspace of the four calls above for up to n new tokens per sequence (0 for
+ * an unsupported problem, n < 0 or n > N). */
 size_t pisa_paged_workspace_bytes(const pisa_params* p, int64_t n);
 
 /* Synchronises `stream`, then copies the workspace status word into

@@ -76,7 +76,7 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
 // launch_pdl, may read the caller's inputs before pdl_wait() and the cleared
 // words only behind it.  (A memset in its place costs a call 2 us.)
 cudaError_t launch_clear(void* ws, size_t bytes, cudaStream_t st);
-// Workspace bytes of the two launchers, the status word's 256 included.
+// Workspace bytes of the two launchers, the status word's 256 included; for calls of up to n tokens.
 size_t paged_decode_ws_bytes(const Prob& pr);
 size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n);
 

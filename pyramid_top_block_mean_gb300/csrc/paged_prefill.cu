@@ -1022,6 +1022,13 @@ struct Plan {
   int64_t ctas;  // without the splits
   size_t ml, o, total;
 };
+void place_parts(const Prob& pr, int64_t parts, Plan* p) {  // of 256 rows each
+  const size_t rows = (size_t)parts * 2 * kRows;
+  size_t o = 256;
+  p->ml = o; o = align_up(o + rows * 2 * 4, 256);
+  p->o = o; o = align_up(o + rows * pr.d * 4, 256);
+  p->total = o;
+}
 Plan make_plan(const Prob& pr, int64_t n) {
   Plan p;
   p.lg_tokens = pr.G == 1 ? 7 : (pr.G == 2 ? 6 : (pr.G == 4 ? 5 : 4));
@@ -1030,11 +1037,7 @@ Plan make_plan(const Prob& pr, int64_t n) {
   p.splits = 1;
   if (p.ctas > 0 && 2 * p.ctas <= kSms)
     p.splits = (int32_t)std::max<int64_t>(1, std::min(kSms / p.ctas, ceil_div64(pr.N, kKeys) / 4));
-  const size_t rows = p.splits > 1 ? (size_t)p.splits * p.ctas * 2 * kRows : 0;
-  size_t o = 256;
-  p.ml = o; o = align_up(o + rows * 2 * 4, 256);
-  p.o = o; o = align_up(o + rows * pr.d * 4, 256);
-  p.total = o;
+  place_parts(pr, p.splits > 1 ? p.splits * p.ctas : 0, &p);
   return p;
 }
 
@@ -1055,7 +1058,16 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const Plan& pl, const CU
 
 }  // namespace
 
-size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) { return make_plan(pr, n).total; }
+// What calls of up to n tokens need.  A call with fewer tokens may split its
+// keys where one with more does not; splits x ctas is at most kSms, and at
+// most the largest split times the most ctas that are split at all.
+size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
+  Plan p = make_plan(pr, n);
+  const int64_t most = ceil_div64(pr.N, kKeys) / 4, heads = pr.B * pr.Hkv;
+  const bool splits = p.ctas > 0 && 2 * heads <= kSms && most > 1;
+  place_parts(pr, splits ? std::min<int64_t>(kSms, most * std::min<int64_t>(p.ctas, kSms / 2)) : 0, &p);
+  return p.total;
+}
 
 cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, const void* q, const Pools& pools,
                                  const int32_t* seq_lens, const int32_t* new_lens, char* ws, void* out,

@@ -554,7 +554,7 @@ class PagedAttention:
         nbytes = paged_workspace_bytes(p, n)
         if nbytes == 0:
             raise ValueError("unsupported problem shape, or n outside [0, N]")
-        nbytes = max(nbytes, paged_workspace_bytes(p, min(p.N, 1)))
+        nbytes = max(nbytes, paged_workspace_bytes(p, min(p.N, 1)))  # (n = 0: decode calls)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.device = self.ws.device
         self._index = self.ws.get_device()

@@ -175,3 +175,20 @@ def test_two_layers_on_two_streams(pisa):
     torch.cuda.synchronize()
     for m, q, want in zip(ms, qs, alone):
         assert torch.equal(m.layer._buffer("dense", q), want)
+
+
+@pytest.mark.parametrize("n", [1, 61, 200, 700, 2048])
+def test_a_layer_takes_fewer_tokens_than_asked_for(pisa, n):
+    """A call of fewer tokens splits its keys where the largest call does not."""
+    B, N, Hq, Hkv, d = 1, 4096, 8, 1, 128
+    m = Model(pisa, B, N, Hq, Hkv, d, n=2560)
+    m.kp.normal_(generator=m.g)
+    m.vp.normal_(generator=m.g)
+    q = torch.randn(B, Hq, n, d, generator=m.g, device="cuda").bfloat16()
+    lens = i32([3700])
+    out = m.layer.dense_prefill(q, m.kp, m.vp, m.table, lens)
+    assert m.layer.device_status() == 0
+    ws = torch.empty(pisa.paged_workspace_bytes(m.p, n), dtype=torch.uint8, device="cuda")
+    want = torch.full_like(q, R.NAN)
+    pisa.dense_prefill_paged(m.p, q, m.kp, m.vp, m.table, lens, ws, want)
+    assert torch.equal(out, want)

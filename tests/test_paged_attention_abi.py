@@ -110,6 +110,16 @@ def test_workspace_sizes(pisa):
     assert pisa.paged_workspace_bytes(pisa.make_params(2, 4096, 16, 4, 96, K=8), 1) == 0
 
 
+@pytest.mark.parametrize("B,N,Hkv,d", [(1, 16384, 1, 128), (2, 4096, 4, 128), (1, 1024, 4, 64), (3, 65536, 5, 64),
+                                       (1, 65536, 76, 128), (1, 65536, 77, 128), (2, 200, 1, 64)])
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_a_workspace_for_n_tokens_serves_fewer(pisa, B, N, Hkv, d, G):
+    p = pisa.make_params(B, N, G * Hkv, Hkv, d, K=8)
+    at = [n for n in (0, 1, 2, 17, 61, 128, 129, 200, 256, 511, 1000, 1024, 2047, 4096, 8192, 16384, 65536) if n <= N]
+    sizes = [pisa.paged_workspace_bytes(p, n) for n in at]
+    assert sizes[0] >= 256 and sizes == sorted(sizes), list(zip(at, sizes))
+
+
 def test_binding_checks_tensors(pisa):
     p = pisa.make_params(2, 128, 4, 2, 64)
     k = torch.zeros(2, 2, 3, 64, dtype=torch.bfloat16)
