@@ -950,8 +950,11 @@ __global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(
   const int64_t i = tile * 2 * tokens + (int64_t)w * tokens + (r & (tokens - 1));
   int64_t len, cnt;
   new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
+  // The lengths are the caller's, the parts the kernel's before.  A CTA without
+  // a row need not wait for them, but the first one always does, so that this
+  // grid, and what follows it in the stream, never ends before that kernel.
+  if (i < cnt || at == 0) pdl_wait();
   if (i >= cnt) return;
-  pdl_wait();  // the lengths are the caller's, the parts the kernel's before
   float M = -INFINITY, L = 0.0f, acc[8] = {};
   constexpr int kBatch = 2;
   for (int s0 = pl; s0 < a.splits; s0 += PL * kBatch) {

@@ -192,3 +192,22 @@ def test_a_layer_takes_fewer_tokens_than_asked_for(pisa, n):
     want = torch.full_like(q, R.NAN)
     pisa.dense_prefill_paged(m.p, q, m.kp, m.vp, m.table, lens, ws, want)
     assert torch.equal(out, want)
+
+
+def test_calls_without_a_new_token_between_others(pisa):
+    """Rows all absent, then present, back to back on one workspace."""
+    B, N, Hq, Hkv, d, n = 2, 8192, 8, 2, 128, 32
+    m = Model(pisa, B, N, Hq, Hkv, d, n=n)
+    m.kp.normal_(generator=m.g)
+    m.vp.normal_(generator=m.g)
+    q = torch.randn(B, Hq, n, d, generator=m.g, device="cuda").bfloat16()
+    lens, some, none = i32([8000, 5001]), i32([n, 5]), i32([0, 0])
+    want = m.layer.dense_prefill(q, m.kp, m.vp, m.table, lens, new_lens=some).clone()
+    for _ in range(20):
+        out = torch.zeros_like(want)
+        rest = torch.full_like(want, R.NAN)
+        pisa.dense_prefill_paged(m.p, q, m.kp, m.vp, m.table, lens, m.layer.ws, rest, new_lens=none)
+        pisa.dense_prefill_paged(m.p, q, m.kp, m.vp, m.table, lens, m.layer.ws, out, new_lens=some)
+        pisa.dense_prefill_paged(m.p, q, m.kp, m.vp, m.table, lens, m.layer.ws, rest, new_lens=none)
+        assert m.layer.device_status() == 0
+        assert torch.equal(out, want) and bool(rest.isnan().all())
