@@ -25,8 +25,8 @@
 // CTAs are persistent: the loader claims the next 256 rows when it has loaded
 // what the current ones need.
 //
-// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 660 us (1660 TFLOP/s of
-// the seen pairs, 86 % of cuBLAS's measured rate), 65536 tokens 10.5 ms (1670),
+// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 655 us (1680 TFLOP/s of
+// the seen pairs, 87 % of cuBLAS's measured rate), 65536 tokens 10.4 ms (1690),
 // 16384 with a tanh cap 945 us, 2 x 4096 tokens (ragged) 87 us, 61 tokens behind
 // 65536 cached ones 48 us.
 //
