@@ -570,13 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[j] = d[j] + e[j];
-        if (mk.cap2 > 0.0f) {
-          // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
-          const float w = ptx::ex2(x[j] * mk.pre * (2.0f * kLog2e));
-          x[j] = fmaf(-2.0f * mk.cap2, __frcp_rn(1.0f + w), mk.cap2);
-        } else {
-          x[j] *= pr.scale2;
-        }
+        x[j] = mk.cap2 > 0.0f ? cap_score(mk, x[j]) : x[j] * pr.scale2;
       }
       const int ka = r16 + grp;
       if (mk.slopes) {

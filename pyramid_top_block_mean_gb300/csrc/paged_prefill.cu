@@ -186,16 +186,29 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// The factor that caps two small scores (MaskArgs::tk).
-__device__ __forceinline__ uint64_t cap_factor(const MaskArgs& m, uint64_t x2) {
-  const uint64_t w2 = mul2(x2, x2);
-  uint64_t f = ptx::fma2(w2, ptx::pack2(m.tk[3], m.tk[3]), ptx::pack2(m.tk[2], m.tk[2]));
-  f = ptx::fma2(w2, f, ptx::pack2(m.tk[1], m.tk[1]));
-  return ptx::fma2(w2, f, ptx::pack2(m.tk[0], m.tk[0]));
+// The factor that caps two small scores: MaskArgs::xk with w = x^2, or uk with w = u^2.
+__device__ __forceinline__ uint64_t cap_factor(const float (&k)[4], uint64_t w2) {
+  uint64_t f = ptx::fma2(w2, ptx::pack2(k[3], k[3]), ptx::pack2(k[2], k[2]));
+  f = ptx::fma2(w2, f, ptx::pack2(k[1], k[1]));
+  return ptx::fma2(w2, f, ptx::pack2(k[0], k[0]));
 }
+__device__ __forceinline__ uint64_t cap_factor(const MaskArgs& m, uint64_t x2) { return cap_factor(m.xk, mul2(x2, x2)); }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// |u| <= 1/2 ? a : b.  (In PTX: over a row's worth of scores the compiler takes
+// the expression for 128 branches and spills 3 KB, three times the time.)
+__device__ __forceinline__ float within_half(float u, float a, float b) {
+  float y;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.le.f32 p, %1, 0f3F000000;\n\t"
+      "selp.f32 %0, %2, %3, p;\n\t}"
+      : "=f"(y)
+      : "f"(fabsf(u)), "f"(a), "f"(b));
   return y;
 }
 
@@ -247,10 +260,7 @@ __device__ __noinline__ void mend_row(const Prob& pr, const MaskArgs& mk, const 
     float s = 0.0f;
     for (int j = 0; j < J; ++j) s = fmaf(x[j], bf16_to_f(a.k[r + 32 * j]), s);
     s = warp_sum(s);
-    if (MODE == 1 && mk.cap2 > 0.0f)
-      s = fmaf(-2.0f * mk.cap2, 1.0f / (1.0f + exp2f(s * mk.pre * (2.0f * kLog2e))), mk.cap2);
-    else
-      s *= pr.scale2;
+    s = MODE == 1 && mk.cap2 > 0.0f ? cap_score(mk, s) : s * pr.scale2;
     s = fmaf(slope, (float)(key - t), s);
     const float top = fmaxf(m, s);
     const float f = m == -INFINITY ? 1.0f : exp2f(m - top), p = exp2f(s - (top == -INFINITY ? 0.0f : top));
@@ -702,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // small scores: a polynomial on the FMA pipe, two at a time (the
             // exponential and the reciprocal of the other way take 12 cycles of
             // the SFU a warp, three times what the softmax takes itself)
-            if (__all_sync(0xffffffffu, fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) <= mk.tlim)) {
+            if (__all_sync(0xffffffffu, fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) <= mk.xlim)) {
               late = !part && !mk.slopes;  // the cap is monotone: the largest score stays the largest
               if (!late) {
 #pragma unroll
@@ -711,11 +721,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                s[c + 1]);
               }
             } else {
-              // tanh u = 1 - 2 / (1 + e^2u): off by a few 2^-24 whatever u is
-              const float pre = mk.pre * (2.0f * kLog2e);
+              // cap_score(), two at a time: the small ones among them take the
+              // polynomial too, since the other form's error is a part of the cap
+              const float pre = mk.pre * (2.0f * kLog2e), cap = mk.cap2;
+              auto large = [&](float x) { return fmaf(-2.0f * cap, rcp_approx(1.0f + ptx::ex2(x * pre)), cap); };
 #pragma unroll
-              for (int c = 0; c < kKeys; ++c)
-                s[c] = fmaf(-2.0f * mk.cap2, rcp_approx(1.0f + ptx::ex2(s[c] * pre)), mk.cap2);
+              for (int c = 0; c < kKeys; c += 2) {
+                const uint64_t x2 = ptx::pack2(s[c], s[c + 1]), u2 = mul2(x2, ptx::pack2(mk.pre, mk.pre));
+                float a0, a1, u0, u1;
+                ptx::unpack2(u2, u0, u1);
+                ptx::unpack2(mul2(x2, cap_factor(mk.uk, mul2(u2, u2))), a0, a1);
+                s[c] = within_half(u0, a0, large(s[c]));
+                s[c + 1] = within_half(u1, a1, large(s[c + 1]));
+              }
             }
           }
           if (mk.slopes) {
