@@ -25,10 +25,10 @@ struct Pools {
 struct MaskArgs {
   float cap2;                  // softcap * log2(e), 0: none
   float pre;                   // with a cap: scale / softcap, the argument of tanh per unit of q . k
-  // cap2 tanh(u) = x (uk[0] + w (uk[1] + w (uk[2] + w uk[3]))) with u = pre x and w = u^2 for |u| <= 1/2, off by less
-  // than 2^-20 of itself: uk[0] is the scale, and the rest makes the largest relative error least.  xk: the same with
-  // w = x^2, for |x| <= xlim; a cap so large that one of these leaves fp32's normal range has an xlim of 0.
-  float uk[4], xk[4], xlim;
+  // cap2 tanh(pre x) = x (tk[0] + w (tk[1] + w (tk[2] + w tk[3]))) with y = by x and w = y^2 for |y| <= lim, which
+  // stands for |pre x| <= 1/2, off by less than 2^-20 of itself: tk[0] is the scale, and the rest makes the largest
+  // relative error least.  by is 1, or pre where a cap is so large that the coefficients would leave fp32's normal range.
+  float tk[4], by, lim;
   int64_t window;              // 0: none
   const float* slopes;         // null: none
   const int32_t* first_key;    // null: none; [B, n]
@@ -67,10 +67,10 @@ __device__ __forceinline__ void key_span(const MaskArgs& m, int64_t b, int64_t n
 // polynomial where the score is small against the cap (a large cap is no cap),
 // tanh u = 1 - 2 / (1 + e^2u), whose error is a few 2^-24 of the cap, elsewhere.
 __device__ __forceinline__ float cap_score(const MaskArgs& m, float x) {
-  const float u = x * m.pre, w = u * u;
-  const float small = x * fmaf(w, fmaf(w, fmaf(w, m.uk[3], m.uk[2]), m.uk[1]), m.uk[0]);
-  const float large = fmaf(-2.0f * m.cap2, __frcp_rn(1.0f + ptx::ex2(u * (2.0f * kLog2e))), m.cap2);
-  return fabsf(u) <= 0.5f ? small : large;
+  const float y = x * m.by, w = y * y;
+  const float small = x * fmaf(w, fmaf(w, fmaf(w, m.tk[3], m.tk[2]), m.tk[1]), m.tk[0]);
+  const float large = fmaf(-2.0f * m.cap2, __frcp_rn(1.0f + ptx::ex2(x * m.pre * (2.0f * kLog2e))), m.cap2);
+  return fabsf(y) <= m.lim ? small : large;
 }
 
 cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const int64_t* qs, const void* k,

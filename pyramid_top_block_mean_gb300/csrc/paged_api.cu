@@ -74,13 +74,12 @@ pisa_status mask_checks(const Prob& pr, const pisa_mask* mask, MaskArgs* m) {
     // tanh(u) / u = 1 + c1 u^2 + c2 u^4 + c3 u^6 on [-1/2, 1/2]: a linear program for the least largest relative
     // error, 6.4e-7
     const double c[4] = {1.0, -0.3332815933841437, 0.13205359737189304, -0.04475064468281561};
+    const double last = fabs(c[3]) * pr.scale2 * pow(m->pre, 6);
+    const bool normal = last >= 1.2e-38 && last <= 3.4e38;
     double f = pr.scale2;
-    for (int i = 0; i < 4; ++i, f *= (double)m->pre * m->pre) {
-      m->uk[i] = (float)(pr.scale2 * c[i]);
-      m->xk[i] = (float)(f * c[i]);
-    }
-    const bool normal = fabsf(m->xk[3]) >= 1.2e-38f && !isinf(m->xk[3]);
-    m->xlim = normal ? 0.5f / m->pre : 0.0f;
+    for (int i = 0; i < 4; ++i, f *= normal ? (double)m->pre * m->pre : 1.0) m->tk[i] = (float)(f * c[i]);
+    m->by = normal ? 1.0f : m->pre;
+    m->lim = normal ? 0.5f / m->pre : 0.5f;
   }
   m->window = mask->window;
   m->slopes = mask->slopes;

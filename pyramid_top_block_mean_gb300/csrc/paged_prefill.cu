@@ -186,29 +186,29 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// The factor that caps two small scores: MaskArgs::xk with w = x^2, or uk with w = u^2.
-__device__ __forceinline__ uint64_t cap_factor(const float (&k)[4], uint64_t w2) {
-  uint64_t f = ptx::fma2(w2, ptx::pack2(k[3], k[3]), ptx::pack2(k[2], k[2]));
-  f = ptx::fma2(w2, f, ptx::pack2(k[1], k[1]));
-  return ptx::fma2(w2, f, ptx::pack2(k[0], k[0]));
+// The factor that caps two small scores, from MaskArgs::by times each.
+__device__ __forceinline__ uint64_t cap_factor(const MaskArgs& m, uint64_t y2) {
+  const uint64_t w2 = mul2(y2, y2);
+  uint64_t f = ptx::fma2(w2, ptx::pack2(m.tk[3], m.tk[3]), ptx::pack2(m.tk[2], m.tk[2]));
+  f = ptx::fma2(w2, f, ptx::pack2(m.tk[1], m.tk[1]));
+  return ptx::fma2(w2, f, ptx::pack2(m.tk[0], m.tk[0]));
 }
-__device__ __forceinline__ uint64_t cap_factor(const MaskArgs& m, uint64_t x2) { return cap_factor(m.xk, mul2(x2, x2)); }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// |u| <= 1/2 ? a : b.  (In PTX: over a row's worth of scores the compiler takes
+// |x| <= lim ? a : b.  (In PTX: over a row's worth of scores the compiler takes
 // the expression for 128 branches and spills 3 KB, three times the time.)
-__device__ __forceinline__ float within_half(float u, float a, float b) {
+__device__ __forceinline__ float within(float x, float lim, float a, float b) {
   float y;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.le.f32 p, %1, 0f3F000000;\n\t"
-      "selp.f32 %0, %2, %3, p;\n\t}"
+      "setp.le.f32 p, %1, %2;\n\t"
+      "selp.f32 %0, %3, %4, p;\n\t}"
       : "=f"(y)
-      : "f"(fabsf(u)), "f"(a), "f"(b));
+      : "f"(fabsf(x)), "f"(lim), "f"(a), "f"(b));
   return y;
 }
 
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this thread's row and the keys that it sees; rows behind the new
       // tokens are computed as if they saw all, and not written
       int32_t lo = 0, hi = 0x7fffffff, t;
-      float slope = 0.0f;
+      float slope = 0.0f, lim = INFINITY;  // such a row has no say in the form of the cap
       {
         const int32_t b = (uint32_t)ip->bh / (uint32_t)pr.Hkv;
         const int32_t i = ip->tile * 2 * tokens + w * tokens + (r & (tokens - 1));
@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           key_span(mk, b, a.n, i, t, ip->len, &l, &u);
           lo = l <= u ? (int32_t)l : 0x7fffffff;
           hi = l <= u ? (int32_t)u : -1;
+          lim = mk.by == 1.0f ? mk.lim : -1.0f;
         }
         if (MODE == 1 && mk.slopes)
           slope = mk.slopes[(ip->bh - b * pr.Hkv) * pr.G + (r >> a.lg_tokens)] * kLog2e;
@@ -711,8 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // small scores: a polynomial on the FMA pipe, two at a time (the
             // exponential and the reciprocal of the other way take 12 cycles of
-            // the SFU a warp, three times what the softmax takes itself)
-            if (__all_sync(0xffffffffu, fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) <= mk.xlim)) {
+            // the SFU a warp, three times what the softmax takes itself).  What
+            // stands at keys that are not seen may decide against it, and
+            // changes no bit: a small score comes out the same both ways
+            if (__all_sync(0xffffffffu, !(fmaxf(ptx::max3(big[0], big[1], big[2]), big[3]) > lim))) {
               late = !part && !mk.slopes;  // the cap is monotone: the largest score stays the largest
               if (!late) {
 #pragma unroll
@@ -723,16 +726,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               // cap_score(), two at a time: the small ones among them take the
               // polynomial too, since the other form's error is a part of the cap
+              const uint64_t by2 = ptx::pack2(mk.by, mk.by);
               const float pre = mk.pre * (2.0f * kLog2e), cap = mk.cap2;
               auto large = [&](float x) { return fmaf(-2.0f * cap, rcp_approx(1.0f + ptx::ex2(x * pre)), cap); };
 #pragma unroll
               for (int c = 0; c < kKeys; c += 2) {
-                const uint64_t x2 = ptx::pack2(s[c], s[c + 1]), u2 = mul2(x2, ptx::pack2(mk.pre, mk.pre));
-                float a0, a1, u0, u1;
-                ptx::unpack2(u2, u0, u1);
-                ptx::unpack2(mul2(x2, cap_factor(mk.uk, mul2(u2, u2))), a0, a1);
-                s[c] = within_half(u0, a0, large(s[c]));
-                s[c + 1] = within_half(u1, a1, large(s[c + 1]));
+                const uint64_t x2 = ptx::pack2(s[c], s[c + 1]);
+                const uint64_t y2 = mul2(x2, by2);
+                float a0, a1, y0, y1;
+                ptx::unpack2(y2, y0, y1);
+                ptx::unpack2(mul2(x2, cap_factor(mk, y2)), a0, a1);
+                s[c] = within(y0, mk.lim, a0, large(s[c]));
+                s[c + 1] = within(y1, mk.lim, a1, large(s[c + 1]));
               }
             }
           }

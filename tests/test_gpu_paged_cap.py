@@ -113,3 +113,28 @@ def test_a_row_computed_anew_is_capped_alike(pisa):
     want, tol = capped(q[0], k[0], v[0], 700, pos, 0.125, 1e8)
     R.within(out[0][:, :150], want[:, :150], tol[:, :150])
     assert bool(out[0][:, 150:].isnan().all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(16, 4, 64), (8, 8, 128), (16, 2, 128)])
+@pytest.mark.parametrize("B,n,new,length", [(64, 64, 40, 40), (16, 100, 83, 700), (2, 30, 30, 5000), (70, 1, 1, 200)])
+def test_what_no_row_sees_changes_no_bit(pisa, Hq, Hkv, d, B, n, new, length):
+    # keys behind the end, in its page and in the page after it, and queries behind the new tokens
+    N = length + 100
+    g = torch.Generator().manual_seed(n)
+    k, v = (torch.randn(B, Hkv, N, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(B, Hq, n, d, generator=g).to(torch.bfloat16).cuda()
+    vp, table = R.paginate(v, [N] * B, seed=1)
+    vp, table = vp.cuda(), table.cuda()
+    layer = pisa.PagedAttention(pisa.make_params(B, N, Hq, Hkv, d), n=n)
+    lens, news = i32([length] * B), i32([new] * B)
+    for kw in (dict(softcap=20.0), dict(softcap=20.0, slopes=torch.full((Hq,), 0.01, device="cuda"))):
+        outs = []
+        for keys, queries in ((0.0, 0.0), (1e4, 0.0), (0.0, 1e4), (float("inf"), 0.0), (R.NAN, R.NAN)):
+            k[:, :, length:] = keys
+            q[:, :, new:] = queries
+            kp, _ = R.paginate(k, [N] * B, seed=1)
+            out = layer.dense_prefill(q, kp.cuda(), vp, table, lens, new_lens=news, mask=pisa.AttentionMask(**kw))
+            outs.append(out[:, :, :new].clone())
+            assert layer.device_status() == 0
+        for other in outs[1:]:
+            assert torch.equal(other, outs[0]), f"{int((other != outs[0]).sum())} elements differ"
