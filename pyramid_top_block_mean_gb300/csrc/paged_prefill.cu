@@ -33,6 +33,7 @@
 // Rows with few tokens and a long cache: the keys of a CTA's rows are split
 // over several CTAs, whose parts a second kernel joins.
 #include <cudaTypedefs.h>
+#include <float.h>
 
 #include <algorithm>
 
@@ -67,11 +68,12 @@ constexpr int kItems = 2;  // items in flight: the loader is at most one ahead
 // of key tiles.
 struct Item {
   int32_t bh, tile, split;  // bh < 0: no more items
+  int32_t number, clean;    // its place among all; taken a second time
   int32_t len, cnt;         // of the sequence; cnt rows before it are new
   int32_t fits;             // its lengths do
   int32_t ja, jb;           // key tiles
   int32_t wa[2], wb[2];     // and those that each row tile takes part in
-  int32_t klo, khi;         // first and last key that any row sees
+  int32_t khi;              // last key that any row sees
   int32_t fill;             // fills of the ring before the item's first
 };
 
@@ -85,6 +87,7 @@ struct Smem {
   Item item[kItems];
   uint32_t tmem;
   int32_t abort, zero, bad_page;
+  int32_t again[kItems];  // a row of the item is not finite
 };
 
 struct Args {
@@ -213,67 +216,125 @@ __device__ __forceinline__ float within(float x, float lim, float a, float b) {
 }
 
 // A weight of zero does not undo a value that is not finite: the MMA takes the
-// values of all keys of a tile into all of its rows.  When a row came out
-// without being finite, a warp looks through the values that the row does not
-// see but that its tiles held; if one of them is to blame, it computes the row
-// anew from the keys that the row sees, one after the other.  (Slow, and only
-// there for that case; it is not inlined to keep the kernel's code small.)
-// Row: token i at position t, head g of key head bh % Hkv, keys lo .. hi; its
-// tiles held the keys ka .. kb; `at` is its place among the parts.
-template <int D, int MODE>
-__device__ __noinline__ void mend_row(const Prob& pr, const MaskArgs& mk, const Args& a, int32_t bh, int32_t i,
-                                      int32_t g, int32_t t, int32_t lo, int32_t hi, int32_t ka, int32_t kb,
-                                      int64_t at) {
-  constexpr int J = D / 32;  // dims lane + 32 j
-  const int lane = threadIdx.x & 31;
-  const int64_t b = (uint32_t)bh / (uint32_t)pr.Hkv;
-  const int h = bh - (int)b * pr.Hkv;
-  const int32_t* trow = a.table + b * a.nb;
-  auto row_of = [&](int32_t key) -> int64_t {  // of the pools; negative: page outside
-    const int32_t page = trow[key / kPage];
-    return page < 0 || page >= a.num_pages ? -1 : (((int64_t)page * pr.Hkv + h) * kPage + key % kPage) * D + lane;
+// values of all keys of a tile into all of its rows.  An item with a row that
+// came out without being finite is therefore taken a second time, "clean": the
+// loader puts zeros in the place of such values, the softmax warps note for
+// each row in which dims it sees one, and those outputs are set at the end.
+// (At the pipeline's pace, so that its waits stay short whatever the cache
+// holds; not inlined, to keep the code of the first way small.)
+
+// A tile's values in shared memory, by the loader warp.
+template <uint32_t BYTES>
+__device__ __noinline__ void clean_tile(uint8_t* tile) {
+  auto clean = [](uint32_t x) {
+    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+    return x;
   };
-  const int32_t s0 = max(lo, ka), s1 = min(hi, kb);
-  bool found = false;
-  for (int32_t key = ka; key <= kb && !found; ++key) {
-    if (key == s0 && s0 <= s1) {
-      key = s1;
-      continue;
+#pragma unroll 4
+  for (uint32_t e = (threadIdx.x & 31) * 16; e < BYTES; e += 512) {
+    uint4 x = *reinterpret_cast<const uint4*>(tile + e);
+    x.x = clean(x.x); x.y = clean(x.y); x.z = clean(x.z); x.w = clean(x.w);
+    *reinterpret_cast<uint4*>(tile + e) = x;
+  }
+}
+
+// The dims in which a row sees values that are +inf or NaN, and -inf or NaN:
+// bit l of word (i, e) stands for dim 64 i + 2 l + e.
+template <int D>
+struct Marks {
+  uint32_t up[D / 64][2], down[D / 64][2];
+};
+
+// Notes what the key tiles ja .. jb - 1 hold for the rows of a warp, a lane's
+// seeing lo .. hi.  (About 1 us a tile, so that the waits on these warps stay
+// within their limits for any cache.)
+template <int D>
+__device__ __noinline__ void mark_tiles(const Args& a, int32_t Hkv, int32_t bh, int32_t ja, int32_t jb, int32_t lo,
+                                        int32_t hi, Marks<D>* marks) {
+  constexpr int kBatch = 16, W = D / 64;  // keys in flight
+  const int lane = threadIdx.x & 31;
+  const int64_t b = (uint32_t)bh / (uint32_t)Hkv;
+  const int64_t h = bh - b * Hkv;
+  // bits 4 i + 2 e and 4 i + 2 e + 1: up and down of dim 64 i + 2 lane + e in the words of a key
+  auto flags = [](uint32_t w, int i) {
+    uint32_t f = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t y = e ? w >> 16 : w & 0xffffu, m = y & 0x7fffu;
+      if (m >= 0x7f80u) f |= (m > 0x7f80u ? 3u : (y >> 15 ? 2u : 1u)) << (4 * i + 2 * e);
     }
-    const int64_t v = row_of(key);
-    bool odd = false;
-    if (v >= 0)
-      for (int j = 0; j < J; ++j) odd |= !(fabsf(bf16_to_f(a.v[v + 32 * j])) < INFINITY);
-    found = __any_sync(0xffffffffu, odd);
+    return f;
+  };
+  auto note = [&](uint32_t f, bool seen) {
+    for (int i = 0; i < W; ++i) {
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t up = __ballot_sync(0xffffffffu, f >> (4 * i + 2 * e) & 1);
+        const uint32_t down = __ballot_sync(0xffffffffu, f >> (4 * i + 2 * e + 1) & 1);
+        if (seen) {
+          marks->up[i][e] |= up;
+          marks->down[i][e] |= down;
+        }
+      }
+    }
+  };
+  for (int32_t key0 = ja * kKeys; key0 < jb * kKeys; key0 += kPage) {
+    const bool none = lo >= key0 + kPage || hi < key0, whole = lo <= key0 && hi >= key0 + kPage - 1;
+    if (__all_sync(0xffffffffu, none)) continue;
+    const int32_t page = a.table[b * a.nb + key0 / kPage];
+    if (page < 0 || page >= a.num_pages) continue;
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + ((int64_t)page * Hkv + h) * kPage * D) + lane;
+    uint32_t f = 0;
+    for (int k0 = 0; k0 < kPage; k0 += kBatch) {
+      uint32_t x[kBatch][W], odd = 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[k][i] = v[(k0 + k) * (D / 2) + 32 * i];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) odd |= (x[k][i] & 0x7fff7fffu) + 0x00800080u;  // a carry where all of an exponent is set
+      if (!__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) continue;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) f |= flags(x[k][i], i);
+    }
+    if (!__any_sync(0xffffffffu, f != 0)) continue;
+    if (__all_sync(0xffffffffu, none || whole)) {
+      note(f, whole);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kPage; ++k) {
+        f = 0;
+        for (int i = 0; i < W; ++i) f |= flags(v[k * (D / 2) + 32 * i], i);
+        note(f, key0 + k >= lo && key0 + k <= hi);
+      }
+    }
   }
-  if (!found) return;
-  const int64_t hq = (int64_t)h * pr.G + g, orow = ((b * pr.Hq + hq) * a.n + i) * D;
-  const float slope = MODE == 1 && mk.slopes ? mk.slopes[hq] * kLog2e : 0.0f;
-  float x[J], acc[J], m = -INFINITY, l = 0.0f;
-  for (int j = 0; j < J; ++j) {
-    x[j] = bf16_to_f(a.q[orow + lane + 32 * j]);
-    acc[j] = 0.0f;
-  }
-  for (int32_t key = s0; key <= s1; ++key) {
-    const int64_t r = row_of(key);
-    if (r < 0) continue;
-    float s = 0.0f;
-    for (int j = 0; j < J; ++j) s = fmaf(x[j], bf16_to_f(a.k[r + 32 * j]), s);
-    s = warp_sum(s);
-    s = MODE == 1 && mk.cap2 > 0.0f ? cap_score(mk, s) : s * pr.scale2;
-    s = fmaf(slope, (float)(key - t), s);
-    const float top = fmaxf(m, s);
-    const float f = m == -INFINITY ? 1.0f : exp2f(m - top), p = exp2f(s - (top == -INFINITY ? 0.0f : top));
-    l = fmaf(l, f, p);
-    for (int j = 0; j < J; ++j) acc[j] = fmaf(p, bf16_to_f(a.v[r + 32 * j]), acc[j] * f);
-    m = top;
-  }
-  if (a.splits > 1) {
-    if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, l);
-    for (int j = 0; j < J; ++j) a.part_o[at * D + lane + 32 * j] = acc[j];
-  } else {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int j = 0; j < J; ++j) a.out[orow + lane + 32 * j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
+}
+
+// Sets the marked outputs of the warp's rows: out + orow, or with splits the
+// part at `at`.
+template <int D>
+__device__ __noinline__ void set_marked(const Args& a, bool row, int64_t orow, int64_t at, const Marks<D>* marks) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the rows' stores come before those that replace them
+  for (unsigned todo = __ballot_sync(0xffffffffu, row); todo; todo &= todo - 1) {
+    const int x = __ffs(todo) - 1;
+    const int64_t to = __shfl_sync(0xffffffffu, a.splits > 1 ? at * D : orow, x);
+    for (int i = 0; i < D / 64; ++i) {
+      for (int e = 0; e < 2; ++e) {
+        const bool up = (__shfl_sync(0xffffffffu, marks->up[i][e], x) >> lane & 1) != 0;
+        const bool down = (__shfl_sync(0xffffffffu, marks->down[i][e], x) >> lane & 1) != 0;
+        if (!up && !down) continue;
+        const float y = up && down ? NAN : (up ? INFINITY : -INFINITY);
+        const int64_t dim = to + 64 * i + 2 * lane + e;
+        if (a.splits > 1) a.part_o[dim] = y;
+        else a.out[dim] = __bfloat16_as_ushort(__float2bfloat16(y));
+      }
+    }
   }
 }
 
@@ -324,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     sm.zero = 0;
     sm.bad_page = 0;
+    for (int k = 0; k < kItems; ++k) sm.again[k] = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
@@ -369,11 +431,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) k = (int32_t)gridDim.x + atomicAdd(a.claimed, 1);
         return __shfl_sync(0xffffffffu, k, 0);
       };
+      // the item that a slot held, where it has to be taken a second time (-1: not)
+      auto to_repeat = [&](int slot) {
+        if (*(volatile int32_t*)&sm.again[slot] == 0) return -1;
+        const int32_t k = sm.item[slot].number;
+        __syncwarp();
+        if (lane == 0) sm.again[slot] = 0;
+        __syncwarp();
+        return k;
+      };
       // the last tokens' items, which see the most keys, come first; a CTA
       // that has loaded what its item needs claims the next one
-      for (int32_t now = blockIdx.x; ok && now < a.items; now = claim()) {
+      int32_t now = blockIdx.x, next = 0;
+      bool clean = false;  // `now` is taken a second time, and `next` follows it
+      while (ok) {
+        if (now >= a.items) {
+          // none left, unless one of the last items, the older one first
+          int32_t back = -1;
+          for (int k = min(items, kItems); k > 0 && back < 0; --k) {
+            const int n = items - k;
+            if (wait(&sm.iempty[n % kItems], n / kItems)) back = to_repeat(n % kItems);
+          }
+          if (!ok || back < 0) break;
+          next = now;
+          now = back;
+          clean = true;
+        }
         uint32_t x = (uint32_t)now;
         Item it;
+        it.number = now;
+        it.clean = clean;
         it.split = (int32_t)(x % (uint32_t)a.splits);
         x /= (uint32_t)a.splits;
         it.bh = (int32_t)(x % heads);
@@ -384,7 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t len, cnt;
         it.fits = new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt);
         if (!it.fits && lane == 0) set_status(a.status, PISA_DEV_BAD_SEQ_LEN);
-        if (i0 >= cnt) continue;
+        if (i0 >= cnt) {
+          now = claim();
+          continue;
+        }
         it.len = (int32_t)len;
         it.cnt = (int32_t)cnt;
         // keys that each row tile sees
@@ -427,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.wb[v] = hi[v] < 0 ? it.jb : min(it.jb, hi[v] / kKeys + 1);
           if (it.wb[v] < it.wa[v]) it.wb[v] = it.wa[v];
         }
-        it.klo = klo;
         it.khi = khi;
         it.fill = fills;
         // lane l: the page of block 2 j + l, -1: none of its keys is seen, -2: outside the pool
@@ -443,7 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int32_t entry = look_up(it.ja);  // under way while the item is handed out
         const int is = items % kItems;
-        if (items >= kItems && !wait(&sm.iempty[is], (items / kItems) + 1)) break;
+        if (items >= kItems) {
+          if (!wait(&sm.iempty[is], (items / kItems) + 1)) break;
+          const int32_t back = to_repeat(is);
+          if (back >= 0) {
+            next = now;
+            now = back;
+            clean = true;
+            continue;
+          }
+        }
         if (lane == 0) {
           sm.item[is] = it;
           ptx::mbar_arrive(ptx::smem_u32(&sm.ifull[is]));
@@ -487,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fills >= kStages && !wait(&sm.empty[st], ph ^ 1)) break;  // the first round finds them empty
             if (lent == st && !take_back()) break;
             const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
-            const bool scrub = kv == 1 && clear;
+            const bool scrub = kv == 1 && (clear || clean);
             const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
             if (lane == 0) {
               if (pages) ptx::mbar_arrive_expect_tx(bar, pages * (kTile / 2));
@@ -518,6 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_uint4(0, 0, 0, 0);
                 }
               }
+              if (clean) {
+                __syncwarp();
+                clean_tile<kTile>(sm.kv[st]);
+              }
               ptx::fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) ptx::mbar_arrive(full);
@@ -537,8 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         advance();
+        now = clean ? next : claim();
+        clean = false;
       }
-      if ((items < kItems || wait(&sm.iempty[items % kItems], (items / kItems) + 1)) && ok && lane == 0) {
+      if (ok && lane == 0) {  // (the slot is free: the last items have been waited for)
         sm.item[items % kItems].bh = -1;
         ptx::mbar_arrive(ptx::smem_u32(&sm.ifull[items % kItems]));
       }
@@ -927,16 +1031,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           pass(pk, dst ? dst + 2 * c : nullptr);
         }
       }
-      if (unsigned todo = __ballot_sync(0xffffffffu, row && finite != 0.0f)) {
-        const int32_t ka = max(ip->klo, wa * kKeys), kb = min(ip->khi, wb * kKeys - 1);
-        __syncwarp();  // the rows' stores come before those that replace them
-        for (; todo; todo &= todo - 1) {
-          const int x = __ffs(todo) - 1;
-          mend_row<D, MODE>(pr, mk, a, ip->bh, __shfl_sync(0xffffffffu, i, x),
-                            __shfl_sync(0xffffffffu, r >> a.lg_tokens, x), __shfl_sync(0xffffffffu, t, x),
-                            __shfl_sync(0xffffffffu, lo, x), __shfl_sync(0xffffffffu, hi, x), ka, kb,
-                            __shfl_sync(0xffffffffu, at, x));
-        }
+      if (ip->clean) {  // (a row of NaN scores is NaN already)
+        Marks<D> marks = {};
+        mark_tiles<D>(a, pr.Hkv, ip->bh, wa, wb, lo, row ? hi : -1, &marks);
+        set_marked<D>(a, row && any && l < INFINITY, ((b * pr.Hq + hq) * a.n + i) * D, at, &marks);
+      } else if (__any_sync(0xffffffffu, row && finite != 0.0f)) {
+        if (lane == 0) *(volatile int32_t*)&sm.again[items % kItems] = 1;
       }
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
       // the copy that fills the stage next comes after these accesses
@@ -998,7 +1098,7 @@ __global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
     if (bm > M) {
-      const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - bm);
+      const float f = M == -INFINITY ? 1.0f : fmaxf(ptx::ex2(M - bm), FLT_MIN);
       L *= f;
 #pragma unroll
       for (int d = 0; d < 8; ++d) acc[d] *= f;
@@ -1007,7 +1107,8 @@ __global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (ml[k].y == 0.0f) continue;  // a part that saw no key wrote no output
-      const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
+      // (a part that weighs nothing still brings its infinities)
+      const float f = ml[k].x == -INFINITY ? 1.0f : fmaxf(ptx::ex2(ml[k].x - M), FLT_MIN);
       L = fmaf(ml[k].y, f, L);
       const float ov[8] = {o[k][0].x, o[k][0].y, o[k][0].z, o[k][0].w, o[k][1].x, o[k][1].y, o[k][1].z, o[k][1].w};
 #pragma unroll
@@ -1029,7 +1130,7 @@ __global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(
 #pragma unroll
   for (int k = 0; k < PL; ++k) {
     if (sm_l[k] == 0.0f) continue;
-    const float f = sm_m[k] == -INFINITY ? 1.0f : ptx::ex2(sm_m[k] - top);
+    const float f = sm_m[k] == -INFINITY ? 1.0f : fmaxf(ptx::ex2(sm_m[k] - top), FLT_MIN);
     total = fmaf(sm_l[k], f, total);
     x = fmaf(sm_o[k][d], f, x);
     y = fmaf(sm_o[k][d + 1], f, y);
