@@ -566,6 +566,10 @@ class PagedAttention:
         flat = torch.zeros(rows * (2 + 2 * n), dtype=_dtype(p), device=self.device)
         self._out = {"dense": flat[:rows].view(one), "selected": flat[rows:2 * rows].view(one),
                      "q": flat[2 * rows:(2 + n) * rows].view(many), "prefill": flat[(2 + n) * rows:].view(many)}
+        if self._index >= 0:  # the zeros are there before the first call, whatever stream that runs on
+            with torch.cuda.device(self._index):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
 
     def _buffer(self, kind: str, like):
         out = self._out[kind]
