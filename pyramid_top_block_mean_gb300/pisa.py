@@ -571,19 +571,25 @@ class PagedAttention:
                 if not torch.cuda.is_current_stream_capturing():
                     torch.cuda.current_stream().synchronize()
 
+    def _fits(self, x, ok: bool):
+        if x.get_device() != self._index:
+            raise ValueError(f"expected tensors on {self.device}, got {x.device}")
+        if not ok:
+            raise ValueError(f"{tuple(x.shape)}: more than the {self.n} new tokens per sequence asked for")
+
     def _buffer(self, kind: str, like):
         out = self._out[kind]
-        if like.get_device() != self._index:
-            raise ValueError(f"expected tensors on {self.device}, got {like.device}")
-        if out.shape == like.shape:
+        same = out.shape == like.shape
+        self._fits(like, same or (like.dim() == out.dim() and like.numel() <= out.numel()))
+        if same:
             return out
-        if like.dim() != out.dim() or like.numel() > out.numel():
-            raise ValueError(f"{tuple(like.shape)}: more than the {self.n} new tokens per sequence asked for")
         return out.view(-1)[:like.numel()].view(like.shape)
 
     def append(self, q, k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_out=None, stream=None):
         """Rotates and appends k and v; returns the rotated queries [B, H_q, n, d] (None when q is None)."""
-        q_out = self._buffer("q", q if q is not None else k)  # (without queries: the check alone)
+        if q is None:
+            self._fits(k, k.dim() == 4 and k.shape[2] <= self.n)
+        q_out = None if q is None else self._buffer("q", q)
         _append(self.p, k, v, k_pages, v_pages, page_table, seq_lens, self._space, self._rope, self._rot,
                 self.interleaved, q, None if q is None else q_out.data_ptr(), k_out, new_lens, stream, True)
         return None if q is None else q_out
