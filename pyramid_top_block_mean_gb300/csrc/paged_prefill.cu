@@ -247,8 +247,8 @@ struct Marks {
 };
 
 // Notes what the key tiles ja .. jb - 1 hold for the rows of a warp, a lane's
-// seeing lo .. hi.  (About 1 us a tile, so that the waits on these warps stay
-// within their limits for any cache.)
+// seeing lo .. hi.  (About 1 us a tile, some 5 us one full of such values, so
+// that the waits on these warps stay within their limits for any cache.)
 template <int D>
 __device__ __noinline__ void mark_tiles(const Args& a, int32_t Hkv, int32_t bh, int32_t ja, int32_t jb, int32_t lo,
                                         int32_t hi, Marks<D>* marks) {
@@ -278,14 +278,16 @@ __device__ __noinline__ void mark_tiles(const Args& a, int32_t Hkv, int32_t bh, 
       }
     }
   };
+  constexpr uint32_t kAll = W == 1 ? 0xfu : 0xffu;
+  bool full = false;  // every dim of the row is marked both ways: it cannot change any more
   for (int32_t key0 = ja * kKeys; key0 < jb * kKeys; key0 += kPage) {
-    const bool none = lo >= key0 + kPage || hi < key0, whole = lo <= key0 && hi >= key0 + kPage - 1;
+    const bool none = full || lo >= key0 + kPage || hi < key0, whole = lo <= key0 && hi >= key0 + kPage - 1;
     if (__all_sync(0xffffffffu, none)) continue;
     const int32_t page = a.table[b * a.nb + key0 / kPage];
     if (page < 0 || page >= a.num_pages) continue;
     const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + ((int64_t)page * Hkv + h) * kPage * D) + lane;
     uint32_t f = 0;
-    for (int k0 = 0; k0 < kPage; k0 += kBatch) {
+    for (int k0 = 0; k0 < kPage && !__all_sync(0xffffffffu, f == kAll); k0 += kBatch) {
       uint32_t x[kBatch][W], odd = 0;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
@@ -312,6 +314,10 @@ __device__ __noinline__ void mark_tiles(const Args& a, int32_t Hkv, int32_t bh, 
         note(f, key0 + k >= lo && key0 + k <= hi);
       }
     }
+    uint32_t both = 0xffffffffu;
+    for (int i = 0; i < W; ++i)
+      for (int e = 0; e < 2; ++e) both &= marks->up[i][e] & marks->down[i][e];
+    full = both == 0xffffffffu;
   }
 }
 
