@@ -758,6 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // MODE 0 keeps the dots and scales them inside the exponent
     const float sc = MODE == 0 ? pr.scale2 : 1.0f;
     const float slack = kSlack / sc;
+    // A weight is 2^(s sc - m sc) by one FMA, with m sc rounded: a factor of the
+    // whole row, unless |m sc| is so large (2^31) that it over- or underflows.
+    // Scores beyond 2^28 lie 2^5 apart at least, so that their row takes the
+    // power of two below sc: m sc is then exact, and as good as all of the
+    // weight stays with the largest.
+    const float pow2 = __uint_as_float(__float_as_uint(sc) & 0x7f800000u);
     bool ok = true;
     int tiles_done = 0, outs_done = 0;
     for (int items = 0;; ++items) {
@@ -785,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           slope = mk.slopes[(ip->bh - b * pr.Hkv) * pr.G + (r >> a.lg_tokens)] * kLog2e;
       }
       const int f0 = ip->fill + 2 * (wa - ip->ja) + 3;  // the fill of the second V
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f, by = sc;
       int st = f0 % kStages, ph = (f0 / kStages) & 1;
       for (int j = wa; j < wb; ++j) {
         ok = true;
@@ -903,7 +909,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool grow = top > m + slack || (m == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow && m > -INFINITY ? ptx::ex2((m - top) * sc) : 1.0f;
-          if (grow) m = top;
+          if (grow) {
+            m = top;
+            if (MODE == 0) by = fabsf(top * sc) < 0x1p28f ? sc : pow2;
+          }
           l *= f;
           if (j > wa && __any_sync(0xffffffffu, f != 1.0f)) {
             // the MMAs into O so far are done: S of this tile was issued after them
@@ -918,8 +927,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float neg = m == -INFINITY ? 0.0f : -m * sc;
-        const uint64_t sc2 = ptx::pack2(sc, sc), neg2 = ptx::pack2(neg, neg);
+        const float neg = m == -INFINITY ? 0.0f : -m * by;
+        const uint64_t by2 = ptx::pack2(by, by), neg2 = ptx::pack2(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
         // weights of the row, 32 at a time, from the exponents of two scores
         auto weights = [&](auto exponents) {
@@ -946,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (MODE == 1 && late) weights([&](uint64_t x2) { return ptx::fma2(x2, cap_factor(mk, x2), neg2); });
-        else weights([&](uint64_t x2) { return ptx::fma2(x2, sc2, neg2); });
+        else weights([&](uint64_t x2) { return ptx::fma2(x2, by2, neg2); });
         float s0, s1;
         ptx::unpack2(ptx::add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
