@@ -394,7 +394,11 @@ void pisa_test_inject_leaf_timeout(uint64_t wait_limit_ns, int32_t drop_first_ke
  * Page table entries behind a sequence's last position are never read, and
  * the positions of its last page behind its length may hold anything, NaN
  * included.  A value that is not finite reaches the queries that see its key
- * and no other. */
+ * and no other; a prompt call that meets some takes 4 to 14 times as long.
+ *
+ * Attention works in fp32 but for the weights of a row, relative to a
+ * reference near its largest score, which are rounded to bf16 (2^-8 of each)
+ * for their product with the values; their sum is taken before that. */
 
 /* Appends n new tokens per sequence to the pages.  k and v [B, H_kv, n, d]
  * and (nullable) q [B, H_q, n, d] may be strided views: k_strides points at
@@ -422,7 +426,8 @@ pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, co
 
 /* What a dense attention call does to a score x = scale * q . k of a query
  * at position t and a key at position j, and which keys it sees:
- *   softcap > 0       x becomes softcap * tanh(x / softcap)
+ *   softcap > 0       x becomes softcap * tanh(x / softcap), off by less than
+ *                     2^-19 of itself (a cap far above the scores is none)
  *   slopes            fp32 [H_q] on the device: x += slopes[h] * (j - t)
  *   window > 0        only keys j > t - window
  *   first_key         int32 [B, n] on the device: only keys j >= first_key[b, i]

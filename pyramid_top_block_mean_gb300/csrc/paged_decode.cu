@@ -14,7 +14,7 @@
 // the GPU and short ones share a CTA; every CTA derives the cut from the
 // lengths on the device.  A producer warp brings the run's pages by TMA
 // (128-byte swizzle, so that every ldmatrix below is free of bank conflicts)
-// into a ring of stages (192 KB in flight on an SM); two groups of four warps
+// into a ring of stages (128 to 192 KB in flight on an SM); two groups of four warps
 // take alternate pages, a warp 16 of a page's 64 keys, and hold their own (m,
 // l, o): S = K q by m16n8k16 MMAs with the heads as the 8 columns, O^T += V^T P
 // with P turned in registers by movmatrix.  A page takes a group about 1300
@@ -25,8 +25,8 @@
 // CTAs, so results do not depend on timing.
 //
 // Measured (GB300): 64 ragged sequences of up to 8192 tokens, 32 / 8 heads, d
-// = 128: 233 us, 6.7 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
-// tokens 150 us (6.5 TB/s); 64 sequences' 35 selected blocks 95 us (6.1 TB/s);
+// = 128: 237 us, 6.6 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
+// tokens 150 us (6.5 TB/s); 64 sequences' 35 selected blocks 97 us (6.0 TB/s);
 // one sequence of 197 tokens 6.8 us.
 #include <algorithm>
 
@@ -677,7 +677,7 @@ struct Ws {
 };
 Ws ws_layout(const Prob& pr) {
   Ws w;
-  size_t o = 256;  // the status word's; the counters follow, so that one memset clears both
+  size_t o = 256;  // the status word's; the counters follow, so that one kernel clears both
   w.counter = o; o = align_up(o + (size_t)pr.B * pr.Hkv * 4, 256);
   w.ml = o; o = align_up(o + (size_t)2 * kMaxCtas * 2 * pr.G * 4, 256);
   w.o = o; o = align_up(o + (size_t)2 * kMaxCtas * pr.G * pr.d * 4, 256);

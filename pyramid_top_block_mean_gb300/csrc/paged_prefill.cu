@@ -25,10 +25,11 @@
 // CTAs are persistent: the loader claims the next 256 rows when it has loaded
 // what the current ones need.
 //
-// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 655 us (1680 TFLOP/s of
-// the seen pairs, 87 % of cuBLAS's measured rate), 65536 tokens 10.4 ms (1690),
-// 16384 with a tanh cap 945 us, 2 x 4096 tokens (ragged) 87 us, 61 tokens behind
-// 65536 cached ones 48 us.
+// Measured (GB300, 16 / 4 heads, d = 128): 16384 tokens 662 us (1660 TFLOP/s of
+// the seen pairs, 86 % of cuBLAS's measured rate), 65536 tokens 10.7 ms (1640),
+// 16384 with a tanh cap 950 to 963 us (1621 where scores pass half the cap),
+// with a distance bias 983, with a window of 1024 141, at d = 64 583 us; prompts
+// of 4096 and 3000 tokens 93 us, 61 tokens behind 65536 cached ones 50 us.
 //
 // Rows with few tokens and a long cache: the keys of a CTA's rows are split
 // over several CTAs, whose parts a second kernel joins.

@@ -84,15 +84,16 @@ inline pisa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PISA_O
 // Counts one kernel launch (process-wide, relaxed atomic); called before every launch.
 void note_launch();
 
-// Launches a kernel of the prefill chain.  With pdl (every kernel of a call
+// Launches a kernel of a call's chain.  With pdl (every kernel of a call
 // but its first) the launch uses programmatic stream serialization: its
 // launch and prologue may overlap the tail of the kernel before it, which
 // is part of the same call.  A call's first kernel is launched plainly, so
 // it keeps full ordering after whatever the caller queued on the stream
-// (copies, event waits).  Every kernel launched here calls pdl_wait()
-// before it touches memory; it blocks until the previous grid has
-// completed and its writes are visible, and returns at once after a plain
-// launch.
+// (copies, event waits), and so do the kernels behind it: they may read the
+// caller's inputs at once, and touch anything else only after pdl_wait().
+// That blocks until the previous grid has completed and its writes are
+// visible, and returns at once after a plain launch.  At least one CTA of
+// each grid calls it, so that no grid ends before the one it follows.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(bool pdl, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args&&... args) {

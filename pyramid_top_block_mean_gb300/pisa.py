@@ -542,8 +542,10 @@ class PagedAttention:
     up to n new tokens per sequence in a call: appending rotated keys and
     values, dense attention of one token or of a prompt, and attention over
     the selector's blocks.  Owns the workspace and one output buffer per kind
-    of call, zeroed once and written again by the next call of its kind; rows
-    behind a sequence's new tokens are not written.
+    of call, zeroed when it is made and written again by the next call of its
+    kind (a call of fewer tokens uses its front).  Rows behind a sequence's new
+    tokens are not written: they hold zeros or what an earlier call left there.
+    Calls may run on any stream, one after the other.
     rope: fp32 [N, rot_dim] as append_paged takes it, or None."""
 
     def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
