@@ -34,7 +34,6 @@
 // Rows with few tokens and a long cache: the keys of a CTA's rows are split
 // over several CTAs, whose parts a second kernel joins.
 #include <cudaTypedefs.h>
-#include <float.h>
 
 #include <algorithm>
 
@@ -1071,6 +1070,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && sm.abort) set_status(a.status, PISA_DEV_TIMEOUT);
 }
 
+// The factor of x among values of weight f: an infinity keeps its own, where
+// the weight came out as nothing too.
+__device__ __forceinline__ float weight_of(float x, float f) { return fabsf(x) == INFINITY ? 1.0f : f; }
+
 // Joins the parts of a row: one CTA per row, 8 dims x every 16th part a
 // thread, so that all loads of a row are in flight at once.
 template <int D>
@@ -1114,21 +1117,20 @@ __global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
     if (bm > M) {
-      const float f = M == -INFINITY ? 1.0f : fmaxf(ptx::ex2(M - bm), FLT_MIN);
+      const float f = M == -INFINITY ? 1.0f : ptx::ex2(M - bm);
       L *= f;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) acc[d] *= f;
+      for (int d = 0; d < 8; ++d) acc[d] *= weight_of(acc[d], f);
       M = bm;
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (ml[k].y == 0.0f) continue;  // a part that saw no key wrote no output
-      // (a part that weighs nothing still brings its infinities)
-      const float f = ml[k].x == -INFINITY ? 1.0f : fmaxf(ptx::ex2(ml[k].x - M), FLT_MIN);
+      const float f = ml[k].x == -INFINITY ? 1.0f : ptx::ex2(ml[k].x - M);
       L = fmaf(ml[k].y, f, L);
       const float ov[8] = {o[k][0].x, o[k][0].y, o[k][0].z, o[k][0].w, o[k][1].x, o[k][1].y, o[k][1].z, o[k][1].w};
 #pragma unroll
-      for (int d = 0; d < 8; ++d) acc[d] = fmaf(ov[d], f, acc[d]);
+      for (int d = 0; d < 8; ++d) acc[d] = fmaf(ov[d], weight_of(ov[d], f), acc[d]);
     }
   }
   if (ch == 0) {
@@ -1146,10 +1148,10 @@ __global__ void __launch_bounds__(D * 2, D == 128 ? 5 : 10) prefill_join_kernel(
 #pragma unroll
   for (int k = 0; k < PL; ++k) {
     if (sm_l[k] == 0.0f) continue;
-    const float f = sm_m[k] == -INFINITY ? 1.0f : fmaxf(ptx::ex2(sm_m[k] - top), FLT_MIN);
+    const float f = sm_m[k] == -INFINITY ? 1.0f : ptx::ex2(sm_m[k] - top);
     total = fmaf(sm_l[k], f, total);
-    x = fmaf(sm_o[k][d], f, x);
-    y = fmaf(sm_o[k][d + 1], f, y);
+    x = fmaf(sm_o[k][d], weight_of(sm_o[k][d], f), x);
+    y = fmaf(sm_o[k][d + 1], weight_of(sm_o[k][d + 1], f), y);
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t hq = (bh % pr.Hkv) * pr.G + (r >> a.lg_tokens);

@@ -213,3 +213,9 @@ def test_rows_that_are_not_finite_for_reasons_of_their_own(pisa):
     assert torch.equal(out.isnan(), nan) and torch.equal(out.isposinf(), inf)
     ok = ~(nan | inf)
     R.within(torch.where(ok, out.double(), want), want, tol)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 8, 8), (128, 32, 8)])
+def test_sprinkled_values_in_all_of_many_items(pisa, d, Hq, Hkv):
+    # several items an SM, each taken twice
+    run(pisa, Hq, Hkv, d, 900, [900, 1000, 1100, 900, 950, 1500], [900, 890, 700, 900, 850, 900], 0.01, seed=9)

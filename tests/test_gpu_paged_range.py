@@ -91,3 +91,23 @@ def test_a_row_whose_scores_grow_from_small_to_large(pisa):
     vp, _ = R.paginate(v.cpu(), [N], seed=5)
     layer_out = layer.dense_prefill(q.to(torch.bfloat16), kk.cuda(), vp.cuda(), table.cuda(), i32([N]))
     check(layer_out[0], q[0], k[0], v[0], torch.arange(N, device="cuda"), 1)
+
+
+def test_large_values_without_weight(pisa):
+    # far keys' values are large, and their weights nothing: a prompt that is split over the keys
+    N, n, d, H = 6000, 30, 64, 2
+    g = torch.Generator().manual_seed(6)
+    k, v, q = (torch.randn(1, H, x, d, generator=g) for x in (N, N, n))
+    v[:, :, :4000] = 1e35
+    k, v, q = (x.to(torch.bfloat16) for x in (k, v, q))
+    kp, table = R.paginate(k, [N], seed=1)
+    vp, _ = R.paginate(v, [N], seed=1)
+    slopes = torch.full((H,), 0.5, device="cuda")
+    layer = pisa.PagedAttention(pisa.make_params(1, N, H, H, d), n=n)
+    pos = torch.arange(N - n, N, device="cuda")
+    q, k, v, kp, vp, table = (x.cuda() for x in (q, k, v, kp, vp, table))
+    out = layer.dense_prefill(q, kp, vp, table, i32([N]), mask=pisa.AttentionMask(slopes=slopes))
+    want, tol = R.dense(q[0], k[0], v[0], N, pos, d ** -0.5, slopes=slopes)
+    R.within(out[0], want, tol)
+    one = layer.dense_decode(q[:, :, -1].contiguous(), kp, vp, table, i32([N]), mask=pisa.AttentionMask(slopes=slopes))
+    R.within(one[0], want[:, -1], tol[:, -1])
