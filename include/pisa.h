@@ -481,6 +481,70 @@ pisa_status pisa_dense_prefill_paged(const pisa_params* p, const pisa_mask* mask
  * an unsupported problem, n < 0 or n > N). */
 size_t pisa_paged_workspace_bytes(const pisa_params* p, int64_t n);
 
+/* ------------------------------------------------------------------------
+ * The same cache in 8 bits, and normed heads.  pisa_cache names the pools, in
+ * one of two formats:
+ *   PISA_CACHE_PARAMS  elements of the dtype of p (the calls above)
+ *   PISA_CACHE_E4M3    k_pages and v_pages [num_pages, H_kv, C, d] of e4m3
+ *                      codes (4 exponent and 3 mantissa bits, largest number
+ *                      448, no infinities), k_scales and v_scales uint8
+ *                      [num_pages, H_kv, C]: a row (position, key head) of
+ *                      codes c stands for c * 2^(scale - 127)
+ * Appending takes for each row the smallest power of two with which its
+ * largest magnitude is at most 448 (from 2^-117 to 2^119, scales 10 to 246;
+ * larger values saturate) and rounds each element of it to the nearest code,
+ * ties to the even one: 2^-4 of the value, or 2^-10 of the power for elements
+ * below 2^-6 of it.  A row with an element that is not finite gets the scale
+ * 255 and zeros: it reads as NaN throughout.  Scales below 10 or from 247 to
+ * 254 and the two codes of e4m3's NaN are never written by this library; what
+ * a call makes of such a row is unspecified, and confined to the queries that
+ * see it.  A row's numbers are numbers of bf16 too, so a call over it
+ * can equal its counterpart on pages of those numbers.
+ *
+ * Workspace, lengths, page tables, faults and what an output holds where
+ * nothing is written: as for the calls above.  With PISA_CACHE_PARAMS the
+ * scales are not read (null). */
+typedef enum { PISA_CACHE_PARAMS = 0, PISA_CACHE_E4M3 = 1 } pisa_cache_format;
+typedef struct {
+  uint32_t struct_size; /* sizeof(pisa_cache) */
+  int32_t format;       /* pisa_cache_format */
+  void* k_pages;        /* 16-byte aligned, as the other pools */
+  void* v_pages;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t num_pages;
+  const int32_t* page_table; /* [B, ceil(N / C)] */
+} pisa_cache;
+
+/* Norms of the heads of new tokens, before their rotation: x becomes
+ * x / sqrt(mean(x^2) + eps) * weight over the d elements of a head, in fp32.
+ * The weights are fp32 [d] on the device, 16-byte aligned, shared by the heads;
+ * without one (null) queries or keys are not normed.  1e-30 <= eps < inf. */
+typedef struct {
+  uint32_t struct_size; /* sizeof(pisa_head_norm) */
+  float eps;
+  const float* q_weight; /* nullable */
+  const float* k_weight; /* nullable */
+} pisa_head_norm;
+
+/* pisa_append_paged into a cache of either format, with norms (null: none).
+ * Keys are normed, rotated and then rounded once, to the pages' format; q_out
+ * and k_out take the dtype of p. */
+pisa_status pisa_cache_append(const pisa_params* p, int64_t n, const void* q, const int64_t* q_strides, const void* k,
+                              const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                              const int32_t* seq_lens, const int32_t* new_lens, const pisa_head_norm* norm,
+                              const float* rope, int32_t rot_dim, int32_t interleaved, const pisa_cache* cache,
+                              void* ws, size_t ws_bytes, void* q_out, void* k_out, void* stream);
+
+/* Reads positions back: token i < new_lens[b] of k_out and v_out [B, H_kv, n,
+ * d] (dtype of p, either nullable) is position seq_lens[b] - new_lens[b] + i of
+ * the cache -- the last tokens, or with new_lens = seq_lens all of them.  A
+ * sequence whose lengths do not fit is skipped whole, a token whose page is
+ * outside the pool is left out. */
+pisa_status pisa_cache_read(const pisa_params* p, int64_t n, const pisa_cache* cache, const int32_t* seq_lens,
+                            const int32_t* new_lens, void* ws, size_t ws_bytes, void* k_out, void* v_out,
+                            void* stream);
+
 /* Synchronises `stream`, then copies the workspace status word into
  * *device_code (PISA_DEV_*).  Returns PISA_ERR_DEVICE when it is non-zero. */
 pisa_status pisa_read_device_status(const void* ws, int32_t* device_code,

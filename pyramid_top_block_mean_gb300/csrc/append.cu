@@ -1,6 +1,7 @@
-// append.cu -- new tokens into the paged cache, keys and queries rotated by
-// their positions on the way.
+// append.cu -- new tokens into the paged cache, keys and queries normed head by
+// head and rotated by their positions on the way, and rows read back from it.
 //
+// A head's norm: x -> x / sqrt(sum x^2 / d + eps) * w, in fp32.
 // For a pair (a, b) of dims with angle theta of the token's position:
 //   (a, b) -> (a cos theta - b sin theta, b cos theta + a sin theta)
 // with the pairs (i, i + rot / 2) or (2i, 2i + 1); cosines and sines come from
@@ -9,6 +10,8 @@
 // Bound by HBM: every row is read once and written once.  A thread owns 32
 // bytes of a row -- the two 16-byte vectors that pair up -- so that a rotation
 // needs no exchange and an in-place call reads its pair before it writes it.
+// What a norm or an e4m3 row needs of the whole row (its sum of squares, its
+// largest magnitude) the 4 to 16 threads of a row exchange by shuffles.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -23,6 +26,8 @@ struct AppendArgs {
   const int32_t *seq_lens, *new_lens, *table;
   const float* rope;
   void *k_pages, *v_pages, *q_out, *k_out;
+  uint8_t *k_scales, *v_scales;
+  NormArgs norm;
   int64_t n, nb, num_pages;
   int32_t* status;
   int32_t rot, interleaved;
@@ -64,16 +69,63 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
+// 1 / sqrt(sum / d + eps) for a row of which this thread holds x[0 .. n); the
+// row's threads are those of `mask`, neighbours.
+template <int N>
+__device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, unsigned mask, int d, float eps) {
+  auto sum_of_squares = [&](float by) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) ss = fmaf(x[j] * by, x[j] * by, ss);
+    for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
+    return ss;
+  };
+  const float ss = sum_of_squares(1.0f);
+  if (ss < 3.0e38f) return 1.0f / sqrtf(ss / d + eps);
+  // squares beyond fp32's range: of the elements over 2^80, where eps is nothing
+  return 0x1p-80f / sqrtf(sum_of_squares(0x1p-80f) / d);
+}
+
+// The scale of a row of which this thread holds x[0 .. N): the smallest power
+// of two with which its largest magnitude is at most 448 = 1.75 2^8 (a carry out
+// of the mantissa where it is above 1.75), 255 if one is not finite.
+template <int N>
+__device__ __forceinline__ uint32_t row_scale(const float (&x)[N], uint32_t units, unsigned mask) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+  for (uint32_t o = 1; o < units; o <<= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+  if (top >= 0x7f800000u) return 255u;
+  const int e = (int)((top + 0x1fffffu) >> 23) - 8;  // biased
+  return (uint32_t)min(max(e, 10), 246);
+}
+
+// The E codes of x over the row's power.
+template <int E>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float* x, uint32_t scale) {
+  const float by = scale == 255u ? 0.0f : __uint_as_float((254u - scale) << 23);
+  uint32_t w[E / 4];
+#pragma unroll
+  for (int j = 0; j < E; j += 4) {
+    w[j / 4] = to_codes(x[j] * by, x[j + 1] * by) | to_codes(x[j + 2] * by, x[j + 3] * by) << 16;
+    if (scale == 255u) w[j / 4] = 0;  // (a product of zero and infinity is not)
+  }
+  if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+
 // One thread: one 32-byte unit of R rows (q, k and v heads, every groups-th)
 // of one token, all of whose loads are in flight together; the token's
-// cosines and sines are read once for them.
-template <typename T, int R>
+// cosines and sines are read once for them.  NORM: with norms; Q8: into e4m3
+// pages.
+template <typename T, int R, bool NORM, bool Q8>
 __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a, int64_t b) {
   constexpr int E = Vec<T>::E;
   const uint32_t units = pr.d / (2 * E);
   const uint32_t kv0 = a.q ? pr.Hq : 0, rows = kv0 + 2 * pr.Hkv, groups = (rows + R - 1) / R;
   const uint32_t per = blockDim.x / units;  // (token, group) pairs of a block
   const uint32_t u = threadIdx.x % units;
+  const unsigned mates = ((1u << units) - 1u) << (threadIdx.x % 32 / units * units);  // the row's threads
   const int64_t y = (int64_t)blockIdx.x * per + threadIdx.x / units;
   const int64_t i = y < (int64_t)0xffffffff ? (int64_t)((uint32_t)y / groups) : y / groups;
   const uint32_t r0 = (uint32_t)(y - i * groups);
@@ -123,22 +175,37 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
     const int64_t h = is_q ? r : (is_v ? r - kv0 - pr.Hkv : r - kv0);
     int e0, e1;
     place(turns && !is_v, &e0, &e1);
-    if (turns && !is_v) {
-      float p[2 * E], o[2 * E];
-      Vec<T>::load(w[k][0], p);
-      Vec<T>::load(w[k][1], p + E);
+    const float* weight = !NORM || is_v ? nullptr : (is_q ? a.norm.q : a.norm.k);
+    float o[2 * E];
+    if (Q8 || weight || (turns && !is_v)) {
+      Vec<T>::load(w[k][0], o);
+      Vec<T>::load(w[k][1], o + E);
+    }
+    if (weight) {
+      const float by = row_norm(o, units, mates, pr.d, a.norm.eps);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const float x = a.interleaved ? p[2 * j] : p[j], z = a.interleaved ? p[2 * j + 1] : p[E + j];
-        const float xr = x * cs[j] - z * sn[j], zr = z * cs[j] + x * sn[j];
-        if (a.interleaved) {
-          o[2 * j] = xr;
-          o[2 * j + 1] = zr;
-        } else {
-          o[j] = xr;
-          o[E + j] = zr;
-        }
+      for (int j = 0; j < E; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(weight + e0 + j);
+        const float4 z = *reinterpret_cast<const float4*>(weight + e1 + j);
+        o[j] *= by * x.x; o[j + 1] *= by * x.y; o[j + 2] *= by * x.z; o[j + 3] *= by * x.w;
+        o[E + j] *= by * z.x; o[E + j + 1] *= by * z.y; o[E + j + 2] *= by * z.z; o[E + j + 3] *= by * z.w;
       }
+    }
+    if (turns && !is_v) {
+      auto turn = [&](float& x, float& z, int j) {
+        const float xr = x * cs[j] - z * sn[j], zr = z * cs[j] + x * sn[j];
+        x = xr;
+        z = zr;
+      };
+      if (a.interleaved) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) turn(o[2 * j], o[2 * j + 1], j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) turn(o[j], o[E + j], j);
+      }
+    }
+    if (weight || (turns && !is_v)) {
       w[k][0] = Vec<T>::store(o);
       w[k][1] = Vec<T>::store(o + E);
     }
@@ -147,51 +214,133 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
       *reinterpret_cast<uint4*>(dst + e0) = w[k][0];
       *reinterpret_cast<uint4*>(dst + e1) = w[k][1];
     }
-    if (!is_q && in_pool) {
-      T* dst = (T*)(is_v ? a.v_pages : a.k_pages) + (((int64_t)page * pr.Hkv + h) * pr.C + pos % pr.C) * pr.d;
+    if (is_q) continue;
+    const int64_t row = ((int64_t)page * pr.Hkv + h) * pr.C + pos % pr.C;
+    if constexpr (Q8) {
+      const uint32_t scale = row_scale(o, units, mates);
+      if (in_pool) {
+        uint8_t* dst = (uint8_t*)(is_v ? a.v_pages : a.k_pages) + row * pr.d;
+        store_codes<E>(dst + e0, o, scale);
+        store_codes<E>(dst + e1, o + E, scale);
+        if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = (uint8_t)scale;
+      }
+    } else if (in_pool) {
+      T* dst = (T*)(is_v ? a.v_pages : a.k_pages) + row * pr.d;
       *reinterpret_cast<uint4*>(dst + e0) = w[k][0];
       *reinterpret_cast<uint4*>(dst + e1) = w[k][1];
     }
   }
 }
 
-// Three CTAs on an SM: with four rows a thread the compiler takes 91 registers
-// if it may, which leaves two (a 2 x 4096-token prompt 15.1 us, against 13.2).
-template <typename T, int R>
-__global__ void __launch_bounds__(256, 3) append_kernel(Prob pr, AppendArgs a) {
-  for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_units<T, R>(pr, a, b);
-  // One CTA looks at every length and page for faults and writes the status
-  // word, so that nothing has to clear it before the call.
-  if (blockIdx.x != 0 || blockIdx.y != 0) return;
+// One CTA looks at every length and page for faults and writes the status
+// word, so that nothing has to clear it before the call.
+__device__ __forceinline__ void write_status(const Prob& pr, const int32_t* seq_lens, const int32_t* new_lens,
+                                             const int32_t* table, int64_t n, int64_t nb, int64_t num_pages,
+                                             int32_t* status) {
   int bad_len = 0, bad_page = 0;
   for (int64_t b = threadIdx.x; b < pr.B; b += blockDim.x) {
     int64_t len, cnt;
-    if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt)) {
+    if (!new_span(seq_lens, new_lens, b, n, pr.N, &len, &cnt)) {
       bad_len = 1;
     } else if (cnt > 0) {
       for (int64_t j = (len - cnt) / pr.C; j <= (len - 1) / pr.C; ++j)
-        bad_page |= (uint32_t)a.table[b * a.nb + j] >= a.num_pages;
+        bad_page |= (uint32_t)table[b * nb + j] >= num_pages;
     }
   }
   bad_len = __syncthreads_or(bad_len);
   bad_page = __syncthreads_or(bad_page);
-  if (threadIdx.x == 0) *a.status = bad_len ? PISA_DEV_BAD_SEQ_LEN : (bad_page ? PISA_DEV_BAD_INDEX : PISA_DEV_OK);
+  if (threadIdx.x == 0) *status = bad_len ? PISA_DEV_BAD_SEQ_LEN : (bad_page ? PISA_DEV_BAD_INDEX : PISA_DEV_OK);
+}
+
+// Three CTAs on an SM: with four rows a thread the compiler takes 91 registers
+// if it may, which leaves two (a 2 x 4096-token prompt 15.1 us, against 13.2).
+template <typename T, int R, bool NORM, bool Q8>
+__global__ void __launch_bounds__(256, R == 4 && (NORM || Q8) ? 2 : 3) append_kernel(Prob pr, AppendArgs a) {
+  for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_units<T, R, NORM, Q8>(pr, a, b);
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    write_status(pr, a.seq_lens, a.new_lens, a.table, a.n, a.nb, a.num_pages, a.status);
+}
+
+struct ReadArgs {
+  const void *k_pages, *v_pages;
+  const uint8_t *k_scales, *v_scales;
+  const int32_t *seq_lens, *new_lens, *table;
+  void *k_out, *v_out;
+  int64_t n, nb, num_pages;
+  int32_t* status;
+};
+
+// 16 elements of a row from the pages.
+template <typename T, bool Q8>
+__device__ __forceinline__ void read_unit(const void* pages, const uint8_t* scales, int64_t row, int e0, int d,
+                                          void* out, int64_t to) {
+  constexpr int V = sizeof(T);  // 16-byte vectors of the output
+  uint4* dst = reinterpret_cast<uint4*>((T*)out + to * d + e0);
+  if constexpr (!Q8) {
+    const uint4* src = reinterpret_cast<const uint4*>((const T*)pages + row * d + e0);
+#pragma unroll
+    for (int j = 0; j < V; ++j) dst[j] = src[j];
+  } else {
+    const uint32_t s = scales[row], f = row_factor(s);
+    const uint4 c = *reinterpret_cast<const uint4*>((const uint8_t*)pages + row * d + e0);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = mul_bf16x2(codes_lo(w[j]), f);
+      x[2 * j + 1] = mul_bf16x2(codes_hi(w[j]), f);
+    }
+    if (row_is_large(s)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = mul_bf16x2(x[j], row_factor_large(s));
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (V == 2)
+        dst[j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      else
+        dst[j] = make_uint4(x[2 * j] << 16, x[2 * j] & 0xffff0000u, x[2 * j + 1] << 16, x[2 * j + 1] & 0xffff0000u);
+    }
+  }
+}
+
+// One thread: 16 dims of one head of one token, of its key and its value.
+template <typename T, bool Q8>
+__global__ void __launch_bounds__(256) read_kernel(Prob pr, ReadArgs a) {
+  const uint32_t units = pr.d / 16;
+  const int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int e0 = 16 * (int)(x % units);
+  const int64_t h = x / units / a.n, i = x / units % a.n;
+  for (int64_t b = blockIdx.y; b < pr.B && h < pr.Hkv; b += gridDim.y) {
+    int64_t len, cnt;
+    if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt) || i >= cnt) continue;
+    const int64_t pos = len - cnt + i;
+    const uint32_t page = (uint32_t)a.table[b * a.nb + pos / pr.C];  // a negative entry is past any pool
+    if (page >= a.num_pages) continue;
+    const int64_t row = ((int64_t)page * pr.Hkv + h) * pr.C + pos % pr.C, to = (b * pr.Hkv + h) * a.n + i;
+    if (a.k_out) read_unit<T, Q8>(a.k_pages, a.k_scales, row, e0, pr.d, a.k_out, to);
+    if (a.v_out) read_unit<T, Q8>(a.v_pages, a.v_scales, row, e0, pr.d, a.v_out, to);
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    write_status(pr, a.seq_lens, a.new_lens, a.table, a.n, a.nb, a.num_pages, a.status);
 }
 
 }  // namespace
 
 cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const int64_t* qs, const void* k,
                                 const int64_t* ks, const void* v, const int64_t* vs, const int32_t* seq_lens,
-                                const int32_t* new_lens, const float* rope, int rot_dim, int interleaved,
-                                void* k_pages, void* v_pages, const int32_t* table, int64_t nb, int64_t num_pages,
-                                int32_t* status, void* q_out, void* k_out, cudaStream_t st) {
+                                const int32_t* new_lens, const NormArgs& norm, const float* rope, int rot_dim,
+                                int interleaved, const Pools& pools, int32_t* status, void* q_out, void* k_out,
+                                cudaStream_t st) {
   AppendArgs a{};
   a.q = q; a.k = k; a.v = v;
   for (int i = 0; i < 3; ++i) { a.qs[i] = qs[i]; a.ks[i] = ks[i]; a.vs[i] = vs[i]; }
-  a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = table;
+  a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = pools.table;
   a.rope = rope; a.rot = rot_dim; a.interleaved = interleaved != 0;
-  a.k_pages = k_pages; a.v_pages = v_pages; a.q_out = q_out; a.k_out = k_out;
-  a.n = n; a.nb = nb; a.num_pages = num_pages; a.status = status;
+  a.k_pages = const_cast<void*>(pools.k); a.v_pages = const_cast<void*>(pools.v);
+  a.k_scales = const_cast<uint8_t*>(pools.ks); a.v_scales = const_cast<uint8_t*>(pools.vs);
+  a.norm = norm; a.q_out = q_out; a.k_out = k_out;
+  a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages; a.status = status;
   const int per = 256 / (pr.d / (pr.dtype == PISA_BF16 ? 16 : 8));
   const int64_t rows = (q ? pr.Hq : 0) + 2 * pr.Hkv;
   // Four rows a thread once that fills the GPU: 13.2 us for 2 x 4096 tokens of
@@ -200,8 +349,33 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   const bool many = pr.B * n * rows * (256 / per) >= 4 * 152 * 2048;
   const dim3 grid((unsigned)ceil_div64(n * ceil_div64(rows, many ? 4 : 1), per),
                   (unsigned)std::min<int64_t>(pr.B, 65535));
-  auto kern = pr.dtype == PISA_BF16 ? (many ? append_kernel<__nv_bfloat16, 4> : append_kernel<__nv_bfloat16, 1>)
-                                    : (many ? append_kernel<float, 4> : append_kernel<float, 1>);
+  const bool normed = norm.q || norm.k, in8 = pools.ks != nullptr;
+  auto pick = [&](auto type) {
+    using T = decltype(type);
+    if (normed)
+      return in8 ? (many ? append_kernel<T, 4, true, true> : append_kernel<T, 1, true, true>)
+                 : (many ? append_kernel<T, 4, true, false> : append_kernel<T, 1, true, false>);
+    return in8 ? (many ? append_kernel<T, 4, false, true> : append_kernel<T, 1, false, true>)
+               : (many ? append_kernel<T, 4, false, false> : append_kernel<T, 1, false, false>);
+  };
+  auto kern = pr.dtype == PISA_BF16 ? pick(__nv_bfloat16()) : pick(float());
+  note_launch();
+  kern<<<grid, 256, 0, st>>>(pr, a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_read_paged(const Prob& pr, int64_t n, const Pools& pools, const int32_t* seq_lens,
+                              const int32_t* new_lens, int32_t* status, void* k_out, void* v_out, cudaStream_t st) {
+  ReadArgs a{};
+  a.k_pages = pools.k; a.v_pages = pools.v;
+  a.k_scales = pools.ks; a.v_scales = pools.vs;
+  a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = pools.table;
+  a.k_out = k_out; a.v_out = v_out;
+  a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages; a.status = status;
+  const dim3 grid((unsigned)ceil_div64(n * pr.Hkv * (pr.d / 16), 256), (unsigned)std::min<int64_t>(pr.B, 65535));
+  const bool in8 = pools.ks != nullptr;
+  auto kern = pr.dtype == PISA_BF16 ? (in8 ? read_kernel<__nv_bfloat16, true> : read_kernel<__nv_bfloat16, false>)
+                                    : (in8 ? read_kernel<float, true> : read_kernel<float, false>);
   note_launch();
   kern<<<grid, 256, 0, st>>>(pr, a);
   return cudaGetLastError();

@@ -57,6 +57,40 @@ pisa_status pool_checks(const Prob& pr, const Pyr& s, const void* k_pages, const
   pools->table = page_table;
   pools->num_pages = num_pages;
   pools->nb = s.nb;
+  pools->ks = pools->vs = nullptr;
+  return PISA_OK;
+}
+
+// A cache whose elements have the dtype of the problem.
+pisa_cache own_cache(const void* k_pages, const void* v_pages, int64_t num_pages, const int32_t* page_table) {
+  return {sizeof(pisa_cache), PISA_CACHE_PARAMS, const_cast<void*>(k_pages), const_cast<void*>(v_pages), nullptr,
+          nullptr, num_pages, page_table};
+}
+
+pisa_status cache_checks(const Prob& pr, const Pyr& s, const pisa_cache* c, const int32_t* seq_lens, const void* ws,
+                         Pools* pools) {
+  if (!c || c->struct_size < sizeof(pisa_cache)) return PISA_ERR_INVALID_ARG;
+  const bool in8 = c->format == PISA_CACHE_E4M3;
+  if (!in8 && c->format != PISA_CACHE_PARAMS) return PISA_ERR_UNSUPPORTED;
+  if (in8 && (!c->k_scales || !c->v_scales)) return PISA_ERR_INVALID_ARG;
+  const pisa_status rc =
+      pool_checks(pr, s, c->k_pages, c->v_pages, c->num_pages, c->page_table, seq_lens, ws, pools);
+  if (rc != PISA_OK || !in8) return rc;
+  if (!aligned16(c->k_scales) || !aligned16(c->v_scales)) return PISA_ERR_MISALIGNED;
+  pools->ks = c->k_scales;
+  pools->vs = c->v_scales;
+  return PISA_OK;
+}
+
+pisa_status norm_checks(const pisa_head_norm* norm, NormArgs* a) {
+  *a = NormArgs{};
+  if (!norm) return PISA_OK;
+  if (norm->struct_size < sizeof(pisa_head_norm)) return PISA_ERR_INVALID_ARG;
+  if (!(norm->eps >= 1e-30f) || isinf(norm->eps)) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(norm->q_weight) || !aligned16(norm->k_weight)) return PISA_ERR_MISALIGNED;
+  a->q = norm->q_weight;
+  a->k = norm->k_weight;
+  a->eps = norm->eps;
   return PISA_OK;
 }
 
@@ -123,13 +157,24 @@ pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, co
                               int32_t interleaved, void* k_pages, void* v_pages, int64_t num_pages,
                               const int32_t* page_table, void* ws, size_t ws_bytes, void* q_out, void* k_out,
                               void* stream) {
-  Prob pr; Pyr s; bool empty = false; Pools pools;
+  const pisa_cache c = own_cache(k_pages, v_pages, num_pages, page_table);
+  return pisa_cache_append(p, n, q, q_strides, k, k_strides, v, v_strides, seq_lens, new_lens, nullptr, rope, rot_dim,
+                           interleaved, &c, ws, ws_bytes, q_out, k_out, stream);
+}
+
+pisa_status pisa_cache_append(const pisa_params* p, int64_t n, const void* q, const int64_t* q_strides, const void* k,
+                              const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                              const int32_t* seq_lens, const int32_t* new_lens, const pisa_head_norm* norm,
+                              const float* rope, int32_t rot_dim, int32_t interleaved, const pisa_cache* cache,
+                              void* ws, size_t ws_bytes, void* q_out, void* k_out, void* stream) {
+  Prob pr; Pyr s; bool empty = false; Pools pools; NormArgs na;
   pisa_status rc = common_checks(p, n, &pr, &s, &empty);
   if (rc != PISA_OK || empty) return rc;
   if (rot_dim < 0 || rot_dim > pr.d || (rope != nullptr) != (rot_dim > 0)) return PISA_ERR_INVALID_ARG;
   if (rot_dim % 16 != 0) return PISA_ERR_UNSUPPORTED;
   if (!k || !v || (q != nullptr) != (q_out != nullptr)) return PISA_ERR_INVALID_ARG;
-  rc = pool_checks(pr, s, k_pages, v_pages, num_pages, page_table, seq_lens, ws, &pools);
+  rc = norm_checks(norm, &na);
+  if (rc == PISA_OK) rc = cache_checks(pr, s, cache, seq_lens, ws, &pools);
   if (rc != PISA_OK) return rc;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
       !aligned16(rope) || !aligned4(new_lens))
@@ -141,10 +186,22 @@ pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, co
   if (rc == PISA_OK) rc = stride_checks(v_strides, pr.B, pr.Hkv, n, pr.d, per16, vs);
   if (rc != PISA_OK) return rc;
   if (ws_bytes < pisa_paged_workspace_bytes(p, n)) return PISA_ERR_WORKSPACE;
-  cudaStream_t st = (cudaStream_t)stream;
-  return cuda_status(launch_append_paged(pr, n, q, qs, k, ks, v, vs, seq_lens, new_lens, rope, rot_dim, interleaved,
-                                         k_pages, v_pages, page_table, s.nb, num_pages, (int32_t*)ws, q_out, k_out,
-                                         st));
+  return cuda_status(launch_append_paged(pr, n, q, qs, k, ks, v, vs, seq_lens, new_lens, na, rope, rot_dim,
+                                         interleaved, pools, (int32_t*)ws, q_out, k_out, (cudaStream_t)stream));
+}
+
+pisa_status pisa_cache_read(const pisa_params* p, int64_t n, const pisa_cache* cache, const int32_t* seq_lens,
+                            const int32_t* new_lens, void* ws, size_t ws_bytes, void* k_out, void* v_out,
+                            void* stream) {
+  Prob pr; Pyr s; bool empty = false; Pools pools;
+  pisa_status rc = common_checks(p, n, &pr, &s, &empty);
+  if (rc != PISA_OK || empty) return rc;
+  rc = cache_checks(pr, s, cache, seq_lens, ws, &pools);
+  if (rc != PISA_OK) return rc;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(new_lens)) return PISA_ERR_MISALIGNED;
+  if (ws_bytes < 256) return PISA_ERR_WORKSPACE;  // the status word's
+  return cuda_status(launch_read_paged(pr, n, pools, seq_lens, new_lens, (int32_t*)ws, k_out, v_out,
+                                       (cudaStream_t)stream));
 }
 
 pisa_status pisa_dense_decode_paged(const pisa_params* p, const pisa_mask* mask, const void* q, const void* k_pages,

@@ -32,6 +32,7 @@ SCORER_LSE, SCORER_MEAN, SCORER_MEAN_VAR = 0, 1, 2
 SUMMARIES_ALL, SUMMARIES_PREFIX = 0, 1
 MODE_PREFILL, MODE_DECODE, MODE_FLAT, MODE_ATTEND = 0, 1, 2, 3
 DEV_OK, DEV_BAD_SEQ_LEN, DEV_TIMEOUT, DEV_BAD_INDEX = 0, 1, 2, 3
+CACHE_PARAMS, CACHE_E4M3 = 0, 1
 
 EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pisa_pyramid_nodes",
             "pisa_pyramid_bytes", "pisa_workspace_bytes", "pisa_build_pyramid", "pisa_select_prefill",
@@ -40,7 +41,7 @@ EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pi
             "pisa_attend_prefill", "pisa_build_pyramid_paged", "pisa_select_decode_paged", "pisa_attend_decode",
             "pisa_read_static_status", "pisa_test_inject_leaf_timeout", "pisa_append_paged",
             "pisa_dense_decode_paged", "pisa_attend_decode_paged", "pisa_dense_prefill_paged",
-            "pisa_paged_workspace_bytes"]
+            "pisa_paged_workspace_bytes", "pisa_cache_append", "pisa_cache_read"]
 
 
 class Params(ctypes.Structure):
@@ -57,8 +58,20 @@ class Mask(ctypes.Structure):
                 ("slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("format", ctypes.c_int32), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_table", ctypes.c_void_p)]
+
+
+class HeadNorm(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
 _P = ctypes.POINTER(Params)
 _M = ctypes.POINTER(Mask)
+_C = ctypes.POINTER(Cache)
 _strides_t = ctypes.c_int64 * 9
 _vp = ctypes.c_void_p
 _lib.pisa_abi_version.restype = ctypes.c_int
@@ -106,6 +119,12 @@ _lib.pisa_attend_decode_paged.restype = ctypes.c_int
 _lib.pisa_dense_prefill_paged.argtypes = [_P, _M, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, _vp,
                                           ctypes.c_size_t, _vp, _vp]
 _lib.pisa_dense_prefill_paged.restype = ctypes.c_int
+_lib.pisa_cache_append.argtypes = [_P, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   ctypes.POINTER(HeadNorm), _vp, ctypes.c_int32, ctypes.c_int32, _C, _vp,
+                                   ctypes.c_size_t, _vp, _vp, _vp]
+_lib.pisa_cache_append.restype = ctypes.c_int
+_lib.pisa_cache_read.argtypes = [_P, ctypes.c_int64, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
+_lib.pisa_cache_read.restype = ctypes.c_int
 _lib.pisa_paged_workspace_bytes.argtypes = [_P, ctypes.c_int64]
 _lib.pisa_paged_workspace_bytes.restype = ctypes.c_size_t
 _lib.pisa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32), _vp]
@@ -316,6 +335,30 @@ def _want_cache(p: Params, k_pages, v_pages, page_table, seq_lens, dtype, index:
             _want(seq_lens, "seq_lens", (B,), torch.int32, index))
 
 
+def _want_pages(p: Params, k_pages, v_pages, page_table, seq_lens, scales, dtype, index: int):
+    """(Cache, seq_lens) of pages in the model's dtype (scales None) or in e4m3."""
+    num = k_pages.shape[0]
+    shape = (num, p.H_kv, p.C, p.d)
+    ks = vs = None
+    if scales is not None:
+        dtype = torch.float8_e4m3fn
+        ks = _want(scales, "scales", (2, num, p.H_kv, p.C), torch.uint8, index)
+        vs = ks + num * p.H_kv * p.C
+    B = p.B
+    return (Cache(ctypes.sizeof(Cache), CACHE_PARAMS if scales is None else CACHE_E4M3,
+                  _want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index),
+                  ks, vs, num, _want(page_table, "page_table", (B, -(-p.N // 64)), torch.int32, index)),
+            _want(seq_lens, "seq_lens", (B,), torch.int32, index))
+
+
+def _head_norm(p: Params, q_norm, k_norm, eps: float, index: int):
+    if q_norm is None and k_norm is None:
+        return None
+    return HeadNorm(ctypes.sizeof(HeadNorm), eps,
+                    None if q_norm is None else _want(q_norm, "q_norm", (p.d,), torch.float32, index),
+                    None if k_norm is None else _want(k_norm, "k_norm", (p.d,), torch.float32, index))
+
+
 def _want_space(ws, index: int):
     """Address and bytes of a workspace."""
     if ws.get_device() != index or not ws.is_contiguous():
@@ -374,7 +417,7 @@ def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, index: int):
 # callers have looked at already: the functions below at each call,
 # PagedAttention when it makes them.
 def _append(p, k, v, k_pages, v_pages, page_table, seq_lens, space, rope, rot, interleaved, q, q_out, k_out, new_lens,
-            stream, check) -> int:
+            scales, norm, stream, check) -> int:
     index, dt = k.get_device(), _dtype(p)
     n = k.shape[2]
     kv_shape = (p.B, p.H_kv, n, p.d)
@@ -383,12 +426,36 @@ def _append(p, k, v, k_pages, v_pages, page_table, seq_lens, space, rope, rot, i
     qp, qs = (None, ks) if q is None else _want_rows(q, "q", (p.B, p.H_q, n, p.d), dt, index)
     strides = _strides_t(*qs[:3], *ks[:3], *vs[:3])
     at = ctypes.addressof(strides)
-    kpp, vpp, num, table, lens = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
-    return _launch(index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, at, kp,
-                   at + 24, vp, at + 48, lens,
-                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), rope, rot,
-                   interleaved, kpp, vpp, num, table, *space, q_out,
-                   None if k_out is None else _want(k_out, "k_out", kv_shape, dt, index))
+    new = None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index)
+    if k_out is not None:
+        k_out = _want(k_out, "k_out", kv_shape, dt, index)
+    if scales is None and norm is None:
+        kpp, vpp, num, table, lens = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+        return _launch(index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, at,
+                       kp, at + 24, vp, at + 48, lens, new, rope, rot, interleaved, kpp, vpp, num, table, *space,
+                       q_out, k_out)
+    cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+    return _launch(index, stream, "pisa_cache_append", check, _lib.pisa_cache_append, ctypes.byref(p), n, qp, at, kp,
+                   at + 24, vp, at + 48, lens, new, norm, rope, rot, interleaved, ctypes.byref(cache), *space, q_out,
+                   k_out)
+
+
+def _either(k_out, v_out):
+    if k_out is None and v_out is None:
+        raise ValueError("neither k_out nor v_out")
+    return v_out if k_out is None else k_out
+
+
+def _read(p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, space, new_lens, scales, stream, check) -> int:
+    one = _either(k_out, v_out)
+    index, dt, n = one.get_device(), _dtype(p), one.shape[2]
+    shape = (p.B, p.H_kv, n, p.d)
+    cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+    return _launch(index, stream, "pisa_cache_read", check, _lib.pisa_cache_read, ctypes.byref(p), n,
+                   ctypes.byref(cache), lens,
+                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space,
+                   None if k_out is None else _want(k_out, "k_out", shape, dt, index),
+                   None if v_out is None else _want(v_out, "v_out", shape, dt, index))
 
 
 def _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, space, out, mask, stream, check) -> int:
@@ -414,17 +481,40 @@ def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space
                    None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space, out)
 
 
+def quantized_pages(p: Params, num_pages: int, device="cuda"):
+    """An 8-bit cache of num_pages pages: (k_pages, v_pages, scales), e4m3
+    [num_pages, H_kv, C, d] twice and uint8 [2, num_pages, H_kv, C], all zero
+    numbers.  The calls below take such pages with their scales."""
+    shape = (num_pages, p.H_kv, p.C, p.d)
+    k_pages = torch.zeros(shape, dtype=torch.float8_e4m3fn, device=device)
+    v_pages = torch.zeros(shape, dtype=torch.float8_e4m3fn, device=device)
+    return k_pages, v_pages, torch.full((2,) + shape[:3], 127, dtype=torch.uint8, device=device)
+
+
 def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, rope=None, interleaved: bool = False,
-                 q=None, q_out=None, k_out=None, new_lens=None, stream=None, check: bool = True) -> int:
+                 q=None, q_out=None, k_out=None, new_lens=None, stream=None, check: bool = True, scales=None,
+                 q_norm=None, k_norm=None, norm_eps: float = 1e-6) -> int:
     """k, v [B, H_kv, n, d] and q [B, H_q, n, d], strided views allowed; rope
-    fp32 [N, rot_dim] (cosines, then sines); seq_lens counts the new tokens."""
+    fp32 [N, rot_dim] (cosines, then sines); seq_lens counts the new tokens.
+    scales: of e4m3 pages (quantized_pages); q_norm, k_norm: fp32 [d], weights
+    of the heads' norms, applied before the rotation."""
     index, rot = k.get_device(), 0 if rope is None else rope.shape[-1]
     if q_out is not None:
         q_out = _want(q_out, "q_out", (p.B, p.H_q, k.shape[2], p.d), _dtype(p), index)
     if rope is not None:
         rope = _want(rope, "rope", (p.N, rot), torch.float32, index)
     return _append(p, k, v, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), rope, rot, interleaved, q,
-                   q_out, k_out, new_lens, stream, check)
+                   q_out, k_out, new_lens, scales, _head_norm(p, q_norm, k_norm, norm_eps, index), stream, check)
+
+
+def read_paged(p: Params, k_out, v_out, k_pages, v_pages, page_table, seq_lens, ws, new_lens=None, scales=None,
+               stream=None, check: bool = True) -> int:
+    """k_out, v_out [B, H_kv, n, d] (either may be None): the last new_lens[b]
+    (None: n) positions of each sequence, from pages in the model's dtype or,
+    with scales, in e4m3."""
+    index = _either(k_out, v_out).get_device()
+    return _read(p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), new_lens, scales,
+                 stream, check)
 
 
 def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out,
@@ -546,10 +636,14 @@ class PagedAttention:
     kind (a call of fewer tokens uses its front).  Rows behind a sequence's new
     tokens are not written: they hold zeros or what an earlier call left there.
     Calls may run on any stream, one after the other.
-    rope: fp32 [N, rot_dim] as append_paged takes it, or None."""
+    rope: fp32 [N, rot_dim] as append_paged takes it, or None; q_norm, k_norm:
+    fp32 [d], weights of the heads' norms before the rotation, or None.  Pages
+    are tensors of the model's dtype or, with their scales, of 8 bits
+    (quantized_pages)."""
 
     def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
-                 device="cuda"):
+                 device="cuda", q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                 norm_eps: float = 1e-6):
         p = Params.from_buffer_copy(p)  # the buffers below are made for these numbers
         self.p, self.n, self.rope, self.interleaved = p, n, rope, interleaved
         self.device = torch.device(device)
@@ -563,6 +657,8 @@ class PagedAttention:
         self._space = _want_space(self.ws, self._index)
         self._rot = 0 if rope is None else rope.shape[-1]
         self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
+        self.q_norm, self.k_norm = q_norm, k_norm
+        self._norm = _head_norm(p, q_norm, k_norm, norm_eps, self._index)
         one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
         rows = p.B * p.H_q * p.d
         flat = torch.zeros(rows * (2 + 2 * n), dtype=_dtype(p), device=self.device)
@@ -587,14 +683,23 @@ class PagedAttention:
             return out
         return out.view(-1)[:like.numel()].view(like.shape)
 
-    def append(self, q, k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_out=None, stream=None):
-        """Rotates and appends k and v; returns the rotated queries [B, H_q, n, d] (None when q is None)."""
+    def append(self, q, k, v, k_pages, v_pages, page_table, seq_lens, new_lens=None, k_out=None, stream=None,
+               scales=None):
+        """Norms, rotates and appends k and v; returns the queries so treated [B, H_q, n, d] (None when q is None)."""
         if q is None:
             self._fits(k, k.dim() == 4 and k.shape[2] <= self.n)
         q_out = None if q is None else self._buffer("q", q)
         _append(self.p, k, v, k_pages, v_pages, page_table, seq_lens, self._space, self._rope, self._rot,
-                self.interleaved, q, None if q is None else q_out.data_ptr(), k_out, new_lens, stream, True)
+                self.interleaved, q, None if q is None else q_out.data_ptr(), k_out, new_lens, scales, self._norm,
+                stream, True)
         return None if q is None else q_out
+
+    def read(self, k_out, v_out, k_pages, v_pages, page_table, seq_lens, new_lens=None, stream=None, scales=None):
+        """Reads the last new_lens[b] (None: n) positions of each sequence back into the caller's k_out and v_out
+        [B, H_kv, n, d], for any n up to the capacity (either may be None)."""
+        self._fits(_either(k_out, v_out), True)
+        _read(self.p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, self._space, new_lens, scales, stream,
+              True)
 
     def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None):
         out = self._buffer("dense", q)

@@ -1,0 +1,112 @@
+"""The entry points of the 8-bit cache and of normed appending refuse bad
+arguments on the host, before any launch (fake addresses: none of these calls
+reaches a GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def pisa():
+    from pyramid_top_block_mean_gb300 import build
+    build.build()
+    from pyramid_top_block_mean_gb300 import pisa as m
+    return m
+
+
+A, MIS, ODD, BIG = 0x10000, 0x10008, 0x10002, 1 << 40
+FIELDS = ("k_pages", "v_pages", "k_scales", "v_scales")
+
+
+def cache(pisa, **kw):
+    c = pisa.Cache(ctypes.sizeof(pisa.Cache), pisa.CACHE_E4M3, A, A, A, A, 10, A)
+    for name, value in kw.items():
+        setattr(c, name, value)
+    return ctypes.byref(c)
+
+
+def norm(pisa, **kw):
+    c = pisa.HeadNorm(ctypes.sizeof(pisa.HeadNorm), 1e-6, A, A)
+    for name, value in kw.items():
+        setattr(c, name, value)
+    return ctypes.byref(c)
+
+
+def calls(pisa, p):
+    """name -> call(cache, **changes) of every entry point that takes a cache."""
+    L, P = pisa.lib(), ctypes.byref(p)
+
+    def append(c, lens=A, ws=A, size=BIG, n=4, norm=None, k=A):
+        return L.pisa_cache_append(P, n, A, None, k, None, A, None, lens, A, norm, A, 64, 0, c, ws, size, A, A, None)
+
+    def read(c, lens=A, ws=A, size=BIG, n=4, out=A, new=A):
+        return L.pisa_cache_read(P, n, c, lens, new, ws, size, out, A, None)
+
+    return dict(append=append, read=read)
+
+
+def test_caches_are_checked(pisa):
+    p = pisa.make_params(2, 4096, 16, 4, 128, K=8)
+    for name, call in calls(pisa, p).items():
+        assert call(None) == -1, name
+        assert call(cache(pisa, struct_size=8)) == -1, name
+        assert call(cache(pisa, format=2)) == -2 and call(cache(pisa, format=-1)) == -2, name
+        assert call(cache(pisa, num_pages=0)) == -1 and call(cache(pisa, num_pages=1 << 31)) == -2, name
+        assert call(cache(pisa, page_table=None)) == -1 and call(cache(pisa, page_table=ODD)) == -3, name
+        for f in FIELDS:
+            assert call(cache(pisa, **{f: None})) == -1, (name, f)
+            assert call(cache(pisa, **{f: MIS})) == -3, (name, f)
+        c = cache(pisa)
+        assert call(c, lens=None) == -1 and call(c, lens=ODD) == -3, name
+        assert call(c, ws=None) == -1 and call(c, ws=MIS) == -3 and call(c, size=16) == -4, name
+
+
+def test_scales_are_not_asked_of_pages_in_the_models_type(pisa):
+    p = pisa.make_params(2, 4096, 16, 4, 128, K=8)
+    own = dict(format=pisa.CACHE_PARAMS, k_scales=None, v_scales=None)
+    for name, call in calls(pisa, p).items():
+        assert call(cache(pisa, **own), size=16) == -4, name  # nothing else is missing
+
+
+def test_norms_are_checked(pisa):
+    p = pisa.make_params(2, 4096, 16, 4, 128, K=8)
+    append = calls(pisa, p)["append"]
+    for kw, code in ((dict(struct_size=4), -1), (dict(eps=0.0), -1), (dict(eps=-1.0), -1), (dict(eps=1e-31), -1),
+                     (dict(eps=float("inf")), -1), (dict(eps=float("nan")), -1), (dict(q_weight=MIS), -3),
+                     (dict(k_weight=MIS), -3)):
+        assert append(cache(pisa), norm=norm(pisa, **kw)) == code, kw
+    assert append(cache(pisa), norm=norm(pisa), size=16) == -4
+
+
+def test_read_refusals(pisa):
+    p = pisa.make_params(2, 4096, 16, 4, 128, K=8)
+    read = calls(pisa, p)["read"]
+    c = cache(pisa)
+    assert read(c, n=-1) == -1 and read(c, n=4097) == -1 and read(c, out=MIS) == -3 and read(c, new=ODD) == -3
+    assert read(c, size=255) == -4 and read(None, n=0) == 0
+    assert calls(pisa, pisa.make_params(2, 4096, 16, 4, 96))["read"](c) == -2
+
+
+def test_binding_checks_8_bit_pages(pisa):
+    p = pisa.make_params(2, 128, 4, 2, 64)
+    k = torch.zeros(2, 2, 3, 64, dtype=torch.bfloat16)
+    kp, vp, scales = pisa.quantized_pages(p, 4, device="cpu")
+    assert kp.shape == vp.shape == (4, 2, 64, 64) and kp.dtype is torch.float8_e4m3fn and scales.shape == (2, 4, 2, 64)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    layer = pisa.PagedAttention(p, n=3, device="cpu")
+    for call in (lambda **kw: layer.append(None, k, k, **kw), lambda **kw: layer.read(k, k, **kw)):
+        for bad in (dict(k_pages=kp.view(torch.uint8)), dict(v_pages=vp.float()), dict(scales=scales[:1]),
+                    dict(scales=scales.float()), dict(scales=scales[:, :3]), dict(scales=None), dict(k_pages=kp[:, :1])):
+            a = dict(k_pages=kp, v_pages=vp, page_table=table, seq_lens=lens, scales=scales) | bad
+            with pytest.raises(ValueError, match="expected contiguous"):
+                call(**a)
+        with pytest.raises(ValueError, match="expected CUDA tensors"):
+            call(k_pages=kp, v_pages=vp, page_table=table, seq_lens=lens, scales=scales)
+    with pytest.raises(ValueError):
+        layer.read(None, None, kp, vp, table, lens, scales=scales)
+    for bad in (torch.ones(32), torch.ones(64).double()):
+        with pytest.raises(ValueError, match="norm"):
+            pisa.PagedAttention(p, n=3, device="cpu", q_norm=bad)
+        with pytest.raises(ValueError, match="norm"):
+            pisa.PagedAttention(p, n=3, device="cpu", k_norm=bad)
