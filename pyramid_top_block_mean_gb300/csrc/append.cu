@@ -69,21 +69,43 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// 1 / sqrt(sum / d + eps) for a row of which this thread holds x[0 .. n); the
-// row's threads are those of `mask`, neighbours.
+// Packed pairs of fp32 values, subnormals kept.
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 1 / sqrt(sum / d + eps) for a row of which this thread holds x[0 .. N); the
+// row's threads are those of `mask`, neighbours.  1 / d is exact.
 template <int N>
-__device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, unsigned mask, int d, float eps) {
-  auto sum_of_squares = [&](float by) {
-    float ss = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) ss = fmaf(x[j] * by, x[j] * by, ss);
+__device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d,
+                                          float eps) {
+  auto row_sum = [&](float ss) {
     for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
     return ss;
   };
-  const float ss = sum_of_squares(1.0f);
-  if (ss < 3.0e38f) return 1.0f / sqrtf(ss / d + eps);
+  uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const uint64_t v = ptx::pack2(x[j], x[j + 1]);
+    part[(j >> 1) & 1] = fma_pair(v, v, part[(j >> 1) & 1]);
+  }
+  float p0, p1, p2, p3;
+  ptx::unpack2(part[0], p0, p1);
+  ptx::unpack2(part[1], p2, p3);
+  const float ss = row_sum((p0 + p1) + (p2 + p3));
+  if (ss < 3.0e38f) return rsqrtf(fmaf(ss, one_over_d, eps));
   // squares beyond fp32's range: of the elements over 2^80, where eps is nothing
-  return 0x1p-80f / sqrtf(sum_of_squares(0x1p-80f) / d);
+  float far = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) far = fmaf(x[j] * 0x1p-80f, x[j] * 0x1p-80f, far);
+  return 0x1p-80f * rsqrtf(row_sum(far) * one_over_d);
 }
 
 // The scale of a row of which this thread holds x[0 .. N): the smallest power
@@ -182,13 +204,13 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
       Vec<T>::load(w[k][1], o + E);
     }
     if (weight) {
-      const float by = row_norm(o, units, mates, pr.d, a.norm.eps);
+      const float by = row_norm(o, units, mates, a.norm.one_over_d, a.norm.eps);
+      const uint64_t by2 = ptx::pack2(by, by);
 #pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(weight + e0 + j);
-        const float4 z = *reinterpret_cast<const float4*>(weight + e1 + j);
-        o[j] *= by * x.x; o[j + 1] *= by * x.y; o[j + 2] *= by * x.z; o[j + 3] *= by * x.w;
-        o[E + j] *= by * z.x; o[E + j + 1] *= by * z.y; o[E + j + 2] *= by * z.z; o[E + j + 3] *= by * z.w;
+      for (int j = 0; j < 2 * E; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(weight + (j < E ? e0 + j : e1 + j - E));
+        ptx::unpack2(mul_pair(ptx::pack2(o[j], o[j + 1]), mul_pair(by2, ptx::pack2(x.x, x.y))), o[j], o[j + 1]);
+        ptx::unpack2(mul_pair(ptx::pack2(o[j + 2], o[j + 3]), mul_pair(by2, ptx::pack2(x.z, x.w))), o[j + 2], o[j + 3]);
       }
     }
     if (turns && !is_v) {
@@ -200,6 +222,15 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
       if (a.interleaved) {
 #pragma unroll
         for (int j = 0; j < E; ++j) turn(o[2 * j], o[2 * j + 1], j);
+      } else if (NORM || Q8) {  // two pairs at a time
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+          const uint64_t x = ptx::pack2(o[j], o[j + 1]), z = ptx::pack2(o[E + j], o[E + j + 1]);
+          const uint64_t c = ptx::pack2(cs[j], cs[j + 1]), sp = ptx::pack2(sn[j], sn[j + 1]);
+          const uint64_t sm = ptx::pack2(-sn[j], -sn[j + 1]);
+          ptx::unpack2(fma_pair(x, c, mul_pair(z, sm)), o[j], o[j + 1]);
+          ptx::unpack2(fma_pair(z, c, mul_pair(x, sp)), o[E + j], o[E + j + 1]);
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j) turn(o[j], o[E + j], j);
@@ -339,7 +370,7 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   a.rope = rope; a.rot = rot_dim; a.interleaved = interleaved != 0;
   a.k_pages = const_cast<void*>(pools.k); a.v_pages = const_cast<void*>(pools.v);
   a.k_scales = const_cast<uint8_t*>(pools.ks); a.v_scales = const_cast<uint8_t*>(pools.vs);
-  a.norm = norm; a.q_out = q_out; a.k_out = k_out;
+  a.norm = norm; a.norm.one_over_d = 1.0f / (float)pr.d; a.q_out = q_out; a.k_out = k_out;
   a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages; a.status = status;
   const int per = 256 / (pr.d / (pr.dtype == PISA_BF16 ? 16 : 8));
   const int64_t rows = (q ? pr.Hq : 0) + 2 * pr.Hkv;

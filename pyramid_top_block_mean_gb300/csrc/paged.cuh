@@ -26,7 +26,7 @@ struct Pools {
 // What appending does besides moving rows: norms (weights null: none), angles.
 struct NormArgs {
   const float *q, *k;
-  float eps;
+  float eps, one_over_d;
 };
 
 // e4m3 rows.  A code c of a row with the scale s stands for c 2^(s - 127): the

@@ -207,6 +207,13 @@ pisa_status pisa_cache_read(const pisa_params* p, int64_t n, const pisa_cache* c
 pisa_status pisa_dense_decode_paged(const pisa_params* p, const pisa_mask* mask, const void* q, const void* k_pages,
                                     const void* v_pages, int64_t num_pages, const int32_t* page_table,
                                     const int32_t* seq_lens, void* ws, size_t ws_bytes, void* out, void* stream) {
+  const pisa_cache c = own_cache(k_pages, v_pages, num_pages, page_table);
+  return pisa_cache_dense_decode(p, mask, q, &c, seq_lens, ws, ws_bytes, out, stream);
+}
+
+pisa_status pisa_cache_dense_decode(const pisa_params* p, const pisa_mask* mask, const void* q,
+                                    const pisa_cache* cache, const int32_t* seq_lens, void* ws, size_t ws_bytes,
+                                    void* out, void* stream) {
   Prob pr; Pyr s; bool empty = false; Pools pools; MaskArgs m;
   pisa_status rc = common_checks(p, 1, &pr, &s, &empty);
   if (rc != PISA_OK || empty) return rc;
@@ -215,7 +222,7 @@ pisa_status pisa_dense_decode_paged(const pisa_params* p, const pisa_mask* mask,
   if (rc != PISA_OK) return rc;
   m.prefix_lens = nullptr;  // the last token sees every key already
   if (!q || !out) return PISA_ERR_INVALID_ARG;
-  rc = pool_checks(pr, s, k_pages, v_pages, num_pages, page_table, seq_lens, ws, &pools);
+  rc = cache_checks(pr, s, cache, seq_lens, ws, &pools);
   if (rc != PISA_OK) return rc;
   if (!aligned16(q) || !aligned16(out)) return PISA_ERR_MISALIGNED;
   if (ws_bytes < paged_decode_ws_bytes(pr)) return PISA_ERR_WORKSPACE;
@@ -225,12 +232,19 @@ pisa_status pisa_dense_decode_paged(const pisa_params* p, const pisa_mask* mask,
 pisa_status pisa_attend_decode_paged(const pisa_params* p, const void* q, const void* k_pages, const void* v_pages,
                                      int64_t num_pages, const int32_t* page_table, const int32_t* seq_lens,
                                      const int32_t* idx, void* ws, size_t ws_bytes, void* out, void* stream) {
+  const pisa_cache c = own_cache(k_pages, v_pages, num_pages, page_table);
+  return pisa_cache_attend_decode(p, q, &c, seq_lens, idx, ws, ws_bytes, out, stream);
+}
+
+pisa_status pisa_cache_attend_decode(const pisa_params* p, const void* q, const pisa_cache* cache,
+                                     const int32_t* seq_lens, const int32_t* idx, void* ws, size_t ws_bytes,
+                                     void* out, void* stream) {
   Prob pr; Pyr s; bool empty = false; Pools pools;
   pisa_status rc = common_checks(p, 1, &pr, &s, &empty);
   if (rc != PISA_OK || empty) return rc;
   if (pr.dtype != PISA_BF16) return PISA_ERR_UNSUPPORTED;  // built for bf16 inputs
   if (!q || !out || !idx) return PISA_ERR_INVALID_ARG;
-  rc = pool_checks(pr, s, k_pages, v_pages, num_pages, page_table, seq_lens, ws, &pools);
+  rc = cache_checks(pr, s, cache, seq_lens, ws, &pools);
   if (rc != PISA_OK) return rc;
   if (!aligned16(q) || !aligned16(out) || !aligned4(idx)) return PISA_ERR_MISALIGNED;
   if (ws_bytes < paged_decode_ws_bytes(pr)) return PISA_ERR_WORKSPACE;

@@ -37,20 +37,23 @@ namespace pisa {
 
 namespace {
 
-constexpr int kWarps = 8;               // consumer warps, 16 keys each: two groups, which take turns at the pages
-constexpr int kCons = 32 * kWarps;      // consumer threads
 constexpr int kMerge = 96;              // threads that merge a part while the consumers are at the next one
-constexpr int kThreads = kCons + 32 + kMerge;  // and the producer warp
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
 
-template <int D, int G>
+// Q8: pages of e4m3.
+template <int D, int G, bool Q8>
 struct Shape {
-  // as many as fit beside the merge buffer; even, so that a stage always goes
-  // to the same group, which then sees each of its phases
-  static constexpr int kStages = D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);
-  static_assert(kStages % 2 == 0, "a group must see every phase of its stages");
-  static constexpr uint32_t kTile = kPage * D * 2;  // bytes of a page's keys
+  static constexpr int kGroups = Q8 ? 3 : 2;       // of consumer warps, which take turns at the pages
+  static constexpr int kWarps = 4 * kGroups;       // 16 keys of a page each
+  static constexpr int kCons = 32 * kWarps;        // consumer threads
+  static constexpr int kThreads = kCons + 32 + kMerge;  // and the producer warp
+  // as many as fit beside the merge buffer; a multiple of the groups, so that
+  // a stage always goes to the same one, which then sees each of its phases
+  static constexpr int kStages = Q8 ? (D == 128 ? 9 : 18) : D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);
+  static_assert(kStages % kGroups == 0, "a group must see every phase of its stages");
+  static constexpr uint32_t kTile = kPage * D * (Q8 ? 1 : 2);  // bytes of a page's keys
+  static constexpr uint32_t kPageBytes = 2 * kTile + (Q8 ? 2 * kPage : 0);  // and values, and scales
 };
 
 // What a stage holds and what to do with it.
@@ -73,17 +76,26 @@ struct Join {
   static constexpr int kStep = kLanes > 1 ? kCols : kMerge;
 };
 
-template <int D, int G>
+template <int D, int G, bool Q8>
 struct Smem {
-  uint8_t kv[Shape<D, G>::kStages][2][Shape<D, G>::kTile];
-  uint16_t q[Shape<D, G>::kStages][G * D];
-  float o[kWarps][G * D];                  // a part's merge
-  float m[kWarps][8], l[kWarps][8];
+  using S = Shape<D, G, Q8>;
+  uint8_t kv[S::kStages][2][S::kTile];
+  uint16_t q[S::kStages][G * D];
+  uint8_t scale[Q8 ? S::kStages : 1][2][Q8 ? kPage : 16];
+  float o[S::kWarps][G * D];                  // a part's merge
+  float m[S::kWarps][8], l[S::kWarps][8];
   float jo[kMerge][8], jm[kMerge], jl[kMerge];
-  Meta meta[Shape<D, G>::kStages], part;
-  uint64_t full[Shape<D, G>::kStages], empty[Shape<D, G>::kStages], mfull, mempty;
+  Meta meta[S::kStages], part;
+  uint64_t full[S::kStages], empty[S::kStages], mfull, mempty;
   int32_t abort, zero, last_part;
 };
+// Where a merge buffer keeps dim c of head g: permuted, so that the stores of
+// a warp's fragments spread over the banks (see the two forms of them below).
+template <int D, bool Q8>
+__device__ __forceinline__ int o_at(int g, int c) {
+  if (!Q8) return g * D + (c ^ (8 * (g >> 1)));
+  return g * D + (c ^ (2 * (c / (D / 8) & (D / 16 - 1))) ^ (2 * (g >> 1 & 1)));
+}
 
 // Parts: fp32 m[G], l[G], o[G][D] per slot; counters of arrived parts per item.
 struct Parts {
@@ -134,6 +146,88 @@ __device__ __forceinline__ bool merge_all(bool ok) {  // true for all merging th
 }
 __device__ __forceinline__ void merge_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMerge) : "memory"); }
 
+// 16-byte piece c of row r of an e4m3 page in shared memory (128- or 64-byte
+// rows, swizzled by TMA over their own length).
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(uint32_t page, int r, int c) {
+  return page + r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 x;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
+  return x;
+}
+
+// The D / 4 codes of quarter t of a row as pairs of bf16 numbers, for scales
+// over 134 short of row_rest.  The 8 lanes of one pass over the banks read two
+// neighbouring rows: quarter t of a row of 128 is its pieces 2 t and 2 t + 1,
+// so that the two rows' pieces never share banks.
+template <int D>
+struct E4m3Rows {
+  uint32_t w[D / 16], f;
+  __device__ __forceinline__ E4m3Rows(uint32_t page, int r, int t, uint32_t scale) : f(row_factor(scale)) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 x = lds16(piece_at<D>(page, r, (D / 64) * t + i));
+      w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+    }
+  }
+  __device__ __forceinline__ uint32_t lo(int j) const { return mul_bf16x2(codes_lo(w[j]), f); }
+  __device__ __forceinline__ uint32_t hi(int j) const { return mul_bf16x2(codes_hi(w[j]), f); }
+};
+__device__ __forceinline__ float row_rest(uint32_t scale) {
+  return __uint_as_float((max(scale, 134u) - 134u + 127u) << 23);
+}
+
+// The D / 8 codes of part g of rows r and r + 1, in pairs of the two rows:
+// dims 2 j and 2 j + 1 of the part as a[j][at] and a[j][at + 1].
+template <int D>
+struct E4m3Columns {
+  static __device__ __forceinline__ void load(uint32_t page, const uint8_t* scales, int r, int g,
+                                              uint32_t (&a)[D / 16][4], int at) {
+    const uint32_t s0 = scales[r], s1 = scales[r + 1];
+    const uint32_t f = __byte_perm(row_factor(s0), row_factor(s1), 0x5410);
+    uint32_t x[2][D / 32];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (D == 128) {
+        const uint4 y = lds16(piece_at<D>(page, r + i, g));
+        x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+      } else {
+        const uint2 y = lds8(piece_at<D>(page, r + i, g >> 1) + 8 * (g & 1));
+        x[i][0] = y.x; x[i][1] = y.y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      // byte k of both rows, each with its sign in the byte above
+      uint32_t y[4];
+      asm("prmt.b32 %0, %1, %2, 0xc480;" : "=r"(y[0]) : "r"(x[0][j]), "r"(x[1][j]));
+      asm("prmt.b32 %0, %1, %2, 0xd591;" : "=r"(y[1]) : "r"(x[0][j]), "r"(x[1][j]));
+      asm("prmt.b32 %0, %1, %2, 0xe6a2;" : "=r"(y[2]) : "r"(x[0][j]), "r"(x[1][j]));
+      asm("prmt.b32 %0, %1, %2, 0xf7b3;" : "=r"(y[3]) : "r"(x[0][j]), "r"(x[1][j]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[2 * j + k / 2][at + (k & 1)] = mul_bf16x2(codes_to_bf16(y[k]), f);
+    }
+    if (row_is_large(s0) || row_is_large(s1)) {
+      const uint32_t f2 = __byte_perm(row_factor_large(s0), row_factor_large(s1), 0x5410);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        a[j][at] = mul_bf16x2(a[j][at], f2);
+        a[j][at + 1] = mul_bf16x2(a[j][at + 1], f2);
+      }
+    }
+  }
+};
+
 // Keys that the query of sequence b sees, and the pages that hold them; a
 // query that sees none has one page, dead.
 struct Span {
@@ -155,18 +249,20 @@ __device__ __forceinline__ Span seq_span(const MaskArgs& m, const int32_t* seq_l
   return s;
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int G, bool Q8>
+__global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     paged_decode_kernel(Prob pr, MaskArgs mk, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap, const uint16_t* __restrict__ q,
+                        const __grid_constant__ CUtensorMap vmap, const uint8_t* __restrict__ kscales,
+                        const uint8_t* __restrict__ vscales, const uint16_t* __restrict__ q,
                         const int32_t* __restrict__ table, int64_t nb, int64_t num_pages,
                         const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ idx, Parts parts,
                         int32_t min_run, int32_t* __restrict__ status, uint16_t* __restrict__ out) {
-  constexpr int kStages = Shape<D, G>::kStages;
-  constexpr uint32_t kTile = Shape<D, G>::kTile;
+  using S = Shape<D, G, Q8>;
+  constexpr int kStages = S::kStages, kGroups = S::kGroups, kWarps = S::kWarps, kCons = S::kCons;
+  constexpr uint32_t kTile = S::kTile;
   constexpr int kHalf = kPage * 128;  // bytes of a tile's 64-column half
   extern __shared__ unsigned char smem_raw[];
-  Smem<D, G>& sm = *reinterpret_cast<Smem<D, G>*>(
+  Smem<D, G, Q8>& sm = *reinterpret_cast<Smem<D, G, Q8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
@@ -181,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), kWarps / 2);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 4);
     }
     ptx::mbar_init(ptx::smem_u32(&sm.mfull), kWarps);
     ptx::mbar_init(ptx::smem_u32(&sm.mempty), kMerge / 32);
@@ -251,12 +347,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         sm.meta[st] = meta;
         const uint32_t full = ptx::smem_u32(&sm.full[st]);
-        const uint32_t bytes = (page >= 0 ? 2 * kTile : 0u) + (meta.first ? (uint32_t)(G * D * 2) : 0u);
+        const uint32_t bytes = (page >= 0 ? S::kPageBytes : 0u) + (meta.first ? (uint32_t)(G * D * 2) : 0u);
         ptx::mbar_arrive_expect_tx(full, bytes);
         if (page >= 0) {
           const int32_t y = (int32_t)(((int64_t)page * pr.Hkv + head) * kPage);
-          ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][0]), &kmap, 0, y, 0, full);
-          ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][1]), &vmap, 0, y, 0, full);
+          if constexpr (Q8) {
+            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][0]), &kmap, 0, y, full);
+            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][1]), &vmap, 0, y, full);
+            ptx::bulk_g2s(ptx::smem_u32(sm.scale[st][0]), kscales + y, kPage, full);
+            ptx::bulk_g2s(ptx::smem_u32(sm.scale[st][1]), vscales + y, kPage, full);
+          } else {
+            ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][0]), &kmap, 0, y, 0, full);
+            ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][1]), &vmap, 0, y, 0, full);
+          }
         }
         if (meta.first)
           ptx::bulk_g2s(ptx::smem_u32(sm.q[st]), q + (seq * pr.Hq + head * G) * D, G * D * 2, full);
@@ -295,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane + 32 < W) r1 = row[lane + 32];
         }
         const int32_t qb = (int32_t)(sp.t / kPage);
-        int32_t left = 0;  // entries of the part that hold a page, not yet emitted; the last two are the groups' last
+        int32_t left = 0;  // entries of the part that hold a page, not yet emitted; the last ones are the groups' last
         uint64_t keep = 0;
         if (idx) {
           const bool k0 = r0 >= 0 && r0 <= qb, k1 = r1 >= 0 && r1 <= qb;
@@ -336,14 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             meta.rel = (int32_t)(key0 - sp.t);
             meta.klo = px < 0 ? kPage : (int16_t)max((int64_t)0, min((int64_t)kPage, sp.lo - key0));
             meta.khi = (int16_t)min((int64_t)(kPage - 1), sp.t - key0);
-            meta.last = --left < 2;
-            meta.first = ++count <= 2;
+            meta.last = --left < kGroups;
+            meta.first = ++count <= kGroups;
             ok = emit(meta, px, h, b);
           }
         }
       }
       // each group has a stage of every part, if an empty one
-      for (; count < 2 && ok; ++count) {
+      for (; count < kGroups && ok; ++count) {
         meta.klo = kPage;
         meta.first = meta.last = 1;
         ok = emit(meta, -1, h, b);
@@ -365,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Meta meta;
       meta.item = -1;
       meta.first = 0;
-      ok = emit(meta, -1, 0, 0) && emit(meta, -1, 0, 0);
+      for (int k = 0; k < kGroups && ok; ++k) ok = emit(meta, -1, 0, 0);
     }
     // every copy lands before the CTA ends
     if (lane == 0)
@@ -391,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* po = parts.o + (int64_t)part.slot * G * D;
       for (int e = mt; e < G * D / 2; e += kMerge) {
         const int g = e / (D / 2), c = 2 * (e % (D / 2));
-        const float* at = sm.o[0] + g * D + (c ^ (8 * (g >> 1)));
+        const float* at = sm.o[0] + o_at<D, Q8>(g, c);
         float a = 0.0f, z = 0.0f, L = 0.0f, M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][g]);
@@ -505,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float oacc[D / 16][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
   float sl0 = 0.0f, sl1 = 0.0f;
-  // group warp / 4 takes every other stage
-  int st = (warp >> 2) - 2, ph = 0, merges = 0;
+  // group warp / 4 takes every second stage (of three groups, every third)
+  int st = (warp >> 2) - kGroups, ph = 0, merges = 0;
   auto wait_merged = [&] {  // the merge buffer is free
     const bool ok = merges == 0 || ptx::mbar_wait_fast(ptx::smem_u32(&sm.mempty), (merges - 1) & 1, abort);
     if (!__all_sync(0xffffffffu, ok)) {
@@ -516,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
   for (;;) {
-    if ((st += 2) >= kStages) {
+    if ((st += kGroups) >= kStages) {
       st -= kStages;
       ph ^= 1;
     }
@@ -530,9 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (meta.first) {
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t* qr = reinterpret_cast<const uint32_t*>(sm.q[st] + (grp < G ? grp : 0) * D + 16 * ks);
-        bq[ks][0] = grp < G ? qr[tig] : 0u;
-        bq[ks][1] = grp < G ? qr[tig + 4] : 0u;
+        // e4m3 keys come in the order of their bytes: the contraction's order is theirs
+        const uint32_t* qr = reinterpret_cast<const uint32_t*>(sm.q[st] + (grp < G ? grp : 0) * D) +
+                             (Q8 ? (D / 8) * tig + 2 * ks : 8 * ks + tig);
+        bq[ks][0] = grp < G ? qr[0] : 0u;
+        bq[ks][1] = grp < G ? qr[Q8 ? 1 : 4] : 0u;
         oacc[ks][0] = oacc[ks][1] = oacc[ks][2] = oacc[ks][3] = 0.0f;
       }
       m0 = m1 = -INFINITY;
@@ -546,7 +651,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (meta.klo <= meta.khi && r16 <= meta.khi && r16 + 15 >= meta.klo) {
       const uint32_t kb = ptx::smem_u32(sm.kv[st][0]), vb = ptx::smem_u32(sm.kv[st][1]);
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains
-      {
+      uint32_t av[D / 16][4];  // the values' fragments, on their way during the softmax
+      if constexpr (Q8) {
+        // A thread's quarter of the rows grp and grp + 8: D / 4 codes of each,
+        // in the order of which they are contracted (its quads of codes are the
+        // four of a step), so that no fragment needs an exchange.
+        const uint32_t s0 = sm.scale[st][0][r16 + grp], s1 = sm.scale[st][0][r16 + grp + 8];
+        const E4m3Rows<D> k0(kb, r16 + grp, tig, s0), k1(kb, r16 + grp + 8, tig, s1);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t a[4] = {k0.lo(ks), k1.lo(ks), k0.hi(ks), k1.hi(ks)};
+          mma16816(ks & 1 ? e : d, a, bq[ks][0], bq[ks][1]);
+        }
+        d[0] *= row_rest(s0); d[1] *= row_rest(s0); d[2] *= row_rest(s1); d[3] *= row_rest(s1);
+        e[0] *= row_rest(s0); e[1] *= row_rest(s0); e[2] *= row_rest(s1); e[3] *= row_rest(s1);
+        // The values' rows are the MMA's columns: a thread takes D / 8 codes of
+        // its four keys, 2 tig, 2 tig + 1 and 8 further, and pairs the keys
+        // byte by byte; the dims D / 8 grp + 2 mt and the next are rows grp and
+        // grp + 8 of step mt.
+        E4m3Columns<D>::load(vb, sm.scale[st][1], r16 + 2 * tig, grp, av, 0);
+        E4m3Columns<D>::load(vb, sm.scale[st][1], r16 + 2 * tig + 8, grp, av, 2);
+      } else {
         uint32_t a[D / 16][4];
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -558,12 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma16816(d, a[ks], bq[ks][0], bq[ks][1]);
           mma16816(e, a[ks + 1], bq[ks + 1][0], bq[ks + 1][1]);
         }
-      }
-      uint32_t av[D / 16][4];  // the values' fragments, on their way during the softmax
 #pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        const int ch = 2 * mt + vch;
-        ldsm4_t(vb + (ch >> 3) * kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), av[mt]);
+        for (int mt = 0; mt < D / 16; ++mt) {
+          const int ch = 2 * mt + vch;
+          ldsm4_t(vb + (ch >> 3) * kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), av[mt]);
+        }
       }
       // keys grp and grp + 8 of this warp's 16, heads 2 tig and 2 tig + 1
       float x[4];
@@ -641,18 +765,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       *reinterpret_cast<float2*>(&sm.m[warp][2 * tig]) = make_float2(m0, m1);
       *reinterpret_cast<float2*>(&sm.l[warp][2 * tig]) = make_float2(l0, l1);
     }
-    // o[warp][head][dim]; the dims of a head are permuted by 8 (head / 2), which spreads tig over the banks
-    float* ow = sm.o[warp];
+    float* ow = sm.o[warp];  // [head][dim], see o_at
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
-      const int c0 = (16 * mt + grp) ^ (8 * tig), c1 = (16 * mt + grp + 8) ^ (8 * tig);
-      if (2 * tig < G) {
-        ow[2 * tig * D + c0] = oacc[mt][0];
-        ow[2 * tig * D + c1] = oacc[mt][2];
-      }
-      if (2 * tig + 1 < G) {
-        ow[(2 * tig + 1) * D + c0] = oacc[mt][1];
-        ow[(2 * tig + 1) * D + c1] = oacc[mt][3];
+      if constexpr (Q8) {
+        const int c = (D / 8) * grp + 2 * mt;  // and the next
+        if (2 * tig < G)
+          *reinterpret_cast<float2*>(ow + o_at<D, Q8>(2 * tig, c)) = make_float2(oacc[mt][0], oacc[mt][2]);
+        if (2 * tig + 1 < G)
+          *reinterpret_cast<float2*>(ow + o_at<D, Q8>(2 * tig + 1, c)) = make_float2(oacc[mt][1], oacc[mt][3]);
+      } else {
+        const int c0 = 16 * mt + grp, c1 = c0 + 8;
+        if (2 * tig < G) {
+          ow[o_at<D, Q8>(2 * tig, c0)] = oacc[mt][0];
+          ow[o_at<D, Q8>(2 * tig, c1)] = oacc[mt][2];
+        }
+        if (2 * tig + 1 < G) {
+          ow[o_at<D, Q8>(2 * tig + 1, c0)] = oacc[mt][1];
+          ow[o_at<D, Q8>(2 * tig + 1, c1)] = oacc[mt][3];
+        }
       }
     }
     __syncwarp();
@@ -685,19 +816,20 @@ Ws ws_layout(const Prob& pr) {
   return w;
 }
 
-template <int D, int G>
+template <int D, int G, bool Q8>
 cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Pools& pools, const int32_t* seq_lens,
                      const int32_t* idx, char* ws, void* out, cudaStream_t st) {
   const Ws w = ws_layout(pr);
   CUtensorMap kmap, vmap;
   const int64_t rows = pools.num_pages * pr.Hkv * kPage;
-  if (!make_tmap_page(&kmap, pools.k, rows, D) || !make_tmap_page(&vmap, pools.v, rows, D))
+  if (Q8 ? !make_tmap_codes(&kmap, pools.k, rows, D, kPage) || !make_tmap_codes(&vmap, pools.v, rows, D, kPage)
+         : !make_tmap_page(&kmap, pools.k, rows, D) || !make_tmap_page(&vmap, pools.v, rows, D))
     return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const size_t smem = sizeof(Smem<D, G>) + 1024;
-  auto kern = paged_decode_kernel<D, G>;
+  const size_t smem = sizeof(Smem<D, G, Q8>) + 1024;
+  auto kern = paged_decode_kernel<D, G, Q8>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_clear(ws, w.counter + (size_t)pr.B * pr.Hkv * 4, st);
@@ -707,8 +839,8 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Poo
   const int64_t grid = std::min<int64_t>(std::min(sm_count(dev), kMaxCtas), ceil_div64(units, kMinRun));
   Parts parts{(int32_t*)(ws + w.counter), (float*)(ws + w.ml), (float*)(ws + w.o)};
   note_launch();
-  return launch_pdl(true, kern, dim3((unsigned)grid), dim3(kThreads), smem, st, pr, m, kmap, vmap,
-                    (const uint16_t*)q, pools.table, pools.nb, pools.num_pages, seq_lens, idx, parts, kMinRun,
+  return launch_pdl(true, kern, dim3((unsigned)grid), dim3(Shape<D, G, Q8>::kThreads), smem, st, pr, m, kmap, vmap,
+                    pools.ks, pools.vs, (const uint16_t*)q, pools.table, pools.nb, pools.num_pages, seq_lens, idx, parts, kMinRun,
                     (int32_t*)ws, (uint16_t*)out);
 }
 
@@ -719,7 +851,9 @@ size_t paged_decode_ws_bytes(const Prob& pr) { return ws_layout(pr).total; }
 cudaError_t launch_paged_decode(const Prob& pr, const MaskArgs& m, const void* q, const Pools& pools,
                                 const int32_t* seq_lens, const int32_t* idx, char* ws, void* out, cudaStream_t st) {
 #define PISA_PD_CASE(DD, GG) \
-  if (pr.d == DD && pr.G == GG) return launch_t<DD, GG>(pr, m, q, pools, seq_lens, idx, ws, out, st);
+  if (pr.d == DD && pr.G == GG)                                                                  \
+    return pools.ks ? launch_t<DD, GG, true>(pr, m, q, pools, seq_lens, idx, ws, out, st) \
+                    : launch_t<DD, GG, false>(pr, m, q, pools, seq_lens, idx, ws, out, st);
   PISA_PD_CASE(128, 1) PISA_PD_CASE(128, 2) PISA_PD_CASE(128, 4) PISA_PD_CASE(128, 8)
   PISA_PD_CASE(64, 1) PISA_PD_CASE(64, 2) PISA_PD_CASE(64, 4) PISA_PD_CASE(64, 8)
 #undef PISA_PD_CASE

@@ -118,6 +118,10 @@ bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int d, int b
 // is 64 rows whole, its 64-column parts one after the other (128-byte swizzle).
 bool make_tmap_page(CUtensorMap* m, const void* base, int64_t rows, int d);
 
+// 2D TMA view [rows, d] of rows of d bytes (e4m3 codes, d 64 or 128): box of
+// box_rows whole rows, swizzled over their own length.
+bool make_tmap_codes(CUtensorMap* m, const void* base, int64_t rows, int d, int box_rows);
+
 // 4D TMA view of bf16 queries [B, Hq, n, d]: box of 64 columns x `tokens`
 // tokens x the G heads of a group, 128-byte swizzle; tokens past n read as zeros.
 bool make_tmap_q(CUtensorMap* m, const void* base, int64_t B, int64_t Hq, int64_t n, int d, int G, int tokens);

@@ -41,7 +41,8 @@ EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pi
             "pisa_attend_prefill", "pisa_build_pyramid_paged", "pisa_select_decode_paged", "pisa_attend_decode",
             "pisa_read_static_status", "pisa_test_inject_leaf_timeout", "pisa_append_paged",
             "pisa_dense_decode_paged", "pisa_attend_decode_paged", "pisa_dense_prefill_paged",
-            "pisa_paged_workspace_bytes", "pisa_cache_append", "pisa_cache_read"]
+            "pisa_paged_workspace_bytes", "pisa_cache_append", "pisa_cache_read",
+            "pisa_cache_dense_decode", "pisa_cache_attend_decode"]
 
 
 class Params(ctypes.Structure):
@@ -125,6 +126,10 @@ _lib.pisa_cache_append.argtypes = [_P, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, 
 _lib.pisa_cache_append.restype = ctypes.c_int
 _lib.pisa_cache_read.argtypes = [_P, ctypes.c_int64, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
 _lib.pisa_cache_read.restype = ctypes.c_int
+_lib.pisa_cache_dense_decode.argtypes = [_P, _M, _vp, _C, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.pisa_cache_dense_decode.restype = ctypes.c_int
+_lib.pisa_cache_attend_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.pisa_cache_attend_decode.restype = ctypes.c_int
 _lib.pisa_paged_workspace_bytes.argtypes = [_P, ctypes.c_int64]
 _lib.pisa_paged_workspace_bytes.restype = ctypes.c_size_t
 _lib.pisa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32), _vp]
@@ -458,15 +463,25 @@ def _read(p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, space, new_le
                    None if v_out is None else _want(v_out, "v_out", shape, dt, index))
 
 
-def _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, space, out, mask, stream, check) -> int:
+def _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, space, out, mask, scales, stream, check) -> int:
     index, dt = q.get_device(), _dtype(p)
+    if scales is not None:
+        cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+        return _launch(index, stream, "pisa_cache_dense_decode", check, _lib.pisa_cache_dense_decode, ctypes.byref(p),
+                       _mask_arg(mask, p, 1, index), _want(q, "q", (p.B, p.H_q, p.d), dt, index), ctypes.byref(cache),
+                       lens, *space, out)
     cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
     return _launch(index, stream, "pisa_dense_decode_paged", check, _lib.pisa_dense_decode_paged, ctypes.byref(p),
                    _mask_arg(mask, p, 1, index), _want(q, "q", (p.B, p.H_q, p.d), dt, index), *cache, *space, out)
 
 
-def _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, space, out, stream, check) -> int:
+def _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, space, out, scales, stream, check) -> int:
     index, dt = q.get_device(), _dtype(p)
+    if scales is not None:
+        cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+        return _launch(index, stream, "pisa_cache_attend_decode", check, _lib.pisa_cache_attend_decode,
+                       ctypes.byref(p), _want(q, "q", (p.B, p.H_q, p.d), dt, index), ctypes.byref(cache), lens,
+                       _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space, out)
     cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
     return _launch(index, stream, "pisa_attend_decode_paged", check, _lib.pisa_attend_decode_paged, ctypes.byref(p),
                    _want(q, "q", (p.B, p.H_q, p.d), dt, index), *cache,
@@ -518,19 +533,20 @@ def read_paged(p: Params, k_out, v_out, k_pages, v_pages, page_table, seq_lens, 
 
 
 def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out,
-                       mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
-    """q and out [B, H_q, d]: attention of one new token per sequence over its whole cache."""
+                       mask: Optional[AttentionMask] = None, stream=None, check: bool = True, scales=None) -> int:
+    """q and out [B, H_q, d]: attention of one new token per sequence over its
+    whole cache (scales: of e4m3 pages)."""
     index = q.get_device()
     return _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index),
-                         _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), mask, stream, check)
+                         _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), mask, scales, stream, check)
 
 
 def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, idx, ws, out, stream=None,
-                        check: bool = True) -> int:
-    """attend_decode over a paged cache; idx int32 [B, H_kv, K+3]."""
+                        check: bool = True, scales=None) -> int:
+    """attend_decode over a paged cache (scales: of e4m3 pages); idx int32 [B, H_kv, K+3]."""
     index = q.get_device()
     return _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, _want_space(ws, index),
-                            _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), stream, check)
+                            _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), scales, stream, check)
 
 
 def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out, new_lens=None,
@@ -701,16 +717,16 @@ class PagedAttention:
         _read(self.p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, self._space, new_lens, scales, stream,
               True)
 
-    def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None):
+    def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None, scales=None):
         out = self._buffer("dense", q)
-        _dense_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, self._space, out.data_ptr(), mask, stream,
-                      True)
+        _dense_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, self._space, out.data_ptr(), mask, scales,
+                      stream, True)
         return out
 
-    def selected_decode(self, q, k_pages, v_pages, page_table, seq_lens, idx, stream=None):
+    def selected_decode(self, q, k_pages, v_pages, page_table, seq_lens, idx, stream=None, scales=None):
         out = self._buffer("selected", q)
-        _selected_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, idx, self._space, out.data_ptr(), stream,
-                         True)
+        _selected_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, idx, self._space, out.data_ptr(), scales,
+                         stream, True)
         return out
 
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None):

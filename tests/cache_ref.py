@@ -87,3 +87,20 @@ def norm_rotate(x, weight, eps, rope, pos, interleaved):
     t = t.clone()
     t[..., a_at], t[..., b_at] = both, both
     return y, t + more
+
+
+def paginate(x, lens, seed=0, extra=3):
+    """Quantises [B, H, N, d] and scatters the rows into a shuffled pool:
+    (codes, scales, table, the rows' numbers in 64 bits).  Positions behind a
+    sequence's length and unused pages hold what is never written: NaN's codes
+    and arbitrary scales, 255 among them."""
+    B, H, N, d = x.shape
+    codes, scale = quantize(x)
+    lens = [max(0, min(int(n), N)) for n in lens]
+    pages, table = R.paginate(codes.view(torch.uint8), lens, extra, seed, 0x7f, torch.uint8)
+    scales, _ = R.paginate(scale[..., None], lens, extra, seed, 255, torch.uint8)
+    rest, _ = R.paginate(torch.zeros(B, H, N, 1), lens, extra, seed, 1.0, torch.float32)
+    g = torch.Generator().manual_seed(seed)
+    odd = torch.randint(0, 256, scales.shape, generator=g).to(torch.uint8)
+    scales = torch.where((rest == 1.0) & (odd < 128), odd, scales)[..., 0].contiguous()
+    return pages.view(torch.float8_e4m3fn), scales, table, numbers(codes, scale)

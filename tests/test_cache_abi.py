@@ -43,7 +43,13 @@ def calls(pisa, p):
     def read(c, lens=A, ws=A, size=BIG, n=4, out=A, new=A):
         return L.pisa_cache_read(P, n, c, lens, new, ws, size, out, A, None)
 
-    return dict(append=append, read=read)
+    def dense(c, lens=A, ws=A, size=BIG, q=A, out=A, mask=None):
+        return L.pisa_cache_dense_decode(P, mask, q, c, lens, ws, size, out, None)
+
+    def selected(c, lens=A, ws=A, size=BIG, q=A, out=A, idx=A):
+        return L.pisa_cache_attend_decode(P, q, c, lens, idx, ws, size, out, None)
+
+    return dict(append=append, read=read, dense=dense, selected=selected)
 
 
 def test_caches_are_checked(pisa):
@@ -110,3 +116,18 @@ def test_binding_checks_8_bit_pages(pisa):
             pisa.PagedAttention(p, n=3, device="cpu", q_norm=bad)
         with pytest.raises(ValueError, match="norm"):
             pisa.PagedAttention(p, n=3, device="cpu", k_norm=bad)
+
+
+def test_attention_refusals(pisa):
+    p = pisa.make_params(2, 4096, 16, 4, 128, K=8)
+    c = cache(pisa)
+    on = calls(pisa, p)
+    for name in set(on) - {"append", "read"}:
+        assert on[name](c, q=None) == -1 and on[name](c, q=MIS) == -3, name
+        for dtype, d, code in (("fp32", 128, -2), ("bf16", 96, -2)):
+            assert calls(pisa, pisa.make_params(2, 4096, 16, 4, d, K=8, dtype=dtype))[name](c) == code, name
+    for name in ("dense", "selected"):
+        assert on[name](c, out=None) == -1 and on[name](c, out=MIS) == -3, name
+    assert on["selected"](c, idx=None) == -1 and on["selected"](c, idx=ODD) == -3
+    bad = pisa.Mask(ctypes.sizeof(pisa.Mask), -1.0, 0, None, None, None)
+    assert on["dense"](c, mask=ctypes.byref(bad)) == -1

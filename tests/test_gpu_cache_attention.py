@@ -1,0 +1,170 @@
+"""GPU tests of attention over 8-bit pages against its 64-bit form on the
+numbers that the pages stand for, every element within the bound derived in
+paged_ref.  Positions behind a sequence's length hold NaN's codes and scales
+of 255 and below."""
+import pytest
+import torch
+
+import cache_ref as C
+import paged_ref as R
+from test_gpu_paged_attention import MARK, i32, slopes_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pisa():
+    from pyramid_top_block_mean_gb300 import pisa as m
+    return m
+
+
+def cache(B, Hkv, N, d, lens, seed, spread=3, change=None):
+    """Rows whose sizes differ by up to 2^spread, so that scales do too."""
+    g = torch.Generator().manual_seed(seed)
+    k, v = (torch.randn(B, Hkv, N, d, generator=g) for _ in range(2))
+    v = v * 2.0 ** torch.randint(-spread, spread + 1, (B, Hkv, N, 1), generator=g)
+    k = k * 2.0 ** (-torch.rand(B, Hkv, N, 1, generator=g) * spread)
+    if change is not None:
+        change(k, v)
+    kp, ks, table, k = C.paginate(k, lens, seed)
+    vp, vs, _, v = C.paginate(v, lens, seed)
+    return k.cuda(), v.cuda(), kp.cuda(), vp.cuda(), torch.stack([ks, vs]).contiguous().cuda(), table.cuda()
+
+
+# ---------------------------------------------------------------- one token
+def run_decode(pisa, B, Hq, Hkv, d, N, lens, seed=0, softcap=0.0, window=0, slopes=False, first=None, amp=2.0,
+               scale=0.0, change=None):
+    k, v, kp, vp, scales, table = cache(B, Hkv, N, d, lens, seed, change=change)
+    q = (torch.randn(B, Hq, d, generator=torch.Generator().manual_seed(seed + 1)) * amp).to(torch.bfloat16).cuda()
+    p = pisa.make_params(B, N, Hq, Hkv, d, scale=scale)
+    layer = pisa.PagedAttention(p)
+    sl = slopes_of(Hq) if slopes else None
+    mask = None
+    if softcap or window or slopes or first is not None:
+        mask = pisa.AttentionMask(softcap, window, sl, None if first is None else i32(first)[:, None].contiguous())
+    out = layer.dense_decode(q, kp, vp, table, i32(lens), mask=mask, scales=scales)
+    status = layer.device_status()
+    for b, n in enumerate(lens):
+        if n < 1 or n > N:
+            assert bool((out[b] == 0).all())
+            continue
+        want, tol = R.dense(q[b][:, None], k[b], v[b], n, torch.tensor([n - 1], device="cuda"),
+                            scale or d ** -0.5, softcap, window, sl, None if first is None else i32([first[b]]))
+        R.within(out[b], want[:, 0], tol[:, 0], f"sequence {b} of length {n}")
+    return status
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 2), (16, 4), (16, 2), (24, 3)])
+def test_decode_lengths(pisa, d, Hq, Hkv):
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 192, 193, 257, 700, 1000]
+    assert run_decode(pisa, len(lens), Hq, Hkv, d, 1000, lens, seed=d + Hq) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=50.0), dict(softcap=1.5, amp=8.0), dict(window=1), dict(window=64),
+                                dict(window=100), dict(slopes=True), dict(softcap=30.0, window=333, slopes=True),
+                                dict(scale=0.5), dict(first=[0, 1, 64, 0, 129, 600]),
+                                dict(first=[1, 1000, 65, 2 ** 31 - 1, -5, 200], window=250),
+                                dict(softcap=3e4, amp=20.0), dict(amp=60.0)])
+def test_decode_masks_and_scores(pisa, kw):
+    assert run_decode(pisa, 6, 8, 2, 128, 777, [1, 64, 65, 300, 777, 641], seed=3, **kw) == 0
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv", [(1, 40000, 8, 1), (2, 20011, 16, 8), (1, 5, 1, 1), (300, 130, 4, 2),
+                                        (12, 4000, 16, 2)])
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_split_over_the_gpu(pisa, B, N, Hq, Hkv, d):
+    lens = [max(1, N - 37 * b) for b in range(B)]
+    assert run_decode(pisa, B, Hq, Hkv, d, N, lens, seed=B) == 0
+
+
+def test_decode_uneven_batch(pisa):
+    lens = [1] * 40 + [9000] + [64] * 40 + [1, 3000]
+    assert run_decode(pisa, len(lens), 8, 2, 64, 9000, lens, seed=11) == 0
+
+
+def test_decode_bad_lengths(pisa):
+    assert run_decode(pisa, 5, 8, 2, 64, 300, [300, 0, 301, -3, 10], seed=12) == pisa.DEV_BAD_SEQ_LEN
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_rows_of_any_size(pisa, d):
+    """Zero rows, and rows from 2^-100 to 2^60 of one: the powers of the values, and of keys and queries against each
+    other, may be anything that fp32 holds."""
+    def far(k, v):
+        k[0, :, ::7], v[0, :, ::5], v[0, :, 3::5] = 0.0, 0.0, v[0, :, 3::5] * 1e-12
+        k[1] *= 2.0 ** 40
+        v[1] *= 2.0 ** -100
+        k[2] *= 2.0 ** -60
+        v[2, :, ::3] *= 2.0 ** 60
+        k[3, :, 100:200] *= 2.0 ** 10  # scales over 134
+        v[3, :, 50:150] *= 2.0 ** 20
+
+    lens, B = [300, 290, 280, 270], 4
+    k, v, kp, vp, scales, table = cache(B, 2, 300, d, lens, 5, change=far)
+    q = torch.randn(B, 4, d, generator=torch.Generator().manual_seed(6)) * 2
+    q[1] *= 2.0 ** -40
+    q[2] *= 2.0 ** 60
+    q[3] *= 2.0 ** -8
+    q = q.to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(B, 300, 4, 2, d))
+    out = layer.dense_decode(q, kp, vp, table, i32(lens), scales=scales)
+    for b, n in enumerate(lens):
+        want, tol = R.dense(q[b][:, None], k[b], v[b], n, torch.tensor([n - 1], device="cuda"), d ** -0.5)
+        R.within(out[b], want[:, 0], tol[:, 0], f"sequence {b}")
+
+
+def test_decode_rows_that_are_not_finite(pisa):
+    """A row that was not finite reads as NaN: so do the heads that see it, and no other."""
+    def poke(k, v):
+        v[0, 0, 70, 3] = float("inf")
+        k[1, 1, 10, 9] = R.NAN
+        k[2, 0, 20, 0] = v[2, 1, 21, 0] = R.NAN
+
+    k, v, kp, vp, scales, table = cache(3, 2, 300, 64, [300] * 3, 5, change=poke)
+    assert int((scales[:, table[:2].long().flatten()] == 255).sum()) >= 2
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(3, 300, 4, 2, 64))
+    mask = pisa.AttentionMask(first_key=i32([[0], [0], [22]]))  # the third sequence's are out of sight
+    out = layer.dense_decode(q, kp, vp, table, i32([300] * 3), mask=mask, scales=scales)
+    assert bool(torch.isnan(out[0, :2]).all()) and bool(torch.isfinite(out[0, 2:]).all())
+    assert bool(torch.isnan(out[1, 2:]).all()) and bool(torch.isfinite(out[1, :2]).all())
+    want, tol = R.dense(q[2][:, None], k[2], v[2], 300, torch.tensor([299], device="cuda"), 0.125, first=i32([22]))
+    R.within(out[2], want[:, 0], tol[:, 0])
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 1 << 20])
+def test_decode_bad_page_counts_as_unseen(pisa, bad):
+    k, v, kp, vp, scales, table = cache(2, 2, 300, 64, [300, 300], 4)
+    table[0, 2] = bad
+    table[1, :] = bad
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(2, 300, 4, 2, 64))
+    keep = torch.ones(1, 300, dtype=torch.bool, device="cuda")
+    keep[:, 128:192] = False
+    out = layer.dense_decode(q, kp, vp, table, i32([300, 300]), scales=scales)
+    assert layer.device_status() == pisa.DEV_BAD_INDEX
+    for h in range(4):
+        o, t = R.attend(q[0, h:h + 1], k[0, h // 2], v[0, h // 2], keep, 64 ** -0.5)
+        R.within(out[0, h], o[0], t[0])
+    assert bool((out[1] == 0).all())
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,K", [(128, 16, 4, 8), (128, 8, 1, 32), (64, 4, 4, 1), (64, 8, 2, 29)])
+def test_selected_decode(pisa, d, Hq, Hkv, K):
+    lens = [1, 64, 65, 500, 2900, 3000]
+    B, N = len(lens), 3000
+    k, v, kp, vp, scales, table = cache(B, Hkv, N, d, lens, K)
+    g = torch.Generator().manual_seed(K + 1)
+    q = torch.randn(B, Hq, d, generator=g).to(torch.bfloat16).cuda()
+    idx = torch.randint(-3, 55, (B, Hkv, K + 3), generator=g).to(torch.int32)  # unsorted, repeated, future, negative
+    idx[0, 0] = -1  # nothing selected: zeros
+    idx[3, :, -1] = idx[3, :, 0]
+    idx = idx.cuda()
+    layer = pisa.PagedAttention(pisa.make_params(B, N, Hq, Hkv, d, K=K))
+    out = layer.selected_decode(q, kp, vp, table, i32(lens), idx, scales=scales)
+    assert layer.device_status() == 0
+    for b, n in enumerate(lens):
+        want, tol = R.selected(q[b], k[b], v[b], n, idx[b], d ** -0.5)
+        R.within(out[b], want, tol, f"sequence {b}")
+    assert bool((out[0, :Hq // Hkv] == 0).all())
