@@ -166,67 +166,101 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
   return x;
 }
 
-// The D / 4 codes of quarter t of a row as pairs of bf16 numbers, for scales
-// over 134 short of row_rest.  The 8 lanes of one pass over the banks read two
-// neighbouring rows: quarter t of a row of 128 is its pieces 2 t and 2 t + 1,
-// so that the two rows' pieces never share banks.
+// The D / 4 codes of quarter t of row r: the contraction's order is theirs, so
+// that they are an MMA's operand as they come.  The 8 lanes of one pass over
+// the banks read two neighbouring rows: quarter t of a row of 128 is its
+// pieces 2 t and 2 t + 1, so that the two rows' pieces never share banks.
 template <int D>
-struct E4m3Rows {
-  uint32_t w[D / 16], f;
-  __device__ __forceinline__ E4m3Rows(uint32_t page, int r, int t, uint32_t scale) : f(row_factor(scale)) {
+__device__ __forceinline__ void row_codes(uint32_t page, int r, int t, uint32_t (&w)[D / 16]) {
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const uint4 x = lds16(piece_at<D>(page, r, (D / 64) * t + i));
-      w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+  for (int i = 0; i < D / 64; ++i) {
+    const uint4 x = lds16(piece_at<D>(page, r, (D / 64) * t + i));
+    w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+  }
+}
+__device__ __forceinline__ void mma16832_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A query as the sum of two e4m3 rows: with s the power of two that brings the
+// head's largest magnitude to 128 .. 256, x = q s is hi + lo / 32.  Of a bf16
+// number, whose 8 bits are twice e4m3's, hi takes four and leaves at most 4 and
+// a sign, so that the sum is exact; below 2^-13 of the largest, where e4m3's
+// steps no longer shrink, it is off by at most 2^-22 of the largest.
+// Returns 1 / s, or NaN for a query that is not finite.
+template <int D>
+__device__ __forceinline__ float split_query(const uint16_t* row, bool there, uint32_t (&hi)[D / 16],
+                                             uint32_t (&lo)[D / 16]) {
+  uint4 w[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    w[i] = there ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7fffu, u[k] >> 16 & 0x7fffu));
+  }
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t e = max(top >> 7, 14u);  // biased; 2^(134 - 127 - e) stays a normal number
+  const float s = __uint_as_float((134u + 127u - e) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float x[4] = {__uint_as_float(u[2 * k] << 16) * s, __uint_as_float(u[2 * k] & 0xffff0000u) * s,
+                          __uint_as_float(u[2 * k + 1] << 16) * s, __uint_as_float(u[2 * k + 1] & 0xffff0000u) * s};
+      const uint32_t c = to_codes(x[0], x[1]) | to_codes(x[2], x[3]) << 16;
+      float y[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        // the number of code n: its bits as a bf16 number times 2^120
+        const uint32_t b = c >> (8 * n);
+        y[n] = (x[n] - __uint_as_float((b & 0x80u) << 24 | (b & 0x7fu) << 20) * 0x1p120f) * 32.0f;
+      }
+      hi[2 * i + k] = c;
+      lo[2 * i + k] = to_codes(y[0], y[1]) | to_codes(y[2], y[3]) << 16;
     }
   }
-  __device__ __forceinline__ uint32_t lo(int j) const { return mul_bf16x2(codes_lo(w[j]), f); }
-  __device__ __forceinline__ uint32_t hi(int j) const { return mul_bf16x2(codes_hi(w[j]), f); }
-};
-__device__ __forceinline__ float row_rest(uint32_t scale) {
-  return __uint_as_float((max(scale, 134u) - 134u + 127u) << 23);
+  return e == 255u ? NAN : __uint_as_float((e + 127u - 134u) << 23);
 }
 
 // The D / 8 codes of part g of rows r and r + 1, in pairs of the two rows:
-// dims 2 j and 2 j + 1 of the part as a[j][at] and a[j][at + 1].
+// dims 2 j and 2 j + 1 of the part as a[j][at] and a[j][at + 1], as bf16 numbers
+// times 2^-120.
 template <int D>
-struct E4m3Columns {
-  static __device__ __forceinline__ void load(uint32_t page, const uint8_t* scales, int r, int g,
-                                              uint32_t (&a)[D / 16][4], int at) {
-    const uint32_t s0 = scales[r], s1 = scales[r + 1];
-    const uint32_t f = __byte_perm(row_factor(s0), row_factor(s1), 0x5410);
-    uint32_t x[2][D / 32];
+__device__ __forceinline__ void column_pairs(uint32_t page, int r, int g, uint32_t (&a)[D / 16][4], int at) {
+  uint32_t x[2][D / 32];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (D == 128) {
-        const uint4 y = lds16(piece_at<D>(page, r + i, g));
-        x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
-      } else {
-        const uint2 y = lds8(piece_at<D>(page, r + i, g >> 1) + 8 * (g & 1));
-        x[i][0] = y.x; x[i][1] = y.y;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      // byte k of both rows, each with its sign in the byte above
-      uint32_t y[4];
-      asm("prmt.b32 %0, %1, %2, 0xc480;" : "=r"(y[0]) : "r"(x[0][j]), "r"(x[1][j]));
-      asm("prmt.b32 %0, %1, %2, 0xd591;" : "=r"(y[1]) : "r"(x[0][j]), "r"(x[1][j]));
-      asm("prmt.b32 %0, %1, %2, 0xe6a2;" : "=r"(y[2]) : "r"(x[0][j]), "r"(x[1][j]));
-      asm("prmt.b32 %0, %1, %2, 0xf7b3;" : "=r"(y[3]) : "r"(x[0][j]), "r"(x[1][j]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) a[2 * j + k / 2][at + (k & 1)] = mul_bf16x2(codes_to_bf16(y[k]), f);
-    }
-    if (row_is_large(s0) || row_is_large(s1)) {
-      const uint32_t f2 = __byte_perm(row_factor_large(s0), row_factor_large(s1), 0x5410);
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        a[j][at] = mul_bf16x2(a[j][at], f2);
-        a[j][at + 1] = mul_bf16x2(a[j][at + 1], f2);
-      }
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (D == 128) {
+      const uint4 y = lds16(piece_at<D>(page, r + i, g));
+      x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+    } else {
+      const uint2 y = lds8(piece_at<D>(page, r + i, g >> 1) + 8 * (g & 1));
+      x[i][0] = y.x; x[i][1] = y.y;
     }
   }
-};
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    // byte k of both rows, each with its sign in the byte above
+    uint32_t y[4];
+    asm("prmt.b32 %0, %1, %2, 0xc480;" : "=r"(y[0]) : "r"(x[0][j]), "r"(x[1][j]));
+    asm("prmt.b32 %0, %1, %2, 0xd591;" : "=r"(y[1]) : "r"(x[0][j]), "r"(x[1][j]));
+    asm("prmt.b32 %0, %1, %2, 0xe6a2;" : "=r"(y[2]) : "r"(x[0][j]), "r"(x[1][j]));
+    asm("prmt.b32 %0, %1, %2, 0xf7b3;" : "=r"(y[3]) : "r"(x[0][j]), "r"(x[1][j]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[2 * j + k / 2][at + (k & 1)] = codes_to_bf16(y[k]);
+  }
+}
 
 // Keys that the query of sequence b sees, and the pages that hold them; a
 // query that sees none has one page, dead.
@@ -604,7 +638,11 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   // ldmatrix rows: lane l addresses row l % 8 of matrix l / 8
   const int krow = r16 + (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
   const int vrow = r16 + (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
-  uint32_t bq[D / 16][2];
+  // the query's fragments; Q8: its upper part and its lower one, each head's
+  // 1 / s, and the largest scale of the values so far
+  uint32_t bq[Q8 ? D / 16 : D / 8], bl[Q8 ? D / 16 : 1];
+  float hf0 = 1.0f, hf1 = 1.0f;
+  int ref = 0;
   float oacc[D / 16][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
   float sl0 = 0.0f, sl1 = 0.0f;
@@ -631,15 +669,21 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     const Meta meta = sm.meta[st];
     if (meta.item < 0) break;
     if (meta.first) {
+      if constexpr (Q8) {
+        const float f = split_query<D>(sm.q[st] + (grp < G ? grp : 0) * D + (D / 4) * tig, grp < G, bq, bl);
+        hf0 = __shfl_sync(0xffffffffu, f, 8 * tig);
+        hf1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+        ref = 0;
+      } else {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        // e4m3 keys come in the order of their bytes: the contraction's order is theirs
-        const uint32_t* qr = reinterpret_cast<const uint32_t*>(sm.q[st] + (grp < G ? grp : 0) * D) +
-                             (Q8 ? (D / 8) * tig + 2 * ks : 8 * ks + tig);
-        bq[ks][0] = grp < G ? qr[0] : 0u;
-        bq[ks][1] = grp < G ? qr[Q8 ? 1 : 4] : 0u;
-        oacc[ks][0] = oacc[ks][1] = oacc[ks][2] = oacc[ks][3] = 0.0f;
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t* qr = reinterpret_cast<const uint32_t*>(sm.q[st] + (grp < G ? grp : 0) * D + 16 * ks);
+          bq[2 * ks] = grp < G ? qr[tig] : 0u;
+          bq[2 * ks + 1] = grp < G ? qr[tig + 4] : 0u;
+        }
       }
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) oacc[mt][0] = oacc[mt][1] = oacc[mt][2] = oacc[mt][3] = 0.0f;
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.0f;
       if (mk.slopes) {
@@ -653,24 +697,20 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains
       uint32_t av[D / 16][4];  // the values' fragments, on their way during the softmax
       if constexpr (Q8) {
-        // A thread's quarter of the rows grp and grp + 8: D / 4 codes of each,
-        // in the order of which they are contracted (its quads of codes are the
-        // four of a step), so that no fragment needs an exchange.
-        const uint32_t s0 = sm.scale[st][0][r16 + grp], s1 = sm.scale[st][0][r16 + grp + 8];
-        const E4m3Rows<D> k0(kb, r16 + grp, tig, s0), k1(kb, r16 + grp + 8, tig, s1);
+        uint32_t k0[D / 16], k1[D / 16];
+        row_codes<D>(kb, r16 + grp, tig, k0);
+        row_codes<D>(kb, r16 + grp + 8, tig, k1);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t a[4] = {k0.lo(ks), k1.lo(ks), k0.hi(ks), k1.hi(ks)};
-          mma16816(ks & 1 ? e : d, a, bq[ks][0], bq[ks][1]);
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          mma16832_e4m3(d, k0[ks], k1[ks], k0[ks + 1], k1[ks + 1], bq[ks], bq[ks + 1]);
+          mma16832_e4m3(e, k0[ks], k1[ks], k0[ks + 1], k1[ks + 1], bl[ks], bl[ks + 1]);
         }
-        d[0] *= row_rest(s0); d[1] *= row_rest(s0); d[2] *= row_rest(s1); d[3] *= row_rest(s1);
-        e[0] *= row_rest(s0); e[1] *= row_rest(s0); e[2] *= row_rest(s1); e[3] *= row_rest(s1);
         // The values' rows are the MMA's columns: a thread takes D / 8 codes of
         // its four keys, 2 tig, 2 tig + 1 and 8 further, and pairs the keys
         // byte by byte; the dims D / 8 grp + 2 mt and the next are rows grp and
         // grp + 8 of step mt.
-        E4m3Columns<D>::load(vb, sm.scale[st][1], r16 + 2 * tig, grp, av, 0);
-        E4m3Columns<D>::load(vb, sm.scale[st][1], r16 + 2 * tig + 8, grp, av, 2);
+        column_pairs<D>(vb, r16 + 2 * tig, grp, av, 0);
+        column_pairs<D>(vb, r16 + 2 * tig + 8, grp, av, 2);
       } else {
         uint32_t a[D / 16][4];
 #pragma unroll
@@ -680,8 +720,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         }
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks += 2) {
-          mma16816(d, a[ks], bq[ks][0], bq[ks][1]);
-          mma16816(e, a[ks + 1], bq[ks + 1][0], bq[ks + 1][1]);
+          mma16816(d, a[ks], bq[2 * ks], bq[2 * ks + 1]);
+          mma16816(e, a[ks + 1], bq[2 * ks + 2], bq[2 * ks + 3]);
         }
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
@@ -691,9 +731,15 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       }
       // keys grp and grp + 8 of this warp's 16, heads 2 tig and 2 tig + 1
       float x[4];
+      if constexpr (Q8) {
+        const uint32_t s0 = sm.scale[st][0][r16 + grp], s1 = sm.scale[st][0][r16 + grp + 8];
+        const float f0 = s0 == 255u ? NAN : __uint_as_float(s0 << 23), f1 = s1 == 255u ? NAN : __uint_as_float(s1 << 23);
+        x[0] = fmaf(e[0], 1.0f / 32, d[0]) * hf0 * f0; x[1] = fmaf(e[1], 1.0f / 32, d[1]) * hf1 * f0;
+        x[2] = fmaf(e[2], 1.0f / 32, d[2]) * hf0 * f1; x[3] = fmaf(e[3], 1.0f / 32, d[3]) * hf1 * f1;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[j] = d[j] + e[j];
+        if constexpr (!Q8) x[j] = d[j] + e[j];
         x[j] = mk.cap2 > 0.0f ? cap_score(mk, x[j]) : x[j] * pr.scale2;
       }
       const int ka = r16 + grp;
@@ -739,7 +785,34 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       l0 += p0 + p2;
       l1 += p1 + p3;
       // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step)
-      const uint32_t b0 = transpose8(pack_bf16(p0, p1)), b1 = transpose8(pack_bf16(p2, p3));
+      uint32_t b0, b1;
+      if constexpr (Q8) {
+        // The rows' powers go with the weights, which keep all of their bits:
+        // relative to the largest power so far (no row's, without a key that is
+        // seen), times 2^60, half way up from the 2^-120 of the codes.
+        int sa = sm.scale[st][1][ka], sb = sm.scale[st][1][ka + 8];
+        if (part) {
+          if (ka < meta.klo || ka > meta.khi) sa = 0;
+          if (ka + 8 < meta.klo || ka + 8 > meta.khi) sb = 0;
+        }
+        const int top = __reduce_max_sync(0xffffffffu, max(sa == 255 ? 0 : sa, sb == 255 ? 0 : sb));
+        if (top > ref) {
+          const float f = __uint_as_float(max(ref - top + 127, 0) << 23);
+          ref = top;
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            oacc[mt][0] *= f; oacc[mt][1] *= f;
+            oacc[mt][2] *= f; oacc[mt][3] *= f;
+          }
+        }
+        const float fa = sa == 255 ? NAN : __uint_as_float(max(sa - ref + 187, 0) << 23);
+        const float fb = sb == 255 ? NAN : __uint_as_float(max(sb - ref + 187, 0) << 23);
+        b0 = transpose8(pack_bf16(p0 * fa, p1 * fa));
+        b1 = transpose8(pack_bf16(p2 * fb, p3 * fb));
+      } else {
+        b0 = transpose8(pack_bf16(p0, p1));
+        b1 = transpose8(pack_bf16(p2, p3));
+      }
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
         if (part) {  // a value that is not seen may be anything
@@ -764,6 +837,15 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     if (grp == 0) {
       *reinterpret_cast<float2*>(&sm.m[warp][2 * tig]) = make_float2(m0, m1);
       *reinterpret_cast<float2*>(&sm.l[warp][2 * tig]) = make_float2(l0, l1);
+    }
+    if constexpr (Q8) {  // O as it is: by 2^(ref - 127) and 2^60, in two steps
+      const int by = ref - 67, half = by >> 1;
+      const float f = __uint_as_float((half + 127) << 23), f2 = __uint_as_float((by - half + 127) << 23);
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        oacc[mt][0] = oacc[mt][0] * f * f2; oacc[mt][1] = oacc[mt][1] * f * f2;
+        oacc[mt][2] = oacc[mt][2] * f * f2; oacc[mt][3] = oacc[mt][3] * f * f2;
+      }
     }
     float* ow = sm.o[warp];  // [head][dim], see o_at
 #pragma unroll

@@ -133,6 +133,38 @@ def test_decode_rows_that_are_not_finite(pisa):
     R.within(out[2], want[:, 0], tol[:, 0])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_small_elements_of_rows(pisa, d):
+    """Elements far below their row's largest: subnormal codes, and queries whose heads and dims differ widely."""
+    def far(k, v):
+        v[:, :, :, 1:] *= 2.0 ** -12
+        k[:, :, :, :d // 2] *= 2.0 ** -11
+    lens, B = [300, 290], 2
+    k, v, kp, vp, scales, table = cache(B, 2, 300, d, lens, 7, change=far)
+    assert int(((kp.view(torch.uint8) & 0x78) == 0).sum()) > 1000  # subnormal codes
+    q = torch.randn(B, 8, d, generator=torch.Generator().manual_seed(8)) * 4
+    q[:, :, d // 2:] *= 2.0 ** -11
+    q *= 2.0 ** torch.arange(-8, 8, 2)[None, :, None]
+    q = q.to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(B, 300, 8, 2, d))
+    out = layer.dense_decode(q, kp, vp, table, i32(lens), scales=scales)
+    for b, n in enumerate(lens):
+        want, tol = R.dense(q[b][:, None], k[b], v[b], n, torch.tensor([n - 1], device="cuda"), d ** -0.5)
+        R.within(out[b], want[:, 0], tol[:, 0], f"sequence {b}")
+
+
+def test_decode_queries_that_are_not_finite(pisa):
+    k, v, kp, vp, scales, table = cache(1, 2, 300, 64, [300], 5)
+    q = torch.randn(1, 8, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    q[0, 1, 60], q[0, 6, 0] = float("inf"), R.NAN
+    layer = pisa.PagedAttention(pisa.make_params(1, 300, 8, 2, 64))
+    out = layer.dense_decode(q, kp, vp, table, i32([300]), scales=scales)
+    rest = [0, 2, 3, 4, 5, 7]
+    want, tol = R.dense(q[0][:, None], k[0], v[0], 300, torch.tensor([299], device="cuda"), 0.125)
+    R.within(out[0, rest], want[rest, 0], tol[rest, 0])
+    assert bool(torch.isnan(out[0, [1, 6]]).all())
+
+
 @pytest.mark.parametrize("bad", [-1, -2 ** 31, 1 << 20])
 def test_decode_bad_page_counts_as_unseen(pisa, bad):
     k, v, kp, vp, scales, table = cache(2, 2, 300, 64, [300, 300], 4)
