@@ -40,6 +40,7 @@ namespace {
 constexpr int kMerge = 96;              // threads that merge a part while the consumers are at the next one
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
+constexpr int kScaleLanes = 2 * kPage / 16;  // lanes that bring a page's scales
 
 // Q8: pages of e4m3.
 template <int D, int G, bool Q8>
@@ -52,8 +53,8 @@ struct Shape {
   // a stage always goes to the same one, which then sees each of its phases
   static constexpr int kStages = Q8 ? (D == 128 ? 9 : 18) : D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);
   static_assert(kStages % kGroups == 0, "a group must see every phase of its stages");
+  static_assert(kGroups * kScaleLanes <= 32, "a warp brings the scales of a stage of every group at once");
   static constexpr uint32_t kTile = kPage * D * (Q8 ? 1 : 2);  // bytes of a page's keys
-  static constexpr uint32_t kPageBytes = 2 * kTile + (Q8 ? 2 * kPage : 0);  // and values, and scales
 };
 
 // What a stage holds and what to do with it.
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1 + (Q8 ? kScaleLanes : 0));
       ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 4);
     }
     ptx::mbar_init(ptx::smem_u32(&sm.mfull), kWarps);
@@ -373,35 +374,51 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     auto over_run = [&](int64_t x) { return T < (int64_t)1 << 32 ? (int64_t)((uint32_t)x / (uint32_t)run) : x / run; };
     int it = 0, st = 0, ph = 0;  // stages filled; the next one and its phase
     bool ok = true;
-    // one stage; page < 0: none to load
-    auto emit = [&](const Meta& meta, int32_t page, int32_t head, int64_t seq) -> bool {
-      if (it >= kStages &&
-          !__all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[st]), ph ^ 1, abort)))
-        return false;
-      if (lane == 0) {
-        sm.meta[st] = meta;
-        const uint32_t full = ptx::smem_u32(&sm.full[st]);
-        const uint32_t bytes = (page >= 0 ? S::kPageBytes : 0u) + (meta.first ? (uint32_t)(G * D * 2) : 0u);
+    // The next n stages (at most kGroups), one a lane from lane `first` on, whose
+    // meta and page it holds (page < 0: none to load): a page's waits, barriers
+    // and addresses take some 600 cycles of a warp, whether for one lane or three.
+    auto emit = [&](int n, int first, const Meta& meta, int32_t page, int32_t head, int64_t seq) -> bool {
+      const int k = lane - first;
+      const bool mine = k >= 0 && k < n;
+      const bool wrap = st + k >= kStages;
+      const int s = mine ? (wrap ? st + k - kStages : st + k) : 0;
+      bool got = true;
+      if (mine && it + k >= kStages)
+        got = ptx::mbar_wait_fast(ptx::smem_u32(&sm.empty[s]), wrap ? ph : ph ^ 1, abort);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      const int32_t y = page >= 0 ? (int32_t)(((int64_t)page * pr.Hkv + head) * kPage) : -1;  // its first row
+      if (mine) {
+        sm.meta[s] = meta;
+        const uint32_t full = ptx::smem_u32(&sm.full[s]);
+        const uint32_t bytes = (page >= 0 ? 2 * kTile : 0u) + (meta.first ? (uint32_t)(G * D * 2) : 0u);
         ptx::mbar_arrive_expect_tx(full, bytes);
         if (page >= 0) {
-          const int32_t y = (int32_t)(((int64_t)page * pr.Hkv + head) * kPage);
           if constexpr (Q8) {
-            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][0]), &kmap, 0, y, full);
-            ptx::tma_load_2d(ptx::smem_u32(sm.kv[st][1]), &vmap, 0, y, full);
-            ptx::bulk_g2s(ptx::smem_u32(sm.scale[st][0]), kscales + y, kPage, full);
-            ptx::bulk_g2s(ptx::smem_u32(sm.scale[st][1]), vscales + y, kPage, full);
+            ptx::tma_load_2d(ptx::smem_u32(sm.kv[s][0]), &kmap, 0, y, full);
+            ptx::tma_load_2d(ptx::smem_u32(sm.kv[s][1]), &vmap, 0, y, full);
           } else {
-            ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][0]), &kmap, 0, y, 0, full);
-            ptx::tma_load_3d(ptx::smem_u32(sm.kv[st][1]), &vmap, 0, y, 0, full);
+            ptx::tma_load_3d(ptx::smem_u32(sm.kv[s][0]), &kmap, 0, y, 0, full);
+            ptx::tma_load_3d(ptx::smem_u32(sm.kv[s][1]), &vmap, 0, y, 0, full);
           }
         }
         if (meta.first)
-          ptx::bulk_g2s(ptx::smem_u32(sm.q[st]), q + (seq * pr.Hq + head * G) * D, G * D * 2, full);
+          ptx::bulk_g2s(ptx::smem_u32(sm.q[s]), q + (seq * pr.Hq + head * G) * D, G * D * 2, full);
+      }
+      if constexpr (Q8) {  // the scales, 16 bytes a lane, all in one go
+        const int r = lane / kScaleLanes, piece = lane % kScaleLanes;
+        const int ys = __shfl_sync(0xffffffffu, y, first + (r < n ? r : 0));
+        const int ss = __shfl_sync(0xffffffffu, s, first + (r < n ? r : 0));
+        if (r < n) {
+          if (ys >= 0)
+            ptx::cp_async_16(ptx::smem_u32(&sm.scale[ss][piece / 4][16 * (piece % 4)]),
+                             (piece < 4 ? kscales : vscales) + ys + 16 * (piece % 4));
+          ptx::cp_async_arrive_noinc(ptx::smem_u32(&sm.full[ss]));
+        }
       }
       __syncwarp();
-      ++it;
-      if (++st == kStages) {
-        st = 0;
+      it += n;
+      if ((st += n) >= kStages) {
+        st -= kStages;
         ph ^= 1;
       }
       return true;
@@ -464,26 +481,27 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
               set_status(status, PISA_DEV_BAD_INDEX);
             }
           }
-          unsigned todo = __ballot_sync(0xffffffffu, mine);
-          while (todo && ok) {
-            const int x = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int32_t bx = __shfl_sync(0xffffffffu, blk, x), px = __shfl_sync(0xffffffffu, page, x);
-            const int64_t key0 = (int64_t)bx * kPage;
-            meta.rel = (int32_t)(key0 - sp.t);
-            meta.klo = px < 0 ? kPage : (int16_t)max((int64_t)0, min((int64_t)kPage, sp.lo - key0));
-            meta.khi = (int16_t)min((int64_t)(kPage - 1), sp.t - key0);
-            meta.last = --left < kGroups;
-            meta.first = ++count <= kGroups;
-            ok = emit(meta, px, h, b);
-          }
+          // lane k takes over the k-th of them
+          const unsigned todo = __ballot_sync(0xffffffffu, mine);
+          const int cnt = __popc(todo), from = __fns(todo, 0, lane + 1) & 31;
+          blk = __shfl_sync(0xffffffffu, blk, from);
+          page = __shfl_sync(0xffffffffu, page, from);
+          const int64_t key0 = (int64_t)blk * kPage;
+          meta.rel = (int32_t)(key0 - sp.t);
+          meta.klo = page < 0 ? kPage : (int16_t)max((int64_t)0, min((int64_t)kPage, sp.lo - key0));
+          meta.khi = (int16_t)min((int64_t)(kPage - 1), sp.t - key0);
+          meta.last = left - lane <= kGroups;
+          meta.first = count + lane < kGroups;
+          for (int k = 0; k < cnt && ok; k += kGroups) ok = emit(min(kGroups, cnt - k), k, meta, page, h, b);
+          left -= cnt;
+          count += cnt;
         }
       }
       // each group has a stage of every part, if an empty one
-      for (; count < kGroups && ok; ++count) {
+      if (count < kGroups && ok) {
         meta.klo = kPage;
         meta.first = meta.last = 1;
-        ok = emit(meta, -1, h, b);
+        ok = emit(kGroups - count, 0, meta, -1, h, b);
       }
       u = i0 + s1;
       if (s1 == np) {
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       Meta meta;
       meta.item = -1;
       meta.first = 0;
-      for (int k = 0; k < kGroups && ok; ++k) ok = emit(meta, -1, 0, 0);
+      ok = emit(kGroups, 0, meta, -1, 0, 0);
     }
     // every copy lands before the CTA ends
     if (lane == 0)
