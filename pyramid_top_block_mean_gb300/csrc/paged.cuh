@@ -61,6 +61,16 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(x) : "r"(w));
   return codes_to_bf16(x);
 }
+// The codes of bytes 0 and 1, and of bytes 2 and 3, in fp16, of which every
+// code is a number (NaN's codes stay NaN).
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 // Two numbers, already over their row's power, to the nearest codes.
 __device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
   uint16_t d;
@@ -113,9 +123,12 @@ __device__ __forceinline__ void key_span(const MaskArgs& m, int64_t b, int64_t n
 // cap2 tanh(pre x), off by less than 2^-19 of itself whatever the cap: the
 // polynomial where the score is small against the cap (a large cap is no cap),
 // tanh u = 1 - 2 / (1 + e^2u), whose error is a few 2^-24 of the cap, elsewhere.
-__device__ __forceinline__ float cap_score(const MaskArgs& m, float x) {
+__device__ __forceinline__ float cap_small(const MaskArgs& m, float x) {
   const float y = x * m.by, w = y * y;
-  const float small = x * fmaf(w, fmaf(w, fmaf(w, m.tk[3], m.tk[2]), m.tk[1]), m.tk[0]);
+  return x * fmaf(w, fmaf(w, fmaf(w, m.tk[3], m.tk[2]), m.tk[1]), m.tk[0]);
+}
+__device__ __forceinline__ float cap_score(const MaskArgs& m, float x) {
+  const float y = x * m.by, small = cap_small(m, x);
   const float large = fmaf(-2.0f * m.cap2, __frcp_rn(1.0f + ptx::ex2(x * m.pre * (2.0f * kLog2e))), m.cap2);
   return fabsf(y) <= m.lim ? small : large;
 }

@@ -24,6 +24,25 @@
 // fp32, and the CTA that brings the last one joins them in the order of the
 // CTAs, so results do not depend on timing.
 //
+// 8-bit pages (Q8) are half the bytes, and the work on them has to keep up: a
+// page's loads take 700 cycles of an SM at the copy rate.
+//   - S = K q by m16n8k32 MMAs on the codes as they are.  A bf16 query is the sum
+//     of two e4m3 rows (split_query), each with its own accumulators, and a
+//     key's power of two is a factor of its scores.
+//   - The values' codes become fp16 (one instruction for two of them), paired
+//     over neighbouring keys by byte permutes, and O^T += V^T P in fp16 with the
+//     powers of two of the rows in P, relative to the largest so far.
+//   - A thread reads whole 16-byte pieces: the order of the contraction, and
+//     of O's rows, is the one in which they come, so that nothing is exchanged,
+//     and the stage is free before the work on it begins.
+//   - Four groups of two warps, 32 keys each: a warp's wait, maxima and
+//     reference serve two tiles of 16.
+// 64 sequences of up to 8192 tokens, capped, 157 us (5.0 TB/s), 2 x 131072
+// tokens 94 us (5.2 TB/s), 64 sequences' 35 selected blocks 70 us (4.2 TB/s).
+// The four schedulers bound it: about 300 instructions for 16 keys, half of
+// them on the integer pipe.  Converting keys and values to bf16 in registers
+// took 214, 124 and 86 us, one stage at a time from the producer 205 and 124.
+//
 // Measured (GB300): 64 ragged sequences of up to 8192 tokens, 32 / 8 heads, d
 // = 128: 237 us, 6.6 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
 // tokens 150 us (6.5 TB/s); 64 sequences' 35 selected blocks 97 us (6.0 TB/s);
@@ -45,15 +64,18 @@ constexpr int kScaleLanes = 2 * kPage / 16;  // lanes that bring a page's scales
 // Q8: pages of e4m3.
 template <int D, int G, bool Q8>
 struct Shape {
-  static constexpr int kGroups = Q8 ? 3 : 2;       // of consumer warps, which take turns at the pages
-  static constexpr int kWarps = 4 * kGroups;       // 16 keys of a page each
+  static constexpr int kGroups = Q8 ? 4 : 2;  // of consumer warps, which take turns at the pages
+  static constexpr int kKeys = Q8 ? 32 : 16;  // of a page a warp takes
+  static constexpr int kGroupWarps = kPage / kKeys;
+  static constexpr int kWarps = kGroupWarps * kGroups;
   static constexpr int kCons = 32 * kWarps;        // consumer threads
   static constexpr int kThreads = kCons + 32 + kMerge;  // and the producer warp
+  static constexpr int kBatch = 2;  // stages that the producer fills at once
   // as many as fit beside the merge buffer; a multiple of the groups, so that
   // a stage always goes to the same one, which then sees each of its phases
-  static constexpr int kStages = Q8 ? (D == 128 ? 9 : 18) : D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);
+  static constexpr int kStages = Q8 ? (D == 128 ? 8 : 16) : D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);
   static_assert(kStages % kGroups == 0, "a group must see every phase of its stages");
-  static_assert(kGroups * kScaleLanes <= 32, "a warp brings the scales of a stage of every group at once");
+  
   static constexpr uint32_t kTile = kPage * D * (Q8 ? 1 : 2);  // bytes of a page's keys
 };
 
@@ -150,21 +172,8 @@ __device__ __forceinline__ void merge_sync() { asm volatile("bar.sync 1, %0;" ::
 // 16-byte piece c of row r of an e4m3 page in shared memory (128- or 64-byte
 // rows, swizzled by TMA over their own length).
 template <int D>
-__device__ __forceinline__ uint32_t piece_at(uint32_t page, int r, int c) {
+__device__ __forceinline__ const uint8_t* piece_at(const uint8_t* page, int r, int c) {
   return page + r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
-}
-__device__ __forceinline__ uint4 lds16(uint32_t at) {
-  uint4 x;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "r"(at)
-               : "memory");
-  return x;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t at) {
-  uint2 x;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
-  return x;
 }
 
 // The D / 4 codes of quarter t of row r: the contraction's order is theirs, so
@@ -172,10 +181,10 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
 // the banks read two neighbouring rows: quarter t of a row of 128 is its
 // pieces 2 t and 2 t + 1, so that the two rows' pieces never share banks.
 template <int D>
-__device__ __forceinline__ void row_codes(uint32_t page, int r, int t, uint32_t (&w)[D / 16]) {
+__device__ __forceinline__ void row_codes(const uint8_t* page, int r, int t, uint32_t (&w)[D / 16]) {
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
-    const uint4 x = lds16(piece_at<D>(page, r, (D / 64) * t + i));
+    const uint4 x = *reinterpret_cast<const uint4*>(piece_at<D>(page, r, (D / 64) * t + i));
     w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
   }
 }
@@ -234,33 +243,39 @@ __device__ __forceinline__ float split_query(const uint16_t* row, bool there, ui
   return e == 255u ? NAN : __uint_as_float((e + 127u - 134u) << 23);
 }
 
-// The D / 8 codes of part g of rows r and r + 1, in pairs of the two rows:
-// dims 2 j and 2 j + 1 of the part as a[j][at] and a[j][at + 1], as bf16 numbers
-// times 2^-120.
+// The D / 8 codes of part g of row r.
 template <int D>
-__device__ __forceinline__ void column_pairs(uint32_t page, int r, int g, uint32_t (&a)[D / 16][4], int at) {
-  uint32_t x[2][D / 32];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (D == 128) {
-      const uint4 y = lds16(piece_at<D>(page, r + i, g));
-      x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
-    } else {
-      const uint2 y = lds8(piece_at<D>(page, r + i, g >> 1) + 8 * (g & 1));
-      x[i][0] = y.x; x[i][1] = y.y;
-    }
+__device__ __forceinline__ void part_codes(const uint8_t* page, int r, int g, uint32_t (&w)[D / 32]) {
+  if constexpr (D == 128) {
+    const uint4 x = *reinterpret_cast<const uint4*>(piece_at<D>(page, r, g));
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(piece_at<D>(page, r, g >> 1) + 8 * (g & 1));
+    w[0] = x.x; w[1] = x.y;
   }
+}
+// Two such parts in pairs: dims 2 j and 2 j + 1 of both as a[j][at] and a[j][at
+// + 1], in fp16, of which every code is a number.
+template <int D>
+__device__ __forceinline__ void pair_codes(const uint32_t (&x)[D / 32], const uint32_t (&y)[D / 32],
+                                           uint32_t (&a)[D / 16][4], int at) {
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
-    // byte k of both rows, each with its sign in the byte above
-    uint32_t y[4];
-    asm("prmt.b32 %0, %1, %2, 0xc480;" : "=r"(y[0]) : "r"(x[0][j]), "r"(x[1][j]));
-    asm("prmt.b32 %0, %1, %2, 0xd591;" : "=r"(y[1]) : "r"(x[0][j]), "r"(x[1][j]));
-    asm("prmt.b32 %0, %1, %2, 0xe6a2;" : "=r"(y[2]) : "r"(x[0][j]), "r"(x[1][j]));
-    asm("prmt.b32 %0, %1, %2, 0xf7b3;" : "=r"(y[3]) : "r"(x[0][j]), "r"(x[1][j]));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) a[2 * j + k / 2][at + (k & 1)] = codes_to_bf16(y[k]);
+    codes_to_half(__byte_perm(x[j], y[j], 0x5140), a[2 * j][at], a[2 * j][at + 1]);
+    codes_to_half(__byte_perm(x[j], y[j], 0x7362), a[2 * j + 1][at], a[2 * j + 1][at + 1]);
   }
+}
+__device__ __forceinline__ void mma16816_half(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 // Keys that the query of sequence b sees, and the pages that hold them; a
@@ -293,7 +308,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
                         const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ idx, Parts parts,
                         int32_t min_run, int32_t* __restrict__ status, uint16_t* __restrict__ out) {
   using S = Shape<D, G, Q8>;
-  constexpr int kStages = S::kStages, kGroups = S::kGroups, kWarps = S::kWarps, kCons = S::kCons;
+  constexpr int kStages = S::kStages, kGroups = S::kGroups, kWarps = S::kWarps, kCons = S::kCons, kBatch = S::kBatch;
   constexpr uint32_t kTile = S::kTile;
   constexpr int kHalf = kPage * 128;  // bytes of a tile's 64-column half
   extern __shared__ unsigned char smem_raw[];
@@ -312,7 +327,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&sm.full[s]), 1 + (Q8 ? kScaleLanes : 0));
-      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), 4);
+      ptx::mbar_init(ptx::smem_u32(&sm.empty[s]), S::kGroupWarps);
     }
     ptx::mbar_init(ptx::smem_u32(&sm.mfull), kWarps);
     ptx::mbar_init(ptx::smem_u32(&sm.mempty), kMerge / 32);
@@ -374,9 +389,9 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     auto over_run = [&](int64_t x) { return T < (int64_t)1 << 32 ? (int64_t)((uint32_t)x / (uint32_t)run) : x / run; };
     int it = 0, st = 0, ph = 0;  // stages filled; the next one and its phase
     bool ok = true;
-    // The next n stages (at most kGroups), one a lane from lane `first` on, whose
+    // The next n stages (at most kBatch), one a lane from lane `first` on, whose
     // meta and page it holds (page < 0: none to load): a page's waits, barriers
-    // and addresses take some 600 cycles of a warp, whether for one lane or three.
+    // and addresses take some 600 cycles of a warp, whether for one lane or two.
     auto emit = [&](int n, int first, const Meta& meta, int32_t page, int32_t head, int64_t seq) -> bool {
       const int k = lane - first;
       const bool mine = k >= 0 && k < n;
@@ -492,16 +507,16 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
           meta.khi = (int16_t)min((int64_t)(kPage - 1), sp.t - key0);
           meta.last = left - lane <= kGroups;
           meta.first = count + lane < kGroups;
-          for (int k = 0; k < cnt && ok; k += kGroups) ok = emit(min(kGroups, cnt - k), k, meta, page, h, b);
+          for (int k = 0; k < cnt && ok; k += kBatch) ok = emit(min(kBatch, cnt - k), k, meta, page, h, b);
           left -= cnt;
           count += cnt;
         }
       }
       // each group has a stage of every part, if an empty one
-      if (count < kGroups && ok) {
+      if (count < kGroups) {
         meta.klo = kPage;
         meta.first = meta.last = 1;
-        ok = emit(kGroups - count, 0, meta, -1, h, b);
+        for (; count < kGroups && ok; count += kBatch) ok = emit(min(kBatch, kGroups - count), 0, meta, -1, h, b);
       }
       u = i0 + s1;
       if (s1 == np) {
@@ -520,7 +535,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       Meta meta;
       meta.item = -1;
       meta.first = 0;
-      ok = emit(kGroups, 0, meta, -1, 0, 0);
+      for (int k = 0; k < kGroups && ok; k += kBatch) ok = emit(min(kBatch, kGroups - k), 0, meta, -1, 0, 0);
     }
     // every copy lands before the CTA ends
     if (lane == 0)
@@ -652,7 +667,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
 
   // ------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
-  const int r16 = 16 * (warp & 3);
+  const int r16 = S::kKeys * (warp % S::kGroupWarps);  // this warp's keys of a page
   // ldmatrix rows: lane l addresses row l % 8 of matrix l / 8
   const int krow = r16 + (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
   const int vrow = r16 + (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
@@ -664,8 +679,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   float oacc[D / 16][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
   float sl0 = 0.0f, sl1 = 0.0f;
-  // group warp / 4 takes every second stage (of three groups, every third)
-  int st = (warp >> 2) - kGroups, ph = 0, merges = 0;
+  // a group takes every kGroups-th stage
+  int st = warp / S::kGroupWarps - kGroups, ph = 0, merges = 0;
   auto wait_merged = [&] {  // the merge buffer is free
     const bool ok = merges == 0 || ptx::mbar_wait_fast(ptx::smem_u32(&sm.mempty), (merges - 1) & 1, abort);
     if (!__all_sync(0xffffffffu, ok)) {
@@ -710,138 +725,250 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         sl1 = 2 * tig + 1 < G ? sl[2 * tig + 1] * kLog2e : 0.0f;
       }
     }
-    if (meta.klo <= meta.khi && r16 <= meta.khi && r16 + 15 >= meta.klo) {
-      const uint32_t kb = ptx::smem_u32(sm.kv[st][0]), vb = ptx::smem_u32(sm.kv[st][1]);
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains
-      uint32_t av[D / 16][4];  // the values' fragments, on their way during the softmax
+    const bool seen_any = meta.klo <= meta.khi && r16 <= meta.khi && r16 + S::kKeys - 1 >= meta.klo;
+    // Q8: 16 keys and their values are 32 registers (of d = 128), so that the
+    // stage is free again before they are worked on.
+    constexpr int T = S::kKeys / 16;  // tiles of 16 keys
+    uint32_t kc[Q8 ? T : 1][2][D / 16], vc[Q8 ? T : 1][4][D / 32];
+    int ksc[T][2], vsc[T][2];  // and the scales
+    if constexpr (Q8) {
+      if (seen_any) {
+#pragma unroll
+        for (int u = 0; u < T; ++u) {
+          const int r = r16 + 16 * u + grp, c = r16 + 16 * u + 2 * tig;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            row_codes<D>(sm.kv[st][0], r + 8 * j, tig, kc[u][j]);
+            part_codes<D>(sm.kv[st][1], c + 8 * j, grp, vc[u][2 * j]);
+            part_codes<D>(sm.kv[st][1], c + 8 * j + 1, grp, vc[u][2 * j + 1]);
+            ksc[u][j] = sm.scale[st][0][r + 8 * j];
+            vsc[u][j] = sm.scale[st][1][r + 8 * j];
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
+    }
+    if (seen_any) {
       if constexpr (Q8) {
-        uint32_t k0[D / 16], k1[D / 16];
-        row_codes<D>(kb, r16 + grp, tig, k0);
-        row_codes<D>(kb, r16 + grp + 8, tig, k1);
+        // keys grp and grp + 8 of each tile, heads 2 tig and 2 tig + 1
+        float x[T][4];
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-          mma16832_e4m3(d, k0[ks], k1[ks], k0[ks + 1], k1[ks + 1], bq[ks], bq[ks + 1]);
-          mma16832_e4m3(e, k0[ks], k1[ks], k0[ks + 1], k1[ks + 1], bl[ks], bl[ks + 1]);
+        for (int u = 0; u < T; ++u) {
+          const uint32_t (&k0)[D / 16] = kc[u][0], (&k1)[D / 16] = kc[u][1];
+          float d[4] = {}, e[4] = {};  // of the query's upper part and its lower one
+#pragma unroll
+          for (int k = 0; k < D / 16; k += 2) {
+            mma16832_e4m3(d, k0[k], k1[k], k0[k + 1], k1[k + 1], bq[k], bq[k + 1]);
+            mma16832_e4m3(e, k0[k], k1[k], k0[k + 1], k1[k + 1], bl[k], bl[k + 1]);
+          }
+          const float fa = ksc[u][0] == 255 ? NAN : __uint_as_float((uint32_t)ksc[u][0] << 23);
+          const float fb = ksc[u][1] == 255 ? NAN : __uint_as_float((uint32_t)ksc[u][1] << 23);
+          x[u][0] = fmaf(e[0], 1.0f / 32, d[0]) * hf0 * fa; x[u][1] = fmaf(e[1], 1.0f / 32, d[1]) * hf1 * fa;
+          x[u][2] = fmaf(e[2], 1.0f / 32, d[2]) * hf0 * fb; x[u][3] = fmaf(e[3], 1.0f / 32, d[3]) * hf1 * fb;
         }
-        // The values' rows are the MMA's columns: a thread takes D / 8 codes of
-        // its four keys, 2 tig, 2 tig + 1 and 8 further, and pairs the keys
-        // byte by byte; the dims D / 8 grp + 2 mt and the next are rows grp and
-        // grp + 8 of step mt.
-        column_pairs<D>(vb, r16 + 2 * tig, grp, av, 0);
-        column_pairs<D>(vb, r16 + 2 * tig + 8, grp, av, 2);
+        if (mk.cap2 > 0.0f) {  // cap_score(), the form of large scores where there are some
+          bool large = false;
+#pragma unroll
+          for (int u = 0; u < T; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) large |= !(fabsf(x[u][j] * mk.by) <= mk.lim);
+          if (__any_sync(0xffffffffu, large)) {
+#pragma unroll
+            for (int u = 0; u < T; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[u][j] = cap_score(mk, x[u][j]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < T; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[u][j] = cap_small(mk, x[u][j]);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < T; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[u][j] *= pr.scale2;
+        }
+        if (mk.slopes) {
+#pragma unroll
+          for (int u = 0; u < T; ++u) {
+            const float ra = (float)(meta.rel + r16 + 16 * u + grp), rb = (float)(meta.rel + r16 + 16 * u + grp + 8);
+            x[u][0] = fmaf(sl0, ra, x[u][0]); x[u][1] = fmaf(sl1, ra, x[u][1]);
+            x[u][2] = fmaf(sl0, rb, x[u][2]); x[u][3] = fmaf(sl1, rb, x[u][3]);
+          }
+        }
+        const bool part = r16 < meta.klo || r16 + S::kKeys - 1 > meta.khi;  // some of the keys are not seen
+        if (part) {
+#pragma unroll
+          for (int u = 0; u < T; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int k = r16 + 16 * u + grp + 8 * j;
+              if (k < meta.klo || k > meta.khi) {
+                x[u][2 * j] = x[u][2 * j + 1] = -INFINITY;
+                vsc[u][j] = 0;  // its power has no say
+              }
+            }
+        }
+        float c0 = fmaxf(x[0][0], x[0][2]), c1 = fmaxf(x[0][1], x[0][3]);
+        int top = 0;
+#pragma unroll
+        for (int u = 0; u < T; ++u) {
+          c0 = ptx::max3(c0, x[u][0], x[u][2]);
+          c1 = ptx::max3(c1, x[u][1], x[u][3]);
+          top = max(top, max(vsc[u][0] == 255 ? 0 : vsc[u][0], vsc[u][1] == 255 ? 0 : vsc[u][1]));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+          c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
+          c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
+        }
+        const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
+        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1 || top > ref)) {
+          float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - n0);
+          float f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= f0;
+          l1 *= f1;
+          if (top > ref) {
+            const float f = __uint_as_float(max(ref - top + 127, 0) << 23);
+            ref = top;
+            f0 *= f;
+            f1 *= f;
+          }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            oacc[mt][0] *= f0; oacc[mt][2] *= f0;
+            oacc[mt][1] *= f1; oacc[mt][3] *= f1;
+          }
+        }
+        // a key without weight: its score is -inf (m is, only if all were)
+        const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+        for (int u = 0; u < T; ++u) {
+          const float p0 = ptx::ex2(x[u][0] - z0), p1 = ptx::ex2(x[u][1] - z1);
+          const float p2 = ptx::ex2(x[u][2] - z0), p3 = ptx::ex2(x[u][3] - z1);
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+          // The rows' powers go with the weights, relative to the largest so far.
+          // P is rounded to fp16 for the MMA, times 2^15: 2^-11 of each weight that
+          // is over 2^-29 of the largest, and 2^-40 of that below.
+          const float fa = vsc[u][0] == 255 ? NAN : __uint_as_float(max(vsc[u][0] - ref + 142, 0) << 23);
+          const float fb = vsc[u][1] == 255 ? NAN : __uint_as_float(max(vsc[u][1] - ref + 142, 0) << 23);
+          const uint32_t b0 = transpose8(pack_half(p0 * fa, p1 * fa)), b1 = transpose8(pack_half(p2 * fb, p3 * fb));
+          // The values' rows are the MMA's columns: a thread takes D / 8 codes of
+          // its four keys, 2 tig, 2 tig + 1 and 8 further, and pairs the keys
+          // byte by byte; the dims D / 8 grp + 2 mt and the next are rows grp and
+          // grp + 8 of step mt.
+          const int k2 = r16 + 16 * u + 2 * tig;
+          uint32_t av[D / 16][4];
+          pair_codes<D>(vc[u][0], vc[u][1], av, 0);
+          pair_codes<D>(vc[u][2], vc[u][3], av, 2);
+          uint32_t va = 0xffffffffu, vz = 0xffffffffu;  // masks of the value pairs
+          if (part) {
+            auto seen = [&](int k) { return k >= meta.klo && k <= meta.khi; };
+            va = (seen(k2) ? 0xffffu : 0u) | (seen(k2 + 1) ? 0xffff0000u : 0u);
+            vz = (seen(k2 + 8) ? 0xffffu : 0u) | (seen(k2 + 9) ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            if (part) {  // a value that is not seen may be anything
+              av[mt][0] &= va; av[mt][1] &= va;
+              av[mt][2] &= vz; av[mt][3] &= vz;
+            }
+            mma16816_half(oacc[mt], av[mt], b0, b1);
+          }
+        }
       } else {
-        uint32_t a[D / 16][4];
+        const uint32_t kb = ptx::smem_u32(sm.kv[st][0]), vb = ptx::smem_u32(sm.kv[st][1]);
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains
+        {
+          uint32_t a[D / 16][4];
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const int ch = 2 * ks + kch;
-          ldsm4(kb + (ch >> 3) * kHalf + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a[ks]);
-        }
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int ch = 2 * ks + kch;
+            ldsm4(kb + (ch >> 3) * kHalf + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a[ks]);
+          }
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-          mma16816(d, a[ks], bq[2 * ks], bq[2 * ks + 1]);
-          mma16816(e, a[ks + 1], bq[2 * ks + 2], bq[2 * ks + 3]);
+          for (int ks = 0; ks < D / 16; ks += 2) {
+            mma16816(d, a[ks], bq[2 * ks], bq[2 * ks + 1]);
+            mma16816(e, a[ks + 1], bq[2 * ks + 2], bq[2 * ks + 3]);
+          }
         }
+        uint32_t av[D / 16][4];  // the values' fragments, on their way during the softmax
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
           const int ch = 2 * mt + vch;
           ldsm4_t(vb + (ch >> 3) * kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), av[mt]);
         }
-      }
-      // keys grp and grp + 8 of this warp's 16, heads 2 tig and 2 tig + 1
-      float x[4];
-      if constexpr (Q8) {
-        const uint32_t s0 = sm.scale[st][0][r16 + grp], s1 = sm.scale[st][0][r16 + grp + 8];
-        const float f0 = s0 == 255u ? NAN : __uint_as_float(s0 << 23), f1 = s1 == 255u ? NAN : __uint_as_float(s1 << 23);
-        x[0] = fmaf(e[0], 1.0f / 32, d[0]) * hf0 * f0; x[1] = fmaf(e[1], 1.0f / 32, d[1]) * hf1 * f0;
-        x[2] = fmaf(e[2], 1.0f / 32, d[2]) * hf0 * f1; x[3] = fmaf(e[3], 1.0f / 32, d[3]) * hf1 * f1;
-      }
+        // keys grp and grp + 8 of this warp's 16, heads 2 tig and 2 tig + 1
+        float x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (!Q8) x[j] = d[j] + e[j];
-        x[j] = mk.cap2 > 0.0f ? cap_score(mk, x[j]) : x[j] * pr.scale2;
-      }
-      const int ka = r16 + grp;
-      if (mk.slopes) {
-        const float ra = (float)(meta.rel + ka), rb = (float)(meta.rel + ka + 8);
-        x[0] = fmaf(sl0, ra, x[0]); x[1] = fmaf(sl1, ra, x[1]);
-        x[2] = fmaf(sl0, rb, x[2]); x[3] = fmaf(sl1, rb, x[3]);
-      }
-      const bool part = r16 < meta.klo || r16 + 15 > meta.khi;  // some of the 16 keys are not seen
-      uint32_t va = 0xffffffffu, vz = 0xffffffffu;              // masks of the value pairs below
-      if (part) {
-        if (ka < meta.klo || ka > meta.khi) x[0] = x[1] = -INFINITY;
-        if (ka + 8 < meta.klo || ka + 8 > meta.khi) x[2] = x[3] = -INFINITY;
-        const int k2 = r16 + 2 * tig;
-        auto seen = [&](int k) { return k >= meta.klo && k <= meta.khi; };
-        va = (seen(k2) ? 0xffffu : 0u) | (seen(k2 + 1) ? 0xffff0000u : 0u);
-        vz = (seen(k2 + 8) ? 0xffffu : 0u) | (seen(k2 + 9) ? 0xffff0000u : 0u);
-      }
-      float c0 = fmaxf(x[0], x[2]), c1 = fmaxf(x[1], x[3]);
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) {
-        c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
-        c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
-      }
-      const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-        const float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - n0);
-        const float f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= f0;
-        l1 *= f1;
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt) {
-          oacc[mt][0] *= f0; oacc[mt][2] *= f0;
-          oacc[mt][1] *= f1; oacc[mt][3] *= f1;
+        for (int j = 0; j < 4; ++j) {
+          x[j] = d[j] + e[j];
+          x[j] = mk.cap2 > 0.0f ? cap_score(mk, x[j]) : x[j] * pr.scale2;
         }
-      }
-      // a key without weight: its score is -inf (m is, only if all were)
-      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-      const float p0 = ptx::ex2(x[0] - z0), p1 = ptx::ex2(x[1] - z1);
-      const float p2 = ptx::ex2(x[2] - z0), p3 = ptx::ex2(x[3] - z1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step)
-      uint32_t b0, b1;
-      if constexpr (Q8) {
-        // The rows' powers go with the weights, which keep all of their bits:
-        // relative to the largest power so far (no row's, without a key that is
-        // seen), times 2^60, half way up from the 2^-120 of the codes.
-        int sa = sm.scale[st][1][ka], sb = sm.scale[st][1][ka + 8];
+        const int ka = r16 + grp;
+        if (mk.slopes) {
+          const float ra = (float)(meta.rel + ka), rb = (float)(meta.rel + ka + 8);
+          x[0] = fmaf(sl0, ra, x[0]); x[1] = fmaf(sl1, ra, x[1]);
+          x[2] = fmaf(sl0, rb, x[2]); x[3] = fmaf(sl1, rb, x[3]);
+        }
+        const bool part = r16 < meta.klo || r16 + 15 > meta.khi;  // some of the 16 keys are not seen
+        uint32_t va = 0xffffffffu, vz = 0xffffffffu;              // masks of the value pairs below
         if (part) {
-          if (ka < meta.klo || ka > meta.khi) sa = 0;
-          if (ka + 8 < meta.klo || ka + 8 > meta.khi) sb = 0;
+          if (ka < meta.klo || ka > meta.khi) x[0] = x[1] = -INFINITY;
+          if (ka + 8 < meta.klo || ka + 8 > meta.khi) x[2] = x[3] = -INFINITY;
+          const int k2 = r16 + 2 * tig;
+          auto seen = [&](int k) { return k >= meta.klo && k <= meta.khi; };
+          va = (seen(k2) ? 0xffffu : 0u) | (seen(k2 + 1) ? 0xffff0000u : 0u);
+          vz = (seen(k2 + 8) ? 0xffffu : 0u) | (seen(k2 + 9) ? 0xffff0000u : 0u);
         }
-        const int top = __reduce_max_sync(0xffffffffu, max(sa == 255 ? 0 : sa, sb == 255 ? 0 : sb));
-        if (top > ref) {
-          const float f = __uint_as_float(max(ref - top + 127, 0) << 23);
-          ref = top;
+        float c0 = fmaxf(x[0], x[2]), c1 = fmaxf(x[1], x[3]);
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+          c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
+          c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
+        }
+        const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
+        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+          const float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - n0);
+          const float f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= f0;
+          l1 *= f1;
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt) {
-            oacc[mt][0] *= f; oacc[mt][1] *= f;
-            oacc[mt][2] *= f; oacc[mt][3] *= f;
+            oacc[mt][0] *= f0; oacc[mt][2] *= f0;
+            oacc[mt][1] *= f1; oacc[mt][3] *= f1;
           }
         }
-        const float fa = sa == 255 ? NAN : __uint_as_float(max(sa - ref + 187, 0) << 23);
-        const float fb = sb == 255 ? NAN : __uint_as_float(max(sb - ref + 187, 0) << 23);
-        b0 = transpose8(pack_bf16(p0 * fa, p1 * fa));
-        b1 = transpose8(pack_bf16(p2 * fb, p3 * fb));
-      } else {
-        b0 = transpose8(pack_bf16(p0, p1));
-        b1 = transpose8(pack_bf16(p2, p3));
-      }
+        // a key without weight: its score is -inf (m is, only if all were)
+        const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+        const float p0 = ptx::ex2(x[0] - z0), p1 = ptx::ex2(x[1] - z1);
+        const float p2 = ptx::ex2(x[2] - z0), p3 = ptx::ex2(x[3] - z1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        // P is rounded to bf16 for the MMA (2^-8 of each weight, the values' own step)
+        const uint32_t b0 = transpose8(pack_bf16(p0, p1)), b1 = transpose8(pack_bf16(p2, p3));
 #pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        if (part) {  // a value that is not seen may be anything
-          av[mt][0] &= va; av[mt][1] &= va;
-          av[mt][2] &= vz; av[mt][3] &= vz;
+        for (int mt = 0; mt < D / 16; ++mt) {
+          if (part) {  // a value that is not seen may be anything
+            av[mt][0] &= va; av[mt][1] &= va;
+            av[mt][2] &= vz; av[mt][3] &= vz;
+          }
+          mma16816(oacc[mt], av[mt], b0, b1);
         }
-        mma16816(oacc[mt], av[mt], b0, b1);
       }
     }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
+    if constexpr (!Q8) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
+    }
     if (!meta.last) continue;
 
     // ------------------ end of a part: hand (m, l, o) to the merging warps
@@ -856,8 +983,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       *reinterpret_cast<float2*>(&sm.m[warp][2 * tig]) = make_float2(m0, m1);
       *reinterpret_cast<float2*>(&sm.l[warp][2 * tig]) = make_float2(l0, l1);
     }
-    if constexpr (Q8) {  // O as it is: by 2^(ref - 127) and 2^60, in two steps
-      const int by = ref - 67, half = by >> 1;
+    if constexpr (Q8) {  // O as it is: by 2^(ref - 127) and 2^-15, in two steps
+      const int by = ref - 142, half = by >> 1;
       const float f = __uint_as_float((half + 127) << 23), f2 = __uint_as_float((by - half + 127) << 23);
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
