@@ -545,14 +545,17 @@ pisa_status pisa_cache_read(const pisa_params* p, int64_t n, const pisa_cache* c
                             const int32_t* new_lens, void* ws, size_t ws_bytes, void* k_out, void* v_out,
                             void* stream);
 
-/* pisa_dense_decode_paged and pisa_attend_decode_paged over a cache of either
- * format. */
+/* pisa_dense_decode_paged, pisa_attend_decode_paged and
+ * pisa_dense_prefill_paged over a cache of either format. */
 pisa_status pisa_cache_dense_decode(const pisa_params* p, const pisa_mask* mask, const void* q,
                                     const pisa_cache* cache, const int32_t* seq_lens, void* ws, size_t ws_bytes,
                                     void* out, void* stream);
 pisa_status pisa_cache_attend_decode(const pisa_params* p, const void* q, const pisa_cache* cache,
                                      const int32_t* seq_lens, const int32_t* idx, void* ws, size_t ws_bytes,
                                      void* out, void* stream);
+pisa_status pisa_cache_dense_prefill(const pisa_params* p, const pisa_mask* mask, int64_t n, const void* q,
+                                     const pisa_cache* cache, const int32_t* seq_lens, const int32_t* new_lens,
+                                     void* ws, size_t ws_bytes, void* out, void* stream);
 
 /* Synchronises `stream`, then copies the workspace status word into
  * *device_code (PISA_DEV_*).  Returns PISA_ERR_DEVICE when it is non-zero. */

@@ -256,6 +256,13 @@ pisa_status pisa_dense_prefill_paged(const pisa_params* p, const pisa_mask* mask
                                      const void* k_pages, const void* v_pages, int64_t num_pages,
                                      const int32_t* page_table, const int32_t* seq_lens, const int32_t* new_lens,
                                      void* ws, size_t ws_bytes, void* out, void* stream) {
+  const pisa_cache c = own_cache(k_pages, v_pages, num_pages, page_table);
+  return pisa_cache_dense_prefill(p, mask, n, q, &c, seq_lens, new_lens, ws, ws_bytes, out, stream);
+}
+
+pisa_status pisa_cache_dense_prefill(const pisa_params* p, const pisa_mask* mask, int64_t n, const void* q,
+                                     const pisa_cache* cache, const int32_t* seq_lens, const int32_t* new_lens,
+                                     void* ws, size_t ws_bytes, void* out, void* stream) {
   Prob pr; Pyr s; bool empty = false; Pools pools; MaskArgs m;
   pisa_status rc = common_checks(p, n, &pr, &s, &empty);
   if (rc != PISA_OK || empty) return rc;
@@ -263,7 +270,7 @@ pisa_status pisa_dense_prefill_paged(const pisa_params* p, const pisa_mask* mask
   rc = mask_checks(pr, mask, &m);
   if (rc != PISA_OK) return rc;
   if (!q || !out) return PISA_ERR_INVALID_ARG;
-  rc = pool_checks(pr, s, k_pages, v_pages, num_pages, page_table, seq_lens, ws, &pools);
+  rc = cache_checks(pr, s, cache, seq_lens, ws, &pools);
   if (rc != PISA_OK) return rc;
   if (!aligned16(q) || !aligned16(out) || !aligned4(new_lens)) return PISA_ERR_MISALIGNED;
   // groups of rows (16 tokens and more of a key head) are numbered in 32 bits

@@ -49,17 +49,24 @@ constexpr int kKeys = 128;  // keys of a tile
 constexpr int kPage = 64;
 constexpr int kMmaWarp = 8;   // warps 0-3 and 4-7: softmax of tile 0 and 1; 8 and 9: their MMAs
 constexpr int kLoadWarp = 10;
-constexpr int kThreads = 384;  // warp 11 only makes up the third warpgroup
-// Registers a thread: the softmax warpgroups hold a row of S each, the third
-// gives up what they need (2 x 216 + 72 = 3 x 168, the launch's share).
+constexpr int kConvWarp = 12;  // Q8: warps 12-15 convert
+// Registers a thread: the softmax warpgroups hold a row of S each, the others
+// give up what they need (2 x 216 + 72 = 3 x 168, the launch's share; with the
+// converting warpgroup 2 x 200 + 64 + 48 = 4 x 128).
 #define PISA_SOFTMAX_REGS "216"
 #define PISA_OTHER_REGS "72"
+#define PISA_SOFTMAX_REGS_Q8 "200"
+#define PISA_OTHER_REGS_Q8 "64"
+#define PISA_CONVERT_REGS_Q8 "48"
 constexpr float kSlack = 8.0f;  // log2 of how far weights may exceed 1
 
-template <int D>
+// Q8: pages of e4m3.
+template <int D, bool Q8>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kThreads = Q8 ? 512 : 384;  // warp 11 only makes up the third warpgroup
+  static constexpr int kStages = D == 128 ? 5 : (Q8 ? 7 : 10);
   static constexpr uint32_t kTile = kKeys * D * 2;  // bytes of a key or value tile, and of a query tile
+  static constexpr uint32_t kCodes = kKeys * D;     // and of a tile in e4m3
 };
 
 constexpr int kItems = 2;  // items in flight: the loader is at most one ahead
@@ -73,15 +80,23 @@ struct Item {
   int32_t fits;             // its lengths do
   int32_t ja, jb;           // key tiles
   int32_t wa[2], wb[2];     // and those that each row tile takes part in
-  int32_t khi;              // last key that any row sees
+  int32_t klo, khi;         // first and last key that any row sees
   int32_t fill;             // fills of the ring before the item's first
 };
 
-template <int D>
+template <int D, bool Q8>
 struct Smem {
-  uint8_t q[2][Cfg<D>::kTile];
-  uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTile];
-  uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
+  using C = Cfg<D, Q8>;
+  uint8_t q[2][C::kTile];
+  uint8_t kv[C::kStages][C::kTile];
+  // Q8: a tile's codes.  Of d = 128 they take the second half of its stage: the
+  // thread that turns a row's codes into its numbers puts the second half of
+  // these where the codes were, and nobody else's.
+  uint8_t codes[Q8 && D == 64 ? C::kStages : 1][Q8 && D == 64 ? C::kCodes : 16];
+  uint8_t scale[Q8 ? C::kStages : 1][Q8 ? kKeys : 16];  // the rows'
+  int32_t have[C::kStages];                             // bit p: page p of the tile is there
+  uint64_t raw[C::kStages];                             // the codes are
+  uint64_t full[C::kStages], empty[C::kStages];
   uint64_t ifull[kItems], iempty[kItems];
   uint64_t qfull[2], qempty[2], scrub, sfull[2], pfull[2][2], odone[2], done[2], lent, rows_out;
   Item item[kItems];
@@ -93,6 +108,7 @@ struct Smem {
 struct Args {
   int64_t n, nb, num_pages;
   const uint16_t *q, *k, *v;
+  const uint8_t *ks, *vs;  // scales of e4m3 rows
   const int32_t *seq_lens, *new_lens, *table;
   int32_t *status, *claimed;  // claimed: items taken beyond each CTA's first
   uint16_t* out;
@@ -321,6 +337,28 @@ __device__ __noinline__ void mark_tiles(const Args& a, int32_t Hkv, int32_t bh, 
   }
 }
 
+// The same for pages of e4m3, whose rows are finite or NaN throughout (scale
+// 255): true for a lane that sees one of the latter.
+__device__ __noinline__ bool sees_nan_row(const Args& a, int32_t Hkv, int32_t bh, int32_t ja, int32_t jb, int32_t lo,
+                                          int32_t hi) {
+  const int lane = threadIdx.x & 31;
+  const int64_t b = (uint32_t)bh / (uint32_t)Hkv;
+  const int64_t h = bh - b * Hkv;
+  bool found = false;
+  for (int32_t key0 = ja * kKeys; key0 < jb * kKeys; key0 += kPage) {
+    const int32_t first = max(lo - key0, 0), last = min(hi - key0, kPage - 1);
+    const bool none = found || first > last;
+    if (__all_sync(0xffffffffu, none)) continue;
+    const int32_t page = a.table[b * a.nb + key0 / kPage];
+    if (page < 0 || page >= a.num_pages) continue;
+    const uint8_t* s = a.vs + ((int64_t)page * Hkv + h) * kPage + lane;
+    const uint32_t m0 = __ballot_sync(0xffffffffu, s[0] == 255), m1 = __ballot_sync(0xffffffffu, s[32] == 255);
+    const uint64_t nan = (uint64_t)m1 << 32 | m0;
+    if (!none) found = (nan >> first & ~0ull >> (kPage - 1 - (last - first))) != 0;
+  }
+  return found;
+}
+
 // Sets the marked outputs of the warp's rows: out + orow, or with splits the
 // part at `at`.
 template <int D>
@@ -345,20 +383,20 @@ __device__ __noinline__ void set_marked(const Args& a, bool row, int64_t orow, i
 }
 
 // MODE 0: scores are scale * q . k; 1: with a cap and / or a distance bias.
-template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int MODE, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ Prob pr, const __grid_constant__ MaskArgs mk,
                          const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
-  constexpr int kStages = Cfg<D>::kStages;
-  constexpr uint32_t kTile = Cfg<D>::kTile;
+  constexpr int kStages = Cfg<D, Q8>::kStages;
+  constexpr uint32_t kTile = Cfg<D, Q8>::kTile;
   constexpr uint32_t kHalf = kKeys * 128;      // bytes of a tile's 64-column half
   constexpr uint32_t kPageHalf = kPage * 128;  // and of a page's
   constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRows, kKeys);
   constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);  // values MN-major
   extern __shared__ unsigned char smem_raw[];
-  Smem<D>& sm =
-      *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Smem<D, Q8>& sm =
+      *reinterpret_cast<Smem<D, Q8>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int32_t* abort = &sm.abort;
 
@@ -369,12 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
-      ptx::mbar_init(ptx::smem_u32(&sm.full[k]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.raw[k]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sm.full[k]), Q8 ? 4 : 1);
       ptx::mbar_init(ptx::smem_u32(&sm.empty[k]), 2);
     }
     for (int k = 0; k < kItems; ++k) {
       ptx::mbar_init(ptx::smem_u32(&sm.ifull[k]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sm.iempty[k]), 10);
+      ptx::mbar_init(ptx::smem_u32(&sm.iempty[k]), Q8 ? 14 : 10);
     }
     ptx::mbar_init(ptx::smem_u32(&sm.scrub), 1);
     ptx::mbar_init(ptx::smem_u32(&sm.lent), 1);
@@ -410,8 +449,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tokens = 1 << a.lg_tokens;  // of one row tile
   const uint32_t heads = (uint32_t)(pr.B * pr.Hkv);
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_OTHER_REGS ";");
+  if (Q8 && warp >= kConvWarp) {
+    // ----------------------------------------------------------- converters
+    // Thread r turns row r of a tile into bf16, exactly: codes to numbers (see
+    // row_factor), 64 of them at a time, into the rows' place of the MMAs'
+    // operand.  The 8 lanes of one pass over the banks have the 8 rows of a
+    // swizzle: no two of their pieces share banks, read or written.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_CONVERT_REGS_Q8 ";");
+    const int r = threadIdx.x & 127;
+    bool ok = true;
+    int st = 0, ph = 0;
+    for (int items = 0;; ++items) {
+      ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(&sm.ifull[items % kItems]),
+                                                             (items / kItems) & 1, abort)) != 0;
+      if (!ok) break;
+      const Item* ip = &sm.item[items % kItems];
+      if (ip->bh < 0) break;
+      const int ja = ip->ja, jb = ip->jb, klo = ip->klo, khi = ip->khi;
+      const bool clean = ip->clean != 0;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.iempty[items % kItems]));
+      for (int f = 0; f < 2 * (jb - ja) && ok; ++f) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_fast(ptx::smem_u32(&sm.raw[st]), ph, abort)) != 0;
+        if (!ok) break;
+        const uint8_t* from = (D == 64 ? sm.codes[D == 64 ? st : 0] : sm.kv[st] + kTile / 2) + r * D;
+        const uint32_t scale = sm.scale[Q8 ? st : 0][r];
+        // A value that no row of the item sees (behind the sequence's end among
+        // them) may be anything, and a weight of zero does not undo a NaN: it
+        // becomes zero; "clean", so does one that is not finite.
+        const int32_t key = (ja + (f >> 1)) * kKeys + r;
+        const bool zero = (f & 1) != 0 && (key < klo || key > khi || (sm.have[st] >> (r / kPage) & 1) == 0 ||
+                                           (clean && scale == 255u));
+        const uint32_t by = zero ? 0u : row_factor(scale), more = row_is_large(scale) ? row_factor_large(scale) : 0u;
+#pragma unroll
+        for (int hh = 0; hh < D / 64; ++hh) {
+          uint4 c[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            c[i] = *reinterpret_cast<const uint4*>(from + (((4 * hh + i) ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
+          uint8_t* to = sm.kv[st] + hh * kHalf + r * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[2 * k] = mul_bf16x2(codes_lo(w[k]), by);
+              x[2 * k + 1] = mul_bf16x2(codes_hi(w[k]), by);
+            }
+            if (more && !zero) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = mul_bf16x2(x[k], more);
+            }
+            *reinterpret_cast<uint4*>(to + (((2 * i) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(to + (((2 * i + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
+        if (++st == kStages) { st = 0; ph ^= 1; }
+      }
+      if (++st == kStages) { st = 0; ph ^= 1; }  // the stage that the rows go out through
+    }
+    if (!ok && lane == 0) *abort = 1;
+  } else if (warp >= 8) {
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_OTHER_REGS_Q8 ";");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_OTHER_REGS ";");
     if (warp == kLoadWarp) {
       // ------------------------------------------------------------ loader
       bool ok = true;
@@ -523,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.wb[v] = hi[v] < 0 ? it.jb : min(it.jb, hi[v] / kKeys + 1);
           if (it.wb[v] < it.wa[v]) it.wb[v] = it.wa[v];
         }
+        it.klo = klo;
         it.khi = khi;
         it.fill = fills;
         // lane l: the page of block 2 j + l, -1: none of its keys is seen, -2: outside the pool
@@ -591,9 +696,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fills >= kStages && !wait(&sm.empty[st], ph ^ 1)) break;  // the first round finds them empty
             if (lent == st && !take_back()) break;
             const uint32_t full = ptx::smem_u32(&sm.full[st]), dst = ptx::smem_u32(sm.kv[st]);
-            const bool scrub = kv == 1 && (clear || clean);
-            const uint32_t bar = scrub ? ptx::smem_u32(&sm.scrub) : full;
-            if (lane == 0) {
+            const bool scrub = !Q8 && kv == 1 && (clear || clean);
+            const uint32_t bar = Q8 ? ptx::smem_u32(&sm.raw[st]) : scrub ? ptx::smem_u32(&sm.scrub) : full;
+            if (Q8 && lane == 0) {  // the converters do the rest
+              sm.have[st] = (pg[0] >= 0 ? 1 : 0) | (pg[1] >= 0 ? 2 : 0);
+              if (pages) ptx::mbar_arrive_expect_tx(bar, pages * kPage * (D + 1));
+              else ptx::mbar_arrive(bar);
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                if (pg[p] < 0) continue;
+                const int32_t y = (int32_t)(((int64_t)pg[p] * pr.Hkv + h) * kPage);
+                ptx::tma_load_2d(ptx::smem_u32(D == 64 ? sm.codes[D == 64 ? st : 0] : sm.kv[st] + kTile / 2) +
+                                     p * (kPage * D),
+                                 kv ? &vmap : &kmap, 0, y, bar);
+                ptx::bulk_g2s(ptx::smem_u32(sm.scale[Q8 ? st : 0]) + p * kPage, (kv ? a.vs : a.ks) + y, kPage, bar);
+              }
+            } else if (!Q8 && lane == 0) {
               if (pages) ptx::mbar_arrive_expect_tx(bar, pages * (kTile / 2));
               else if (!scrub) ptx::mbar_arrive(bar);
 #pragma unroll
@@ -640,6 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(ptx::smem_u32(&sm.lent));
           // nobody else sees it filled or releases it: rows_out says when it is free
           ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
+          if (Q8) {
+            for (int k = 1; k < 4; ++k) ptx::mbar_arrive(ptx::smem_u32(&sm.full[st]));
+            ptx::mbar_arrive(ptx::smem_u32(&sm.raw[st]));
+          }
           ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
           ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
         }
@@ -658,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int v = 0; v < 2; ++v)
           if (qfills[v]) ptx::mbar_wait_fast(ptx::smem_u32(&sm.qfull[v]), (qfills[v] - 1) & 1, &sm.zero);
         for (int f = max(0, fills - kStages); f < fills; ++f)
-          ptx::mbar_wait_fast(ptx::smem_u32(&sm.full[f % kStages]), (f / kStages) & 1, &sm.zero);
+          ptx::mbar_wait_fast(ptx::smem_u32(Q8 ? &sm.raw[f % kStages] : &sm.full[f % kStages]), (f / kStages) & 1,
+                              &sm.zero);
       }
       __syncwarp();
     } else if (warp < kLoadWarp) {
@@ -751,7 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 " PISA_SOFTMAX_REGS ";");
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 " PISA_SOFTMAX_REGS_Q8 ";");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 " PISA_SOFTMAX_REGS ";");
     const int w = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * D;
@@ -1048,7 +1172,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ip->clean) {  // (a row of NaN scores is NaN already)
         Marks<D> marks = {};
-        mark_tiles<D>(a, pr.Hkv, ip->bh, wa, wb, lo, row ? hi : -1, &marks);
+        if constexpr (Q8) {
+          if (sees_nan_row(a, pr.Hkv, ip->bh, wa, wb, lo, row ? hi : -1)) {
+            for (int k = 0; k < D / 64; ++k)
+              for (int e = 0; e < 2; ++e) marks.up[k][e] = marks.down[k][e] = 0xffffffffu;
+          }
+        } else {
+          mark_tiles<D>(a, pr.Hkv, ip->bh, wa, wb, lo, row ? hi : -1, &marks);
+        }
         set_marked<D>(a, row && any && l < INFINITY, ((b * pr.Hq + hq) * a.n + i) * D, at, &marks);
       } else if (__any_sync(0xffffffffu, row && finite != 0.0f)) {
         if (lane == 0) *(volatile int32_t*)&sm.again[items % kItems] = 1;
@@ -1186,15 +1317,16 @@ Plan make_plan(const Prob& pr, int64_t n) {
   return p;
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool Q8>
 cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const Plan& pl, const CUtensorMap& qmap,
                      const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& a, int num_sms, cudaStream_t st) {
-  const size_t smem = sizeof(Smem<D>) + 1024;
-  auto kern = paged_prefill_kernel<D, MODE>;
+  const size_t smem = sizeof(Smem<D, Q8>) + 1024;
+  auto kern = paged_prefill_kernel<D, MODE, Q8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   note_launch();
-  e = launch_pdl(true, kern, dim3((unsigned)std::min<int64_t>(a.items, num_sms)), dim3(kThreads), smem, st, pr, m,
+  e = launch_pdl(true, kern, dim3((unsigned)std::min<int64_t>(a.items, num_sms)), dim3(Cfg<D, Q8>::kThreads), smem,
+                 st, pr, m,
                  qmap, kmap, vmap, a);
   if (e != cudaSuccess || pl.splits == 1) return e;
   note_launch();
@@ -1220,8 +1352,9 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   const Plan pl = make_plan(pr, n);
   CUtensorMap qmap, kmap, vmap;
   const int64_t rows = pools.num_pages * pr.Hkv * kPage;
-  if (!make_tmap_rows(&kmap, pools.k, rows, pr.d, kPage) || !make_tmap_rows(&vmap, pools.v, rows, pr.d, kPage) ||
-      !make_tmap_q(&qmap, q, pr.B, pr.Hq, n, pr.d, pr.G, 1 << pl.lg_tokens))
+  const bool in8 = pools.ks != nullptr;
+  if (!(in8 ? make_tmap_codes : make_tmap_rows)(&kmap, pools.k, rows, pr.d, kPage) ||
+      !(in8 ? make_tmap_codes : make_tmap_rows)(&vmap, pools.v, rows, pr.d, kPage) || !make_tmap_q(&qmap, q, pr.B, pr.Hq, n, pr.d, pr.G, 1 << pl.lg_tokens))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_clear(ws, 256, st);
   if (e != cudaSuccess) return e;
@@ -1229,6 +1362,7 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   a.n = n; a.nb = pools.nb; a.num_pages = pools.num_pages;
   a.q = (const uint16_t*)q; a.k = (const uint16_t*)pools.k; a.v = (const uint16_t*)pools.v;
   a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = pools.table;
+  a.ks = pools.ks; a.vs = pools.vs;
   a.status = (int32_t*)ws;
   a.claimed = (int32_t*)ws + 32;  // cleared with the status word
   a.out = (uint16_t*)out;
@@ -1242,11 +1376,15 @@ cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, c
   if (sms < 1) return cudaErrorInvalidDevice;
   a.tiles = pl.tiles; a.splits = pl.splits; a.lg_tokens = pl.lg_tokens;
   const bool shaped = m.cap2 > 0.0f || m.slopes;  // scores that are more than scaled dots
-  if (pr.d == 128)
-    return shaped ? launch_t<128, 1>(pr, m, pl, qmap, kmap, vmap, a, sms, st)
-                  : launch_t<128, 0>(pr, m, pl, qmap, kmap, vmap, a, sms, st);
-  return shaped ? launch_t<64, 1>(pr, m, pl, qmap, kmap, vmap, a, sms, st)
-                : launch_t<64, 0>(pr, m, pl, qmap, kmap, vmap, a, sms, st);
+  auto go = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (in8)
+      return shaped ? launch_t<D, 1, true>(pr, m, pl, qmap, kmap, vmap, a, sms, st)
+                    : launch_t<D, 0, true>(pr, m, pl, qmap, kmap, vmap, a, sms, st);
+    return shaped ? launch_t<D, 1, false>(pr, m, pl, qmap, kmap, vmap, a, sms, st)
+                  : launch_t<D, 0, false>(pr, m, pl, qmap, kmap, vmap, a, sms, st);
+  };
+  return pr.d == 128 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 64>());
 }
 
 }  // namespace pisa

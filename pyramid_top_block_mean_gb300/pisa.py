@@ -42,7 +42,7 @@ EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pi
             "pisa_read_static_status", "pisa_test_inject_leaf_timeout", "pisa_append_paged",
             "pisa_dense_decode_paged", "pisa_attend_decode_paged", "pisa_dense_prefill_paged",
             "pisa_paged_workspace_bytes", "pisa_cache_append", "pisa_cache_read",
-            "pisa_cache_dense_decode", "pisa_cache_attend_decode"]
+            "pisa_cache_dense_decode", "pisa_cache_attend_decode", "pisa_cache_dense_prefill"]
 
 
 class Params(ctypes.Structure):
@@ -130,6 +130,8 @@ _lib.pisa_cache_dense_decode.argtypes = [_P, _M, _vp, _C, _vp, _vp, ctypes.c_siz
 _lib.pisa_cache_dense_decode.restype = ctypes.c_int
 _lib.pisa_cache_attend_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_cache_attend_decode.restype = ctypes.c_int
+_lib.pisa_cache_dense_prefill.argtypes = [_P, _M, ctypes.c_int64, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.pisa_cache_dense_prefill.restype = ctypes.c_int
 _lib.pisa_paged_workspace_bytes.argtypes = [_P, ctypes.c_int64]
 _lib.pisa_paged_workspace_bytes.restype = ctypes.c_size_t
 _lib.pisa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32), _vp]
@@ -488,8 +490,16 @@ def _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, space, o
                    _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space, out)
 
 
-def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, stream, check) -> int:
+def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, scales, stream,
+                   check) -> int:
     index, dt, n = q.get_device(), _dtype(p), q.shape[2]
+    if scales is not None:
+        cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+        return _launch(index, stream, "pisa_cache_dense_prefill", check, _lib.pisa_cache_dense_prefill,
+                       ctypes.byref(p), _mask_arg(mask, p, n, index), n,
+                       _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), ctypes.byref(cache), lens,
+                       None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space,
+                       out)
     cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
     return _launch(index, stream, "pisa_dense_prefill_paged", check, _lib.pisa_dense_prefill_paged, ctypes.byref(p),
                    _mask_arg(mask, p, n, index), n, _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), *cache,
@@ -550,11 +560,13 @@ def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, id
 
 
 def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out, new_lens=None,
-                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True) -> int:
-    """q and out [B, H_q, n, d]: attention of n new tokens per sequence over the pages that hold them already."""
+                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True, scales=None) -> int:
+    """q and out [B, H_q, n, d]: attention of n new tokens per sequence over the
+    pages that hold them already (scales: of e4m3 pages)."""
     index = q.get_device()
     return _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, _want_space(ws, index),
-                          _want(out, "out", (p.B, p.H_q, q.shape[2], p.d), _dtype(p), index), mask, stream, check)
+                          _want(out, "out", (p.B, p.H_q, q.shape[2], p.d), _dtype(p), index), mask, scales, stream,
+                          check)
 
 
 def read_device_status(ws: torch.Tensor, stream=None) -> int:
@@ -729,10 +741,11 @@ class PagedAttention:
                          stream, True)
         return out
 
-    def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None):
+    def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None,
+                      scales=None):
         out = self._buffer("prefill", q)
         _dense_prefill(self.p, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space, out.data_ptr(), mask,
-                       stream, True)
+                       scales, stream, True)
         return out
 
     def device_status(self, stream=None) -> int:

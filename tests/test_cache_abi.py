@@ -49,7 +49,10 @@ def calls(pisa, p):
     def selected(c, lens=A, ws=A, size=BIG, q=A, out=A, idx=A):
         return L.pisa_cache_attend_decode(P, q, c, lens, idx, ws, size, out, None)
 
-    return dict(append=append, read=read, dense=dense, selected=selected)
+    def prefill(c, lens=A, ws=A, size=BIG, q=A, out=A, mask=None, n=4, new=A):
+        return L.pisa_cache_dense_prefill(P, mask, n, q, c, lens, new, ws, size, out, None)
+
+    return dict(append=append, read=read, dense=dense, selected=selected, prefill=prefill)
 
 
 def test_caches_are_checked(pisa):
@@ -126,8 +129,10 @@ def test_attention_refusals(pisa):
         assert on[name](c, q=None) == -1 and on[name](c, q=MIS) == -3, name
         for dtype, d, code in (("fp32", 128, -2), ("bf16", 96, -2)):
             assert calls(pisa, pisa.make_params(2, 4096, 16, 4, d, K=8, dtype=dtype))[name](c) == code, name
-    for name in ("dense", "selected"):
+    for name in ("dense", "selected", "prefill"):
         assert on[name](c, out=None) == -1 and on[name](c, out=MIS) == -3, name
     assert on["selected"](c, idx=None) == -1 and on["selected"](c, idx=ODD) == -3
     bad = pisa.Mask(ctypes.sizeof(pisa.Mask), -1.0, 0, None, None, None)
-    assert on["dense"](c, mask=ctypes.byref(bad)) == -1
+    assert on["dense"](c, mask=ctypes.byref(bad)) == -1 and on["prefill"](c, mask=ctypes.byref(bad)) == -1
+    assert on["prefill"](c, n=-1) == -1 and on["prefill"](c, n=4097) == -1 and on["prefill"](c, new=ODD) == -3
+    assert on["prefill"](None, n=0) == 0

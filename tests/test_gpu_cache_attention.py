@@ -200,3 +200,144 @@ def test_selected_decode(pisa, d, Hq, Hkv, K):
         want, tol = R.selected(q[b], k[b], v[b], n, idx[b], d ** -0.5)
         R.within(out[b], want, tol, f"sequence {b}")
     assert bool((out[0, :Hq // Hkv] == 0).all())
+
+
+# ------------------------------------------------------------------- prompts
+def run_prefill(pisa, Hq, Hkv, d, N, n, lens, new, seed=0, softcap=0.0, window=0, slopes=False, first=None,
+                prefix=None, amp=2.0, scale=0.0, status=0, change=None, poke=None):
+    B = len(lens)
+    k, v, kp, vp, scales, table = cache(B, Hkv, N, d, lens, seed, change=change)
+    if poke is not None:
+        poke(scales, table)
+    q = (torch.randn(B, Hq, n, d, generator=torch.Generator().manual_seed(seed + 1)) * amp).to(torch.bfloat16).cuda()
+    p = pisa.make_params(B, N, Hq, Hkv, d, scale=scale)
+    ws = torch.empty(pisa.paged_workspace_bytes(p, n), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, MARK)
+    sl = slopes_of(Hq) if slopes else None
+    mask = None
+    if softcap or window or slopes or first is not None or prefix is not None:
+        mask = pisa.AttentionMask(softcap, window, sl, first, None if prefix is None else i32(prefix))
+    pisa.dense_prefill_paged(p, q, kp, vp, table, i32(lens), ws, out, i32(new), mask, scales=scales)
+    assert pisa.read_device_status(ws) == status
+    for b in range(B):
+        cnt = min(max(new[b], 0), n)
+        if not (0 <= new[b] <= min(n, lens[b]) and lens[b] <= N):
+            assert bool((out[b, :, :cnt] == 0).all())
+        elif cnt:
+            pos = torch.arange(lens[b] - cnt, lens[b], device="cuda")
+            want, tol = R.dense(q[b, :, :cnt], k[b], v[b], lens[b], pos, scale or d ** -0.5, softcap, window, sl,
+                                None if first is None else first[b, :cnt], 0 if prefix is None else prefix[b])
+            R.within(out[b, :, :cnt], want, tol, f"sequence {b}")
+        assert bool((out[b, :, cnt:] == MARK).all()), "rows behind the new tokens were written"
+    return out
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 2, 2), (64, 16, 2), (128, 3, 3), (128, 4, 2), (128, 8, 2), (128, 8, 1)])
+@pytest.mark.parametrize("n,lens,new", [
+    (1, [1, 2, 130, 500], [1, 1, 1, 1]), (3, [3, 66, 500, 0], [3, 2, 1, 0]),
+    (64, [64, 128, 500, 65], [64, 64, 60, 1]), (129, [129, 130, 500, 256], [129, 65, 127, 128]),
+    (300, [300, 311, 500, 299], [300, 300, 257, 299])])
+def test_prefill_lengths(pisa, d, Hq, Hkv, n, lens, new):
+    run_prefill(pisa, Hq, Hkv, d, 500, n, lens, new, seed=n + d)
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=50.0), dict(softcap=1.5, amp=8.0), dict(window=1), dict(window=100),
+                                dict(slopes=True), dict(prefix=[0, 50, 300, 1000]), dict(scale=0.5),
+                                dict(softcap=30.0, window=200, slopes=True, prefix=[10, 0, 400, 250]),
+                                dict(softcap=3e4, amp=20.0), dict(amp=60.0)])
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 8, 2), (64, 2, 2)])
+def test_prefill_masks_and_scores(pisa, d, Hq, Hkv, kw):
+    run_prefill(pisa, Hq, Hkv, d, 600, 280, [280, 281, 600, 400], [280, 200, 280, 100], seed=9, **kw)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (2, 2)])
+def test_prefill_documents_and_empty_rows(pisa, Hq, Hkv):
+    first = torch.zeros(3, 280, dtype=torch.int32)
+    pos = torch.arange(280)
+    first[0] = pos // 97 * 97                 # three documents
+    first[1] = 2 ** 31 - 1                    # no row sees a key
+    first[1, ::3] = 5
+    first[2] = torch.randint(-10, 700, (280,), generator=torch.Generator().manual_seed(3))  # no order at all
+    run_prefill(pisa, Hq, Hkv, 128, 600, 280, [280, 280, 600], [280, 280, 280], seed=10, first=first.cuda())
+    run_prefill(pisa, Hq, Hkv, 64, 600, 280, [280, 280, 600], [280, 280, 280], seed=10, first=first.cuda(),
+                prefix=[100, 100, 600], window=150)
+
+
+@pytest.mark.parametrize("n,past,B", [(1, 30000, 1), (16, 30000, 1), (61, 20000, 2), (130, 9000, 1)])
+def test_prefill_few_rows_behind_a_long_cache(pisa, n, past, B):
+    run_prefill(pisa, 8, 2, 128, past + n, n, [past + n - 100 * b for b in range(B)], [n] * B, seed=n)
+    run_prefill(pisa, 8, 2, 64, past + n, n, [past + n - 100 * b for b in range(B)], [n] * B, seed=n, softcap=20.0,
+                window=past // 2)
+
+
+def test_prefill_many_sequences(pisa):
+    B = 70
+    lens = [1 + 7 * b for b in range(B)]
+    run_prefill(pisa, 2, 1, 64, 500, 90, lens, [min(90, x) for x in lens], seed=4)
+
+
+def test_prefill_long_prompt(pisa):
+    run_prefill(pisa, 4, 1, 128, 3000, 2500, [3000, 2500], [2500, 2400], seed=7)
+    run_prefill(pisa, 4, 1, 64, 3000, 2500, [3000, 2500], [2500, 2400], seed=7)
+
+
+def test_prefill_bad_lengths(pisa):
+    run_prefill(pisa, 8, 2, 64, 300, 70, [300, 301, 60, 100, -1, 70], [70, 70, 70, 71, 3, -2], seed=5,
+                status=pisa.DEV_BAD_SEQ_LEN)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_rows_of_any_size(pisa, d):
+    def far(k, v):
+        k[0, :, ::7], v[0, :, ::5], v[0, :, 3::5] = 0.0, 0.0, v[0, :, 3::5] * 1e-12
+        v[1] *= 2.0 ** -100
+        k[1, :, 100:200] *= 2.0 ** 12  # scales over 134
+        v[1, :, 50:150] *= 2.0 ** 121
+    run_prefill(pisa, 4, 2, d, 300, 200, [300, 290], [200, 180], seed=5, change=far)
+
+
+def test_prefill_bad_page_counts_as_unseen(pisa):
+    k, v, kp, vp, scales, table = cache(1, 2, 300, 64, [300], 4)
+    for bad in (-1, 1 << 20):
+        table[0, 2] = bad
+        q = torch.randn(1, 4, 200, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+        layer = pisa.PagedAttention(pisa.make_params(1, 300, 4, 2, 64), n=200)
+        out = layer.dense_prefill(q, kp, vp, table, i32([300]), scales=scales)
+        assert layer.device_status() == pisa.DEV_BAD_INDEX
+        key, pos = torch.arange(300, device="cuda"), torch.arange(100, 300, device="cuda")
+        keep = (key[None] <= pos[:, None]) & (key[None] // 64 != 2)
+        for h in range(4):
+            o, t = R.attend(q[0, h], k[0, h // 2], v[0, h // 2], keep, 0.125)
+            R.within(out[0, h], o, t)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0, slopes=True), dict(window=40)])
+@pytest.mark.parametrize("n,N", [(280, 600), (280, 280), (30, 3000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_rows_that_are_not_finite(pisa, d, n, N, kw):
+    """A key or value row that was not finite reads as NaN: so do the rows that see it, and no other; the last case
+    is split over the keys."""
+    Hq, Hkv = 4, 2
+    late = N - n // 2  # seen by the later half of the new tokens alone
+
+    def poke(k, v):
+        v[0, 0, late, 3] = float("inf")
+        k[0, 1, late + 3, 9] = R.NAN
+
+    k, v, kp, vp, scales, table = cache(1, Hkv, N, d, [N], 6, change=poke)
+    q = (torch.randn(1, Hq, n, d, generator=torch.Generator().manual_seed(7)) * 2).to(torch.bfloat16).cuda()
+    sl = slopes_of(Hq) if kw.get("slopes") else None
+    mask = pisa.AttentionMask(kw.get("softcap", 0.0), kw.get("window", 0), sl)
+    layer = pisa.PagedAttention(pisa.make_params(1, N, Hq, Hkv, d), n=n)
+    out = layer.dense_prefill(q, kp, vp, table, i32([N]), mask=mask, scales=scales)[0]
+    assert layer.device_status() == 0
+    pos = torch.arange(N - n, N, device="cuda")
+    lo, _ = R.spans(pos, N, kw.get("window", 0))
+    want, tol = R.dense(q[0], torch.nan_to_num(k[0]), torch.nan_to_num(v[0]), N, pos, d ** -0.5,
+                        kw.get("softcap", 0.0), kw.get("window", 0), sl)
+    for h in range(Hq):
+        at = late if h < 2 else late + 3
+        sees = (pos >= at) & (lo <= at)
+        assert int(sees.sum()) > 0 and int((~sees).sum()) >= n // 2
+        assert bool(torch.isnan(out[h, sees]).all())
+        R.within(out[h, ~sees], want[h, ~sees], tol[h, ~sees], "rows that see finite values")
