@@ -514,6 +514,8 @@ typedef struct {
   uint8_t* v_scales;
   int64_t num_pages;
   const int32_t* page_table; /* [B, ceil(N / C)] */
+  void* scratch;             /* nullable, 16-byte aligned; see pisa_cache_scratch_bytes */
+  size_t scratch_bytes;
 } pisa_cache;
 
 /* Norms of the heads of new tokens, before their rotation: x becomes
@@ -556,6 +558,15 @@ pisa_status pisa_cache_attend_decode(const pisa_params* p, const void* q, const 
 pisa_status pisa_cache_dense_prefill(const pisa_params* p, const pisa_mask* mask, int64_t n, const void* q,
                                      const pisa_cache* cache, const int32_t* seq_lens, const int32_t* new_lens,
                                      void* ws, size_t ws_bytes, void* out, void* stream);
+
+/* Bytes of cache->scratch with which pisa_cache_dense_prefill takes a prompt of
+ * n tokens faster: it then expands the pages that the call can see to bf16
+ * there first (about 4 B N H_kv d bytes), which long prompts read many times.
+ * 0: no use is made of any (few tokens, pages in the dtype of p, or more than
+ * 4 GiB).  Without that many bytes the call reads the codes themselves, with
+ * the same results.  Like the workspace, it may be used by any number of calls
+ * that do not overlap. */
+size_t pisa_cache_scratch_bytes(const pisa_params* p, int32_t format, int64_t n);
 
 /* Synchronises `stream`, then copies the workspace status word into
  * *device_code (PISA_DEV_*).  Returns PISA_ERR_DEVICE when it is non-zero. */

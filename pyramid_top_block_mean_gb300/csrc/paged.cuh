@@ -21,6 +21,8 @@ struct Pools {
   const int32_t* table;
   int64_t num_pages, nb;
   const uint8_t *ks, *vs;
+  void* scratch;  // nullable: room for e4m3 pages expanded to bf16
+  size_t scratch_bytes;
 };
 
 // What appending does besides moving rows: norms (weights null: none), angles.
@@ -140,6 +142,11 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
                                 cudaStream_t st);
 cudaError_t launch_read_paged(const Prob& pr, int64_t n, const Pools& pools, const int32_t* seq_lens,
                               const int32_t* new_lens, int32_t* status, void* k_out, void* v_out, cudaStream_t st);
+// Expands the e4m3 pages that a call of n tokens (with a window, 0: none) can see
+// to bf16 pages: page j of sequence b becomes page b nb + j of `wide`, whose
+// table it gets (-1 for one outside the pool).
+cudaError_t launch_expand_paged(const Prob& pr, int64_t n, int64_t window, const Pools& codes, const Pools& wide,
+                                const int32_t* seq_lens, const int32_t* new_lens, cudaStream_t st);
 cudaError_t launch_paged_decode(const Prob& pr, const MaskArgs& m, const void* q, const Pools& pools,
                                 const int32_t* seq_lens, const int32_t* idx, char* ws, void* out, cudaStream_t st);
 cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, const void* q, const Pools& pools,
@@ -153,5 +160,6 @@ cudaError_t launch_clear(void* ws, size_t bytes, cudaStream_t st);
 // Workspace bytes of the two launchers, the status word's 256 included; for calls of up to n tokens.
 size_t paged_decode_ws_bytes(const Prob& pr);
 size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n);
+size_t paged_prefill_scratch_bytes(const Prob& pr, int64_t n);
 
 }  // namespace pisa

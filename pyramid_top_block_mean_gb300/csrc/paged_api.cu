@@ -58,13 +58,15 @@ pisa_status pool_checks(const Prob& pr, const Pyr& s, const void* k_pages, const
   pools->num_pages = num_pages;
   pools->nb = s.nb;
   pools->ks = pools->vs = nullptr;
+  pools->scratch = nullptr;
+  pools->scratch_bytes = 0;
   return PISA_OK;
 }
 
 // A cache whose elements have the dtype of the problem.
 pisa_cache own_cache(const void* k_pages, const void* v_pages, int64_t num_pages, const int32_t* page_table) {
   return {sizeof(pisa_cache), PISA_CACHE_PARAMS, const_cast<void*>(k_pages), const_cast<void*>(v_pages), nullptr,
-          nullptr, num_pages, page_table};
+          nullptr, num_pages, page_table, nullptr, 0};
 }
 
 pisa_status cache_checks(const Prob& pr, const Pyr& s, const pisa_cache* c, const int32_t* seq_lens, const void* ws,
@@ -76,9 +78,11 @@ pisa_status cache_checks(const Prob& pr, const Pyr& s, const pisa_cache* c, cons
   const pisa_status rc =
       pool_checks(pr, s, c->k_pages, c->v_pages, c->num_pages, c->page_table, seq_lens, ws, pools);
   if (rc != PISA_OK || !in8) return rc;
-  if (!aligned16(c->k_scales) || !aligned16(c->v_scales)) return PISA_ERR_MISALIGNED;
+  if (!aligned16(c->k_scales) || !aligned16(c->v_scales) || !aligned16(c->scratch)) return PISA_ERR_MISALIGNED;
   pools->ks = c->k_scales;
   pools->vs = c->v_scales;
+  pools->scratch = c->scratch;
+  pools->scratch_bytes = c->scratch_bytes;
   return PISA_OK;
 }
 
@@ -149,6 +153,12 @@ size_t pisa_paged_workspace_bytes(const pisa_params* p, int64_t n) {
   Prob pr; Pyr s;
   if (check_params(p, &pr, &s) != PISA_OK || n < 0 || n > pr.N) return 0;
   return std::max(paged_decode_ws_bytes(pr), paged_prefill_ws_bytes(pr, n));
+}
+
+size_t pisa_cache_scratch_bytes(const pisa_params* p, int32_t format, int64_t n) {
+  Prob pr; Pyr s;
+  if (check_params(p, &pr, &s) != PISA_OK || n < 0 || n > pr.N || format != PISA_CACHE_E4M3) return 0;
+  return paged_prefill_scratch_bytes(pr, n);
 }
 
 pisa_status pisa_append_paged(const pisa_params* p, int64_t n, const void* q, const int64_t* q_strides,

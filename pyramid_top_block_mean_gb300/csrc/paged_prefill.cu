@@ -52,12 +52,12 @@ constexpr int kLoadWarp = 10;
 constexpr int kConvWarp = 12;  // Q8: warps 12-15 convert
 // Registers a thread: the softmax warpgroups hold a row of S each, the others
 // give up what they need (2 x 216 + 72 = 3 x 168, the launch's share; with the
-// converting warpgroup 2 x 200 + 64 + 48 = 4 x 128).
+// converting warpgroup 2 x 192 + 64 + 64 = 4 x 128).
 #define PISA_SOFTMAX_REGS "216"
 #define PISA_OTHER_REGS "72"
-#define PISA_SOFTMAX_REGS_Q8 "200"
+#define PISA_SOFTMAX_REGS_Q8 "192"
 #define PISA_OTHER_REGS_Q8 "64"
-#define PISA_CONVERT_REGS_Q8 "48"
+#define PISA_CONVERT_REGS_Q8 "64"
 constexpr float kSlack = 8.0f;  // log2 of how far weights may exceed 1
 
 // Q8: pages of e4m3.
@@ -451,9 +451,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
 
   if (Q8 && warp >= kConvWarp) {
     // ----------------------------------------------------------- converters
-    // Thread r turns row r of a tile into bf16, exactly: codes to numbers (see
-    // row_factor), 64 of them at a time, into the rows' place of the MMAs'
-    // operand.  The 8 lanes of one pass over the banks have the 8 rows of a
+    // Thread r turns row r of a tile into bf16, exactly (codes to numbers: see
+    // row_factor), into the row's place of the MMAs' operand.  The 8 lanes of one pass over the banks have the 8 rows of a
     // swizzle: no two of their pieces share banks, read or written.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " PISA_CONVERT_REGS_Q8 ";");
     const int r = threadIdx.x & 127;
@@ -481,29 +480,26 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         const bool zero = (f & 1) != 0 && (key < klo || key > khi || (sm.have[st] >> (r / kPage) & 1) == 0 ||
                                            (clean && scale == 255u));
         const uint32_t by = zero ? 0u : row_factor(scale), more = row_is_large(scale) ? row_factor_large(scale) : 0u;
+        uint4 c[D / 16];
 #pragma unroll
-        for (int hh = 0; hh < D / 64; ++hh) {
-          uint4 c[4];
+        for (int i = 0; i < D / 16; ++i)
+          c[i] = *reinterpret_cast<const uint4*>(from + ((i ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            c[i] = *reinterpret_cast<const uint4*>(from + (((4 * hh + i) ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
-          uint8_t* to = sm.kv[st] + hh * kHalf + r * 128;
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+          uint32_t x[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[2 * k] = mul_bf16x2(codes_lo(w[k]), by);
-              x[2 * k + 1] = mul_bf16x2(codes_hi(w[k]), by);
-            }
-            if (more && !zero) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) x[k] = mul_bf16x2(x[k], more);
-            }
-            *reinterpret_cast<uint4*>(to + (((2 * i) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4*>(to + (((2 * i + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] = mul_bf16x2(codes_lo(w[k]), by);
+            x[2 * k + 1] = mul_bf16x2(codes_hi(w[k]), by);
           }
+          if (more && !zero) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = mul_bf16x2(x[k], more);
+          }
+          uint8_t* to = sm.kv[st] + (i >> 2) * kHalf + r * 128;
+          *reinterpret_cast<uint4*>(to + (((2 * i & 7) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(to + (((2 * i + 1 & 7) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -1346,10 +1342,35 @@ size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
   return p.total;
 }
 
-cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, const void* q, const Pools& pools,
+// The bytes of e4m3 pages expanded to bf16 for calls of n tokens, and of the
+// table of the expanded ones in front of them; 0: the call reads the codes
+// itself.  Expanding costs a key and value of a head some 24 ns / 128 of the
+// whole GPU, reading the codes each 256-row item 6 (its converters share the
+// shared memory's bandwidth with the MMAs): five items a key head and more are
+// faster expanded.  (16 / 4 heads, behind 8192 tokens: 8192 new ones EXPANDED
+// against 776 us.)  Not beyond 4 GiB.
+constexpr int kExpandTiles = 5;
+size_t paged_prefill_scratch_bytes(const Prob& pr, int64_t n) {
+  if (make_plan(pr, n).tiles < kExpandTiles) return 0;
+  const size_t pages = (size_t)pr.B * (size_t)ceil_div64(pr.N, kPage);
+  const size_t total = align_up(pages * 4, 256) + pages * pr.Hkv * kPage * pr.d * 4;
+  return total <= ((size_t)1 << 32) ? total : 0;
+}
+
+cudaError_t launch_paged_prefill(const Prob& pr, const MaskArgs& m, int64_t n, const void* q, const Pools& given,
                                  const int32_t* seq_lens, const int32_t* new_lens, char* ws, void* out,
                                  cudaStream_t st) {
   const Plan pl = make_plan(pr, n);
+  Pools pools = given;
+  const size_t scratch = pools.ks ? paged_prefill_scratch_bytes(pr, n) : 0;
+  if (scratch > 0 && pools.scratch && pools.scratch_bytes >= scratch) {
+    const int64_t pages = pr.B * pools.nb;
+    char* at = (char*)pools.scratch + align_up((size_t)pages * 4, 256);
+    Pools wide{at, at + (size_t)pages * pr.Hkv * kPage * pr.d * 2, (const int32_t*)pools.scratch, pages, pools.nb};
+    const cudaError_t e = launch_expand_paged(pr, n, m.window, pools, wide, seq_lens, new_lens, st);
+    if (e != cudaSuccess) return e;
+    pools = wide;
+  }
   CUtensorMap qmap, kmap, vmap;
   const int64_t rows = pools.num_pages * pr.Hkv * kPage;
   const bool in8 = pools.ks != nullptr;

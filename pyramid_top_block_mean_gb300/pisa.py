@@ -42,7 +42,8 @@ EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pi
             "pisa_read_static_status", "pisa_test_inject_leaf_timeout", "pisa_append_paged",
             "pisa_dense_decode_paged", "pisa_attend_decode_paged", "pisa_dense_prefill_paged",
             "pisa_paged_workspace_bytes", "pisa_cache_append", "pisa_cache_read",
-            "pisa_cache_dense_decode", "pisa_cache_attend_decode", "pisa_cache_dense_prefill"]
+            "pisa_cache_dense_decode", "pisa_cache_attend_decode", "pisa_cache_dense_prefill",
+            "pisa_cache_scratch_bytes"]
 
 
 class Params(ctypes.Structure):
@@ -62,7 +63,8 @@ class Mask(ctypes.Structure):
 class Cache(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("format", ctypes.c_int32), ("k_pages", ctypes.c_void_p),
                 ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
-                ("num_pages", ctypes.c_int64), ("page_table", ctypes.c_void_p)]
+                ("num_pages", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("scratch", ctypes.c_void_p),
+                ("scratch_bytes", ctypes.c_size_t)]
 
 
 class HeadNorm(ctypes.Structure):
@@ -132,6 +134,8 @@ _lib.pisa_cache_attend_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_s
 _lib.pisa_cache_attend_decode.restype = ctypes.c_int
 _lib.pisa_cache_dense_prefill.argtypes = [_P, _M, ctypes.c_int64, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_cache_dense_prefill.restype = ctypes.c_int
+_lib.pisa_cache_scratch_bytes.argtypes = [_P, ctypes.c_int32, ctypes.c_int64]
+_lib.pisa_cache_scratch_bytes.restype = ctypes.c_size_t
 _lib.pisa_paged_workspace_bytes.argtypes = [_P, ctypes.c_int64]
 _lib.pisa_paged_workspace_bytes.restype = ctypes.c_size_t
 _lib.pisa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32), _vp]
@@ -354,7 +358,7 @@ def _want_pages(p: Params, k_pages, v_pages, page_table, seq_lens, scales, dtype
     B = p.B
     return (Cache(ctypes.sizeof(Cache), CACHE_PARAMS if scales is None else CACHE_E4M3,
                   _want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index),
-                  ks, vs, num, _want(page_table, "page_table", (B, -(-p.N // 64)), torch.int32, index)),
+                  ks, vs, num, _want(page_table, "page_table", (B, -(-p.N // 64)), torch.int32, index), None, 0),
             _want(seq_lens, "seq_lens", (B,), torch.int32, index))
 
 
@@ -490,11 +494,13 @@ def _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, space, o
                    _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space, out)
 
 
-def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, scales, stream,
+def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, scales, scratch, stream,
                    check) -> int:
     index, dt, n = q.get_device(), _dtype(p), q.shape[2]
     if scales is not None:
         cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+        if scratch is not None:
+            cache.scratch, cache.scratch_bytes = _want_space(scratch, index)
         return _launch(index, stream, "pisa_cache_dense_prefill", check, _lib.pisa_cache_dense_prefill,
                        ctypes.byref(p), _mask_arg(mask, p, n, index), n,
                        _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), ctypes.byref(cache), lens,
@@ -504,6 +510,11 @@ def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space
     return _launch(index, stream, "pisa_dense_prefill_paged", check, _lib.pisa_dense_prefill_paged, ctypes.byref(p),
                    _mask_arg(mask, p, n, index), n, _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), *cache,
                    None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space, out)
+
+
+def cache_scratch_bytes(p: Params, n: int) -> int:
+    """Bytes with which prompts of n tokens over e4m3 pages are faster (0: none are of use)."""
+    return _lib.pisa_cache_scratch_bytes(ctypes.byref(p), CACHE_E4M3, n)
 
 
 def quantized_pages(p: Params, num_pages: int, device="cuda"):
@@ -560,13 +571,15 @@ def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, id
 
 
 def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out, new_lens=None,
-                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True, scales=None) -> int:
+                        mask: Optional[AttentionMask] = None, stream=None, check: bool = True, scales=None,
+                        scratch=None) -> int:
     """q and out [B, H_q, n, d]: attention of n new tokens per sequence over the
-    pages that hold them already (scales: of e4m3 pages)."""
+    pages that hold them already (scales: of e4m3 pages; scratch: a tensor of
+    cache_scratch_bytes for long prompts over them)."""
     index = q.get_device()
     return _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, _want_space(ws, index),
-                          _want(out, "out", (p.B, p.H_q, q.shape[2], p.d), _dtype(p), index), mask, scales, stream,
-                          check)
+                          _want(out, "out", (p.B, p.H_q, q.shape[2], p.d), _dtype(p), index), mask, scales, scratch,
+                          stream, check)
 
 
 def read_device_status(ws: torch.Tensor, stream=None) -> int:
@@ -685,6 +698,7 @@ class PagedAttention:
         self._space = _want_space(self.ws, self._index)
         self._rot = 0 if rope is None else rope.shape[-1]
         self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
+        self._scratch, self._scratch_bytes = None, cache_scratch_bytes(p, n)  # made by the first prompt over 8-bit pages
         self.q_norm, self.k_norm = q_norm, k_norm
         self._norm = _head_norm(p, q_norm, k_norm, norm_eps, self._index)
         one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
@@ -744,8 +758,10 @@ class PagedAttention:
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None,
                       scales=None):
         out = self._buffer("prefill", q)
+        if scales is not None and self._scratch_bytes and self._scratch is None:  # kept for the calls that follow
+            self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.device)
         _dense_prefill(self.p, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space, out.data_ptr(), mask,
-                       scales, stream, True)
+                       scales, self._scratch, stream, True)
         return out
 
     def device_status(self, stream=None) -> int:

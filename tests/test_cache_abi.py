@@ -20,7 +20,7 @@ FIELDS = ("k_pages", "v_pages", "k_scales", "v_scales")
 
 
 def cache(pisa, **kw):
-    c = pisa.Cache(ctypes.sizeof(pisa.Cache), pisa.CACHE_E4M3, A, A, A, A, 10, A)
+    c = pisa.Cache(ctypes.sizeof(pisa.Cache), pisa.CACHE_E4M3, A, A, A, A, 10, A, None, 0)
     for name, value in kw.items():
         setattr(c, name, value)
     return ctypes.byref(c)
@@ -66,6 +66,7 @@ def test_caches_are_checked(pisa):
         for f in FIELDS:
             assert call(cache(pisa, **{f: None})) == -1, (name, f)
             assert call(cache(pisa, **{f: MIS})) == -3, (name, f)
+        assert call(cache(pisa, scratch=MIS)) == -3, name
         c = cache(pisa)
         assert call(c, lens=None) == -1 and call(c, lens=ODD) == -3, name
         assert call(c, ws=None) == -1 and call(c, ws=MIS) == -3 and call(c, size=16) == -4, name
@@ -136,3 +137,12 @@ def test_attention_refusals(pisa):
     assert on["dense"](c, mask=ctypes.byref(bad)) == -1 and on["prefill"](c, mask=ctypes.byref(bad)) == -1
     assert on["prefill"](c, n=-1) == -1 and on["prefill"](c, n=4097) == -1 and on["prefill"](c, new=ODD) == -3
     assert on["prefill"](None, n=0) == 0
+
+
+def test_scratch_sizes(pisa):
+    p = pisa.make_params(2, 4096, 16, 4, 128, K=8)
+    sizes = [pisa.cache_scratch_bytes(p, n) for n in (0, 1, 61, 2048, 4096)]
+    assert sizes[:3] == [0, 0, 0] and sizes[3] == sizes[4] >= 4 * 2 * 4096 * 4 * 128
+    assert pisa.cache_scratch_bytes(p, -1) == 0 and pisa.cache_scratch_bytes(p, 4097) == 0
+    assert pisa.cache_scratch_bytes(pisa.make_params(64, 131072, 32, 8, 128), 8192) == 0  # 34 GB
+    assert pisa.lib().pisa_cache_scratch_bytes(ctypes.byref(p), pisa.CACHE_PARAMS, 4096) == 0

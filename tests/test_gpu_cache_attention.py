@@ -229,6 +229,13 @@ def run_prefill(pisa, Hq, Hkv, d, N, n, lens, new, seed=0, softcap=0.0, window=0
                                 None if first is None else first[b, :cnt], 0 if prefix is None else prefix[b])
             R.within(out[b, :, :cnt], want, tol, f"sequence {b}")
         assert bool((out[b, :, cnt:] == MARK).all()), "rows behind the new tokens were written"
+    scratch = pisa.cache_scratch_bytes(p, n)
+    if scratch:  # the same from expanded pages, bit for bit
+        wide = torch.full_like(q, MARK)
+        pisa.dense_prefill_paged(p, q, kp, vp, table, i32(lens), ws, wide, i32(new), mask, scales=scales,
+                                 scratch=torch.full((scratch,), 255, dtype=torch.uint8, device="cuda"))
+        assert pisa.read_device_status(ws) == status
+        assert torch.equal(torch.nan_to_num(wide, 9.0), torch.nan_to_num(out, 9.0))
     return out
 
 
@@ -274,6 +281,46 @@ def test_prefill_many_sequences(pisa):
     B = 70
     lens = [1 + 7 * b for b in range(B)]
     run_prefill(pisa, 2, 1, 64, 500, 90, lens, [min(90, x) for x in lens], seed=4)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(window=300, softcap=20.0), dict(prefix=[1500, 0, 10], slopes=True)])
+def test_prefill_expanded_pages(pisa, d, kw):
+    """Prompts long enough to have their pages expanded: ragged, with a sequence of bad lengths, a page outside the
+    pool that no row of it sees, and scales over 134."""
+    def large(k, v):
+        k[1, :, 700:900] *= 2.0 ** 11
+        v[0, :, 1000:1100] *= 2.0 ** 20
+
+    def poke(scales, table):
+        if kw.get("window"):
+            table[0, :5] = -1  # gone: the window has left them
+    n = 1100
+    p = pisa.make_params(3, 2000, 8, 2, d)
+    assert pisa.cache_scratch_bytes(p, n) > 0
+    run_prefill(pisa, 8, 2, d, 2000, n, [1777, 1200, 2001], [n, 1001, 500], seed=3, change=large, poke=poke,
+                status=pisa.DEV_BAD_SEQ_LEN, **kw)
+
+
+def test_prefill_expanded_pages_that_are_not_finite(pisa):
+    def poke(k, v):
+        v[0, 0, 900, 3] = float("inf")
+        k[0, 1, 1500, 9] = R.NAN
+    n, N = 1100, 1999
+    k, v, kp, vp, scales, table = cache(1, 2, N, 64, [N], 6, change=poke)
+    table[0, 3] = 1 << 20
+    q = (torch.randn(1, 8, n, 64, generator=torch.Generator().manual_seed(7)) * 2).to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(1, N, 8, 2, 64), n=n)
+    out = layer.dense_prefill(q, kp, vp, table, i32([N]), scales=scales)[0]
+    assert layer._scratch is not None and layer.device_status() == pisa.DEV_BAD_INDEX
+    pos = torch.arange(N - n, N, device="cuda")
+    for h in range(8):
+        sees = pos >= (900 if h < 4 else 1500)
+        keep = torch.arange(N, device="cuda")[None] <= pos[:, None]
+        keep[:, 192:256] = False  # the page that is not there
+        want, tol = R.attend(q[0, h], torch.nan_to_num(k[0, h // 4]), torch.nan_to_num(v[0, h // 4]), keep, 0.125)
+        assert bool(torch.isnan(out[h, sees]).all())
+        R.within(out[h, ~sees], want[~sees], tol[~sees])
 
 
 def test_prefill_long_prompt(pisa):
