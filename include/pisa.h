@@ -498,8 +498,8 @@ size_t pisa_paged_workspace_bytes(const pisa_params* p, int64_t n);
  * 255 and zeros: it reads as NaN throughout.  Scales below 10 or from 247 to
  * 254 and the two codes of e4m3's NaN are never written by this library; what
  * a call makes of such a row is unspecified, and confined to the queries that
- * see it.  A row's numbers are numbers of bf16 too, so a call over it
- * can equal its counterpart on pages of those numbers.
+ * see it.  A row's numbers are numbers of bf16 too, so each call below equals
+ * its counterpart above on pages of those numbers, but for the order of sums.
  *
  * Workspace, lengths, page tables, faults and what an output holds where
  * nothing is written: as for the calls above.  With PISA_CACHE_PARAMS the
@@ -567,6 +567,14 @@ pisa_status pisa_cache_dense_prefill(const pisa_params* p, const pisa_mask* mask
  * the same results.  Like the workspace, it may be used by any number of calls
  * that do not overlap. */
 size_t pisa_cache_scratch_bytes(const pisa_params* p, int32_t format, int64_t n);
+
+/* pisa_build_pyramid_paged and pisa_select_decode_paged over a cache of either
+ * format (its values are not read: v_pages and v_scales may be null). */
+pisa_status pisa_cache_build_pyramid(const pisa_params* p, const pisa_cache* cache, const int32_t* seq_lens,
+                                     float* pyramid, void* ws, size_t ws_bytes, void* stream);
+pisa_status pisa_cache_select_decode(const pisa_params* p, const void* q, const pisa_cache* cache,
+                                     const int32_t* seq_lens, float* pyramid, void* ws, size_t ws_bytes,
+                                     int32_t* out_idx, float* out_score, int32_t* trace, void* stream);
 
 /* Synchronises `stream`, then copies the workspace status word into
  * *device_code (PISA_DEV_*).  Returns PISA_ERR_DEVICE when it is non-zero. */

@@ -312,19 +312,10 @@ __device__ __forceinline__ void read_unit(const void* pages, const uint8_t* scal
 #pragma unroll
     for (int j = 0; j < V; ++j) dst[j] = src[j];
   } else {
-    const uint32_t s = scales[row], f = row_factor(s);
+    const uint32_t s = scales[row];
     const uint4 c = *reinterpret_cast<const uint4*>((const uint8_t*)pages + row * d + e0);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = mul_bf16x2(codes_lo(w[j]), f);
-      x[2 * j + 1] = mul_bf16x2(codes_hi(w[j]), f);
-    }
-    if (row_is_large(s)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = mul_bf16x2(x[j], row_factor_large(s));
-    }
+    const uint4 lo = row_pairs(make_uint2(c.x, c.y), s), hi = row_pairs(make_uint2(c.z, c.w), s);
+    const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if constexpr (V == 2)

@@ -20,6 +20,7 @@
 //     heads per tile), fp32 keys by CUDA-core FMAs; then the Top-K with the
 //     forced blocks.
 // The step is bound by HBM: it reads ~2K leaf tiles per (sequence, key head).
+#include "e4m3.cuh"
 #include "pisa_common.cuh"
 #include "pisa_internal.h"
 #include "tc_ptx.cuh"
@@ -49,6 +50,7 @@ struct DecSmem {
   alignas(16) uint32_t key[kMaxCand];  // rank keys of the current list (0 past its end)
   int32_t scan[4];
   int32_t nkept2, nl;
+  alignas(16) uint8_t scale[kDecWarps][kNBuf][64];  // of a chunk's e4m3 rows
   uint64_t bar_rows, bar_leaf[kDecWarps][kNBuf];
   int32_t abort;
   int32_t zero;  // stays 0
@@ -105,7 +107,8 @@ __device__ __forceinline__ int scan64(int v, int32_t* scratch, int* total) {
   return (warp == 1 ? w0 : 0) + x - v;
 }
 
-template <int D, int G>
+// Q8: pages of e4m3 keys, which become the same bf16 numbers in registers.
+template <int D, int G, bool Q8>
 __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, const void* __restrict__ q,
                                                              const void* __restrict__ kc, KeyPages kp,
                                                              const int32_t* __restrict__ seq_lens, float* pyr,
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
     return;
   }
   const bool bf16 = pr.dtype == PISA_BF16;
-  const int esz = bf16 ? 2 : 4;
+  const int esz = Q8 ? 1 : bf16 ? 2 : 4;
   const int64_t t = len - 1, qb = t / s.C;
   if (kp.table) {
     // every page the step can read (leaves 0..qb) must be in the pool
@@ -166,6 +169,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
     const char* src = reinterpret_cast<const char*>(kc) + (leaf_row(kp, pr.Hkv, s.N, s.C, b, h, qb) * D) * esz;
     const int chunks = (int)(n_leaf * D * esz / 16);
     for (int c = tid; c < chunks; c += kDecThreads) ptx::cp_async_16(ptx::smem_u32(keys + 16 * c), src + 16 * c);
+    unsigned char* ksc = keys + 16384;  // scales of e4m3 keys, behind their C * D bytes
+    if (Q8 && tid < 4)
+      ptx::cp_async_16(ptx::smem_u32(ksc + 16 * tid),
+                       kp.scales + leaf_row(kp, pr.Hkv, s.N, s.C, b, h, qb) + 16 * tid);
     for (int w = tid; w < s.L * (D / 4); w += kDecThreads) {
       const int level = 2 + w / (D / 4);
       const int c4 = w % (D / 4);
@@ -181,8 +188,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
       // leaf: keys in index order, IEEE fp32 adds, one division (as the build)
       float acc = 0.0f;
       for (int64_t i = 0; i < n_leaf; ++i) {
-        const float v = bf16 ? bf16_to_f(reinterpret_cast<const uint16_t*>(keys)[i * D + tid])
-                             : reinterpret_cast<const float*>(keys)[i * D + tid];
+        const float v = Q8 ? code_number(keys[i * D + tid], ksc[i])
+                        : bf16 ? bf16_to_f(reinterpret_cast<const uint16_t*>(keys)[i * D + tid])
+                               : reinterpret_cast<const float*>(keys)[i * D + tid];
         acc = __fadd_rn(acc, v);
       }
       float m = __fdiv_rn(acc, (float)n_leaf);
@@ -418,7 +426,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
       // m16n8k16 MMAs give 16 keys x 8 columns (the G heads) per tile, and
       // every lane keeps an online max / sum for its two heads (2t, 2t+1)
       // over its keys (rows g and g+8 of each tile).
-      constexpr int KPC = kChunkBytes / (D * 2);  // keys per chunk: 16 (d = 128) or 32 (d = 64)
+      constexpr int ES = Q8 ? 1 : 2;
+      constexpr int KPC = kChunkBytes / (D * ES);  // keys per chunk: 16 (d = 128) or 32 (d = 64), of e4m3 twice that
       const int cpl = s.C / KPC;
       const int nlw = nl > warp ? (nl - warp + kDecWarps - 1) / kDecWarps : 0;
       const int nch = nlw * cpl;
@@ -440,11 +449,11 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
         if (lane == 0) {
           const int64_t leaf = sm.leaf[warp + (c / cpl) * kDecWarps];
           const uint32_t bar = ptx::smem_u32(&sm.bar_leaf[warp][c % kNBuf]);
-          ptx::mbar_arrive_expect_tx(bar, KPC * D * 2);
+          const int64_t row = leaf_row(kp, pr.Hkv, s.N, s.C, b, h, leaf) + (c % cpl) * KPC;
+          ptx::mbar_arrive_expect_tx(bar, KPC * (D * ES + (Q8 ? 1 : 0)));
           ptx::bulk_g2s(ptx::smem_u32(st + (c % kNBuf) * kChunkBytes),
-                        reinterpret_cast<const uint16_t*>(kc) +
-                            (leaf_row(kp, pr.Hkv, s.N, s.C, b, h, leaf) + (c % cpl) * KPC) * D,
-                        KPC * D * 2, bar);
+                        reinterpret_cast<const unsigned char*>(kc) + row * D * ES, KPC * D * ES, bar);
+          if (Q8) ptx::bulk_g2s(ptx::smem_u32(sm.scale[warp][c % kNBuf]), kp.scales + row, KPC, bar);
         }
       };
       int issued = 0, waited = 0;
@@ -475,11 +484,18 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
         for (int mt = 0; mt < KPC / 16; ++mt) {
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           const int r0 = 16 * mt + grp, r1 = r0 + 8;
+          const uint32_t sc0 = Q8 ? sm.scale[warp][bf][r0] : 0u, sc1 = Q8 ? sm.scale[warp][bf][r1] : 0u;
 #pragma unroll
           for (int bb = 0; bb < D / 32; ++bb) {
             // dims 32 bb + 8 t + {0..7} of keys r0 and r1 (the k-step mapping of the B fragments)
-            const uint4 a0 = *reinterpret_cast<const uint4*>(buf + r0 * D * 2 + 64 * bb + 16 * tig);
-            const uint4 a1 = *reinterpret_cast<const uint4*>(buf + r1 * D * 2 + 64 * bb + 16 * tig);
+            uint4 a0, a1;
+            if (Q8) {
+              a0 = row_pairs(*reinterpret_cast<const uint2*>(buf + r0 * D + 32 * bb + 8 * tig), sc0);
+              a1 = row_pairs(*reinterpret_cast<const uint2*>(buf + r1 * D + 32 * bb + 8 * tig), sc1);
+            } else {
+              a0 = *reinterpret_cast<const uint4*>(buf + r0 * D * 2 + 64 * bb + 16 * tig);
+              a1 = *reinterpret_cast<const uint4*>(buf + r1 * D * 2 + 64 * bb + 16 * tig);
+            }
             mma_bf16_16816(d, a0.x, a1.x, a0.y, a1.y, bq[bb][0], bq[bb][1]);
             mma_bf16_16816(d, a0.z, a1.z, a0.w, a1.w, bq[bb][2], bq[bb][3]);
           }
@@ -673,12 +689,12 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
   }
 }
 
-template <int D, int G>
+template <int D, int G, bool Q8>
 static cudaError_t launch_decode_t(const Prob& pr, const Pyr& s, const void* q, const void* kc,
                                    const KeyPages& kp, const int32_t* seq_lens, float* pyr, int32_t* status, int32_t* out_idx,
                                    float* out_score, int32_t* trace, cudaStream_t st) {
   const size_t smem = sizeof(DecSmem<G>) + 128;
-  auto kern = decode_kernel<D, G>;
+  auto kern = decode_kernel<D, G, Q8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   note_launch();
@@ -693,8 +709,10 @@ cudaError_t launch_decode(const Prob& pr, const Pyr& s, const void* q, const voi
                           cudaStream_t st) {
   if (s.L * pr.d * 4 > 16384) return cudaErrorInvalidValue;  // sibling rows must fit their staging slot
 #define PISA_DEC_CASE(DD, GG) \
-  if (pr.d == DD && pr.G == GG)  \
-    return launch_decode_t<DD, GG>(pr, s, q, kc, kp, seq_lens, pyr, status, out_idx, out_score, trace, st);
+  if (pr.d == DD && pr.G == GG)                                                                                       \
+    return kp.scales                                                                                                  \
+               ? launch_decode_t<DD, GG, true>(pr, s, q, kc, kp, seq_lens, pyr, status, out_idx, out_score, trace, st) \
+               : launch_decode_t<DD, GG, false>(pr, s, q, kc, kp, seq_lens, pyr, status, out_idx, out_score, trace, st);
   PISA_DEC_CASE(128, 1) PISA_DEC_CASE(128, 2) PISA_DEC_CASE(128, 4) PISA_DEC_CASE(128, 8)
   PISA_DEC_CASE(64, 1) PISA_DEC_CASE(64, 2) PISA_DEC_CASE(64, 4) PISA_DEC_CASE(64, 8)
 #undef PISA_DEC_CASE

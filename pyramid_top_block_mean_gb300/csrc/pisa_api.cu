@@ -189,7 +189,7 @@ pisa_status pisa_build_pyramid(const pisa_params* p, const void* k, const int32_
   if (pr.B * pr.Hkv * pr.N == 0) return PISA_OK;
   if (!k || !pyramid) return PISA_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(pyramid)) return PISA_ERR_MISALIGNED;
-  return cuda_status(launch_build_pyramid(pr, s, k, KeyPages{nullptr, 0, 0}, seq_lens, pyramid, nullptr,
+  return cuda_status(launch_build_pyramid(pr, s, k, KeyPages{nullptr, 0, 0, nullptr}, seq_lens, pyramid, nullptr,
                                           (cudaStream_t)stream));
 }
 
@@ -202,13 +202,39 @@ static pisa_status paged_checks(const Prob& pr, const Pyr& s, const void* k_page
   kp->table = page_table;
   kp->max_pages = s.nb;
   kp->num_pages = num_pages;
+  kp->scales = nullptr;
   (void)pr;
   return PISA_OK;
+}
+
+// The keys of a cache of either format.
+static pisa_status cache_key_checks(const Prob& pr, const Pyr& s, const pisa_cache* c, KeyPages* kp) {
+  if (!c || c->struct_size < sizeof(pisa_cache)) return PISA_ERR_INVALID_ARG;
+  const bool in8 = c->format == PISA_CACHE_E4M3;
+  if (!in8 && c->format != PISA_CACHE_PARAMS) return PISA_ERR_UNSUPPORTED;
+  if (in8 && !c->k_scales) return PISA_ERR_INVALID_ARG;
+  const pisa_status rc = paged_checks(pr, s, c->k_pages, c->num_pages, c->page_table, kp);
+  if (rc != PISA_OK || !in8) return rc;
+  if (pr.dtype != PISA_BF16) return PISA_ERR_UNSUPPORTED;  // the numbers of e4m3 rows are taken in bf16
+  if (!aligned16(c->k_scales)) return PISA_ERR_MISALIGNED;
+  kp->scales = c->k_scales;
+  return PISA_OK;
+}
+
+static pisa_cache key_cache(const void* k_pages, int64_t num_pages, const int32_t* page_table) {
+  return {sizeof(pisa_cache), PISA_CACHE_PARAMS, const_cast<void*>(k_pages), nullptr, nullptr, nullptr, num_pages,
+          page_table, nullptr, 0};
 }
 
 pisa_status pisa_build_pyramid_paged(const pisa_params* p, const void* k_pages, int64_t num_pages,
                                      const int32_t* page_table, const int32_t* seq_lens, float* pyramid, void* ws,
                                      size_t ws_bytes, void* stream) {
+  const pisa_cache c = key_cache(k_pages, num_pages, page_table);
+  return pisa_cache_build_pyramid(p, &c, seq_lens, pyramid, ws, ws_bytes, stream);
+}
+
+pisa_status pisa_cache_build_pyramid(const pisa_params* p, const pisa_cache* cache, const int32_t* seq_lens,
+                                     float* pyramid, void* ws, size_t ws_bytes, void* stream) {
   Prob pr; Pyr s;
   pisa_status rc = check_params(p, &pr, &s);
   if (rc != PISA_OK) return rc;
@@ -217,11 +243,11 @@ pisa_status pisa_build_pyramid_paged(const pisa_params* p, const void* k_pages, 
   if (!aligned16(pyramid) || !aligned16(ws) || ((uintptr_t)seq_lens & 3u)) return PISA_ERR_MISALIGNED;
   if (ws_bytes < decode_ws_bytes(pr, s)) return PISA_ERR_WORKSPACE;
   KeyPages kp;
-  rc = paged_checks(pr, s, k_pages, num_pages, page_table, &kp);
+  rc = cache_key_checks(pr, s, cache, &kp);
   if (rc != PISA_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
   if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return PISA_ERR_CUDA;
-  return cuda_status(launch_build_pyramid(pr, s, k_pages, kp, seq_lens, pyramid, (int32_t*)ws, st));
+  return cuda_status(launch_build_pyramid(pr, s, cache->k_pages, kp, seq_lens, pyramid, (int32_t*)ws, st));
 }
 
 // Checks shared by the prefill entry points.
@@ -327,7 +353,7 @@ pisa_status pisa_select_decode(const pisa_params* p, const void* q, const void* 
   int32_t* status = (int32_t*)ws;
   cudaError_t e = cudaMemsetAsync(status, 0, 256, st);
   if (e != cudaSuccess) return PISA_ERR_CUDA;
-  return cuda_status(launch_decode(pr, s, q, k_cache, KeyPages{nullptr, 0, 0}, seq_lens, pyramid, status, out_idx,
+  return cuda_status(launch_decode(pr, s, q, k_cache, KeyPages{nullptr, 0, 0, nullptr}, seq_lens, pyramid, status, out_idx,
                                    out_score, trace, st));
 }
 
@@ -335,6 +361,13 @@ pisa_status pisa_select_decode_paged(const pisa_params* p, const void* q, const 
                                      const int32_t* page_table, const int32_t* seq_lens, float* pyramid, void* ws,
                                      size_t ws_bytes, int32_t* out_idx, float* out_score, int32_t* trace,
                                      void* stream) {
+  const pisa_cache c = key_cache(k_pages, num_pages, page_table);
+  return pisa_cache_select_decode(p, q, &c, seq_lens, pyramid, ws, ws_bytes, out_idx, out_score, trace, stream);
+}
+
+pisa_status pisa_cache_select_decode(const pisa_params* p, const void* q, const pisa_cache* cache,
+                                     const int32_t* seq_lens, float* pyramid, void* ws, size_t ws_bytes,
+                                     int32_t* out_idx, float* out_score, int32_t* trace, void* stream) {
   Prob pr; Pyr s;
   pisa_status rc = check_params(p, &pr, &s);
   if (rc != PISA_OK) return rc;
@@ -347,12 +380,12 @@ pisa_status pisa_select_decode_paged(const pisa_params* p, const void* q, const 
     return PISA_ERR_MISALIGNED;
   if (ws_bytes < decode_ws_bytes(pr, s)) return PISA_ERR_WORKSPACE;
   KeyPages kp;
-  rc = paged_checks(pr, s, k_pages, num_pages, page_table, &kp);
+  rc = cache_key_checks(pr, s, cache, &kp);
   if (rc != PISA_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
   int32_t* status = (int32_t*)ws;
   if (cudaMemsetAsync(status, 0, 256, st) != cudaSuccess) return PISA_ERR_CUDA;
-  return cuda_status(launch_decode(pr, s, q, k_pages, kp, seq_lens, pyramid, status, out_idx, out_score, trace, st));
+  return cuda_status(launch_decode(pr, s, q, cache->k_pages, kp, seq_lens, pyramid, status, out_idx, out_score, trace, st));
 }
 
 pisa_status pisa_select_flat(const pisa_params* p, const void* q, const float* pyramid, void* ws, size_t ws_bytes,

@@ -191,6 +191,7 @@ __device__ __forceinline__ void mom_merge(Moments& a, float nb, float meanb, flo
 struct KeyPages {
   const int32_t* table;  // null: contiguous
   int64_t max_pages, num_pages;
+  const uint8_t* scales;  // [num_pages, Hkv, C] of e4m3 keys; null: keys of the problem's dtype
 };
 __device__ __forceinline__ int64_t leaf_row(const KeyPages& kp, int64_t Hkv, int64_t N, int64_t C, int64_t b,
                                             int64_t h, int64_t leaf) {

@@ -13,6 +13,7 @@
 //    This pass reads the whole key tensor once and is HBM-bound.
 //  build_upper: one CTA per (sequence, key head) for levels 6..L (1/16 of the
 //    nodes; reads level 5 from L2).
+#include "e4m3.cuh"
 #include "pisa_common.cuh"
 #include "pisa_internal.h"
 #include "tc_ptx.cuh"
@@ -37,13 +38,14 @@ constexpr uint64_t kBuildWaitNs = 4000000000ull;
 template <int D>
 constexpr int leaves_per_round() { return kBuildThreads / D; }  // one thread per (leaf, dim)
 
-static size_t build_lower_smem(int d, bool bf16, int C) {
-  const size_t stage = (size_t)(kBuildThreads / d) * C * d * (bf16 ? 2 : 4);
-  return 128 + kBuildStages * stage + (size_t)kLeavesPerCta * d * 4 + 64;
+static size_t build_lower_smem(int d, int esz, int C) {
+  const size_t leaves = kBuildThreads / d;
+  const size_t stage = leaves * C * d * esz;
+  return 128 + kBuildStages * stage + (size_t)kLeavesPerCta * d * 4 + 64 + (esz == 1 ? kBuildStages * leaves * C : 0);
 }
 
-// kPaged: keys through a page table (compiled separately, so the contiguous
-// kernel keeps its registers and occupancy).
+// kPaged: keys through a page table; kCodes: which are e4m3 (compiled
+// separately, so the contiguous kernel keeps its registers and occupancy).
 //
 // The CTA's leaves are taken in rounds of 256 / D (one thread per leaf and
 // dimension).  Thread 0 copies a round's raw keys into a shared-memory stage
@@ -53,7 +55,7 @@ static size_t build_lower_smem(int d, bool bf16, int C) {
 // over the leaf's keys in key order with IEEE fp32 adds and one division,
 // as the decode step recomputes its current leaf (decode.cu), so an
 // incrementally updated pyramid equals a fresh build bit for bit.
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kCodes>
 __global__ void __launch_bounds__(kBuildThreads) build_lower_kernel(Prob pr, Pyr s, const void* __restrict__ k,
                                                                    KeyPages kp, const int32_t* __restrict__ seq_lens,
                                                                    float* __restrict__ pyr, int32_t* __restrict__ status) {
@@ -63,11 +65,12 @@ __global__ void __launch_bounds__(kBuildThreads) build_lower_kernel(Prob pr, Pyr
   extern __shared__ unsigned char bsm_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(bsm_raw) + 127) & ~(uintptr_t)127);
   const bool bf16 = pr.dtype == PISA_BF16;
-  const uint32_t esz = bf16 ? 2u : 4u;
+  const uint32_t esz = kCodes ? 1u : bf16 ? 2u : 4u;
   const uint32_t leaf_bytes = (uint32_t)s.C * D * esz;
   const uint32_t stage_bytes = LPR * leaf_bytes;
   float (*sm)[D] = reinterpret_cast<float (*)[D]>(base + kBuildStages * stage_bytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(base + kBuildStages * stage_bytes + kLeavesPerCta * D * 4);
+  uint8_t* scales = reinterpret_cast<uint8_t*>(full) + 64;  // [stage][leaf][C] of e4m3 keys
   __shared__ int32_t abort_flag;
   const int64_t b = blockIdx.z, h = blockIdx.y;
   const int64_t leaf0 = (int64_t)blockIdx.x * kLeavesPerCta;
@@ -100,6 +103,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_lower_kernel(Prob pr, Pyr
     for (int j = 0; j < LPR; ++j) {
       cnts[j] = leaf_count(leaf0 + r * LPR + j, true);
       total += (uint32_t)cnts[j] * D * esz;
+      if (kCodes && cnts[j] > 0) total += (uint32_t)s.C;
     }
     const uint32_t bar = ptx::smem_u32(&full[st]);
     ptx::mbar_arrive_expect_tx(bar, total);
@@ -109,6 +113,7 @@ __global__ void __launch_bounds__(kBuildThreads) build_lower_kernel(Prob pr, Pyr
       const int64_t row = leaf_row(kp, pr.Hkv, s.N, s.C, b, h, leaf0 + r * LPR + j);
       ptx::bulk_g2s(ptx::smem_u32(base + st * stage_bytes + j * leaf_bytes), kbytes + row * D * esz,
                     (uint32_t)cnts[j] * D * esz, bar);
+      if (kCodes) ptx::bulk_g2s(ptx::smem_u32(scales + (st * LPR + j) * s.C), kp.scales + row, (uint32_t)s.C, bar);
     }
   };
 
@@ -131,7 +136,11 @@ __global__ void __launch_bounds__(kBuildThreads) build_lower_kernel(Prob pr, Pyr
     float m = 0.0f;
     if (ok && cnt > 0) {
       const unsigned char* src = base + st * stage_bytes + lr * leaf_bytes + c * esz;
-      if (bf16) {
+      if (kCodes) {
+        const uint8_t* sc = scales + (st * LPR + lr) * s.C;
+#pragma unroll 8
+        for (int64_t i = 0; i < cnt; ++i) m = __fadd_rn(m, code_number(src[i * D], sc[i]));
+      } else if (bf16) {
 #pragma unroll 8
         for (int64_t i = 0; i < cnt; ++i)
           m = __fadd_rn(m, __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(src + i * D * 2) << 16));
@@ -289,9 +298,10 @@ cudaError_t launch_build_pyramid(const Prob& pr, const Pyr& s, const void* k, co
                                  const int32_t* seq_lens, float* pyr, int32_t* status, cudaStream_t st) {
   if (pr.B == 0 || pr.Hkv == 0 || s.nb == 0) return cudaSuccess;
   dim3 g1((unsigned)ceil_div64(s.nb, kLeavesPerCta), (unsigned)pr.Hkv, (unsigned)pr.B);
-  const size_t smem = build_lower_smem(pr.d, pr.dtype == PISA_BF16, (int)s.C);
-  auto kern = kp.table ? (pr.d == 128 ? build_lower_kernel<128, true> : build_lower_kernel<64, true>)
-                       : (pr.d == 128 ? build_lower_kernel<128, false> : build_lower_kernel<64, false>);
+  const size_t smem = build_lower_smem(pr.d, kp.scales ? 1 : pr.dtype == PISA_BF16 ? 2 : 4, (int)s.C);
+  auto kern = kp.scales  ? (pr.d == 128 ? build_lower_kernel<128, true, true> : build_lower_kernel<64, true, true>)
+              : kp.table ? (pr.d == 128 ? build_lower_kernel<128, true, false> : build_lower_kernel<64, true, false>)
+                         : (pr.d == 128 ? build_lower_kernel<128, false, false> : build_lower_kernel<64, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   note_launch();

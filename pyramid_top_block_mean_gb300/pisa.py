@@ -43,7 +43,7 @@ EXPORTED = ["pisa_abi_version", "pisa_status_string", "pisa_pyramid_levels", "pi
             "pisa_dense_decode_paged", "pisa_attend_decode_paged", "pisa_dense_prefill_paged",
             "pisa_paged_workspace_bytes", "pisa_cache_append", "pisa_cache_read",
             "pisa_cache_dense_decode", "pisa_cache_attend_decode", "pisa_cache_dense_prefill",
-            "pisa_cache_scratch_bytes"]
+            "pisa_cache_scratch_bytes", "pisa_cache_build_pyramid", "pisa_cache_select_decode"]
 
 
 class Params(ctypes.Structure):
@@ -134,6 +134,10 @@ _lib.pisa_cache_attend_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_s
 _lib.pisa_cache_attend_decode.restype = ctypes.c_int
 _lib.pisa_cache_dense_prefill.argtypes = [_P, _M, ctypes.c_int64, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_cache_dense_prefill.restype = ctypes.c_int
+_lib.pisa_cache_build_pyramid.argtypes = [_P, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.pisa_cache_build_pyramid.restype = ctypes.c_int
+_lib.pisa_cache_select_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp]
+_lib.pisa_cache_select_decode.restype = ctypes.c_int
 _lib.pisa_cache_scratch_bytes.argtypes = [_P, ctypes.c_int32, ctypes.c_int64]
 _lib.pisa_cache_scratch_bytes.restype = ctypes.c_size_t
 _lib.pisa_paged_workspace_bytes.argtypes = [_P, ctypes.c_int64]
@@ -269,9 +273,26 @@ def select_flat(p: Params, q, pyramid, ws, out_idx, out_score=None, stream=None,
     return rc
 
 
+def _key_cache(p: Params, k_pages, page_table, scales) -> Cache:
+    """The keys of an 8-bit cache."""
+    index, num = k_pages.get_device(), k_pages.shape[0]
+    return Cache(ctypes.sizeof(Cache), CACHE_E4M3,
+                 _want(k_pages, "k_pages", (num, p.H_kv, p.C, p.d), torch.float8_e4m3fn, index), None,
+                 _want(scales, "scales", (2, num, p.H_kv, p.C), torch.uint8, index), None, num, page_table.data_ptr(),
+                 None, 0)
+
+
 def build_pyramid_paged(p: Params, k_pages, page_table, pyramid, ws, seq_lens=None, stream=None,
-                        check: bool = True) -> int:
-    """k_pages [num_pages, H_kv, C, d]; page_table int32 [B, ceil(N / C)]."""
+                        check: bool = True, scales=None) -> int:
+    """k_pages [num_pages, H_kv, C, d]; page_table int32 [B, ceil(N / C)];
+    scales: of e4m3 pages."""
+    if scales is not None:
+        rc = _lib.pisa_cache_build_pyramid(ctypes.byref(p), ctypes.byref(_key_cache(p, k_pages, page_table, scales)),
+                                           _ptr(seq_lens), _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(),
+                                           _stream(stream))
+        if check:
+            _check(rc, "pisa_cache_build_pyramid")
+        return rc
     rc = _lib.pisa_build_pyramid_paged(ctypes.byref(p), _ptr(k_pages), k_pages.shape[0], _ptr(page_table),
                                        _ptr(seq_lens), _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(),
                                        _stream(stream))
@@ -281,7 +302,16 @@ def build_pyramid_paged(p: Params, k_pages, page_table, pyramid, ws, seq_lens=No
 
 
 def select_decode_paged(p: Params, q, k_pages, page_table, seq_lens, pyramid, ws, out_idx, out_score=None,
-                        trace=None, stream=None, check: bool = True) -> int:
+                        trace=None, stream=None, check: bool = True, scales=None) -> int:
+    """select_decode over pages (scales: of e4m3 pages)."""
+    if scales is not None:
+        rc = _lib.pisa_cache_select_decode(ctypes.byref(p), _ptr(q),
+                                           ctypes.byref(_key_cache(p, k_pages, page_table, scales)), _ptr(seq_lens),
+                                           _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out_idx),
+                                           _ptr(out_score), _ptr(trace), _stream(stream))
+        if check:
+            _check(rc, "pisa_cache_select_decode")
+        return rc
     rc = _lib.pisa_select_decode_paged(ctypes.byref(p), _ptr(q), _ptr(k_pages), k_pages.shape[0], _ptr(page_table),
                                        _ptr(seq_lens), _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(),
                                        _ptr(out_idx), _ptr(out_score), _ptr(trace), _stream(stream))
@@ -624,12 +654,12 @@ class Selector:
                       stream)
         return self.out_idx, self.out_score
 
-    def build_paged(self, k_pages, page_table, seq_lens=None, stream=None):
-        build_pyramid_paged(self.p, k_pages, page_table, self.pyramid, self.ws, seq_lens, stream)
+    def build_paged(self, k_pages, page_table, seq_lens=None, stream=None, scales=None):
+        build_pyramid_paged(self.p, k_pages, page_table, self.pyramid, self.ws, seq_lens, stream, scales=scales)
 
-    def decode_paged(self, q, k_pages, page_table, seq_lens, trace=None, stream=None):
+    def decode_paged(self, q, k_pages, page_table, seq_lens, trace=None, stream=None, scales=None):
         select_decode_paged(self.p, q, k_pages, page_table, seq_lens, self.pyramid, self.ws, self.out_idx,
-                            self.out_score, trace, stream)
+                            self.out_score, trace, stream, scales=scales)
         return self.out_idx, self.out_score
 
     def flat(self, q, k=None, stream=None, build: bool = True):

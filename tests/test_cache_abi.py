@@ -146,3 +146,32 @@ def test_scratch_sizes(pisa):
     assert pisa.cache_scratch_bytes(p, -1) == 0 and pisa.cache_scratch_bytes(p, 4097) == 0
     assert pisa.cache_scratch_bytes(pisa.make_params(64, 131072, 32, 8, 128), 8192) == 0  # 34 GB
     assert pisa.lib().pisa_cache_scratch_bytes(ctypes.byref(p), pisa.CACHE_PARAMS, 4096) == 0
+
+
+def test_selector_refusals(pisa):
+    L = pisa.lib()
+    p, f32 = (pisa.make_params(2, 4096, 16, 4, 128, K=8, dtype=t) for t in ("bf16", "fp32"))
+
+    def build(c, p=p, ws=A, size=BIG, pyramid=A):
+        return L.pisa_cache_build_pyramid(ctypes.byref(p), c, A, pyramid, ws, size, None)
+
+    def select(c, p=p, ws=A, size=BIG, pyramid=A, q=A, lens=A, idx=A):
+        return L.pisa_cache_select_decode(ctypes.byref(p), q, c, lens, pyramid, ws, size, idx, None, None, None)
+
+    for call in (build, select):
+        assert call(None) == -1 and call(cache(pisa, struct_size=8)) == -1
+        assert call(cache(pisa, format=2)) == -2 and call(cache(pisa), p=f32) == -2
+        for f in ("k_pages", "k_scales"):
+            assert call(cache(pisa, **{f: None})) == -1 and call(cache(pisa, **{f: MIS})) == -3
+        assert call(cache(pisa, num_pages=0)) == -1
+        assert call(cache(pisa, page_table=None)) == -1 and call(cache(pisa, page_table=ODD)) == -3
+        c = cache(pisa, v_pages=None, v_scales=None)
+        assert call(c, pyramid=None) == -1 and call(c, pyramid=MIS) == -3 and call(c, size=16) == -4
+        assert call(c, ws=None) == -1 and call(c, ws=MIS) == -3
+    c = cache(pisa)
+    assert select(c, q=None) == -1 and select(c, lens=None) == -1 and select(c, idx=None) == -1
+    kp, _, scales = pisa.quantized_pages(p, 4, device="cpu")
+    table = torch.zeros(2, 64, dtype=torch.int32)
+    for bad in (dict(k_pages=kp.float()), dict(scales=scales[:1]), dict(scales=scales.float())):
+        with pytest.raises(ValueError, match="expected contiguous"):
+            pisa.build_pyramid_paged(p, **(dict(k_pages=kp, page_table=table, pyramid=None, ws=None, scales=scales) | bad))
