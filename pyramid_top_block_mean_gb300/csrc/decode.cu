@@ -485,13 +485,19 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           const int r0 = 16 * mt + grp, r1 = r0 + 8;
           const uint32_t sc0 = Q8 ? sm.scale[warp][bf][r0] : 0u, sc1 = Q8 ? sm.scale[warp][bf][r1] : 0u;
+          const uint32_t f0 = row_factor(sc0), f1 = row_factor(sc1);
+          const bool large = Q8 && __any_sync(0xffffffffu, row_is_large(sc0) || row_is_large(sc1));
 #pragma unroll
           for (int bb = 0; bb < D / 32; ++bb) {
             // dims 32 bb + 8 t + {0..7} of keys r0 and r1 (the k-step mapping of the B fragments)
             uint4 a0, a1;
             if (Q8) {
-              a0 = row_pairs(*reinterpret_cast<const uint2*>(buf + r0 * D + 32 * bb + 8 * tig), sc0);
-              a1 = row_pairs(*reinterpret_cast<const uint2*>(buf + r1 * D + 32 * bb + 8 * tig), sc1);
+              a0 = code_pairs(*reinterpret_cast<const uint2*>(buf + r0 * D + 32 * bb + 8 * tig), f0);
+              a1 = code_pairs(*reinterpret_cast<const uint2*>(buf + r1 * D + 32 * bb + 8 * tig), f1);
+              if (large) {
+                a0 = mul_pairs(a0, row_factor_large(sc0));
+                a1 = mul_pairs(a1, row_factor_large(sc1));
+              }
             } else {
               a0 = *reinterpret_cast<const uint4*>(buf + r0 * D * 2 + 64 * bb + 16 * tig);
               a1 = *reinterpret_cast<const uint4*>(buf + r1 * D * 2 + 64 * bb + 16 * tig);

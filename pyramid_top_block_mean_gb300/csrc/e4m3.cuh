@@ -54,16 +54,17 @@ __device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Eight codes of a row with the scale s as bf16 numbers.
+// Four pairs times a factor; eight codes as pairs of bf16 numbers times a factor
+// (row_factor), and as those of a row with any scale.
+__device__ __forceinline__ uint4 mul_pairs(uint4 x, uint32_t f) {
+  return make_uint4(mul_bf16x2(x.x, f), mul_bf16x2(x.y, f), mul_bf16x2(x.z, f), mul_bf16x2(x.w, f));
+}
+__device__ __forceinline__ uint4 code_pairs(uint2 w, uint32_t f) {
+  return mul_pairs(make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y)), f);
+}
 __device__ __forceinline__ uint4 row_pairs(uint2 w, uint32_t scale) {
-  const uint32_t f = row_factor(scale);
-  uint4 x = make_uint4(mul_bf16x2(codes_lo(w.x), f), mul_bf16x2(codes_hi(w.x), f), mul_bf16x2(codes_lo(w.y), f),
-                       mul_bf16x2(codes_hi(w.y), f));
-  if (row_is_large(scale)) {
-    const uint32_t more = row_factor_large(scale);
-    x = make_uint4(mul_bf16x2(x.x, more), mul_bf16x2(x.y, more), mul_bf16x2(x.z, more), mul_bf16x2(x.w, more));
-  }
-  return x;
+  const uint4 x = code_pairs(w, row_factor(scale));
+  return row_is_large(scale) ? mul_pairs(x, row_factor_large(scale)) : x;
 }
 // The number of one code of a row with the scale s, in fp32.
 __device__ __forceinline__ float code_number(uint32_t c, uint32_t scale) {

@@ -137,9 +137,20 @@ __global__ void __launch_bounds__(kBuildThreads) build_lower_kernel(Prob pr, Pyr
     if (ok && cnt > 0) {
       const unsigned char* src = base + st * stage_bytes + lr * leaf_bytes + c * esz;
       if (kCodes) {
+        // a code's bits as an fp32 number times 2^-120, and its row's power
         const uint8_t* sc = scales + (st * LPR + lr) * s.C;
+        auto bits = [&](int64_t i) {
+          return __uint_as_float((uint32_t)(int32_t) reinterpret_cast<const int8_t*>(src)[i * D] << 20 & 0x87f00000u);
+        };
+        uint32_t top = 0;  // one word for four keys: any scale over 134?
+        for (int i = 0; i < (int)s.C / 4; ++i) top |= __vcmpgtu4(reinterpret_cast<const uint32_t*>(sc)[i], 0x86868686u);
+        if (top == 0) {
 #pragma unroll 8
-        for (int64_t i = 0; i < cnt; ++i) m = __fadd_rn(m, code_number(src[i * D], sc[i]));
+          for (int64_t i = 0; i < cnt; ++i)
+            m = __fadd_rn(m, __fmul_rn(bits(i), __uint_as_float((uint32_t)sc[i] + 120u << 23)));
+        } else {
+          for (int64_t i = 0; i < cnt; ++i) m = __fadd_rn(m, code_number(src[i * D], sc[i]));
+        }
       } else if (bf16) {
 #pragma unroll 8
         for (int64_t i = 0; i < cnt; ++i)
