@@ -81,15 +81,9 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 1 / sqrt(sum / d + eps) for a row of which this thread holds x[0 .. N); the
-// row's threads are those of `mask`, neighbours.  1 / d is exact.
+// Of a row of which this thread holds x[0 .. N): its part of the sum of squares.
 template <int N>
-__device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d,
-                                          float eps) {
-  auto row_sum = [&](float ss) {
-    for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
-    return ss;
-  };
+__device__ __forceinline__ float sum_of_squares(const float (&x)[N]) {
   uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
   for (int j = 0; j < N; j += 2) {
@@ -99,27 +93,49 @@ __device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, u
   float p0, p1, p2, p3;
   ptx::unpack2(part[0], p0, p1);
   ptx::unpack2(part[1], p2, p3);
-  const float ss = row_sum((p0 + p1) + (p2 + p3));
-  if (ss < 3.0e38f) return rsqrtf(fmaf(ss, one_over_d, eps));
-  // squares beyond fp32's range: of the elements over 2^80, where eps is nothing
-  float far = 0.0f;
+  return (p0 + p1) + (p2 + p3);
+}
+// 1 / sqrt(mean of squares) of a row whose squares leave fp32's range: from the
+// elements over 2^80, where eps is nothing.  The row's threads are those of
+// `mask`, neighbours; 1 / d is exact.
+template <int N>
+__device__ __forceinline__ float far_row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d) {
+  float ss = 0.0f;
 #pragma unroll
-  for (int j = 0; j < N; ++j) far = fmaf(x[j] * 0x1p-80f, x[j] * 0x1p-80f, far);
-  return 0x1p-80f * rsqrtf(row_sum(far) * one_over_d);
+  for (int j = 0; j < N; ++j) ss = fmaf(x[j] * 0x1p-80f, x[j] * 0x1p-80f, ss);
+  for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
+  return 0x1p-80f * rsqrtf(ss * one_over_d);
+}
+// 1 / sqrt(sum / d + eps) of a row.
+template <int N>
+__device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d,
+                                          float eps) {
+  float ss = sum_of_squares(x);
+  for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
+  return ss < 3.0e38f ? rsqrtf(fmaf(ss, one_over_d, eps)) : far_row_norm(x, units, mask, one_over_d);
 }
 
-// The scale of a row of which this thread holds x[0 .. N): the smallest power
-// of two with which its largest magnitude is at most 448 = 1.75 2^8 (a carry out
-// of the mantissa where it is above 1.75), 255 if one is not finite.
+// The bits of the largest magnitude among x (those of infinities and NaN lie above all others').
 template <int N>
-__device__ __forceinline__ uint32_t row_scale(const float (&x)[N], uint32_t units, unsigned mask) {
+__device__ __forceinline__ uint32_t largest_bits(const float (&x)[N]) {
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-  for (uint32_t o = 1; o < units; o <<= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+  return top;
+}
+// The scale of a row with that largest magnitude: the smallest power of two
+// with which it is at most 448 = 1.75 2^8 (a carry out of the mantissa where it
+// is above 1.75), 255 if it is not finite.
+__device__ __forceinline__ uint32_t scale_of_bits(uint32_t top) {
   if (top >= 0x7f800000u) return 255u;
   const int e = (int)((top + 0x1fffffu) >> 23) - 8;  // biased
   return (uint32_t)min(max(e, 10), 246);
+}
+template <int N>
+__device__ __forceinline__ uint32_t row_scale(const float (&x)[N], uint32_t units, unsigned mask) {
+  uint32_t top = largest_bits(x);
+  for (uint32_t o = 1; o < units; o <<= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+  return scale_of_bits(top);
 }
 
 // The E codes of x over the row's power.
@@ -263,6 +279,156 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
   }
 }
 
+// Long calls with norms or into e4m3 pages: a CTA takes R heads of one kind (q,
+// k or v) of its tokens, a thread one 32-byte unit of each, so that all of a
+// CTA's threads do the same, the weights and angles of the unit are read once
+// for its R rows, and their sums go through the shuffles side by side.
+template <typename T, int R, bool NORM, bool Q8>
+__device__ __forceinline__ void append_heads(const Prob& pr, const AppendArgs& a, int64_t b) {
+  constexpr int E = Vec<T>::E;
+  const uint32_t units = pr.d / (2 * E);
+  const uint32_t gq = a.q ? (pr.Hq + R - 1) / R : 0, gk = (pr.Hkv + R - 1) / R, groups = gq + 2 * gk;
+  const uint32_t chunk = blockIdx.x / groups, g = blockIdx.x - chunk * groups;
+  const bool is_q = g < gq, is_v = g >= gq + gk;
+  const int h0 = R * (int)(is_q ? g : is_v ? g - gq - gk : g - gq), H = is_q ? pr.Hq : pr.Hkv;
+  const uint32_t u = threadIdx.x % units;
+  const unsigned mates = ((1u << units) - 1u) << (threadIdx.x % 32 / units * units);  // the row's threads
+  const int64_t i = (int64_t)chunk * (blockDim.x / units) + threadIdx.x / units;
+  if (i >= a.n) return;
+  int64_t len, cnt;
+  if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt) || i >= cnt) return;
+  const int64_t pos = len - cnt + i;
+  const uint32_t page = is_q ? 0u : (uint32_t)a.table[b * a.nb + pos / pr.C];  // a negative entry is past any pool
+  const bool in_pool = !is_q && page < a.num_pages;
+  const int half = a.rot / 2;
+  const bool turns = !is_v && (int)(2 * E * u) < a.rot;  // this unit's dims are among the rotated ones
+  const bool split = turns && !a.interleaved;
+  const int e0 = split ? E * u : 2 * E * u, e1 = split ? E * u + half : 2 * E * u + E;
+  const int64_t* sd = is_q ? a.qs : (is_v ? a.vs : a.ks);
+  const T* src = (const T*)(is_q ? a.q : (is_v ? a.v : a.k)) + b * sd[0] + h0 * sd[1] + i * sd[2];
+  uint4 w[R][2];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (h0 + k >= H) break;
+    w[k][0] = *reinterpret_cast<const uint4*>(src + k * sd[1] + e0);
+    w[k][1] = *reinterpret_cast<const uint4*>(src + k * sd[1] + e1);
+  }
+  float cs[E], sn[E];
+  if (turns) {
+    const float* at = a.rope + pos * a.rot + E * u;
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(at + j), s = *reinterpret_cast<const float4*>(at + half + j);
+      cs[j] = c.x; cs[j + 1] = c.y; cs[j + 2] = c.z; cs[j + 3] = c.w;
+      sn[j] = s.x; sn[j + 1] = s.y; sn[j + 2] = s.z; sn[j + 3] = s.w;
+    }
+  }
+  const float* weight = !NORM || is_v ? nullptr : (is_q ? a.norm.q : a.norm.k);
+  uint64_t wt[E];
+  float by[R];
+  if (weight) {
+#pragma unroll
+    for (int j = 0; j < 2 * E; j += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(weight + (j < E ? e0 + j : e1 + j - E));
+      wt[j / 2] = ptx::pack2(x.x, x.y);
+      wt[j / 2 + 1] = ptx::pack2(x.z, x.w);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float x[2 * E];
+      Vec<T>::load(w[k][0], x);
+      Vec<T>::load(w[k][1], x + E);
+      by[k] = h0 + k < H ? sum_of_squares(x) : 0.0f;
+    }
+    for (uint32_t o = 1; o < units; o <<= 1) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) by[k] += __shfl_xor_sync(mates, by[k], o);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (by[k] < 3.0e38f) {
+        by[k] = rsqrtf(fmaf(by[k], a.norm.one_over_d, a.norm.eps));
+      } else {
+        float x[2 * E];
+        Vec<T>::load(w[k][0], x);
+        Vec<T>::load(w[k][1], x + E);
+        by[k] = far_row_norm(x, units, mates, a.norm.one_over_d);
+      }
+    }
+  }
+  // row k, normed and rotated
+  auto finish = [&](int k, float (&x)[2 * E]) {
+    Vec<T>::load(w[k][0], x);
+    Vec<T>::load(w[k][1], x + E);
+    if (weight) {
+      const uint64_t by2 = ptx::pack2(by[k], by[k]);
+#pragma unroll
+      for (int j = 0; j < 2 * E; j += 2)
+        ptx::unpack2(mul_pair(ptx::pack2(x[j], x[j + 1]), mul_pair(by2, wt[j / 2])), x[j], x[j + 1]);
+    }
+    if (!turns) return;
+    if (a.interleaved) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float p = x[2 * j], z = x[2 * j + 1];
+        x[2 * j] = p * cs[j] - z * sn[j];
+        x[2 * j + 1] = z * cs[j] + p * sn[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; j += 2) {
+        const uint64_t p = ptx::pack2(x[j], x[j + 1]), z = ptx::pack2(x[E + j], x[E + j + 1]);
+        const uint64_t c = ptx::pack2(cs[j], cs[j + 1]), s = ptx::pack2(sn[j], sn[j + 1]);
+        ptx::unpack2(fma_pair(p, c, mul_pair(z, ptx::pack2(-sn[j], -sn[j + 1]))), x[j], x[j + 1]);
+        ptx::unpack2(fma_pair(z, c, mul_pair(p, s)), x[E + j], x[E + j + 1]);
+      }
+    }
+  };
+  const bool kept = Q8 && !is_q;  // the rows go into e4m3 pages: their numbers are made twice, once for the scale
+  uint32_t top[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    top[k] = 0;
+    if (h0 + k >= H) break;
+    uint4 y0 = w[k][0], y1 = w[k][1];
+    if (kept || weight || turns) {
+      float x[2 * E];
+      finish(k, x);
+      if (kept) top[k] = largest_bits(x);
+      y0 = Vec<T>::store(x);
+      y1 = Vec<T>::store(x + E);
+    }
+    if (is_q || (!is_v && a.k_out)) {
+      T* dst = (T*)(is_q ? a.q_out : a.k_out) + ((b * H + h0 + k) * a.n + i) * pr.d;
+      *reinterpret_cast<uint4*>(dst + e0) = y0;
+      *reinterpret_cast<uint4*>(dst + e1) = y1;
+    }
+    if (!Q8 && in_pool) {
+      T* dst = (T*)(is_v ? a.v_pages : a.k_pages) + (((int64_t)page * H + h0 + k) * pr.C + pos % pr.C) * pr.d;
+      *reinterpret_cast<uint4*>(dst + e0) = y0;
+      *reinterpret_cast<uint4*>(dst + e1) = y1;
+    }
+  }
+  if (!kept) return;
+  for (uint32_t s = 1; s < units; s <<= 1) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) top[k] = max(top[k], __shfl_xor_sync(mates, top[k], s));
+  }
+  if (!in_pool) return;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (h0 + k >= H) break;
+    float x[2 * E];
+    finish(k, x);
+    const uint32_t scale = scale_of_bits(top[k]);
+    const int64_t row = ((int64_t)page * H + h0 + k) * pr.C + pos % pr.C;
+    uint8_t* dst = (uint8_t*)(is_v ? a.v_pages : a.k_pages) + row * pr.d;
+    store_codes<E>(dst + e0, x, scale);
+    store_codes<E>(dst + e1, x + E, scale);
+    if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = (uint8_t)scale;
+  }
+}
+
 // One CTA looks at every length and page for faults and writes the status
 // word, so that nothing has to clear it before the call.
 __device__ __forceinline__ void write_status(const Prob& pr, const int32_t* seq_lens, const int32_t* new_lens,
@@ -285,9 +451,13 @@ __device__ __forceinline__ void write_status(const Prob& pr, const int32_t* seq_
 
 // Three CTAs on an SM: with four rows a thread the compiler takes 91 registers
 // if it may, which leaves two (a 2 x 4096-token prompt 15.1 us, against 13.2).
-template <typename T, int R, bool NORM, bool Q8>
-__global__ void __launch_bounds__(256, R == 4 && (NORM || Q8) ? 2 : 3) append_kernel(Prob pr, AppendArgs a) {
-  for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) append_units<T, R, NORM, Q8>(pr, a, b);
+// HEADS: append_heads().
+template <typename T, int R, bool NORM, bool Q8, bool HEADS>
+__global__ void __launch_bounds__(256, HEADS ? 2 : 3) append_kernel(Prob pr, AppendArgs a) {
+  for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) {
+    if constexpr (HEADS) append_heads<T, R, NORM, Q8>(pr, a, b);
+    else append_units<T, R, NORM, Q8>(pr, a, b);
+  }
   if (blockIdx.x == 0 && blockIdx.y == 0)
     write_status(pr, a.seq_lens, a.new_lens, a.table, a.n, a.nb, a.num_pages, a.status);
 }
@@ -409,16 +579,21 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   // 16 + 2 x 4 heads (12.0 us at the copy rate), where one row a thread took
   // 18.2; a step of 64 tokens (2.7 us) has too few rows to give up any thread.
   const bool many = pr.B * n * rows * (256 / per) >= 4 * 152 * 2048;
-  const dim3 grid((unsigned)ceil_div64(n * ceil_div64(rows, many ? 4 : 1), per),
+  const bool normed = norm.q || norm.k, in8 = pools.ks != nullptr, heads = many && (normed || in8) && n >= per;
+  const int R = heads || (many && !normed && !in8) ? 4 : 1;
+  const int64_t groups = (q ? ceil_div64(pr.Hq, R) : 0) + 2 * ceil_div64(pr.Hkv, R);
+  const dim3 grid((unsigned)(heads ? ceil_div64(n, per) * groups : ceil_div64(n * ceil_div64(rows, R), per)),
                   (unsigned)std::min<int64_t>(pr.B, 65535));
-  const bool normed = norm.q || norm.k, in8 = pools.ks != nullptr;
   auto pick = [&](auto type) {
     using T = decltype(type);
-    if (normed)
-      return in8 ? (many ? append_kernel<T, 4, true, true> : append_kernel<T, 1, true, true>)
-                 : (many ? append_kernel<T, 4, true, false> : append_kernel<T, 1, true, false>);
-    return in8 ? (many ? append_kernel<T, 4, false, true> : append_kernel<T, 1, false, true>)
-               : (many ? append_kernel<T, 4, false, false> : append_kernel<T, 1, false, false>);
+    auto form = [&](auto nn, auto qq) {
+      constexpr bool N = decltype(nn)::value, Q = decltype(qq)::value;
+      if (heads) return append_kernel<T, 4, N, Q, N || Q>;
+      return R == 4 ? append_kernel<T, 4, false, false, false> : append_kernel<T, 1, N, Q, false>;
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    return normed ? (in8 ? form(Yes(), Yes()) : form(Yes(), No())) : (in8 ? form(No(), Yes()) : form(No(), No()));
   };
   auto kern = pr.dtype == PISA_BF16 ? pick(__nv_bfloat16()) : pick(float());
   note_launch();
