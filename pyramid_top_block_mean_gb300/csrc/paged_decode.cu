@@ -59,6 +59,7 @@ namespace {
 constexpr int kMerge = 96;              // threads that merge a part while the consumers are at the next one
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
+constexpr float kSlack = 8.0f;          // Q8: log2 of how far weights may exceed 1
 constexpr int kScaleLanes = 2 * kPage / 16;  // lanes that bring a page's scales
 
 // Q8: pages of e4m3.
@@ -762,8 +763,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
             mma16832_e4m3(d, k0[k], k1[k], k0[k + 1], k1[k + 1], bq[k], bq[k + 1]);
             mma16832_e4m3(e, k0[k], k1[k], k0[k + 1], k1[k + 1], bl[k], bl[k + 1]);
           }
-          const float fa = ksc[u][0] == 255 ? NAN : __uint_as_float((uint32_t)ksc[u][0] << 23);
-          const float fb = ksc[u][1] == 255 ? NAN : __uint_as_float((uint32_t)ksc[u][1] << 23);
+          // (255 makes an infinity of it, and NaN of the product: such a row's codes are zero)
+          const float fa = __uint_as_float((uint32_t)ksc[u][0] << 23), fb = __uint_as_float((uint32_t)ksc[u][1] << 23);
           x[u][0] = fmaf(e[0], 1.0f / 32, d[0]) * hf0 * fa; x[u][1] = fmaf(e[1], 1.0f / 32, d[1]) * hf1 * fa;
           x[u][2] = fmaf(e[2], 1.0f / 32, d[2]) * hf0 * fb; x[u][3] = fmaf(e[3], 1.0f / 32, d[3]) * hf1 * fb;
         }
@@ -817,16 +818,27 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         for (int u = 0; u < T; ++u) {
           c0 = ptx::max3(c0, x[u][0], x[u][2]);
           c1 = ptx::max3(c1, x[u][1], x[u][3]);
-          top = max(top, max(vsc[u][0] == 255 ? 0 : vsc[u][0], vsc[u][1] == 255 ? 0 : vsc[u][1]));
+          top = max(top, max(vsc[u][0], vsc[u][1]));
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        // The reference follows the maximum when that has grown by 2^8, the
+        // largest power as it grows: as a rule neither, and one vote says so.  A
+        // row of NaN (255) is over every power.
+        if (__any_sync(0xffffffffu, c0 > m0 + kSlack || c1 > m1 + kSlack || top > ref)) {
+          top = 0;
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) {
-          c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
-          c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
-        }
-        const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
-        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1 || top > ref)) {
+          for (int u = 0; u < T; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (vsc[u][j] == 255) x[u][2 * j] = x[u][2 * j + 1] = NAN;
+              else top = max(top, vsc[u][j]);
+            }
+          top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) {
+            c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
+            c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
+          }
+          const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
           float f0 = m0 == -INFINITY ? 0.0f : ptx::ex2(m0 - n0);
           float f1 = m1 == -INFINITY ? 0.0f : ptx::ex2(m1 - n1);
           m0 = n0;
@@ -854,10 +866,10 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
           l0 += p0 + p2;
           l1 += p1 + p3;
           // The rows' powers go with the weights, relative to the largest so far.
-          // P is rounded to fp16 for the MMA, times 2^15: 2^-11 of each weight that
-          // is over 2^-29 of the largest, and 2^-40 of that below.
-          const float fa = vsc[u][0] == 255 ? NAN : __uint_as_float(max(vsc[u][0] - ref + 142, 0) << 23);
-          const float fb = vsc[u][1] == 255 ? NAN : __uint_as_float(max(vsc[u][1] - ref + 142, 0) << 23);
+          // P is rounded to fp16 for the MMA, times 2^7: 2^-11 of each weight that is
+          // over 2^-21 of the reference, and 2^-32 of that below.
+          const float fa = __uint_as_float(max(vsc[u][0] - ref + 134, 0) << 23);
+          const float fb = __uint_as_float(max(vsc[u][1] - ref + 134, 0) << 23);
           const uint32_t b0 = transpose8(pack_half(p0 * fa, p1 * fa)), b1 = transpose8(pack_half(p2 * fb, p3 * fb));
           // The values' rows are the MMA's columns: a thread takes D / 8 codes of
           // its four keys, 2 tig, 2 tig + 1 and 8 further, and pairs the keys
@@ -983,8 +995,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       *reinterpret_cast<float2*>(&sm.m[warp][2 * tig]) = make_float2(m0, m1);
       *reinterpret_cast<float2*>(&sm.l[warp][2 * tig]) = make_float2(l0, l1);
     }
-    if constexpr (Q8) {  // O as it is: by 2^(ref - 127) and 2^-15, in two steps
-      const int by = ref - 142, half = by >> 1;
+    if constexpr (Q8) {  // O as it is: by 2^(ref - 127) and 2^-7, in two steps
+      const int by = ref - 134, half = by >> 1;
       const float f = __uint_as_float((half + 127) << 23), f2 = __uint_as_float((by - half + 127) << 23);
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
