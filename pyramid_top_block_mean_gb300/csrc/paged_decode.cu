@@ -672,13 +672,23 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   // ldmatrix rows: lane l addresses row l % 8 of matrix l / 8
   const int krow = r16 + (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
   const int vrow = r16 + (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
+  // FOLD (up to four heads): of an MMA's eight columns the heads' upper parts are
+  // the first four and their lower ones the others, so that one takes both.
+  // The lanes of the first four (tig < 2) then go on with the keys grp of a tile
+  // and those of the others with the keys grp + 8, each with heads hd and hd +
+  // 1; as columns of P they hold those keys alone, with an m, l and o of
+  // their own.
+  constexpr bool FOLD = Q8 && G <= 4;
+  constexpr int KL = FOLD ? 1 : 2;  // keys of a tile that a lane goes on with
+  const bool low = !FOLD || tig < 2;
+  const int hd = FOLD ? 2 * (tig & 1) : 2 * tig, kofs = low ? 0 : 8;
   // the query's fragments; Q8: its upper part and its lower one, each head's
   // 1 / s, and the largest scale of the values so far
-  uint32_t bq[Q8 ? D / 16 : D / 8], bl[Q8 ? D / 16 : 1];
+  uint32_t bq[Q8 ? D / 16 : D / 8], bl[Q8 && !FOLD ? D / 16 : 1];
   float hf0 = 1.0f, hf1 = 1.0f;
   int ref = 0;
   float oacc[D / 16][4];
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads 2 tig, 2 tig + 1
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads hd, hd + 1
   float sl0 = 0.0f, sl1 = 0.0f;
   // a group takes every kGroups-th stage
   int st = warp / S::kGroupWarps - kGroups, ph = 0, merges = 0;
@@ -704,9 +714,19 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     if (meta.item < 0) break;
     if (meta.first) {
       if constexpr (Q8) {
-        const float f = split_query<D>(sm.q[st] + (grp < G ? grp : 0) * D + (D / 4) * tig, grp < G, bq, bl);
-        hf0 = __shfl_sync(0xffffffffu, f, 8 * tig);
-        hf1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+        const int head = FOLD ? grp & 3 : grp;
+        const uint16_t* row = sm.q[st] + (head < G ? head : 0) * D + (D / 4) * tig;
+        float f;
+        if constexpr (FOLD) {
+          uint32_t rest[D / 16];
+          f = split_query<D>(row, head < G, bq, rest);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) bq[k] = grp < 4 ? bq[k] : rest[k];
+        } else {
+          f = split_query<D>(row, head < G, bq, bl);
+        }
+        hf0 = __shfl_sync(0xffffffffu, f, 4 * hd);
+        hf1 = __shfl_sync(0xffffffffu, f, 4 * hd + 4);
         ref = 0;
       } else {
 #pragma unroll
@@ -722,8 +742,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       l0 = l1 = 0.0f;
       if (mk.slopes) {
         const float* sl = mk.slopes + (int64_t)(meta.item % pr.Hkv) * G;
-        sl0 = 2 * tig < G ? sl[2 * tig] * kLog2e : 0.0f;
-        sl1 = 2 * tig + 1 < G ? sl[2 * tig + 1] * kLog2e : 0.0f;
+        sl0 = hd < G ? sl[hd] * kLog2e : 0.0f;
+        sl1 = hd + 1 < G ? sl[hd + 1] * kLog2e : 0.0f;
       }
     }
     const bool seen_any = meta.klo <= meta.khi && r16 <= meta.khi && r16 + S::kKeys - 1 >= meta.klo;
@@ -731,7 +751,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     // stage is free again before they are worked on.
     constexpr int T = S::kKeys / 16;  // tiles of 16 keys
     uint32_t kc[Q8 ? T : 1][2][D / 16], vc[Q8 ? T : 1][4][D / 32];
-    int ksc[T][2], vsc[T][2];  // and the scales
+    int ksc[T][KL], vsc[T][KL];  // and the scales
     if constexpr (Q8) {
       if (seen_any) {
 #pragma unroll
@@ -742,8 +762,11 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
             row_codes<D>(sm.kv[st][0], r + 8 * j, tig, kc[u][j]);
             part_codes<D>(sm.kv[st][1], c + 8 * j, grp, vc[u][2 * j]);
             part_codes<D>(sm.kv[st][1], c + 8 * j + 1, grp, vc[u][2 * j + 1]);
-            ksc[u][j] = sm.scale[st][0][r + 8 * j];
-            vsc[u][j] = sm.scale[st][1][r + 8 * j];
+          }
+#pragma unroll
+          for (int j = 0; j < KL; ++j) {
+            ksc[u][j] = sm.scale[st][0][r + kofs + 8 * j];
+            vsc[u][j] = sm.scale[st][1][r + kofs + 8 * j];
           }
         }
       }
@@ -752,74 +775,98 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     }
     if (seen_any) {
       if constexpr (Q8) {
-        // keys grp and grp + 8 of each tile, heads 2 tig and 2 tig + 1
-        float x[T][4];
+        // keys grp + kofs (and 8 further) of each tile, heads hd and hd + 1
+        float x[T][2 * KL];
 #pragma unroll
         for (int u = 0; u < T; ++u) {
           const uint32_t (&k0)[D / 16] = kc[u][0], (&k1)[D / 16] = kc[u][1];
-          float d[4] = {}, e[4] = {};  // of the query's upper part and its lower one
+          float d[4] = {}, e[4] = {};  // of the query's upper part and its lower one; FOLD: two chains of both
 #pragma unroll
           for (int k = 0; k < D / 16; k += 2) {
-            mma16832_e4m3(d, k0[k], k1[k], k0[k + 1], k1[k + 1], bq[k], bq[k + 1]);
-            mma16832_e4m3(e, k0[k], k1[k], k0[k + 1], k1[k + 1], bl[k], bl[k + 1]);
+            if constexpr (FOLD) {
+              mma16832_e4m3(k & 2 ? e : d, k0[k], k1[k], k0[k + 1], k1[k + 1], bq[k], bq[k + 1]);
+            } else {
+              mma16832_e4m3(d, k0[k], k1[k], k0[k + 1], k1[k + 1], bq[k], bq[k + 1]);
+              mma16832_e4m3(e, k0[k], k1[k], k0[k + 1], k1[k + 1], bl[k], bl[k + 1]);
+            }
           }
-          // (255 makes an infinity of it, and NaN of the product: such a row's codes are zero)
-          const float fa = __uint_as_float((uint32_t)ksc[u][0] << 23), fb = __uint_as_float((uint32_t)ksc[u][1] << 23);
-          x[u][0] = fmaf(e[0], 1.0f / 32, d[0]) * hf0 * fa; x[u][1] = fmaf(e[1], 1.0f / 32, d[1]) * hf1 * fa;
-          x[u][2] = fmaf(e[2], 1.0f / 32, d[2]) * hf0 * fb; x[u][3] = fmaf(e[3], 1.0f / 32, d[3]) * hf1 * fb;
+          if constexpr (FOLD) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] += e[j];
+            // each half of the lanes sends what the other goes on with
+            const float r0 = __shfl_xor_sync(0xffffffffu, low ? d[2] : d[0], 2);
+            const float r1 = __shfl_xor_sync(0xffffffffu, low ? d[3] : d[1], 2);
+            x[u][0] = low ? fmaf(r0, 1.0f / 32, d[0]) : fmaf(d[2], 1.0f / 32, r0);
+            x[u][1] = low ? fmaf(r1, 1.0f / 32, d[1]) : fmaf(d[3], 1.0f / 32, r1);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2 * KL; ++j) x[u][j] = fmaf(e[j], 1.0f / 32, d[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < KL; ++j) {
+            // (255 makes an infinity of it, and NaN of the product: such a row's codes are zero)
+            const float f = __uint_as_float((uint32_t)ksc[u][j] << 23);
+            x[u][2 * j] = x[u][2 * j] * hf0 * f;
+            x[u][2 * j + 1] = x[u][2 * j + 1] * hf1 * f;
+          }
         }
         if (mk.cap2 > 0.0f) {  // cap_score(), the form of large scores where there are some
           bool large = false;
 #pragma unroll
           for (int u = 0; u < T; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) large |= !(fabsf(x[u][j] * mk.by) <= mk.lim);
+            for (int j = 0; j < 2 * KL; ++j) large |= !(fabsf(x[u][j] * mk.by) <= mk.lim);
           if (__any_sync(0xffffffffu, large)) {
 #pragma unroll
             for (int u = 0; u < T; ++u)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[u][j] = cap_score(mk, x[u][j]);
+              for (int j = 0; j < 2 * KL; ++j) x[u][j] = cap_score(mk, x[u][j]);
           } else {
 #pragma unroll
             for (int u = 0; u < T; ++u)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[u][j] = cap_small(mk, x[u][j]);
+              for (int j = 0; j < 2 * KL; ++j) x[u][j] = cap_small(mk, x[u][j]);
           }
         } else {
 #pragma unroll
           for (int u = 0; u < T; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[u][j] *= pr.scale2;
+            for (int j = 0; j < 2 * KL; ++j) x[u][j] *= pr.scale2;
         }
+        const int ka = r16 + grp + kofs;  // this lane's first key
         if (mk.slopes) {
 #pragma unroll
-          for (int u = 0; u < T; ++u) {
-            const float ra = (float)(meta.rel + r16 + 16 * u + grp), rb = (float)(meta.rel + r16 + 16 * u + grp + 8);
-            x[u][0] = fmaf(sl0, ra, x[u][0]); x[u][1] = fmaf(sl1, ra, x[u][1]);
-            x[u][2] = fmaf(sl0, rb, x[u][2]); x[u][3] = fmaf(sl1, rb, x[u][3]);
-          }
+          for (int u = 0; u < T; ++u)
+#pragma unroll
+            for (int j = 0; j < KL; ++j) {
+              const float back = (float)(meta.rel + ka + 16 * u + 8 * j);
+              x[u][2 * j] = fmaf(sl0, back, x[u][2 * j]);
+              x[u][2 * j + 1] = fmaf(sl1, back, x[u][2 * j + 1]);
+            }
         }
         const bool part = r16 < meta.klo || r16 + S::kKeys - 1 > meta.khi;  // some of the keys are not seen
         if (part) {
 #pragma unroll
           for (int u = 0; u < T; ++u)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int k = r16 + 16 * u + grp + 8 * j;
+            for (int j = 0; j < KL; ++j) {
+              const int k = ka + 16 * u + 8 * j;
               if (k < meta.klo || k > meta.khi) {
                 x[u][2 * j] = x[u][2 * j + 1] = -INFINITY;
                 vsc[u][j] = 0;  // its power has no say
               }
             }
         }
-        float c0 = fmaxf(x[0][0], x[0][2]), c1 = fmaxf(x[0][1], x[0][3]);
+        float c0 = -INFINITY, c1 = -INFINITY;
         int top = 0;
 #pragma unroll
-        for (int u = 0; u < T; ++u) {
-          c0 = ptx::max3(c0, x[u][0], x[u][2]);
-          c1 = ptx::max3(c1, x[u][1], x[u][3]);
-          top = max(top, max(vsc[u][0], vsc[u][1]));
-        }
+        for (int u = 0; u < T; ++u)
+#pragma unroll
+          for (int j = 0; j < KL; ++j) {
+            c0 = fmaxf(c0, x[u][2 * j]);
+            c1 = fmaxf(c1, x[u][2 * j + 1]);
+            top = max(top, vsc[u][j]);
+          }
         // The reference follows the maximum when that has grown by 2^8, the
         // largest power as it grows: as a rule neither, and one vote says so.  A
         // row of NaN (255) is over every power.
@@ -828,7 +875,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
 #pragma unroll
           for (int u = 0; u < T; ++u)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < KL; ++j) {
               if (vsc[u][j] == 255) x[u][2 * j] = x[u][2 * j + 1] = NAN;
               else top = max(top, vsc[u][j]);
             }
@@ -861,16 +908,23 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
         for (int u = 0; u < T; ++u) {
-          const float p0 = ptx::ex2(x[u][0] - z0), p1 = ptx::ex2(x[u][1] - z1);
-          const float p2 = ptx::ex2(x[u][2] - z0), p3 = ptx::ex2(x[u][3] - z1);
-          l0 += p0 + p2;
-          l1 += p1 + p3;
           // The rows' powers go with the weights, relative to the largest so far.
           // P is rounded to fp16 for the MMA, times 2^7: 2^-11 of each weight that is
           // over 2^-21 of the reference, and 2^-32 of that below.
-          const float fa = __uint_as_float(max(vsc[u][0] - ref + 134, 0) << 23);
-          const float fb = __uint_as_float(max(vsc[u][1] - ref + 134, 0) << 23);
-          const uint32_t b0 = transpose8(pack_half(p0 * fa, p1 * fa)), b1 = transpose8(pack_half(p2 * fb, p3 * fb));
+          uint32_t pk[2] = {0u, 0u};
+#pragma unroll
+          for (int j = 0; j < KL; ++j) {
+            const float p0 = ptx::ex2(x[u][2 * j] - z0), p1 = ptx::ex2(x[u][2 * j + 1] - z1);
+            l0 += p0;
+            l1 += p1;
+            const float f = __uint_as_float(max(vsc[u][j] - ref + 134, 0) << 23);
+            pk[j] = pack_half(p0 * f, p1 * f);
+          }
+          if constexpr (FOLD) {
+            pk[1] = low ? 0u : pk[0];
+            pk[0] = low ? pk[0] : 0u;
+          }
+          const uint32_t b0 = transpose8(pk[0]), b1 = transpose8(pk[1]);
           // The values' rows are the MMA's columns: a thread takes D / 8 codes of
           // its four keys, 2 tig, 2 tig + 1 and 8 further, and pairs the keys
           // byte by byte; the dims D / 8 grp + 2 mt and the next are rows grp and
@@ -988,6 +1042,24 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     for (int o = 4; o <= 16; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if constexpr (FOLD) {  // both halves of the lanes' keys into one (m, l, o)
+      const float o0 = __shfl_xor_sync(0xffffffffu, m0, 2), o1 = __shfl_xor_sync(0xffffffffu, m1, 2);
+      const float M0 = fmaxf(m0, o0), M1 = fmaxf(m1, o1);
+      // without a maximum a half saw no key (or nothing but NaN scores)
+      const float a0 = m0 == -INFINITY ? 1.0f : ptx::ex2(m0 - M0), a1 = m1 == -INFINITY ? 1.0f : ptx::ex2(m1 - M1);
+      m0 = M0;
+      m1 = M1;
+      l0 *= a0;
+      l1 *= a1;
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        oacc[mt][0] *= a0; oacc[mt][1] *= a1; oacc[mt][2] *= a0; oacc[mt][3] *= a1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) oacc[mt][j] += __shfl_xor_sync(0xffffffffu, oacc[mt][j], 2);
+      }
     }
     if (!wait_merged()) break;
     if (warp == 0 && lane == 0) sm.part = meta;
