@@ -11,7 +11,10 @@
 // bytes of a row -- the two 16-byte vectors that pair up -- so that a rotation
 // needs no exchange and an in-place call reads its pair before it writes it.
 // What a norm or an e4m3 row needs of the whole row (its sum of squares, its
-// largest magnitude) the 4 to 16 threads of a row exchange by shuffles.
+// largest magnitude) the 4 to 16 threads of a row exchange by shuffles.  Two
+// prompts of up to 4096 tokens, 16 / 4 heads (floor 12.0 us): normed 22 us (32
+// with heads of all kinds in a warp, one row's sum after the other), normed
+// into e4m3 pages 27 us, read back from there 7.3 us.
 #include <algorithm>
 
 #include "paged.cuh"

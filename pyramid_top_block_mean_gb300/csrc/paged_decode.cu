@@ -27,21 +27,27 @@
 // 8-bit pages (Q8) are half the bytes, and the work on them has to keep up: a
 // page's loads take 700 cycles of an SM at the copy rate.
 //   - S = K q by m16n8k32 MMAs on the codes as they are.  A bf16 query is the sum
-//     of two e4m3 rows (split_query), each with its own accumulators, and a
-//     key's power of two is a factor of its scores.
+//     of two e4m3 rows (split_query): for up to four heads both are columns of
+//     one MMA, for eight each has its own.  A key's power of two is a factor of
+//     its scores.
 //   - The values' codes become fp16 (one instruction for two of them), paired
 //     over neighbouring keys by byte permutes, and O^T += V^T P in fp16 with the
 //     powers of two of the rows in P, relative to the largest so far.
+//   - The reference of the weights follows the maximum only when that has
+//     grown by 2^8: as a rule one vote takes the place of the reductions.
 //   - A thread reads whole 16-byte pieces: the order of the contraction, and
 //     of O's rows, is the one in which they come, so that nothing is exchanged,
 //     and the stage is free before the work on it begins.
-//   - Four groups of two warps, 32 keys each: a warp's wait, maxima and
-//     reference serve two tiles of 16.
-// 64 sequences of up to 8192 tokens, capped, 157 us (5.0 TB/s), 2 x 131072
-// tokens 94 us (5.2 TB/s), 64 sequences' 35 selected blocks 70 us (4.2 TB/s).
-// The four schedulers bound it: about 300 instructions for 16 keys, half of
-// them on the integer pipe.  Converting keys and values to bf16 in registers
-// took 214, 124 and 86 us, one stage at a time from the producer 205 and 124.
+//   - Four groups of two warps, 32 keys each; the producer fills two stages at
+//     a time, whose waits and addresses then share their latency.
+// 64 sequences of up to 8192 tokens, capped, 136 us (5.8 TB/s), 2 x 131072
+// tokens 88 us (5.6 TB/s), 64 sequences' 35 selected blocks 66 us (4.4 TB/s).
+// With the work left out the loads alone take 125 and 81 us.  Steps: keys and
+// values converted to bf16 in registers 214, 124 and 86 us; keys as operands,
+// a stage at a time 205 and 124; a stage of every group at once 199 and 101;
+// fp16 values, early release, 32 keys a warp 157 and 94; votes 150 and 91;
+// both parts of the queries in one MMA 133 and 84 (kernel times).  Two producer
+// warps in turn: 154 and 92 against 150 and 91.
 //
 // Measured (GB300): 64 ragged sequences of up to 8192 tokens, 32 / 8 heads, d
 // = 128: 237 us, 6.6 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
@@ -72,6 +78,7 @@ struct Shape {
   static constexpr int kCons = 32 * kWarps;        // consumer threads
   static constexpr int kThreads = kCons + 32 + kMerge;  // and the producer warp
   static constexpr int kBatch = 2;  // stages that the producer fills at once
+  static_assert(!Q8 || kBatch * kScaleLanes <= 32, "a warp brings the scales of a batch at once");
   // as many as fit beside the merge buffer; a multiple of the groups, so that
   // a stage always goes to the same one, which then sees each of its phases
   static constexpr int kStages = Q8 ? (D == 128 ? 8 : 16) : D == 128 ? (G == 8 ? 4 : 6) : (G == 8 ? 10 : 12);

@@ -33,6 +33,17 @@
 //
 // Rows with few tokens and a long cache: the keys of a CTA's rows are split
 // over several CTAs, whose parts a second kernel joins.
+//
+// 8-bit pages (Q8): TMA brings a tile's codes into its stage, and a fourth
+// warpgroup turns them into the bf16 numbers that they stand for in place
+// (exactly: the results are those over bf16 pages of these numbers), which is
+// all that the MMAs see.  Shared memory, which the MMAs saturate, bounds that:
+// 4400 cycles a step, of which 300 are the hand-over, 300 the register split,
+// and 1000 the conversion (without its arithmetic 690 of 785 us, without its
+// accesses 566).  So a long prompt expands the pages to bf16 first and reads
+// those.  8192 tokens behind 8192: 551 us (1497 TFLOP/s; 785 from the codes), 61
+// behind 65536 from the codes 56 us.  (Two warps for the keys and two for the
+// values, each with a step's time for its tile: 928 us.)
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1344,14 +1355,16 @@ size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
 
 // The bytes of e4m3 pages expanded to bf16 for calls of n tokens, and of the
 // table of the expanded ones in front of them; 0: the call reads the codes
-// itself.  Expanding costs a key and value of a head some 24 ns / 128 of the
-// whole GPU, reading the codes each 256-row item 6 (its converters share the
-// shared memory's bandwidth with the MMAs): five items a key head and more are
-// faster expanded.  (16 / 4 heads, behind 8192 tokens: 8192 new ones EXPANDED
-// against 776 us.)  Not beyond 4 GiB.
-constexpr int kExpandTiles = 5;
+// itself.  Expanding moves the cache once (16384 positions of 4 heads 16 us),
+// reading the codes costs every 256-row item about half its time again, since
+// its converters share the shared memory's bandwidth with the MMAs.  Measured
+// codes / expanded (us), one sequence behind 8192 (65536) cached tokens: 16 / 4
+// heads of 128 with 5 items a key head 52 / 56 (196 / 189), with 8 73 / 72 (323 /
+// 276), with 32 177 / 135 (1159 / 825); 32 / 8 heads of 64 with 8 86 / 87 (429 /
+// 415), with 16 122 / 113 (807 / 732).  Without a cached part it loses some 5
+// us up to 16 items.  Not beyond 4 GiB.
 size_t paged_prefill_scratch_bytes(const Prob& pr, int64_t n) {
-  if (make_plan(pr, n).tiles < kExpandTiles) return 0;
+  if (make_plan(pr, n).tiles < (pr.d == 128 ? 8 : 16)) return 0;
   const size_t pages = (size_t)pr.B * (size_t)ceil_div64(pr.N, kPage);
   const size_t total = align_up(pages * 4, 256) + pages * pr.Hkv * kPage * pr.d * 4;
   return total <= ((size_t)1 << 32) ? total : 0;

@@ -710,7 +710,9 @@ class PagedAttention:
     rope: fp32 [N, rot_dim] as append_paged takes it, or None; q_norm, k_norm:
     fp32 [d], weights of the heads' norms before the rotation, or None.  Pages
     are tensors of the model's dtype or, with their scales, of 8 bits
-    (quantized_pages)."""
+    (quantized_pages).  The first prompt over 8-bit pages makes a scratch of
+    cache_scratch_bytes (0 to 4 GiB) where there is room for it, kept for the
+    prompts that follow."""
 
     def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
                  device="cuda", q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
@@ -788,8 +790,11 @@ class PagedAttention:
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None,
                       scales=None):
         out = self._buffer("prefill", q)
-        if scales is not None and self._scratch_bytes and self._scratch is None:  # kept for the calls that follow
-            self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.device)
+        if scales is not None and self._scratch_bytes and self._scratch is None:
+            try:
+                self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.device)
+            except torch.OutOfMemoryError:  # slower without, and the same results
+                self._scratch_bytes = 0
         _dense_prefill(self.p, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space, out.data_ptr(), mask,
                        scales, self._scratch, stream, True)
         return out
