@@ -526,10 +526,12 @@ struct ExpandArgs {
   int64_t n, window;
 };
 
-// One CTA: a page of a sequence, all heads; a thread 16 dims of a row of keys
-// and of values at a time.
+// One CTA: a page of a sequence and a key head; a thread 16 dims of a row of
+// keys and of values at a time.  (16384 positions of 4 heads; a CTA for all
+// heads of a page, a quarter of the grid, 16 us.)
 __global__ void __launch_bounds__(256) expand_kernel(Prob pr, ExpandArgs a) {
   const int64_t j = blockIdx.x, nb = a.codes.nb;
+  const int h = blockIdx.z;
   for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) {
     int64_t len, cnt;
     if (!new_span(a.seq_lens, a.new_lens, b, a.n, pr.N, &len, &cnt) || cnt == 0 || j > (len - 1) / pr.C) continue;
@@ -538,16 +540,15 @@ __global__ void __launch_bounds__(256) expand_kernel(Prob pr, ExpandArgs a) {
     const uint32_t page = (uint32_t)a.codes.table[b * nb + j];  // a negative entry is past any pool
     const bool in_pool = page < a.codes.num_pages;
     const int64_t to = b * nb + j;
-    if (threadIdx.x == 0) const_cast<int32_t*>(a.wide.table)[to] = in_pool ? (int32_t)to : -1;
+    if (h == 0 && threadIdx.x == 0) const_cast<int32_t*>(a.wide.table)[to] = in_pool ? (int32_t)to : -1;
     if (!in_pool) continue;
-    const int units = pr.d / 16, rows = pr.Hkv * (int)pr.C;
-    for (int x = threadIdx.x; x < rows * units; x += blockDim.x) {
-      const int64_t row = x / units;
-      const int e0 = 16 * (x % units);
-      read_unit<__nv_bfloat16, true>(a.codes.k, a.codes.ks, (int64_t)page * rows + row, e0, pr.d,
-                                     const_cast<void*>(a.wide.k), to * rows + row);
-      read_unit<__nv_bfloat16, true>(a.codes.v, a.codes.vs, (int64_t)page * rows + row, e0, pr.d,
-                                     const_cast<void*>(a.wide.v), to * rows + row);
+    const int units = pr.d / 16;
+    const int64_t from = ((int64_t)page * pr.Hkv + h) * pr.C, row0 = (to * pr.Hkv + h) * pr.C;
+#pragma unroll 2
+    for (int x = threadIdx.x; x < (int)pr.C * units; x += 256) {
+      const int r = x / units, e0 = 16 * (x % units);
+      read_unit<__nv_bfloat16, true>(a.codes.k, a.codes.ks, from + r, e0, pr.d, const_cast<void*>(a.wide.k), row0 + r);
+      read_unit<__nv_bfloat16, true>(a.codes.v, a.codes.vs, from + r, e0, pr.d, const_cast<void*>(a.wide.v), row0 + r);
     }
   }
 }
@@ -558,7 +559,8 @@ cudaError_t launch_expand_paged(const Prob& pr, int64_t n, int64_t window, const
                                 const int32_t* seq_lens, const int32_t* new_lens, cudaStream_t st) {
   const ExpandArgs a{codes, wide, seq_lens, new_lens, n, window};
   note_launch();
-  expand_kernel<<<dim3((unsigned)codes.nb, (unsigned)std::min<int64_t>(pr.B, 65535)), 256, 0, st>>>(pr, a);
+  expand_kernel<<<dim3((unsigned)codes.nb, (unsigned)std::min<int64_t>(pr.B, 65535), (unsigned)pr.Hkv), 256, 0, st>>>(
+      pr, a);
   return cudaGetLastError();
 }
 

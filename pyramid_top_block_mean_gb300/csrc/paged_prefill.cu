@@ -41,7 +41,7 @@
 // 4400 cycles a step, of which 300 are the hand-over, 300 the register split,
 // and 1000 the conversion (without its arithmetic 690 of 785 us, without its
 // accesses 566).  So a long prompt expands the pages to bf16 first and reads
-// those.  8192 tokens behind 8192: 551 us (1497 TFLOP/s; 785 from the codes), 61
+// those.  8192 tokens behind 8192: 547 us (1507 TFLOP/s; 785 from the codes), 61
 // behind 65536 from the codes 56 us.  (Two warps for the keys and two for the
 // values, each with a step's time for its tile: 928 us.)
 #include <cudaTypedefs.h>
@@ -1355,7 +1355,7 @@ size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
 
 // The bytes of e4m3 pages expanded to bf16 for calls of n tokens, and of the
 // table of the expanded ones in front of them; 0: the call reads the codes
-// itself.  Expanding moves the cache once (16384 positions of 4 heads 16 us),
+// itself.  Expanding moves the cache once (16384 positions of 4 heads 12 us),
 // reading the codes costs every 256-row item about half its time again, since
 // its converters share the shared memory's bandwidth with the MMAs.  Measured
 // codes / expanded (us), one sequence behind 8192 (65536) cached tokens: 16 / 4
@@ -1364,7 +1364,7 @@ size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
 // 415), with 16 122 / 113 (807 / 732).  Without a cached part it loses some 5
 // us up to 16 items.  Not beyond 4 GiB.
 size_t paged_prefill_scratch_bytes(const Prob& pr, int64_t n) {
-  if (make_plan(pr, n).tiles < (pr.d == 128 ? 8 : 16)) return 0;
+  if (make_plan(pr, n).tiles < (pr.d == 128 ? 8 : 16) || pr.Hkv > 65535) return 0;  // (a grid's third dimension)
   const size_t pages = (size_t)pr.B * (size_t)ceil_div64(pr.N, kPage);
   const size_t total = align_up(pages * 4, 256) + pages * pr.Hkv * kPage * pr.d * 4;
   return total <= ((size_t)1 << 32) ? total : 0;

@@ -204,6 +204,17 @@ def test_two_layers_on_two_streams(pisa):
         assert torch.equal(m.layer._buffer("dense", q), a) and torch.equal(m.layer._buffer("prefill", x), b)
 
 
+def test_without_room_for_a_scratch(pisa):
+    m = Model(pisa, 1, 3000, 8, 2, 128, n=2500)
+    q = m.append(2500, [2500], [2500]).clone()
+    want = m.layer.dense_prefill(q, *m.cache(), i32([2500]), scales=m.scales).clone()
+    assert m.layer._scratch is not None
+    m.layer._scratch, m.layer._scratch_bytes = None, 1 << 45
+    for _ in range(2):
+        assert torch.equal(m.layer.dense_prefill(q, *m.cache(), i32([2500]), scales=m.scales), want)
+    assert m.layer._scratch is None
+
+
 def test_repeated_calls_agree_bit_for_bit(pisa):
     m = Model(pisa, 2, 5000, 8, 2, 128, n=4000)
     m.append(4000, [4000, 3777], [4000, 3777])
