@@ -12,9 +12,9 @@
 // needs no exchange and an in-place call reads its pair before it writes it.
 // What a norm or an e4m3 row needs of the whole row (its sum of squares, its
 // largest magnitude) the 4 to 16 threads of a row exchange by shuffles.  Two
-// prompts of up to 4096 tokens, 16 / 4 heads (floor 12.0 us): normed 22 us (32
-// with heads of all kinds in a warp, one row's sum after the other), normed
-// into e4m3 pages 27 us, read back from there 7.3 us.
+// prompts of up to 4096 tokens, 16 / 4 heads (floor 12.0 us): normed 20.6 us
+// (32 with heads of all kinds in a warp, one row's sum after the other), normed
+// into e4m3 pages 25.6 us, read back from there 7.3 us.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -387,6 +387,10 @@ __device__ __forceinline__ void append_heads(const Prob& pr, const AppendArgs& a
       }
     }
   };
+  const int64_t ostep = a.n * pr.d, pstep = pr.C * pr.d;  // from head to head
+  T* out = is_q ? (T*)a.q_out : is_v ? nullptr : (T*)a.k_out;
+  if (out) out += ((b * H + h0) * a.n + i) * pr.d;
+  const int64_t row0 = ((int64_t)page * H + h0) * pr.C + pos % pr.C;
   const bool kept = Q8 && !is_q;  // the rows go into e4m3 pages: their numbers are made twice, once for the scale
   uint32_t top[R];
 #pragma unroll
@@ -401,13 +405,13 @@ __device__ __forceinline__ void append_heads(const Prob& pr, const AppendArgs& a
       y0 = Vec<T>::store(x);
       y1 = Vec<T>::store(x + E);
     }
-    if (is_q || (!is_v && a.k_out)) {
-      T* dst = (T*)(is_q ? a.q_out : a.k_out) + ((b * H + h0 + k) * a.n + i) * pr.d;
+    if (out) {
+      T* dst = out + k * ostep;
       *reinterpret_cast<uint4*>(dst + e0) = y0;
       *reinterpret_cast<uint4*>(dst + e1) = y1;
     }
     if (!Q8 && in_pool) {
-      T* dst = (T*)(is_v ? a.v_pages : a.k_pages) + (((int64_t)page * H + h0 + k) * pr.C + pos % pr.C) * pr.d;
+      T* dst = (T*)(is_v ? a.v_pages : a.k_pages) + row0 * pr.d + k * pstep;
       *reinterpret_cast<uint4*>(dst + e0) = y0;
       *reinterpret_cast<uint4*>(dst + e1) = y1;
     }
@@ -424,11 +428,10 @@ __device__ __forceinline__ void append_heads(const Prob& pr, const AppendArgs& a
     float x[2 * E];
     finish(k, x);
     const uint32_t scale = scale_of_bits(top[k]);
-    const int64_t row = ((int64_t)page * H + h0 + k) * pr.C + pos % pr.C;
-    uint8_t* dst = (uint8_t*)(is_v ? a.v_pages : a.k_pages) + row * pr.d;
+    uint8_t* dst = (uint8_t*)(is_v ? a.v_pages : a.k_pages) + row0 * pr.d + k * pstep;
     store_codes<E>(dst + e0, x, scale);
     store_codes<E>(dst + e1, x + E, scale);
-    if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = (uint8_t)scale;
+    if (u == 0) (is_v ? a.v_scales : a.k_scales)[row0 + k * pr.C] = (uint8_t)scale;
   }
 }
 
@@ -454,9 +457,10 @@ __device__ __forceinline__ void write_status(const Prob& pr, const int32_t* seq_
 
 // Three CTAs on an SM: with four rows a thread the compiler takes 91 registers
 // if it may, which leaves two (a 2 x 4096-token prompt 15.1 us, against 13.2).
-// HEADS: append_heads().
+// HEADS: append_heads(), by CTAs of 128 threads.
+constexpr int kHeadsThreads = 128;
 template <typename T, int R, bool NORM, bool Q8, bool HEADS>
-__global__ void __launch_bounds__(256, HEADS ? 2 : 3) append_kernel(Prob pr, AppendArgs a) {
+__global__ void __launch_bounds__(HEADS ? kHeadsThreads : 256, HEADS ? 4 : 3) append_kernel(Prob pr, AppendArgs a) {
   for (int64_t b = blockIdx.y; b < pr.B; b += gridDim.y) {
     if constexpr (HEADS) append_heads<T, R, NORM, Q8>(pr, a, b);
     else append_units<T, R, NORM, Q8>(pr, a, b);
@@ -584,10 +588,11 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   // 16 + 2 x 4 heads (12.0 us at the copy rate), where one row a thread took
   // 18.2; a step of 64 tokens (2.7 us) has too few rows to give up any thread.
   const bool many = pr.B * n * rows * (256 / per) >= 4 * 152 * 2048;
-  const bool normed = norm.q || norm.k, in8 = pools.ks != nullptr, heads = many && (normed || in8) && n >= per;
+  const bool normed = norm.q || norm.k, in8 = pools.ks != nullptr, heads = many && (normed || in8) && n >= per / 2;
   const int R = heads || (many && !normed && !in8) ? 4 : 1;
   const int64_t groups = (q ? ceil_div64(pr.Hq, R) : 0) + 2 * ceil_div64(pr.Hkv, R);
-  const dim3 grid((unsigned)(heads ? ceil_div64(n, per) * groups : ceil_div64(n * ceil_div64(rows, R), per)),
+  const int threads = heads ? kHeadsThreads : 256, hper = kHeadsThreads / (256 / per);
+  const dim3 grid((unsigned)(heads ? ceil_div64(n, hper) * groups : ceil_div64(n * ceil_div64(rows, R), per)),
                   (unsigned)std::min<int64_t>(pr.B, 65535));
   auto pick = [&](auto type) {
     using T = decltype(type);
@@ -602,7 +607,7 @@ cudaError_t launch_append_paged(const Prob& pr, int64_t n, const void* q, const 
   };
   auto kern = pr.dtype == PISA_BF16 ? pick(__nv_bfloat16()) : pick(float());
   note_launch();
-  kern<<<grid, 256, 0, st>>>(pr, a);
+  kern<<<grid, threads, 0, st>>>(pr, a);
   return cudaGetLastError();
 }
 
