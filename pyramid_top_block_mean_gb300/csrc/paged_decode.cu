@@ -205,6 +205,24 @@ __device__ __forceinline__ void mma16832_e4m3(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two fp16 numbers as codes and those of 32 times what they leave.
+__device__ __forceinline__ void split_pair(uint32_t x, uint32_t& c, uint32_t& r) {
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, h;\n\t"
+      "sub.rn.f16x2 y, %2, y;\n\t"
+      "mul.rn.f16x2 y, y, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, y;\n\t"
+      "cvt.u32.u16 %0, h;\n\t"
+      "cvt.u32.u16 %1, l;\n\t}"
+      : "=r"(c), "=r"(r)
+      : "r"(x), "r"(0x50005000u));  // 32 in fp16
+}
 // A query as the sum of two e4m3 rows: with s the power of two that brings the
 // head's largest magnitude to 128 .. 256, x = q s is hi + lo / 32.  Of a bf16
 // number, whose 8 bits are twice e4m3's, hi takes four and leaves at most 4 and
@@ -218,13 +236,14 @@ __device__ __forceinline__ float split_query(const uint16_t* row, bool there, ui
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
     w[i] = there ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0u, 0u, 0u, 0u);
-  uint32_t top = 0;
+  uint32_t pair = 0;  // largest magnitudes of the even and the odd elements
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7fffu, u[k] >> 16 & 0x7fffu));
+    for (int k = 0; k < 4; ++k) pair = __vmaxu2(pair, u[k] & 0x7fff7fffu);
   }
+  uint32_t top = max(pair & 0xffffu, pair >> 16);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const uint32_t e = max(top >> 7, 14u);  // biased; 2^(134 - 127 - e) stays a normal number
@@ -234,18 +253,15 @@ __device__ __forceinline__ float split_query(const uint16_t* row, bool there, ui
     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float x[4] = {__uint_as_float(u[2 * k] << 16) * s, __uint_as_float(u[2 * k] & 0xffff0000u) * s,
-                          __uint_as_float(u[2 * k + 1] << 16) * s, __uint_as_float(u[2 * k + 1] & 0xffff0000u) * s};
-      const uint32_t c = to_codes(x[0], x[1]) | to_codes(x[2], x[3]) << 16;
-      float y[4];
+      uint32_t c[2], r[2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        // the number of code n: its bits as a bf16 number times 2^120
-        const uint32_t b = c >> (8 * n);
-        y[n] = (x[n] - __uint_as_float((b & 0x80u) << 24 | (b & 0x7fu) << 20) * 0x1p120f) * 32.0f;
+      for (int n = 0; n < 2; ++n) {  // in fp16, of which x and the rest are numbers (down to 2^-24)
+        const uint32_t v = u[2 * k + n];
+        const uint32_t x = pack_half(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
+        split_pair(x, c[n], r[n]);
       }
-      hi[2 * i + k] = c;
-      lo[2 * i + k] = to_codes(y[0], y[1]) | to_codes(y[2], y[3]) << 16;
+      hi[2 * i + k] = c[0] | c[1] << 16;
+      lo[2 * i + k] = r[0] | r[1] << 16;
     }
   }
   return e == 255u ? NAN : __uint_as_float((e + 127u - 134u) << 23);
@@ -279,11 +295,6 @@ __device__ __forceinline__ void mma16816_half(float (&d)[4], const uint32_t (&a)
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
 }
 
 // Keys that the query of sequence b sees, and the pages that hold them; a
@@ -1118,7 +1129,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
 
 // Pages a CTA takes at least.  Joining costs 2 us and a page 0.4: 197 tokens of 4
 // heads 6.8 us with 4 (one CTA a head), 8.2 with 2, 9.2 with 8; 4096 tokens 10.0,
-// 10.8 and 10.6.
+// 10.8 and 10.6.  Over 8-bit pages, with the clearing kernel: 197 tokens 8.6, 10.0
+// and 11.3, 4096 tokens 11.2 and, with 2, 12.5.
 constexpr int kMinRun = 4;
 
 struct Ws {

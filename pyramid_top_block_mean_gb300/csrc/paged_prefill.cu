@@ -1355,7 +1355,7 @@ size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
 
 // The bytes of e4m3 pages expanded to bf16 for calls of n tokens, and of the
 // table of the expanded ones in front of them; 0: the call reads the codes
-// itself.  Expanding moves the cache once (16384 positions of 4 heads 12 us),
+// itself.  Expanding moves the cache once (16384 positions of 4 heads 14 us),
 // reading the codes costs every 256-row item about half its time again, since
 // its converters share the shared memory's bandwidth with the MMAs.  Measured
 // codes / expanded (us), one sequence behind 8192 (65536) cached tokens: 16 / 4
