@@ -1,7 +1,8 @@
 // append.cu -- new tokens into the paged cache, keys and queries normed head by
 // head and rotated by their positions on the way, and rows read back from it.
 //
-// A head's norm: x -> x / sqrt(sum x^2 / d + eps) * w, in fp32.
+// A head's norm: x -> x / sqrt(sum x^2 / d + eps) * w, in fp32 and in that
+// order (the root's reciprocal times a weight may leave fp32's range).
 // For a pair (a, b) of dims with angle theta of the token's position:
 //   (a, b) -> (a cos theta - b sin theta, b cos theta + a sin theta)
 // with the pairs (i, i + rot / 2) or (2i, 2i + 1); cosines and sines come from
@@ -228,8 +229,8 @@ __device__ __forceinline__ void append_units(const Prob& pr, const AppendArgs& a
 #pragma unroll
       for (int j = 0; j < 2 * E; j += 4) {
         const float4 x = *reinterpret_cast<const float4*>(weight + (j < E ? e0 + j : e1 + j - E));
-        ptx::unpack2(mul_pair(ptx::pack2(o[j], o[j + 1]), mul_pair(by2, ptx::pack2(x.x, x.y))), o[j], o[j + 1]);
-        ptx::unpack2(mul_pair(ptx::pack2(o[j + 2], o[j + 3]), mul_pair(by2, ptx::pack2(x.z, x.w))), o[j + 2], o[j + 3]);
+        ptx::unpack2(mul_pair(mul_pair(ptx::pack2(o[j], o[j + 1]), by2), ptx::pack2(x.x, x.y)), o[j], o[j + 1]);
+        ptx::unpack2(mul_pair(mul_pair(ptx::pack2(o[j + 2], o[j + 3]), by2), ptx::pack2(x.z, x.w)), o[j + 2], o[j + 3]);
       }
     }
     if (turns && !is_v) {
@@ -367,7 +368,7 @@ __device__ __forceinline__ void append_heads(const Prob& pr, const AppendArgs& a
       const uint64_t by2 = ptx::pack2(by[k], by[k]);
 #pragma unroll
       for (int j = 0; j < 2 * E; j += 2)
-        ptx::unpack2(mul_pair(ptx::pack2(x[j], x[j + 1]), mul_pair(by2, wt[j / 2])), x[j], x[j + 1]);
+        ptx::unpack2(mul_pair(mul_pair(ptx::pack2(x[j], x[j + 1]), by2), wt[j / 2]), x[j], x[j + 1]);
     }
     if (!turns) return;
     if (a.interleaved) {

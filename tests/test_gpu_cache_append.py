@@ -192,6 +192,25 @@ def test_norms_of_any_size(pisa, size):
         R.within(out, y, t + torch.finfo(dt).eps / 2 * (y.abs() + t) + 2e-38, "normed")
 
 
+@pytest.mark.parametrize("n", [70, 6500])
+@pytest.mark.parametrize("size,weight,eps", [(3e37, 1e-3, 1e-6), (1e-15, 1e30, 1e-30)])
+def test_norms_whose_factor_times_the_weight_leaves_fp32(pisa, size, weight, eps, n):
+    """The quotient x / rms is near one where 1 / rms and the weight are at the ends of fp32's range."""
+    g = torch.Generator().manual_seed(4)
+    p = pisa.make_params(1, n, 16, 4, 64, dtype="fp32")
+    q, k = ((torch.randn(1, h, n, 64, generator=g) * size).clamp(-3.3e38, 3.3e38).cuda() for h in (16, 4))
+    w = ((1 + torch.rand(64, generator=g)) * weight).cuda()
+    pages = -(-n // 64)
+    pool = torch.zeros(pages, 4, 64, 64, device="cuda")
+    ws = torch.empty(pisa.paged_workspace_bytes(p, n), dtype=torch.uint8, device="cuda")
+    q_out, k_out = torch.zeros_like(q), torch.zeros_like(k)
+    pisa.append_paged(p, k, k, pool, pool.clone(), i32([list(range(pages))]), i32([n]), ws, q=q, q_out=q_out,
+                      k_out=k_out, q_norm=w, k_norm=w, norm_eps=eps)
+    for x, out in ((q, q_out), (k, k_out)):
+        y, t = C.norm_rotate(x, w, float(torch.tensor(eps)), None, None, False)
+        R.within(out, y, t + 2.0 ** -24 * (y.abs() + t), "normed")
+
+
 def test_faults(pisa):
     """A length that does not fit skips its sequence; a page outside the pool is not written and not read."""
     p, q, k, v, pools, table, ws, scales, w = setup(pisa, 3, 300, 70, 4, 2, 64, "bf16", True, seed=9)
