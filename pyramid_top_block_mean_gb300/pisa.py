@@ -791,8 +791,9 @@ class PagedAttention:
                       scales=None):
         out = self._buffer("prefill", q)
         if scales is not None and self._scratch_bytes and self._scratch is None:
-            try:
-                self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.device)
+            try:  # in the order of the call's stream, so that no earlier owner of the memory still writes it
+                with torch.cuda.stream(stream):
+                    self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.ws.device)
             except torch.OutOfMemoryError:  # slower without, and the same results
                 self._scratch_bytes = 0
         _dense_prefill(self.p, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space, out.data_ptr(), mask,

@@ -251,3 +251,18 @@ def test_offsets_past_32_bits(pisa):
     want, tol = R.dense(q[0], got[0][0], got[1][0], 200, torch.arange(200, device="cuda"), 128 ** -0.5)
     R.within(out[0], want, tol)
     R.within(one[0], want[:, 199], tol[:, 199])
+
+
+def test_a_scratch_belongs_to_the_stream_of_its_call(pisa):
+    """Memory that the current stream may still write is not taken for a call on another."""
+    m = Model(pisa, 1, 2048, 16, 4, 128, n=512)
+    q = m.append(512, [512], [512])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.ones(m.layer._scratch_bytes, dtype=torch.uint8, device="cuda")
+    at = busy.data_ptr()
+    del busy
+    out = m.layer.dense_prefill(q, *m.cache(), i32([512]), scales=m.scales, stream=side)
+    torch.cuda.synchronize()
+    assert m.layer._scratch.data_ptr() != at
+    check(m, out[0], q[0], [512], 0, 512)
