@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -74,9 +75,11 @@ class HeadNorm(ctypes.Structure):
 
 _P = ctypes.POINTER(Params)
 _M = ctypes.POINTER(Mask)
-_C = ctypes.POINTER(Cache)
-_strides_t = ctypes.c_int64 * 9
 _vp = ctypes.c_void_p
+# A Cache and three strides as bytes, which take a third of the time of ctypes objects.
+_pack_cache = struct.Struct("@IiPPPPqPPN").pack
+_pack_strides = struct.Struct("@qqq").pack
+assert struct.calcsize("@IiPPPPqPPN") == ctypes.sizeof(Cache)
 _lib.pisa_abi_version.restype = ctypes.c_int
 _lib.pisa_kernel_launches.restype = ctypes.c_uint64
 _lib.pisa_status_string.argtypes = [ctypes.c_int]
@@ -123,20 +126,20 @@ _lib.pisa_dense_prefill_paged.argtypes = [_P, _M, ctypes.c_int64, _vp, _vp, _vp,
                                           ctypes.c_size_t, _vp, _vp]
 _lib.pisa_dense_prefill_paged.restype = ctypes.c_int
 _lib.pisa_cache_append.argtypes = [_P, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                   ctypes.POINTER(HeadNorm), _vp, ctypes.c_int32, ctypes.c_int32, _C, _vp,
+                                   ctypes.POINTER(HeadNorm), _vp, ctypes.c_int32, ctypes.c_int32, _vp, _vp,
                                    ctypes.c_size_t, _vp, _vp, _vp]
 _lib.pisa_cache_append.restype = ctypes.c_int
-_lib.pisa_cache_read.argtypes = [_P, ctypes.c_int64, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
+_lib.pisa_cache_read.argtypes = [_P, ctypes.c_int64, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
 _lib.pisa_cache_read.restype = ctypes.c_int
-_lib.pisa_cache_dense_decode.argtypes = [_P, _M, _vp, _C, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.pisa_cache_dense_decode.argtypes = [_P, _M, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_cache_dense_decode.restype = ctypes.c_int
-_lib.pisa_cache_attend_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.pisa_cache_attend_decode.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_cache_attend_decode.restype = ctypes.c_int
-_lib.pisa_cache_dense_prefill.argtypes = [_P, _M, ctypes.c_int64, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+_lib.pisa_cache_dense_prefill.argtypes = [_P, _M, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
 _lib.pisa_cache_dense_prefill.restype = ctypes.c_int
-_lib.pisa_cache_build_pyramid.argtypes = [_P, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.pisa_cache_build_pyramid.argtypes = [_P, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 _lib.pisa_cache_build_pyramid.restype = ctypes.c_int
-_lib.pisa_cache_select_decode.argtypes = [_P, _vp, _C, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp]
+_lib.pisa_cache_select_decode.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp]
 _lib.pisa_cache_select_decode.restype = ctypes.c_int
 _lib.pisa_cache_scratch_bytes.argtypes = [_P, ctypes.c_int32, ctypes.c_int64]
 _lib.pisa_cache_scratch_bytes.restype = ctypes.c_size_t
@@ -359,36 +362,41 @@ def _want(t, name: str, shape, dtype, index: int) -> int:
 
 
 def _want_rows(t, name: str, shape, dtype, index: int):
-    """Address and strides of a [B, H, n, d] view with adjacent elements in a row."""
+    """Address and strides (as the C side reads them) of a [B, H, n, d] view with adjacent elements in a row."""
     st = t.stride()
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or st[3] != 1:
         _refuse(t, name, shape, dtype, index, "row-contiguous")
-    return t.data_ptr(), st
+    return t.data_ptr(), _pack_strides(st[0], st[1], st[2])
 
 
-def _want_cache(p: Params, k_pages, v_pages, page_table, seq_lens, dtype, index: int):
+def _want_cache(dims, k_pages, v_pages, page_table, seq_lens, index: int):
     """(k_pages, v_pages, number of pages, page_table, seq_lens) as the calls take them."""
+    B, _, H_kv, d, C, nb, _, dtype = dims
     num = k_pages.shape[0]
-    shape = (num, p.H_kv, p.C, p.d)
-    B = p.B
+    shape = (num, H_kv, C, d)
     return (_want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index), num,
-            _want(page_table, "page_table", (B, -(-p.N // 64)), torch.int32, index),
+            _want(page_table, "page_table", (B, nb), torch.int32, index),
             _want(seq_lens, "seq_lens", (B,), torch.int32, index))
 
 
-def _want_pages(p: Params, k_pages, v_pages, page_table, seq_lens, scales, dtype, index: int):
-    """(Cache, seq_lens) of pages in the model's dtype (scales None) or in e4m3."""
+def _dims(p: Params):
+    """What the paged calls look at, read once (a field takes as long as an attribute of a tensor)."""
+    return p.B, p.H_q, p.H_kv, p.d, p.C, -(-p.N // 64), p.K + 3, _dtype(p)
+
+
+def _want_pages(dims, k_pages, v_pages, page_table, seq_lens, scales, index: int, scratch=(0, 0)):
+    """(Cache as bytes, seq_lens) of pages in the model's dtype (scales None) or in e4m3."""
+    B, _, H_kv, d, C, nb, _, dtype = dims
     num = k_pages.shape[0]
-    shape = (num, p.H_kv, p.C, p.d)
-    ks = vs = None
+    shape = (num, H_kv, C, d)
+    fmt, ks, vs = CACHE_PARAMS, 0, 0
     if scales is not None:
-        dtype = torch.float8_e4m3fn
-        ks = _want(scales, "scales", (2, num, p.H_kv, p.C), torch.uint8, index)
-        vs = ks + num * p.H_kv * p.C
-    B = p.B
-    return (Cache(ctypes.sizeof(Cache), CACHE_PARAMS if scales is None else CACHE_E4M3,
-                  _want(k_pages, "k_pages", shape, dtype, index), _want(v_pages, "v_pages", shape, dtype, index),
-                  ks, vs, num, _want(page_table, "page_table", (B, -(-p.N // 64)), torch.int32, index), None, 0),
+        fmt, dtype = CACHE_E4M3, torch.float8_e4m3fn
+        ks = _want(scales, "scales", (2, num, H_kv, C), torch.uint8, index)
+        vs = ks + num * H_kv * C
+    return (_pack_cache(ctypes.sizeof(Cache), fmt, _want(k_pages, "k_pages", shape, dtype, index),
+                        _want(v_pages, "v_pages", shape, dtype, index), ks, vs, num,
+                        _want(page_table, "page_table", (B, nb), torch.int32, index), *scratch),
             _want(seq_lens, "seq_lens", (B,), torch.int32, index))
 
 
@@ -457,28 +465,26 @@ def _mask_arg(mask: Optional[AttentionMask], p: Params, n: int, index: int):
 # The calls proper, with a workspace, outputs and angles (addresses) that their
 # callers have looked at already: the functions below at each call,
 # PagedAttention when it makes them.
-def _append(p, k, v, k_pages, v_pages, page_table, seq_lens, space, rope, rot, interleaved, q, q_out, k_out, new_lens,
-            scales, norm, stream, check) -> int:
-    index, dt = k.get_device(), _dtype(p)
-    n = k.shape[2]
-    kv_shape = (p.B, p.H_kv, n, p.d)
+def _append(p, dims, k, v, k_pages, v_pages, page_table, seq_lens, space, rope, rot, interleaved, q, q_out, k_out,
+            new_lens, scales, norm, stream, check) -> int:
+    index, n = k.get_device(), k.shape[2]
+    B, H_q, H_kv, d, _, _, _, dt = dims
+    kv_shape = (B, H_kv, n, d)
     kp, ks = _want_rows(k, "k", kv_shape, dt, index)
     vp, vs = _want_rows(v, "v", kv_shape, dt, index)
-    qp, qs = (None, ks) if q is None else _want_rows(q, "q", (p.B, p.H_q, n, p.d), dt, index)
-    strides = _strides_t(*qs[:3], *ks[:3], *vs[:3])
-    at = ctypes.addressof(strides)
-    new = None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index)
+    qp = qs = None
+    if q is not None:
+        qp, qs = _want_rows(q, "q", (B, H_q, n, d), dt, index)
+    new = None if new_lens is None else _want(new_lens, "new_lens", (B,), torch.int32, index)
     if k_out is not None:
         k_out = _want(k_out, "k_out", kv_shape, dt, index)
     if scales is None and norm is None:
-        kpp, vpp, num, table, lens = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
-        return _launch(index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, at,
-                       kp, at + 24, vp, at + 48, lens, new, rope, rot, interleaved, kpp, vpp, num, table, *space,
-                       q_out, k_out)
-    cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
-    return _launch(index, stream, "pisa_cache_append", check, _lib.pisa_cache_append, ctypes.byref(p), n, qp, at, kp,
-                   at + 24, vp, at + 48, lens, new, norm, rope, rot, interleaved, ctypes.byref(cache), *space, q_out,
-                   k_out)
+        kpp, vpp, num, table, lens = _want_cache(dims, k_pages, v_pages, page_table, seq_lens, index)
+        return _launch(index, stream, "pisa_append_paged", check, _lib.pisa_append_paged, ctypes.byref(p), n, qp, qs,
+                       kp, ks, vp, vs, lens, new, rope, rot, interleaved, kpp, vpp, num, table, *space, q_out, k_out)
+    cache, lens = _want_pages(dims, k_pages, v_pages, page_table, seq_lens, scales, index)
+    return _launch(index, stream, "pisa_cache_append", check, _lib.pisa_cache_append, ctypes.byref(p), n, qp, qs, kp,
+                   ks, vp, vs, lens, new, norm, rope, rot, interleaved, cache, *space, q_out, k_out)
 
 
 def _either(k_out, v_out):
@@ -487,59 +493,62 @@ def _either(k_out, v_out):
     return v_out if k_out is None else k_out
 
 
-def _read(p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, space, new_lens, scales, stream, check) -> int:
+def _read(p, dims, k_out, v_out, k_pages, v_pages, page_table, seq_lens, space, new_lens, scales, stream,
+          check) -> int:
     one = _either(k_out, v_out)
-    index, dt, n = one.get_device(), _dtype(p), one.shape[2]
-    shape = (p.B, p.H_kv, n, p.d)
-    cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
-    return _launch(index, stream, "pisa_cache_read", check, _lib.pisa_cache_read, ctypes.byref(p), n,
-                   ctypes.byref(cache), lens,
-                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space,
+    index, n = one.get_device(), one.shape[2]
+    B, _, H_kv, d, _, _, _, dt = dims
+    shape = (B, H_kv, n, d)
+    cache, lens = _want_pages(dims, k_pages, v_pages, page_table, seq_lens, scales, index)
+    return _launch(index, stream, "pisa_cache_read", check, _lib.pisa_cache_read, ctypes.byref(p), n, cache, lens,
+                   None if new_lens is None else _want(new_lens, "new_lens", (B,), torch.int32, index), *space,
                    None if k_out is None else _want(k_out, "k_out", shape, dt, index),
                    None if v_out is None else _want(v_out, "v_out", shape, dt, index))
 
 
-def _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, space, out, mask, scales, stream, check) -> int:
-    index, dt = q.get_device(), _dtype(p)
+def _dense_decode(p, dims, q, k_pages, v_pages, page_table, seq_lens, space, out, mask, scales, stream, check) -> int:
+    index = q.get_device()
+    B, H_q, _, d, _, _, _, dt = dims
     if scales is not None:
-        cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+        cache, lens = _want_pages(dims, k_pages, v_pages, page_table, seq_lens, scales, index)
         return _launch(index, stream, "pisa_cache_dense_decode", check, _lib.pisa_cache_dense_decode, ctypes.byref(p),
-                       _mask_arg(mask, p, 1, index), _want(q, "q", (p.B, p.H_q, p.d), dt, index), ctypes.byref(cache),
-                       lens, *space, out)
-    cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+                       _mask_arg(mask, p, 1, index), _want(q, "q", (B, H_q, d), dt, index), cache, lens, *space, out)
+    cache = _want_cache(dims, k_pages, v_pages, page_table, seq_lens, index)
     return _launch(index, stream, "pisa_dense_decode_paged", check, _lib.pisa_dense_decode_paged, ctypes.byref(p),
-                   _mask_arg(mask, p, 1, index), _want(q, "q", (p.B, p.H_q, p.d), dt, index), *cache, *space, out)
+                   _mask_arg(mask, p, 1, index), _want(q, "q", (B, H_q, d), dt, index), *cache, *space, out)
 
 
-def _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, space, out, scales, stream, check) -> int:
-    index, dt = q.get_device(), _dtype(p)
+def _selected_decode(p, dims, q, k_pages, v_pages, page_table, seq_lens, idx, space, out, scales, stream,
+                     check) -> int:
+    index = q.get_device()
+    B, H_q, H_kv, d, _, _, W, dt = dims
     if scales is not None:
-        cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
+        cache, lens = _want_pages(dims, k_pages, v_pages, page_table, seq_lens, scales, index)
         return _launch(index, stream, "pisa_cache_attend_decode", check, _lib.pisa_cache_attend_decode,
-                       ctypes.byref(p), _want(q, "q", (p.B, p.H_q, p.d), dt, index), ctypes.byref(cache), lens,
-                       _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space, out)
-    cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+                       ctypes.byref(p), _want(q, "q", (B, H_q, d), dt, index), cache, lens,
+                       _want(idx, "idx", (B, H_kv, W), torch.int32, index), *space, out)
+    cache = _want_cache(dims, k_pages, v_pages, page_table, seq_lens, index)
     return _launch(index, stream, "pisa_attend_decode_paged", check, _lib.pisa_attend_decode_paged, ctypes.byref(p),
-                   _want(q, "q", (p.B, p.H_q, p.d), dt, index), *cache,
-                   _want(idx, "idx", (p.B, p.H_kv, p.K + 3), torch.int32, index), *space, out)
+                   _want(q, "q", (B, H_q, d), dt, index), *cache,
+                   _want(idx, "idx", (B, H_kv, W), torch.int32, index), *space, out)
 
 
-def _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, scales, scratch, stream,
-                   check) -> int:
-    index, dt, n = q.get_device(), _dtype(p), q.shape[2]
+def _dense_prefill(p, dims, q, k_pages, v_pages, page_table, seq_lens, new_lens, space, out, mask, scales, scratch,
+                   stream, check) -> int:
+    index, n = q.get_device(), q.shape[2]
+    B, H_q, _, d, _, _, _, dt = dims
     if scales is not None:
-        cache, lens = _want_pages(p, k_pages, v_pages, page_table, seq_lens, scales, dt, index)
-        if scratch is not None:
-            cache.scratch, cache.scratch_bytes = _want_space(scratch, index)
+        cache, lens = _want_pages(dims, k_pages, v_pages, page_table, seq_lens, scales, index,
+                                  (0, 0) if scratch is None else _want_space(scratch, index))
         return _launch(index, stream, "pisa_cache_dense_prefill", check, _lib.pisa_cache_dense_prefill,
-                       ctypes.byref(p), _mask_arg(mask, p, n, index), n,
-                       _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), ctypes.byref(cache), lens,
-                       None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space,
+                       ctypes.byref(p), _mask_arg(mask, p, n, index), n, _want(q, "q", (B, H_q, n, d), dt, index),
+                       cache, lens,
+                       None if new_lens is None else _want(new_lens, "new_lens", (B,), torch.int32, index), *space,
                        out)
-    cache = _want_cache(p, k_pages, v_pages, page_table, seq_lens, dt, index)
+    cache = _want_cache(dims, k_pages, v_pages, page_table, seq_lens, index)
     return _launch(index, stream, "pisa_dense_prefill_paged", check, _lib.pisa_dense_prefill_paged, ctypes.byref(p),
-                   _mask_arg(mask, p, n, index), n, _want(q, "q", (p.B, p.H_q, n, p.d), dt, index), *cache,
-                   None if new_lens is None else _want(new_lens, "new_lens", (p.B,), torch.int32, index), *space, out)
+                   _mask_arg(mask, p, n, index), n, _want(q, "q", (B, H_q, n, d), dt, index), *cache,
+                   None if new_lens is None else _want(new_lens, "new_lens", (B,), torch.int32, index), *space, out)
 
 
 def cache_scratch_bytes(p: Params, n: int) -> int:
@@ -569,8 +578,9 @@ def append_paged(p: Params, k, v, k_pages, v_pages, page_table, seq_lens, ws, ro
         q_out = _want(q_out, "q_out", (p.B, p.H_q, k.shape[2], p.d), _dtype(p), index)
     if rope is not None:
         rope = _want(rope, "rope", (p.N, rot), torch.float32, index)
-    return _append(p, k, v, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), rope, rot, interleaved, q,
-                   q_out, k_out, new_lens, scales, _head_norm(p, q_norm, k_norm, norm_eps, index), stream, check)
+    return _append(p, _dims(p), k, v, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), rope, rot,
+                   interleaved, q, q_out, k_out, new_lens, scales, _head_norm(p, q_norm, k_norm, norm_eps, index),
+                   stream, check)
 
 
 def read_paged(p: Params, k_out, v_out, k_pages, v_pages, page_table, seq_lens, ws, new_lens=None, scales=None,
@@ -579,8 +589,8 @@ def read_paged(p: Params, k_out, v_out, k_pages, v_pages, page_table, seq_lens, 
     (None: n) positions of each sequence, from pages in the model's dtype or,
     with scales, in e4m3."""
     index = _either(k_out, v_out).get_device()
-    return _read(p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), new_lens, scales,
-                 stream, check)
+    return _read(p, _dims(p), k_out, v_out, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index), new_lens,
+                 scales, stream, check)
 
 
 def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws, out,
@@ -588,7 +598,7 @@ def dense_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws,
     """q and out [B, H_q, d]: attention of one new token per sequence over its
     whole cache (scales: of e4m3 pages)."""
     index = q.get_device()
-    return _dense_decode(p, q, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index),
+    return _dense_decode(p, _dims(p), q, k_pages, v_pages, page_table, seq_lens, _want_space(ws, index),
                          _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), mask, scales, stream, check)
 
 
@@ -596,7 +606,7 @@ def attend_decode_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, id
                         check: bool = True, scales=None) -> int:
     """attend_decode over a paged cache (scales: of e4m3 pages); idx int32 [B, H_kv, K+3]."""
     index = q.get_device()
-    return _selected_decode(p, q, k_pages, v_pages, page_table, seq_lens, idx, _want_space(ws, index),
+    return _selected_decode(p, _dims(p), q, k_pages, v_pages, page_table, seq_lens, idx, _want_space(ws, index),
                             _want(out, "out", (p.B, p.H_q, p.d), _dtype(p), index), scales, stream, check)
 
 
@@ -607,7 +617,7 @@ def dense_prefill_paged(p: Params, q, k_pages, v_pages, page_table, seq_lens, ws
     pages that hold them already (scales: of e4m3 pages; scratch: a tensor of
     cache_scratch_bytes for long prompts over them)."""
     index = q.get_device()
-    return _dense_prefill(p, q, k_pages, v_pages, page_table, seq_lens, new_lens, _want_space(ws, index),
+    return _dense_prefill(p, _dims(p), q, k_pages, v_pages, page_table, seq_lens, new_lens, _want_space(ws, index),
                           _want(out, "out", (p.B, p.H_q, q.shape[2], p.d), _dtype(p), index), mask, scales, scratch,
                           stream, check)
 
@@ -726,11 +736,13 @@ class PagedAttention:
         nbytes = max(nbytes, paged_workspace_bytes(p, min(p.N, 1)))  # (n = 0: decode calls)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.device = self.ws.device
+        self._dims = _dims(p)
         self._index = self.ws.get_device()
         self._space = _want_space(self.ws, self._index)
         self._rot = 0 if rope is None else rope.shape[-1]
         self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
-        self._scratch, self._scratch_bytes = None, cache_scratch_bytes(p, n)  # made by the first prompt over 8-bit pages
+        self._scratch = None  # made by the first prompt over 8-bit pages
+        self._scratch_bytes = cache_scratch_bytes(p, n)
         self.q_norm, self.k_norm = q_norm, k_norm
         self._norm = _head_norm(p, q_norm, k_norm, norm_eps, self._index)
         one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
@@ -763,7 +775,7 @@ class PagedAttention:
         if q is None:
             self._fits(k, k.dim() == 4 and k.shape[2] <= self.n)
         q_out = None if q is None else self._buffer("q", q)
-        _append(self.p, k, v, k_pages, v_pages, page_table, seq_lens, self._space, self._rope, self._rot,
+        _append(self.p, self._dims, k, v, k_pages, v_pages, page_table, seq_lens, self._space, self._rope, self._rot,
                 self.interleaved, q, None if q is None else q_out.data_ptr(), k_out, new_lens, scales, self._norm,
                 stream, True)
         return None if q is None else q_out
@@ -772,19 +784,19 @@ class PagedAttention:
         """Reads the last new_lens[b] (None: n) positions of each sequence back into the caller's k_out and v_out
         [B, H_kv, n, d], for any n up to the capacity (either may be None)."""
         self._fits(_either(k_out, v_out), True)
-        _read(self.p, k_out, v_out, k_pages, v_pages, page_table, seq_lens, self._space, new_lens, scales, stream,
-              True)
+        _read(self.p, self._dims, k_out, v_out, k_pages, v_pages, page_table, seq_lens, self._space, new_lens, scales,
+              stream, True)
 
     def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None, scales=None):
         out = self._buffer("dense", q)
-        _dense_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, self._space, out.data_ptr(), mask, scales,
-                      stream, True)
+        _dense_decode(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, self._space, out.data_ptr(), mask,
+                      scales, stream, True)
         return out
 
     def selected_decode(self, q, k_pages, v_pages, page_table, seq_lens, idx, stream=None, scales=None):
         out = self._buffer("selected", q)
-        _selected_decode(self.p, q, k_pages, v_pages, page_table, seq_lens, idx, self._space, out.data_ptr(), scales,
-                         stream, True)
+        _selected_decode(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, idx, self._space,
+                         out.data_ptr(), scales, stream, True)
         return out
 
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None,
@@ -796,8 +808,8 @@ class PagedAttention:
                     self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.ws.device)
             except torch.OutOfMemoryError:  # slower without, and the same results
                 self._scratch_bytes = 0
-        _dense_prefill(self.p, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space, out.data_ptr(), mask,
-                       scales, self._scratch, stream, True)
+        _dense_prefill(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space,
+                       out.data_ptr(), mask, scales, self._scratch, stream, True)
         return out
 
     def device_status(self, stream=None) -> int:
