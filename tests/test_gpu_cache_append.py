@@ -122,6 +122,26 @@ def test_four_rows_a_thread(pisa):
         check(q, k, v, pools, scales, table, lens, new, rope, False, w, 1e-6, q_out, k_out)
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,rot,inter,with_q", [
+    ("bf16", 10, 5, 128, 64, True, True), ("bf16", 8, 1, 128, 128, False, True), ("bf16", 5, 5, 64, 48, False, False),
+    ("fp32", 6, 3, 64, 64, False, True), ("fp32", 2, 2, 128, 0, False, False)])
+@pytest.mark.parametrize("in8", [False, True])
+def test_heads_that_are_no_multiple_of_four(pisa, dtype, Hq, Hkv, d, rot, inter, with_q, in8):
+    """The same form with groups of fewer than four heads, with and without queries."""
+    B, n, N = 4, 8000, 8100
+    p, q, k, v, pools, table, ws, scales, w = setup(pisa, B, N, n, Hq, Hkv, d, dtype, in8, seed=2)
+    rope = rope_table(N, rot).cuda() if rot else None
+    lens, new = [8100, 7999, 8000, 31], [8000, 7911, 0, 30]
+    q_out, k_out = (torch.full((B, h, n, d), MARK, dtype=q.dtype, device="cuda") for h in (Hq, Hkv))
+    pisa.append_paged(p, k, v, *pools, table, i32(lens), ws, rope, inter, q if with_q else None,
+                      q_out if with_q else None, k_out, i32(new), scales=scales, q_norm=w[0], k_norm=w[1])
+    assert pisa.read_device_status(ws) == 0
+    if not with_q:  # (what check() looks at besides)
+        pisa.append_paged(p, k, v, *pools, table, i32(lens), ws, rope, inter, q, q_out, None, i32(new), scales=scales,
+                          q_norm=w[0], k_norm=w[1])
+    check(q, k, v, pools, scales, table, lens, new, rope, inter, w, 1e-6, q_out, k_out)
+
+
 def edge_rows(d, dt):
     """Rows at the edges of the scales: zero, at and just over 448 times a power, large, small, not finite."""
     rows = []
