@@ -824,8 +824,8 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
           for (int j = 0; j < KL; ++j) {
             // (255 makes an infinity of it, and NaN of the product: such a row's codes are zero)
             const float f = __uint_as_float((uint32_t)ksc[u][j] << 23);
-            x[u][2 * j] = x[u][2 * j] * hf0 * f;
-            x[u][2 * j + 1] = x[u][2 * j + 1] * hf1 * f;
+            x[u][2 * j] *= hf0 * f;  // the powers first: one of them may take x out of fp32's range
+            x[u][2 * j + 1] *= hf1 * f;
           }
         }
         if (mk.cap2 > 0.0f) {  // cap_score(), the form of large scores where there are some

@@ -114,6 +114,28 @@ def test_decode_rows_of_any_size(pisa, d):
         R.within(out[b], want[:, 0], tol[:, 0], f"sequence {b}")
 
 
+@pytest.mark.parametrize("Hq", [2, 8])
+def test_decode_queries_and_keys_at_both_ends_of_the_range(pisa, Hq):
+    """Queries up to 2^127 and keys that make moderate scores of them, and the other way round."""
+    d, lens = 128, [70, 70]
+
+    def far(k, v):
+        k[0] *= 2.0 ** -112
+        k[1] *= 2.0 ** 110
+
+    k, v, kp, vp, scales, table = cache(2, 1, 70, d, lens, 8, spread=0, change=far)
+    q = torch.randn(2, Hq, d, generator=torch.Generator().manual_seed(9))
+    q[0] *= 2.0 ** 125 / q[0].abs().amax(dim=-1, keepdim=True) * 3.5
+    q[1] *= 2.0 ** -112
+    q = q.to(torch.bfloat16).cuda()
+    layer = pisa.PagedAttention(pisa.make_params(2, 70, Hq, 1, d, scale=2.0 ** -12))
+    out = layer.dense_decode(q, kp, vp, table, i32(lens), scales=scales)
+    assert layer.device_status() == 0
+    for b in range(2):
+        want, tol = R.dense(q[b][:, None], k[b], v[b], 70, torch.tensor([69], device="cuda"), 2.0 ** -12)
+        R.within(out[b], want[:, 0], tol[:, 0], f"sequence {b}")
+
+
 def test_decode_rows_that_are_not_finite(pisa):
     """A row that was not finite reads as NaN: so do the heads that see it, and no other."""
     def poke(k, v):
