@@ -266,3 +266,34 @@ def test_a_scratch_belongs_to_the_stream_of_its_call(pisa):
     torch.cuda.synchronize()
     assert m.layer._scratch.data_ptr() != at
     check(m, out[0], q[0], [512], 0, 512)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 16, 4), (64, 8, 1)])
+def test_selector_equals_itself_for_keys_of_any_size(pisa, d, Hq, Hkv):
+    """Scales over 134 in some leaves, among others and alone, and rows near the smallest power."""
+    lens = [1000, 999, 700, 1000]
+    g = torch.Generator().manual_seed(d)
+    k = torch.randn(4, Hkv, 1000, d, generator=g)
+    k[0, :, 100:300] *= 2.0 ** 20
+    k[1] *= 2.0 ** torch.randint(0, 40, (Hkv, 1000, 1), generator=g)
+    k[2] *= 2.0 ** -112
+    k[3, :, ::7] = 0.0
+    k[3, :, 640:704] *= 2.0 ** -130
+    kp, ks, table, _ = C.paginate(k, lens, seed=2)
+    kp, scales, table = kp.cuda(), torch.stack([ks, ks]).contiguous().cuda(), table.cuda()
+    wide_pages = C.numbers(kp, scales[0]).to(torch.bfloat16)
+    p = pisa.make_params(4, 1000, Hq, Hkv, d, K=4)
+    before = i32([n - 1 for n in lens])
+    got, want = pisa.Selector(p, mode="decode"), pisa.Selector(p, mode="decode")
+    for s in (got, want):
+        s.pyramid.zero_()
+    got.build_paged(kp, table, before, scales=scales)
+    want.build_paged(wide_pages, table, before)
+    assert torch.equal(got.pyramid, want.pyramid)
+    q = torch.randn(4, Hq, d, generator=g)
+    q[2] *= 2.0 ** 100
+    q = q.to(torch.bfloat16).cuda()
+    a, x = got.decode_paged(q, kp, table, i32(lens), scales=scales)
+    b, y = want.decode_paged(q, wide_pages, table, i32(lens))
+    assert got.device_status() == 0
+    assert torch.equal(a, b) and torch.equal(x, y) and torch.equal(got.pyramid, want.pyramid)
