@@ -34,12 +34,13 @@ constexpr int kChunkBytes = 4096;
 constexpr int kNBuf = kStageBytes / kChunkBytes;
 constexpr uint64_t kDecWaitNs = 4000000000ull;
 
-template <int G>
+// ScaleBytes: of a chunk's e4m3 rows (0: rows of the problem's dtype).
+template <int G, int ScaleBytes>
 struct DecSmem {
   alignas(128) unsigned char stage[kDecWarps][kStageBytes];  // 48 KB staging
   int32_t cand[kMaxCand], nxt[kMaxCand];
   float x[kMaxCand][G], xn[kMaxCand][G];
-  int32_t has_x[kMaxCand], has_xn[kMaxCand];
+  uint8_t has_x[kMaxCand], has_xn[kMaxCand];
   int32_t work[2 * kMaxCand];
   int32_t slot0[kMaxCand], slot1[kMaxCand];
   float y[2 * kMaxCand][G];
@@ -50,10 +51,21 @@ struct DecSmem {
   alignas(16) uint32_t key[kMaxCand];  // rank keys of the current list (0 past its end)
   int32_t scan[4];
   int32_t nkept2, nl;
-  alignas(16) uint8_t scale[kDecWarps][kNBuf][64];  // of a chunk's e4m3 rows
+  alignas(16) uint8_t scale[ScaleBytes ? kDecWarps : 1][kNBuf][ScaleBytes ? ScaleBytes : 16];
   uint64_t bar_rows, bar_leaf[kDecWarps][kNBuf];
   int32_t abort;
   int32_t zero;  // stays 0
+};
+// With groups of up to four heads four CTAs are on an SM: 64 sequences of 8 key
+// heads are then one wave of the GPU (131 us at 131072 keys; as two waves, with
+// three on an SM, 192).
+constexpr size_t kFourOnAnSm = 228 * 1024 / 4 - 1024;
+template <int D, int G, bool Q8>
+struct DecShape {
+  static constexpr int kKeys = kChunkBytes / (D * (Q8 ? 1 : 2));  // of a chunk: 16 (d = 128) or 32 (d = 64), of e4m3 twice that
+  using Smem = DecSmem<G, Q8 ? kKeys : 0>;
+  static constexpr size_t kBytes = sizeof(Smem) + 128;
+  static_assert(G > 4 || kBytes <= kFourOnAnSm, "four CTAs fit on an SM");
 };
 
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -117,7 +129,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
   constexpr int DPL = D / 32;
   constexpr int NB = 32 / G;
   extern __shared__ unsigned char dsm_raw[];
-  DecSmem<G>& sm = *reinterpret_cast<DecSmem<G>*>((reinterpret_cast<uintptr_t>(dsm_raw) + 127) & ~(uintptr_t)127);
+  using Smem = typename DecShape<D, G, Q8>::Smem;
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(dsm_raw) + 127) & ~(uintptr_t)127);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bh = blockIdx.x, b = bh / pr.Hkv, h = bh % pr.Hkv;
   const int K = pr.K, W = K + 3;
@@ -427,7 +440,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(Prob pr, Pyr s, con
       // every lane keeps an online max / sum for its two heads (2t, 2t+1)
       // over its keys (rows g and g+8 of each tile).
       constexpr int ES = Q8 ? 1 : 2;
-      constexpr int KPC = kChunkBytes / (D * ES);  // keys per chunk: 16 (d = 128) or 32 (d = 64), of e4m3 twice that
+      constexpr int KPC = DecShape<D, G, Q8>::kKeys;
       const int cpl = s.C / KPC;
       const int nlw = nl > warp ? (nl - warp + kDecWarps - 1) / kDecWarps : 0;
       const int nch = nlw * cpl;
@@ -699,7 +712,7 @@ template <int D, int G, bool Q8>
 static cudaError_t launch_decode_t(const Prob& pr, const Pyr& s, const void* q, const void* kc,
                                    const KeyPages& kp, const int32_t* seq_lens, float* pyr, int32_t* status, int32_t* out_idx,
                                    float* out_score, int32_t* trace, cudaStream_t st) {
-  const size_t smem = sizeof(DecSmem<G>) + 128;
+  const size_t smem = DecShape<D, G, Q8>::kBytes;
   auto kern = decode_kernel<D, G, Q8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
