@@ -30,9 +30,12 @@
 //     of two e4m3 rows (split_query): for up to four heads both are columns of
 //     one MMA, for eight each has its own.  A key's power of two is a factor of
 //     its scores.
-//   - The values' codes become fp16 (one instruction for two of them), paired
-//     over neighbouring keys by byte permutes, and O^T += V^T P in fp16 with the
-//     powers of two of the rows in P, relative to the largest so far.
+//   - The values' codes become bf16 as their bits stand (c 2^-120), paired over
+//     neighbouring keys by byte permutes, and O^T += V^T P in bf16 with the powers
+//     of two of the rows in P.  bf16 has fp32's range: a weight keeps its 8 bits
+//     however small it is, and whatever the sizes of the other rows.  (In fp16,
+//     two codes an instruction, 64 x 8k took 136 us for 139, but weights far
+//     below the largest row's were lost.)
 //   - The reference of the weights follows the maximum only when that has
 //     grown by 2^8: as a rule one vote takes the place of the reductions.
 //   - A thread reads whole 16-byte pieces: the order of the contraction, and
@@ -40,14 +43,14 @@
 //     and the stage is free before the work on it begins.
 //   - Four groups of two warps, 32 keys each; the producer fills two stages at
 //     a time, whose waits and addresses then share their latency.
-// 64 sequences of up to 8192 tokens, capped, 136 us (5.8 TB/s), 2 x 131072
-// tokens 88 us (5.6 TB/s), 64 sequences' 35 selected blocks 66 us (4.4 TB/s).
+// 64 sequences of up to 8192 tokens, capped, 139 us (5.7 TB/s), 2 x 131072
+// tokens 90 us (5.5 TB/s), 64 sequences' 35 selected blocks 68 us (4.3 TB/s).
 // With the work left out the loads alone take 125 and 81 us.  Steps: keys and
 // values converted to bf16 in registers 214, 124 and 86 us; keys as operands,
 // a stage at a time 205 and 124; a stage of every group at once 199 and 101;
 // fp16 values, early release, 32 keys a warp 157 and 94; votes 150 and 91;
-// both parts of the queries in one MMA 133 and 84 (kernel times).  Two producer
-// warps in turn: 154 and 92 against 150 and 91.
+// both parts of the queries in one MMA 133 and 84; values' bits as bf16 137 and
+// 87 (kernel times).  Two producer warps in turn: 154 and 92 against 150 and 91.
 //
 // Measured (GB300): 64 ragged sequences of up to 8192 tokens, 32 / 8 heads, d
 // = 128: 237 us, 6.6 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
@@ -66,6 +69,11 @@ constexpr int kMerge = 96;              // threads that merge a part while the c
 constexpr int kPage = 64;
 constexpr int kMaxCtas = 1024;          // part slots in the workspace: two per CTA
 constexpr float kSlack = 8.0f;          // Q8: log2 of how far weights may exceed 1
+// Q8: P = p 2^(scale - 127 + 111) and values times 2^-120 give O times 2^-9.  Of
+// rows over 448 2^kNear that P would leave the range (with p up to 2^8, 2^126):
+// from there on a part has P = p 2^(scale - 127), values times 2^-34 and so O.
+constexpr int kNear = 134, kNearLift = 111, kNearO = 9, kFarO = 34;
+constexpr uint32_t kFarValues = (uint32_t)(127 + 120 - kFarO) * 0x800080u;
 constexpr int kScaleLanes = 2 * kPage / 16;  // lanes that bring a page's scales
 
 // Q8: pages of e4m3.
@@ -279,24 +287,24 @@ __device__ __forceinline__ void part_codes(const uint8_t* page, int r, int g, ui
   }
 }
 // Two such parts in pairs: dims 2 j and 2 j + 1 of both as a[j][at] and a[j][at
-// + 1], in fp16, of which every code is a number.
+// + 1], in bf16 times 2^-120 (a byte of each and their signs' copies by one prmt).
+template <int kSelector>
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t y) {
+  uint32_t w;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(w) : "r"(x), "r"(y), "n"(kSelector));
+  return codes_to_bf16(w);
+}
 template <int D>
 __device__ __forceinline__ void pair_codes(const uint32_t (&x)[D / 32], const uint32_t (&y)[D / 32],
                                            uint32_t (&a)[D / 16][4], int at) {
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
-    codes_to_half(__byte_perm(x[j], y[j], 0x5140), a[2 * j][at], a[2 * j][at + 1]);
-    codes_to_half(__byte_perm(x[j], y[j], 0x7362), a[2 * j + 1][at], a[2 * j + 1][at + 1]);
+    a[2 * j][at] = code_pair<0xc480>(x[j], y[j]);
+    a[2 * j][at + 1] = code_pair<0xd591>(x[j], y[j]);
+    a[2 * j + 1][at] = code_pair<0xe6a2>(x[j], y[j]);
+    a[2 * j + 1][at + 1] = code_pair<0xf7b3>(x[j], y[j]);
   }
 }
-__device__ __forceinline__ void mma16816_half(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Keys that the query of sequence b sees, and the pages that hold them; a
 // query that sees none has one page, dead.
 struct Span {
@@ -701,10 +709,10 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   const bool low = !FOLD || tig < 2;
   const int hd = FOLD ? 2 * (tig & 1) : 2 * tig, kofs = low ? 0 : 8;
   // the query's fragments; Q8: its upper part and its lower one, each head's
-  // 1 / s, and the largest scale of the values so far
+  // 1 / s, and whether the part has seen rows over 448 2^kNear
   uint32_t bq[Q8 ? D / 16 : D / 8], bl[Q8 && !FOLD ? D / 16 : 1];
   float hf0 = 1.0f, hf1 = 1.0f;
-  int ref = 0;
+  bool far = false;
   float oacc[D / 16][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads hd, hd + 1
   float sl0 = 0.0f, sl1 = 0.0f;
@@ -745,7 +753,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         }
         hf0 = __shfl_sync(0xffffffffu, f, 4 * hd);
         hf1 = __shfl_sync(0xffffffffu, f, 4 * hd + 4);
-        ref = 0;
+        far = false;
       } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -885,10 +893,10 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
             c1 = fmaxf(c1, x[u][2 * j + 1]);
             top = max(top, vsc[u][j]);
           }
-        // The reference follows the maximum when that has grown by 2^8, the
-        // largest power as it grows: as a rule neither, and one vote says so.  A
-        // row of NaN (255) is over every power.
-        if (__any_sync(0xffffffffu, c0 > m0 + kSlack || c1 > m1 + kSlack || top > ref)) {
+        // The reference follows the maximum when that has grown by 2^8, and rows of
+        // any size change P's and O's units: as a rule neither, and one vote says so.
+        // A row of NaN (255) is over every power.
+        if (__any_sync(0xffffffffu, c0 > m0 + kSlack || c1 > m1 + kSlack || top > (far ? 254 : kNear))) {
           top = 0;
 #pragma unroll
           for (int u = 0; u < T; ++u)
@@ -910,11 +918,10 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
           m1 = n1;
           l0 *= f0;
           l1 *= f1;
-          if (top > ref) {
-            const float f = __uint_as_float(max(ref - top + 127, 0) << 23);
-            ref = top;
-            f0 *= f;
-            f1 *= f;
+          if (!far && top > kNear) {
+            far = true;
+            f0 *= 1.0f / (1 << (kFarO - kNearO));
+            f1 *= 1.0f / (1 << (kFarO - kNearO));
           }
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt) {
@@ -926,17 +933,16 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
         for (int u = 0; u < T; ++u) {
-          // The rows' powers go with the weights, relative to the largest so far.
-          // P is rounded to fp16 for the MMA, times 2^7: 2^-11 of each weight that is
-          // over 2^-21 of the reference, and 2^-32 of that below.
+          // The rows' powers go with the weights.  P is rounded to bf16 for the MMA:
+          // 2^-9 of each weight.
           uint32_t pk[2] = {0u, 0u};
 #pragma unroll
           for (int j = 0; j < KL; ++j) {
             const float p0 = ptx::ex2(x[u][2 * j] - z0), p1 = ptx::ex2(x[u][2 * j + 1] - z1);
             l0 += p0;
             l1 += p1;
-            const float f = __uint_as_float(max(vsc[u][j] - ref + 134, 0) << 23);
-            pk[j] = pack_half(p0 * f, p1 * f);
+            const float f = __uint_as_float((uint32_t)(vsc[u][j] + (far ? 0 : kNearLift)) << 23);
+            pk[j] = pack_bf16(p0 * f, p1 * f);
           }
           if constexpr (FOLD) {
             pk[1] = low ? 0u : pk[0];
@@ -951,6 +957,12 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
           uint32_t av[D / 16][4];
           pair_codes<D>(vc[u][0], vc[u][1], av, 0);
           pair_codes<D>(vc[u][2], vc[u][3], av, 2);
+          if (far) {
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) av[mt][j] = mul_bf16x2(av[mt][j], kFarValues);
+          }
           uint32_t va = 0xffffffffu, vz = 0xffffffffu;  // masks of the value pairs
           if (part) {
             auto seen = [&](int k) { return k >= meta.klo && k <= meta.khi; };
@@ -963,7 +975,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
               av[mt][0] &= va; av[mt][1] &= va;
               av[mt][2] &= vz; av[mt][3] &= vz;
             }
-            mma16816_half(oacc[mt], av[mt], b0, b1);
+            mma16816(oacc[mt], av[mt], b0, b1);
           }
         }
       } else {
@@ -1085,13 +1097,11 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
       *reinterpret_cast<float2*>(&sm.m[warp][2 * tig]) = make_float2(m0, m1);
       *reinterpret_cast<float2*>(&sm.l[warp][2 * tig]) = make_float2(l0, l1);
     }
-    if constexpr (Q8) {  // O as it is: by 2^(ref - 127) and 2^-7, in two steps
-      const int by = ref - 134, half = by >> 1;
-      const float f = __uint_as_float((half + 127) << 23), f2 = __uint_as_float((by - half + 127) << 23);
+    if constexpr (Q8) {  // O as it is
+      const float f = __uint_as_float((uint32_t)(127 + (far ? kFarO : kNearO)) << 23);
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt) {
-        oacc[mt][0] = oacc[mt][0] * f * f2; oacc[mt][1] = oacc[mt][1] * f * f2;
-        oacc[mt][2] = oacc[mt][2] * f * f2; oacc[mt][3] = oacc[mt][3] * f * f2;
+        oacc[mt][0] *= f; oacc[mt][1] *= f; oacc[mt][2] *= f; oacc[mt][3] *= f;
       }
     }
     float* ow = sm.o[warp];  // [head][dim], see o_at
