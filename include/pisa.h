@@ -499,7 +499,9 @@ size_t pisa_paged_workspace_bytes(const pisa_params* p, int64_t n);
  * 254 and the two codes of e4m3's NaN are never written by this library; what
  * a call makes of such a row is unspecified, and confined to the queries that
  * see it.  A row's numbers are numbers of bf16 too, so each call below equals
- * its counterpart above on pages of those numbers, but for the order of sums.
+ * its counterpart above on pages of those numbers, but for the order of sums;
+ * the decode calls' scores may be off by 2^-11 (in log2 units) where a query has
+ * elements below 2^-14 of its largest.
  *
  * Workspace, lengths, page tables, faults and what an output holds where
  * nothing is written: as for the calls above.  With PISA_CACHE_PARAMS the

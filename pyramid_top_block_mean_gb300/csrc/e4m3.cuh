@@ -38,6 +38,16 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(x) : "r"(w));
   return codes_to_bf16(x);
 }
+// The codes of bytes 0 and 1, and of bytes 2 and 3, in fp16, of which every
+// code is a number (NaN's codes stay NaN).
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 // Two numbers, already over their row's power, to the nearest codes.
 __device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
   uint16_t d;

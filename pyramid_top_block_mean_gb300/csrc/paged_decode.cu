@@ -29,7 +29,9 @@
 //   - S = K q by m16n8k32 MMAs on the codes as they are.  A bf16 query is the sum
 //     of two e4m3 rows (split_query): for up to four heads both are columns of
 //     one MMA, for eight each has its own.  A key's power of two is a factor of
-//     its scores.
+//     its scores.  Of a query with dims far below its largest the two rows leave
+//     something out: where that may count with a page's keys (a bound, found with
+//     the query, on their scales), its scores are made again in bf16.
 //   - The values' codes become bf16 as their bits stand (c 2^-120), paired over
 //     neighbouring keys by byte permutes, and O^T += V^T P in bf16 with the powers
 //     of two of the rows in P.  bf16 has fp32's range: a weight keeps its 8 bits
@@ -43,19 +45,22 @@
 //     and the stage is free before the work on it begins.
 //   - Four groups of two warps, 32 keys each; the producer fills two stages at
 //     a time, whose waits and addresses then share their latency.
-// 64 sequences of up to 8192 tokens, capped, 139 us (5.7 TB/s), 2 x 131072
-// tokens 90 us (5.5 TB/s), 64 sequences' 35 selected blocks 68 us (4.3 TB/s).
+// 64 sequences of up to 8192 tokens, capped, 140 us (5.6 TB/s), 2 x 131072
+// tokens 90 us (5.5 TB/s), 64 sequences' 35 selected blocks 69 us (4.3 TB/s).
 // With the work left out the loads alone take 125 and 81 us.  Steps: keys and
 // values converted to bf16 in registers 214, 124 and 86 us; keys as operands,
 // a stage at a time 205 and 124; a stage of every group at once 199 and 101;
 // fp16 values, early release, 32 keys a warp 157 and 94; votes 150 and 91;
 // both parts of the queries in one MMA 133 and 84; values' bits as bf16 137 and
-// 87 (kernel times).  Two producer warps in turn: 154 and 92 against 150 and 91.
+// 87; the look at what queries leave out 138 and 87 (kernel times).  Two producer
+// warps in turn: 154 and 92 against 150 and 91.
 //
 // Measured (GB300): 64 ragged sequences of up to 8192 tokens, 32 / 8 heads, d
 // = 128: 237 us, 6.6 TB/s of keys and values (the copy rate is 6.8); 2 x 131072
 // tokens 150 us (6.5 TB/s); 64 sequences' 35 selected blocks 97 us (6.0 TB/s);
 // one sequence of 197 tokens 6.8 us.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "paged.cuh"
@@ -123,6 +128,8 @@ struct Smem {
   uint8_t scale[Q8 ? S::kStages : 1][2][Q8 ? kPage : 16];
   float o[S::kWarps][G * D];                  // a part's merge
   float m[S::kWarps][8], l[S::kWarps][8];
+  // Q8: the columns' 1 / s, and a page's scores for which the query's parts do not do
+  float by[Q8 ? S::kWarps : 1][8], more[Q8 && G <= 4 ? S::kWarps : 1][2][2][Q8 && G <= 4 ? 32 : 1];
   float jo[kMerge][8], jm[kMerge], jl[kMerge];
   Meta meta[S::kStages], part;
   uint64_t full[S::kStages], empty[S::kStages], mfull, mempty;
@@ -234,28 +241,34 @@ __device__ __forceinline__ void split_pair(uint32_t x, uint32_t& c, uint32_t& r)
 // A query as the sum of two e4m3 rows: with s the power of two that brings the
 // head's largest magnitude to 128 .. 256, x = q s is hi + lo / 32.  Of a bf16
 // number, whose 8 bits are twice e4m3's, hi takes four and leaves at most 4 and
-// a sign, so that the sum is exact; below 2^-13 of the largest, where e4m3's
-// steps no longer shrink, it is off by at most 2^-22 of the largest.
+// a sign, so that the sum is exact; for |x| < 2^-7, where e4m3's steps no longer
+// shrink, it is off by up to 2^-15: `off` says whether there are such elements.
 // Returns 1 / s, or NaN for a query that is not finite.
 template <int D>
 __device__ __forceinline__ float split_query(const uint16_t* row, bool there, uint32_t (&hi)[D / 16],
-                                             uint32_t (&lo)[D / 16]) {
+                                             uint32_t (&lo)[D / 16], bool& off) {
   uint4 w[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
     w[i] = there ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0u, 0u, 0u, 0u);
-  uint32_t pair = 0;  // largest magnitudes of the even and the odd elements
+  uint32_t pair = 0;             // largest magnitudes of the even and the odd elements
+  uint32_t least = 0x7fff7fffu;  // and their smallest but zero, less 1 + 2^15 (zeros: 2^15 - 1)
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) pair = __vmaxu2(pair, u[k] & 0x7fff7fffu);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a = u[k] & 0x7fff7fffu;
+      pair = __vmaxu2(pair, a);
+      least = __vmins2(least, a + 0x7fff7fffu);
+    }
   }
   uint32_t top = max(pair & 0xffffu, pair >> 16);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const uint32_t e = max(top >> 7, 14u);  // biased; 2^(134 - 127 - e) stays a normal number
   const float s = __uint_as_float((134u + 127u - e) << 23);
+  off = min((int)(int16_t)(least & 0xffffu), (int)(int16_t)(least >> 16)) + 32769 < ((int)e - 14) << 7;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -273,6 +286,64 @@ __device__ __forceinline__ float split_query(const uint16_t* row, bool there, ui
     }
   }
   return e == 255u ? NAN : __uint_as_float((e + 127u - 134u) << 23);
+}
+
+// What split_query() leaves out of a thread's elements, as a sum of magnitudes.
+template <int D>
+__device__ __forceinline__ float left_out(const uint16_t* row, float by) {
+  const float s = __uint_as_float((254u << 23) - __float_as_uint(by));  // by is a power of two
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < D / 4; i += 2) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(row + i);
+    const float x = __uint_as_float(v << 16) * s, z = __uint_as_float(v & 0xffff0000u) * s;
+    uint32_t c, r, ch, rh;
+    split_pair(pack_half(x, z), c, r);
+    codes_to_half(c | r << 16, ch, rh);
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&ch));
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&rh));
+    sum += fabsf(x - hi.x - lo.x * (1.0f / 32)) + fabsf(z - hi.y - lo.y * (1.0f / 32));
+  }
+  return sum;
+}
+
+// Scores times s of a tile of 16 keys, in bf16: of queries that leave too much
+// out.  by: the heads' 1 / s.  d is the MMA's result, for columns past the heads
+// zero.
+template <int D, int G>
+__device__ __forceinline__ void whole_scores(const uint8_t* keys, const uint16_t* row, const float* by, float (&d)[4]) {
+  const int grp = threadIdx.x >> 2 & 7, tig = threadIdx.x & 3;
+  const bool there = grp < G;
+  row += (there ? grp : 0) * D + (D / 4) * tig;
+  keys += grp * D + (D / 4) * tig;
+  const uint32_t s2 = (254u - (__float_as_uint(by[grp]) >> 23)) * 0x800080u;
+  d[0] = d[1] = d[2] = d[3] = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < D / 16; ++i) {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + 4 * i);
+    const uint32_t x0 = *reinterpret_cast<const uint32_t*>(keys + 4 * i);
+    const uint32_t x1 = *reinterpret_cast<const uint32_t*>(keys + 8 * D + 4 * i);
+    const uint4 p = code_pairs(make_uint2(x0, x1), row_factor(127));
+    const uint32_t a[4] = {p.x, p.z, p.y, p.w};
+    mma16816(d, a, there ? mul_bf16x2(w.x, s2) : 0u, there ? mul_bf16x2(w.y, s2) : 0u);
+  }
+}
+// The same of two tiles, as the lanes go on with them where both parts are
+// columns of one MMA.  (A call, whose registers are not the caller's: in the
+// loop itself 64 sequences of up to 8192 tokens take 143.8 us for 140.7; of eight
+// heads it is the other way round, 155.6 for 163.6.)
+template <int D, int G>
+__device__ __noinline__ void whole_folded(const uint8_t* keys, const uint16_t* row, const float* by, float* x) {
+  const int lane = threadIdx.x & 31;
+  const bool low = (lane & 3) < 2;
+#pragma unroll 1
+  for (int u = 0; u < 2; ++u) {
+    float d[4];
+    whole_scores<D, G>(keys + 16 * u * D, row, by, d);
+    const float r0 = __shfl_xor_sync(0xffffffffu, d[2], 2), r1 = __shfl_xor_sync(0xffffffffu, d[3], 2);
+    x[64 * u + lane] = low ? d[0] : r0;
+    x[64 * u + 32 + lane] = low ? d[1] : r1;
+  }
 }
 
 // The D / 8 codes of part g of row r.
@@ -329,7 +400,8 @@ __device__ __forceinline__ Span seq_span(const MaskArgs& m, const int32_t* seq_l
 template <int D, int G, bool Q8>
 __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     paged_decode_kernel(Prob pr, MaskArgs mk, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap, const uint8_t* __restrict__ kscales,
+                        const __grid_constant__ CUtensorMap vmap, const uint8_t* __restrict__ kcodes,
+                        const uint8_t* __restrict__ kscales,
                         const uint8_t* __restrict__ vscales, const uint16_t* __restrict__ q,
                         const int32_t* __restrict__ table, int64_t nb, int64_t num_pages,
                         const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ idx, Parts parts,
@@ -713,6 +785,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
   uint32_t bq[Q8 ? D / 16 : D / 8], bl[Q8 && !FOLD ? D / 16 : 1];
   float hf0 = 1.0f, hf1 = 1.0f;
   bool far = false;
+  int most_scale = 255;  // of keys for which the two parts do
   float oacc[D / 16][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // heads hd, hd + 1
   float sl0 = 0.0f, sl1 = 0.0f;
@@ -743,17 +816,33 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         const int head = FOLD ? grp & 3 : grp;
         const uint16_t* row = sm.q[st] + (head < G ? head : 0) * D + (D / 4) * tig;
         float f;
+        bool off;
         if constexpr (FOLD) {
           uint32_t rest[D / 16];
-          f = split_query<D>(row, head < G, bq, rest);
+          f = split_query<D>(row, head < G, bq, rest, off);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) bq[k] = grp < 4 ? bq[k] : rest[k];
         } else {
-          f = split_query<D>(row, head < G, bq, bl);
+          f = split_query<D>(row, head < G, bq, bl, off);
         }
         hf0 = __shfl_sync(0xffffffffu, f, 4 * hd);
         hf1 = __shfl_sync(0xffffffffu, f, 4 * hd + 4);
         far = false;
+        most_scale = 255;
+        if (__any_sync(0xffffffffu, off)) {
+          float left = grp < G ? left_out<D>(row, f) : 0.0f;
+          left += __shfl_xor_sync(0xffffffffu, left, 1);
+          left += __shfl_xor_sync(0xffffffffu, left, 2);
+          left *= f;
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) left = fmaxf(left, __shfl_xor_sync(0xffffffffu, left, o));
+          // it adds up to 448 times a key's power times `left` in a score: 2^-11 (log2
+          // units) and less are let be
+          const uint32_t bits = __float_as_uint(left * 448.0f * fabsf(pr.scale2));
+          most_scale = bits == 0u ? 255 : 127 - 11 - ((int)(bits >> 23) - 126);
+          if (tig == 0) sm.by[warp][grp] = f;
+          __syncwarp();
+        }
       } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -778,6 +867,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
     constexpr int T = S::kKeys / 16;  // tiles of 16 keys
     uint32_t kc[Q8 ? T : 1][2][D / 16], vc[Q8 ? T : 1][4][D / 32];
     int ksc[T][KL], vsc[T][KL];  // and the scales
+    bool large_key = false;      // of one for which the query's parts do not do
     if constexpr (Q8) {
       if (seen_any) {
 #pragma unroll
@@ -792,6 +882,7 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < KL; ++j) {
             ksc[u][j] = sm.scale[st][0][r + kofs + 8 * j];
+            large_key |= ksc[u][j] > most_scale;
             vsc[u][j] = sm.scale[st][1][r + kofs + 8 * j];
           }
         }
@@ -896,7 +987,41 @@ __global__ void __launch_bounds__(Shape<D, G, Q8>::kThreads, 1)
         // The reference follows the maximum when that has grown by 2^8, and rows of
         // any size change P's and O's units: as a rule neither, and one vote says so.
         // A row of NaN (255) is over every power.
-        if (__any_sync(0xffffffffu, c0 > m0 + kSlack || c1 > m1 + kSlack || top > (far ? 254 : kNear))) {
+        if (__any_sync(0xffffffffu, large_key || c0 > m0 + kSlack || c1 > m1 + kSlack || top > (far ? 254 : kNear))) {
+          if (__any_sync(0xffffffffu, large_key)) {  // the scores again, of the codes and the query in bf16
+            const int64_t b = meta.item / pr.Hkv, key0 = meta.rel + (int64_t)seq_lens[b] - 1;
+            const int64_t row0 = ((int64_t)table[b * nb + key0 / kPage] * pr.Hkv + meta.item % pr.Hkv) * kPage + r16;
+            const uint16_t* row = q + (int64_t)meta.item * G * D;
+            if constexpr (FOLD) whole_folded<D, G>(kcodes + row0 * D, row, sm.by[warp], sm.more[warp][0][0]);
+            c0 = c1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < T; ++u) {
+              float d[4];
+              if constexpr (FOLD) {
+                d[0] = sm.more[warp][u][0][lane];
+                d[1] = sm.more[warp][u][1][lane];
+              } else {
+                whole_scores<D, G>(kcodes + (row0 + 16 * u) * D, row, sm.by[warp], d);
+              }
+#pragma unroll
+              for (int j = 0; j < KL; ++j) {
+                const int k = ka + 16 * u + 8 * j;
+                const float f = __uint_as_float((uint32_t)kscales[row0 + k - r16] << 23), back = (float)(meta.rel + k);
+                const bool hidden = k < meta.klo || k > meta.khi;
+                float y0 = d[2 * j] * (hf0 * f), y1 = d[2 * j + 1] * (hf1 * f);
+                y0 = mk.cap2 > 0.0f ? cap_score(mk, y0) : y0 * pr.scale2;
+                y1 = mk.cap2 > 0.0f ? cap_score(mk, y1) : y1 * pr.scale2;
+                if (mk.slopes) {
+                  y0 = fmaf(sl0, back, y0);
+                  y1 = fmaf(sl1, back, y1);
+                }
+                x[u][2 * j] = hidden ? -INFINITY : y0;
+                x[u][2 * j + 1] = hidden ? -INFINITY : y1;
+                c0 = fmaxf(c0, x[u][2 * j]);
+                c1 = fmaxf(c1, x[u][2 * j + 1]);
+              }
+            }
+          }
           top = 0;
 #pragma unroll
           for (int u = 0; u < T; ++u)
@@ -1180,8 +1305,8 @@ cudaError_t launch_t(const Prob& pr, const MaskArgs& m, const void* q, const Poo
   Parts parts{(int32_t*)(ws + w.counter), (float*)(ws + w.ml), (float*)(ws + w.o)};
   note_launch();
   return launch_pdl(true, kern, dim3((unsigned)grid), dim3(Shape<D, G, Q8>::kThreads), smem, st, pr, m, kmap, vmap,
-                    pools.ks, pools.vs, (const uint16_t*)q, pools.table, pools.nb, pools.num_pages, seq_lens, idx, parts, kMinRun,
-                    (int32_t*)ws, (uint16_t*)out);
+                    (const uint8_t*)pools.k, pools.ks, pools.vs, (const uint16_t*)q, pools.table, pools.nb,
+                    pools.num_pages, seq_lens, idx, parts, kMinRun, (int32_t*)ws, (uint16_t*)out);
 }
 
 }  // namespace

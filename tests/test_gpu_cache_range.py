@@ -1,7 +1,7 @@
-"""GPU tests of decode over 8-bit pages where the rows' sizes or the weights
-spread far apart: a value row much larger than the others with next to no
-weight, rows whose weights span fp32's range.  Every element within the bound
-derived in paged_ref."""
+"""GPU tests of decode over 8-bit pages where the rows' sizes, the weights or the
+queries' dims spread far apart: a value row much larger than the others with
+next to no weight, rows whose weights span fp32's range, queries with a dim
+that no key answers.  Every element within the bound derived in paged_ref."""
 import pytest
 import torch
 
@@ -109,3 +109,31 @@ def test_weights_over_all_of_fp32(pisa, d, Hq, Hkv):
         k[b, :, :, 0] = -(10.0 * size) / (4.0 * d ** -0.5)
         v[b, :, :, 16:] = torch.where((torch.arange(d)[None, 16:] % 10) == size[:, None], v[b, :, :, 16:], 0.0)
     check_dense(pisa, q.to(torch.bfloat16).cuda(), *pages(k, v, lens, 8), lens, N)
+
+
+@pytest.mark.parametrize("gap", [10, 14, 18, 24, 60, 120])
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 2, 2), (128, 8, 2), (64, 4, 1), (64, 16, 2), (128, 8, 1)])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(window=70)])
+def test_a_query_dim_that_no_key_answers(pisa, d, Hq, Hkv, gap, kw):
+    g = torch.Generator().manual_seed(gap)
+    lens, N = [300, 290, 64], 300
+    k, v = (torch.randn(3, Hkv, N, d, generator=g) for _ in range(2))
+    q = torch.randn(3, Hq, d, generator=g) * 2
+    q[..., 5] = 2.0 ** gap * 3
+    q[0, 1, 5] = 1.0  # and a head without
+    k[..., 5] = 0.0
+    k[1, :, ::3] *= 2.0 ** -6
+    check_dense(pisa, q.to(torch.bfloat16).cuda(), *pages(k, v, lens, 9), lens, N, **kw)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 8, 2), (64, 16, 2)])
+def test_query_dims_of_many_sizes(pisa, d, Hq, Hkv):
+    """Dims from 2^-30 of a query's largest to it, and keys that make up for it: products of one size, large scores."""
+    g = torch.Generator().manual_seed(4)
+    lens, N = [300, 250], 300
+    size = 2.0 ** -(torch.arange(d) % 31).float()
+    k, v = (torch.randn(2, Hkv, N, d, generator=g) for _ in range(2))
+    q = torch.randn(2, Hq, d, generator=g) * size * 2.0 ** 12
+    k[..., :] *= torch.where(torch.arange(d) % 31 > 15, 1.0, 0.0)
+    k[1] *= 2.0 ** 14
+    check_dense(pisa, q.to(torch.bfloat16).cuda(), *pages(k, v, lens, 4), lens, N)
