@@ -281,8 +281,24 @@ def _key_cache(p: Params, k_pages, page_table, scales) -> Cache:
     index, num = k_pages.get_device(), k_pages.shape[0]
     return Cache(ctypes.sizeof(Cache), CACHE_E4M3,
                  _want(k_pages, "k_pages", (num, p.H_kv, p.C, p.d), torch.float8_e4m3fn, index), None,
-                 _want(scales, "scales", (2, num, p.H_kv, p.C), torch.uint8, index), None, num, page_table.data_ptr(),
-                 None, 0)
+                 _want(scales, "scales", (2, num, p.H_kv, p.C), torch.uint8, index), None, num,
+                 _want(page_table, "page_table", (p.B, -(-p.N // p.C)), torch.int32, index), None, 0)
+
+
+def _own_keys(p: Params, k_pages):
+    """Pages in the model's dtype: not those of 8 bits without their scales, of which twice the bytes would be read."""
+    if k_pages.dtype is not _dtype(p):
+        num, need = k_pages.shape[0], 2 if p.dtype == BF16 else 4
+        if k_pages.numel() * k_pages.element_size() < num * p.H_kv * p.C * p.d * need:
+            raise ValueError(f"k_pages: {num} pages of {_dtype(p)} are more than {tuple(k_pages.shape)} of "
+                             f"{k_pages.dtype} (8-bit pages are read with their scales)")
+
+
+def _want_room(t, name: str, count: int, dtype, index: int) -> int:
+    """Address of a contiguous tensor of `count` elements at least."""
+    if t.dtype is not dtype or t.numel() < count or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, (count,), dtype, index, "contiguous")
+    return t.data_ptr()
 
 
 def build_pyramid_paged(p: Params, k_pages, page_table, pyramid, ws, seq_lens=None, stream=None,
@@ -290,12 +306,13 @@ def build_pyramid_paged(p: Params, k_pages, page_table, pyramid, ws, seq_lens=No
     """k_pages [num_pages, H_kv, C, d]; page_table int32 [B, ceil(N / C)];
     scales: of e4m3 pages."""
     if scales is not None:
-        rc = _lib.pisa_cache_build_pyramid(ctypes.byref(p), ctypes.byref(_key_cache(p, k_pages, page_table, scales)),
-                                           _ptr(seq_lens), _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(),
-                                           _stream(stream))
-        if check:
-            _check(rc, "pisa_cache_build_pyramid")
-        return rc
+        cache, index = _key_cache(p, k_pages, page_table, scales), k_pages.get_device()
+        return _launch(index, stream, "pisa_cache_build_pyramid", check, _lib.pisa_cache_build_pyramid,
+                       ctypes.byref(p), ctypes.byref(cache),
+                       None if seq_lens is None else _want(seq_lens, "seq_lens", (p.B,), torch.int32, index),
+                       _want_room(pyramid, "pyramid", pyramid_bytes(p) // 4, torch.float32, index),
+                       *_want_space(ws, index))
+    _own_keys(p, k_pages)
     rc = _lib.pisa_build_pyramid_paged(ctypes.byref(p), _ptr(k_pages), k_pages.shape[0], _ptr(page_table),
                                        _ptr(seq_lens), _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(),
                                        _stream(stream))
@@ -308,13 +325,16 @@ def select_decode_paged(p: Params, q, k_pages, page_table, seq_lens, pyramid, ws
                         trace=None, stream=None, check: bool = True, scales=None) -> int:
     """select_decode over pages (scales: of e4m3 pages)."""
     if scales is not None:
-        rc = _lib.pisa_cache_select_decode(ctypes.byref(p), _ptr(q),
-                                           ctypes.byref(_key_cache(p, k_pages, page_table, scales)), _ptr(seq_lens),
-                                           _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out_idx),
-                                           _ptr(out_score), _ptr(trace), _stream(stream))
-        if check:
-            _check(rc, "pisa_cache_select_decode")
-        return rc
+        cache, index, W = _key_cache(p, k_pages, page_table, scales), k_pages.get_device(), p.B * p.H_kv * (p.K + 3)
+        return _launch(index, stream, "pisa_cache_select_decode", check, _lib.pisa_cache_select_decode,
+                       ctypes.byref(p), _want_room(q, "q", p.B * p.H_q * p.d, _dtype(p), index), ctypes.byref(cache),
+                       _want(seq_lens, "seq_lens", (p.B,), torch.int32, index),
+                       _want_room(pyramid, "pyramid", pyramid_bytes(p) // 4, torch.float32, index),
+                       *_want_space(ws, index), _want_room(out_idx, "out_idx", W, torch.int32, index),
+                       None if out_score is None else _want_room(out_score, "out_score", W, torch.float32, index),
+                       None if trace is None else
+                       _want_room(trace, "trace", p.B * p.H_kv * pyramid_levels(p) * p.K, torch.int32, index))
+    _own_keys(p, k_pages)
     rc = _lib.pisa_select_decode_paged(ctypes.byref(p), _ptr(q), _ptr(k_pages), k_pages.shape[0], _ptr(page_table),
                                        _ptr(seq_lens), _ptr(pyramid), _ptr(ws), ws.numel() * ws.element_size(),
                                        _ptr(out_idx), _ptr(out_score), _ptr(trace), _stream(stream))
