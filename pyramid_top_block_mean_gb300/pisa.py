@@ -736,7 +736,9 @@ class PagedAttention:
     of call, zeroed when it is made and written again by the next call of its
     kind (a call of fewer tokens uses its front).  Rows behind a sequence's new
     tokens are not written: they hold zeros or what an earlier call left there.
-    Calls may run on any stream, one after the other.
+    Calls may run on any stream, one after the other; the buffers stay whole
+    until they have run, also when the object is gone before (of a captured
+    graph they are its maker's to keep, as all memory that it uses).
     rope: fp32 [N, rot_dim] as append_paged takes it, or None; q_norm, k_norm:
     fp32 [d], weights of the heads' norms before the rotation, or None.  Pages
     are tensors of the model's dtype or, with their scales, of 8 bits
@@ -768,12 +770,24 @@ class PagedAttention:
         one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
         rows = p.B * p.H_q * p.d
         flat = torch.zeros(rows * (2 + 2 * n), dtype=_dtype(p), device=self.device)
+        self._owned, self._streams = [self.ws, flat], {}  # buffers, and the streams that use them
         self._out = {"dense": flat[:rows].view(one), "selected": flat[rows:2 * rows].view(one),
                      "q": flat[2 * rows:(2 + n) * rows].view(many), "prefill": flat[(2 + n) * rows:].view(many)}
         if self._index >= 0:  # the zeros are there before the first call, whatever stream that runs on
             with torch.cuda.device(self._index):
+                stream = torch.cuda.current_stream()
+                self._streams[stream.cuda_stream] = stream
                 if not torch.cuda.is_current_stream_capturing():
-                    torch.cuda.current_stream().synchronize()
+                    stream.synchronize()
+
+    def _used_on(self, stream):
+        """After a call: the allocator hears of a stream that the buffers were not made on."""
+        st = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+        if st in self._streams or torch.cuda.is_current_stream_capturing():
+            return
+        self._streams[st] = torch.cuda.current_stream(self.device) if stream is None else stream
+        for x in self._owned:
+            x.record_stream(self._streams[st])
 
     def _fits(self, x, ok: bool):
         if x.get_device() != self._index:
@@ -798,6 +812,7 @@ class PagedAttention:
         _append(self.p, self._dims, k, v, k_pages, v_pages, page_table, seq_lens, self._space, self._rope, self._rot,
                 self.interleaved, q, None if q is None else q_out.data_ptr(), k_out, new_lens, scales, self._norm,
                 stream, True)
+        self._used_on(stream)
         return None if q is None else q_out
 
     def read(self, k_out, v_out, k_pages, v_pages, page_table, seq_lens, new_lens=None, stream=None, scales=None):
@@ -806,17 +821,20 @@ class PagedAttention:
         self._fits(_either(k_out, v_out), True)
         _read(self.p, self._dims, k_out, v_out, k_pages, v_pages, page_table, seq_lens, self._space, new_lens, scales,
               stream, True)
+        self._used_on(stream)
 
     def dense_decode(self, q, k_pages, v_pages, page_table, seq_lens, mask=None, stream=None, scales=None):
         out = self._buffer("dense", q)
         _dense_decode(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, self._space, out.data_ptr(), mask,
                       scales, stream, True)
+        self._used_on(stream)
         return out
 
     def selected_decode(self, q, k_pages, v_pages, page_table, seq_lens, idx, stream=None, scales=None):
         out = self._buffer("selected", q)
         _selected_decode(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, idx, self._space,
                          out.data_ptr(), scales, stream, True)
+        self._used_on(stream)
         return out
 
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None,
@@ -826,10 +844,14 @@ class PagedAttention:
             try:  # in the order of the call's stream, so that no earlier owner of the memory still writes it
                 with torch.cuda.stream(stream):
                     self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.ws.device)
+                self._owned.append(self._scratch)
+                for s in self._streams.values():
+                    self._scratch.record_stream(s)
             except torch.OutOfMemoryError:  # slower without, and the same results
                 self._scratch_bytes = 0
         _dense_prefill(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space,
                        out.data_ptr(), mask, scales, self._scratch, stream, True)
+        self._used_on(stream)
         return out
 
     def device_status(self, stream=None) -> int:
