@@ -742,9 +742,10 @@ class PagedAttention:
     rope: fp32 [N, rot_dim] as append_paged takes it, or None; q_norm, k_norm:
     fp32 [d], weights of the heads' norms before the rotation, or None.  Pages
     are tensors of the model's dtype or, with their scales, of 8 bits
-    (quantized_pages).  The first prompt over 8-bit pages makes a scratch of
-    cache_scratch_bytes (0 to 4 GiB) where there is room for it, kept for the
-    prompts that follow."""
+    (quantized_pages).  The first long prompt over 8-bit pages makes a scratch of
+    cache_scratch_bytes (up to 4 GiB) where there is room for it, kept for the
+    prompts that follow; without room they do without, and some later one asks
+    again."""
 
     def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
                  device="cuda", q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
@@ -763,8 +764,9 @@ class PagedAttention:
         self._space = _want_space(self.ws, self._index)
         self._rot = 0 if rope is None else rope.shape[-1]
         self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
-        self._scratch = None  # made by the first prompt over 8-bit pages
+        self._scratch = None  # made by the first prompt over 8-bit pages that makes use of one
         self._scratch_bytes = cache_scratch_bytes(p, n)
+        self._scratch_skip = self._scratch_wait = 0  # prompts that do not ask for it, after the last that found no room
         self.q_norm, self.k_norm = q_norm, k_norm
         self._norm = _head_norm(p, q_norm, k_norm, norm_eps, self._index)
         one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
@@ -788,6 +790,20 @@ class PagedAttention:
         self._streams[st] = torch.cuda.current_stream(self.device) if stream is None else stream
         for x in self._owned:
             x.record_stream(self._streams[st])
+
+    def _make_scratch(self, stream):
+        if self._scratch_skip > 0:  # (an allocation that fails gives back all that the allocator holds)
+            self._scratch_skip -= 1
+            return
+        try:  # in the order of the call's stream, so that no earlier owner of the memory still writes it
+            with torch.cuda.stream(stream):
+                self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.ws.device)
+        except torch.OutOfMemoryError:  # slower without, and the same results
+            self._scratch_skip = self._scratch_wait = min(2 * self._scratch_wait + 1, 255)
+            return
+        self._owned.append(self._scratch)
+        for s in self._streams.values():
+            self._scratch.record_stream(s)
 
     def _fits(self, x, ok: bool):
         if x.get_device() != self._index:
@@ -840,15 +856,9 @@ class PagedAttention:
     def dense_prefill(self, q, k_pages, v_pages, page_table, seq_lens, new_lens=None, mask=None, stream=None,
                       scales=None):
         out = self._buffer("prefill", q)
-        if scales is not None and self._scratch_bytes and self._scratch is None:
-            try:  # in the order of the call's stream, so that no earlier owner of the memory still writes it
-                with torch.cuda.stream(stream):
-                    self._scratch = torch.empty(self._scratch_bytes, dtype=torch.uint8, device=self.ws.device)
-                self._owned.append(self._scratch)
-                for s in self._streams.values():
-                    self._scratch.record_stream(s)
-            except torch.OutOfMemoryError:  # slower without, and the same results
-                self._scratch_bytes = 0
+        if scales is not None and self._scratch is None and self._scratch_bytes:
+            if cache_scratch_bytes(self.p, q.shape[2]):
+                self._make_scratch(stream)
         _dense_prefill(self.p, self._dims, q, k_pages, v_pages, page_table, seq_lens, new_lens, self._space,
                        out.data_ptr(), mask, scales, self._scratch, stream, True)
         self._used_on(stream)

@@ -1,9 +1,10 @@
 """GPU tests of what a PagedAttention owns: its buffers stay whole until calls
-on other streams have run."""
+on other streams have run, and the scratch of long prompts over 8-bit pages is
+made when a prompt needs it, and when there is room."""
 import pytest
 import torch
 
-from test_gpu_cache_layer import Model, i32
+from test_gpu_cache_layer import Model, check, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,30 @@ def test_buffers_outlive_pending_calls_on_another_stream(pisa, what):
     del block, m.layer
     assert not taken(nbytes, {address}) or side.query()
     torch.cuda.synchronize()
+
+
+def test_a_prompt_of_few_tokens_makes_no_scratch(pisa):
+    m = Model(pisa, 1, 3000, 8, 2, 128, n=2500)
+    q = m.append(10, [10], [10]).clone()
+    out = m.layer.dense_prefill(q, *m.cache(), i32([10]), scales=m.scales)
+    check(m, out[0], q[0], [10], 0, 10)
+    assert m.layer._scratch is None
+    q = m.append(2400, [2410], [2400]).clone()
+    out = m.layer.dense_prefill(q, *m.cache(), i32([2410]), scales=m.scales)
+    check(m, out[0], q[0], [2410], 0, 2400)
+    assert m.layer._scratch is not None
+
+
+def test_a_scratch_is_asked_for_again(pisa):
+    """A prompt that found no room does not take it from all that follow."""
+    m = Model(pisa, 1, 3000, 8, 2, 128, n=2500)
+    q = m.append(2500, [2500], [2500]).clone()
+    want = m.layer.dense_prefill(q, *m.cache(), i32([2500]), scales=m.scales).clone()
+    size = m.layer._scratch_bytes
+    m.layer._scratch, m.layer._scratch_bytes = None, 1 << 45
+    assert torch.equal(m.layer.dense_prefill(q, *m.cache(), i32([2500]), scales=m.scales), want)
+    assert m.layer._scratch is None
+    m.layer._scratch_bytes = m.layer._scratch_bytes and size  # there is room again
+    for _ in range(5):
+        assert torch.equal(m.layer.dense_prefill(q, *m.cache(), i32([2500]), scales=m.scales), want)
+    assert m.layer._scratch is not None
