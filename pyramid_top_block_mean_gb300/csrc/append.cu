@@ -99,24 +99,28 @@ __device__ __forceinline__ float sum_of_squares(const float (&x)[N]) {
   ptx::unpack2(part[1], p2, p3);
   return (p0 + p1) + (p2 + p3);
 }
-// 1 / sqrt(mean of squares) of a row whose squares leave fp32's range: from the
-// elements over 2^80, where eps is nothing.  The row's threads are those of
-// `mask`, neighbours; 1 / d is exact.
+// 1 / sqrt(sum / d + eps) of a row whose squares, or their mean and eps, leave
+// fp32's range: from the elements over 2^80 and eps over 2^160.  The row's
+// threads are those of `mask`, neighbours; 1 / d is exact.
 template <int N>
-__device__ __forceinline__ float far_row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d) {
+__device__ __forceinline__ float far_row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d,
+                                              float eps) {
   float ss = 0.0f;
 #pragma unroll
   for (int j = 0; j < N; ++j) ss = fmaf(x[j] * 0x1p-80f, x[j] * 0x1p-80f, ss);
   for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
-  return 0x1p-80f * rsqrtf(ss * one_over_d);
+  return 0x1p-80f * rsqrtf(fmaf(ss, one_over_d, eps * 0x1p-80f * 0x1p-80f));
 }
+// Whether the sum and what the root is taken of are in range.
+__device__ __forceinline__ bool near_row(float sum, float mean) { return sum < 3.0e38f && mean < 3.0e38f; }
 // 1 / sqrt(sum / d + eps) of a row.
 template <int N>
 __device__ __forceinline__ float row_norm(const float (&x)[N], uint32_t units, unsigned mask, float one_over_d,
                                           float eps) {
   float ss = sum_of_squares(x);
   for (uint32_t o = 1; o < units; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
-  return ss < 3.0e38f ? rsqrtf(fmaf(ss, one_over_d, eps)) : far_row_norm(x, units, mask, one_over_d);
+  const float mean = fmaf(ss, one_over_d, eps);
+  return near_row(ss, mean) ? rsqrtf(mean) : far_row_norm(x, units, mask, one_over_d, eps);
 }
 
 // The bits of the largest magnitude among x (those of infinities and NaN lie above all others').
@@ -350,13 +354,14 @@ __device__ __forceinline__ void append_heads(const Prob& pr, const AppendArgs& a
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      if (by[k] < 3.0e38f) {
-        by[k] = rsqrtf(fmaf(by[k], a.norm.one_over_d, a.norm.eps));
+      const float mean = fmaf(by[k], a.norm.one_over_d, a.norm.eps);
+      if (near_row(by[k], mean)) {
+        by[k] = rsqrtf(mean);
       } else {
         float x[2 * E];
         Vec<T>::load(w[k][0], x);
         Vec<T>::load(w[k][1], x + E);
-        by[k] = far_row_norm(x, units, mates, a.norm.one_over_d);
+        by[k] = far_row_norm(x, units, mates, a.norm.one_over_d, a.norm.eps);
       }
     }
   }

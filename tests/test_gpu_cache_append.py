@@ -268,3 +268,23 @@ def test_keys_in_place(pisa):
                       q_norm=w[0], k_norm=w[1])
     assert torch.equal(q0, want_q) and torch.equal(k0, want_k)
     assert all(torch.equal(a, b) for a, b in zip(first, [x.view(torch.uint8) for x in pools] + [scales]))
+
+
+@pytest.mark.parametrize("n", [70, 6500])
+@pytest.mark.parametrize("eps", [1e35, 3e38, 3.4e38])
+@pytest.mark.parametrize("size", [1.0, 3e18, 1e19, 1e25])
+def test_norms_with_a_large_eps(pisa, size, eps, n):
+    """eps counts in rows whose squares leave fp32's range, too, and their sum with it may."""
+    g = torch.Generator().manual_seed(5)
+    p = pisa.make_params(1, n, 16, 4, 64, dtype="fp32")
+    q, k = ((torch.randn(1, h, n, 64, generator=g) * size).cuda() for h in (16, 4))
+    w = ((1 + torch.rand(64, generator=g)) * 1e3).cuda()
+    pages = -(-n // 64)
+    pool = torch.zeros(pages, 4, 64, 64, device="cuda")
+    ws = torch.empty(pisa.paged_workspace_bytes(p, n), dtype=torch.uint8, device="cuda")
+    q_out, k_out = torch.zeros_like(q), torch.zeros_like(k)
+    pisa.append_paged(p, k, k, pool, pool.clone(), i32([list(range(pages))]), i32([n]), ws, q=q, q_out=q_out,
+                      k_out=k_out, q_norm=w, k_norm=w, norm_eps=eps)
+    for x, out in ((q, q_out), (k, k_out)):
+        y, t = C.norm_rotate(x, w, float(torch.tensor(eps)), None, None, False)
+        R.within(out, y, t + 2.0 ** -24 * (y.abs() + t) + 1e-37, "normed")
