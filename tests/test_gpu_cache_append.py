@@ -288,3 +288,22 @@ def test_norms_with_a_large_eps(pisa, size, eps, n):
     for x, out in ((q, q_out), (k, k_out)):
         y, t = C.norm_rotate(x, w, float(torch.tensor(eps)), None, None, False)
         R.within(out, y, t + 2.0 ** -24 * (y.abs() + t) + 1e-37, "normed")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("in8,inter", [(False, False), (True, False), (True, True)])
+def test_prompts_in_place(pisa, dtype, in8, inter):
+    """test_keys_in_place of long calls, whose CTAs take several heads."""
+    B, n, N = 2, 4000, 4100
+    p, q, k, v, pools, table, ws, scales, w = setup(pisa, B, N, n, 16, 4, 128, dtype, in8, seed=6)
+    rope = rope_table(N, 128).cuda()
+    q0, k0, v0 = (x.contiguous() for x in (q, k, v))
+    lens, new = i32([4100, 4000]), i32([4000, 3900])
+    want_q, want_k = q0.clone(), k0.clone()  # (rows behind the new tokens stay as they were)
+    pisa.append_paged(p, k0, v0, *pools, table, lens, ws, rope, inter, q0, want_q, want_k, new, scales=scales,
+                      q_norm=w[0], k_norm=w[1])
+    first = [x.view(torch.uint8).clone() for x in pools]
+    pisa.append_paged(p, k0, v0, *pools, table, lens, ws, rope, inter, q0, q0, k0, new, scales=scales, q_norm=w[0],
+                      k_norm=w[1])
+    assert torch.equal(q0, want_q) and torch.equal(k0, want_k)
+    assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(first, pools))
