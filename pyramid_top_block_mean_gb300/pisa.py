@@ -745,11 +745,12 @@ class PagedAttention:
     (quantized_pages).  The first long prompt over 8-bit pages makes a scratch of
     cache_scratch_bytes (up to 4 GiB) where there is room for it, kept for the
     prompts that follow; without room they do without, and some later one asks
-    again."""
+    again.  It is twice the size of the 8-bit cache itself: layers whose calls do
+    not overlap share one as `scratch`, a tensor of that many bytes."""
 
     def __init__(self, p: Params, n: int = 1, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
                  device="cuda", q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
-                 norm_eps: float = 1e-6):
+                 norm_eps: float = 1e-6, scratch: Optional[torch.Tensor] = None):
         p = Params.from_buffer_copy(p)  # the buffers below are made for these numbers
         self.p, self.n, self.rope, self.interleaved = p, n, rope, interleaved
         self.device = torch.device(device)
@@ -764,15 +765,18 @@ class PagedAttention:
         self._space = _want_space(self.ws, self._index)
         self._rot = 0 if rope is None else rope.shape[-1]
         self._rope = None if rope is None else _want(rope, "rope", (p.N, self._rot), torch.float32, self._index)
-        self._scratch = None  # made by the first prompt over 8-bit pages that makes use of one
+        self._scratch = scratch  # None: made by the first prompt over 8-bit pages that makes use of one
         self._scratch_bytes = cache_scratch_bytes(p, n)
+        if scratch is not None and _want_space(scratch, self._index)[1] < self._scratch_bytes:
+            raise ValueError(f"scratch: expected {self._scratch_bytes} bytes, got {tuple(scratch.shape)} {scratch.dtype}")
         self._scratch_skip = self._scratch_wait = 0  # prompts that do not ask for it, after the last that found no room
         self.q_norm, self.k_norm = q_norm, k_norm
         self._norm = _head_norm(p, q_norm, k_norm, norm_eps, self._index)
         one, many = (p.B, p.H_q, p.d), (p.B, p.H_q, n, p.d)
         rows = p.B * p.H_q * p.d
         flat = torch.zeros(rows * (2 + 2 * n), dtype=_dtype(p), device=self.device)
-        self._owned, self._streams = [self.ws, flat], {}  # buffers, and the streams that use them
+        # buffers, and the streams that use them
+        self._owned, self._streams = [x for x in (self.ws, flat, scratch) if x is not None], {}
         self._out = {"dense": flat[:rows].view(one), "selected": flat[rows:2 * rows].view(one),
                      "q": flat[2 * rows:(2 + n) * rows].view(many), "prefill": flat[(2 + n) * rows:].view(many)}
         if self._index >= 0:  # the zeros are there before the first call, whatever stream that runs on

@@ -1,6 +1,6 @@
-"""The selector's calls over 8-bit pages look at every tensor that they are
-given: shapes, types, devices and layouts that do not fit are refused before
-anything reads them (on the CPU: no call gets as far as a GPU)."""
+"""The selector's calls over 8-bit pages and PagedAttention look at every tensor
+that they are given: shapes, types, devices and layouts that do not fit are
+refused before anything reads them (on the CPU: no call gets as far as a GPU)."""
 import pytest
 import torch
 
@@ -69,3 +69,14 @@ def test_8_bit_pages_without_their_scales(pisa, made):
         pisa.build_pyramid_paged(p, **a)
     with pytest.raises(ValueError, match="8-bit pages"):
         pisa.select_decode_paged(p, **a, **b)
+
+
+def test_a_scratch_of_too_few_bytes(pisa):
+    p = pisa.make_params(1, 2048, 8, 2, 64)
+    size = pisa.cache_scratch_bytes(p, 2048)
+    assert size > 0
+    for bad in (torch.zeros(size - 1, dtype=torch.uint8), torch.zeros(2, size, dtype=torch.uint8)[:, ::2]):
+        with pytest.raises(ValueError):
+            pisa.PagedAttention(p, n=2048, device="cpu", scratch=bad)
+    pisa.PagedAttention(p, n=2048, device="cpu", scratch=torch.zeros(size, dtype=torch.uint8))
+    pisa.PagedAttention(p, n=16, device="cpu", scratch=torch.zeros(1, dtype=torch.uint8))  # of no use to it

@@ -70,3 +70,20 @@ def test_a_scratch_is_asked_for_again(pisa):
     for _ in range(5):
         assert torch.equal(m.layer.dense_prefill(q, *m.cache(), i32([2500]), scales=m.scales), want)
     assert m.layer._scratch is not None
+
+
+def test_layers_share_a_scratch(pisa):
+    """Two layers of one scratch: calls in turn, results of their own, and nothing else allocated."""
+    ms = [Model(pisa, 1, 3000, 8, 2, 128, n=2500, seed=s) for s in range(2)]
+    qs = [m.append(2500, [2500], [2500]).clone() for m in ms]
+    lens = i32([2500])
+    want = [m.layer.dense_prefill(q, *m.cache(), lens, scales=m.scales).clone() for m, q in zip(ms, qs)]
+    shared = torch.zeros(pisa.cache_scratch_bytes(ms[0].p, 2500), dtype=torch.uint8, device="cuda")
+    layers = [pisa.PagedAttention(m.p, n=2500, scratch=shared) for m in ms]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(2):
+        for m, layer, q, y in zip(ms, layers, qs, want):
+            assert torch.equal(layer.dense_prefill(q, *m.cache(), lens, scales=m.scales), y)
+    assert torch.cuda.memory_allocated() == before
+    assert shared.any()  # the pages went through it
