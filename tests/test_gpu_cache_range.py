@@ -65,6 +65,17 @@ def test_a_large_row_without_weight(pisa, d, Hq, Hkv, gap, nats, attended):
     check_dense(pisa, q, *rest, lens, 300)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 2, 2), (128, 8, 2), (64, 16, 2)])
+@pytest.mark.parametrize("gap,nats", [(112, 300), (112, 60), (80, 40)])
+def test_small_values_beside_a_large_row(pisa, d, Hq, Hkv, gap, nats):
+    """Rows of 2^-93, near the end of the bound's range, and one that is not small."""
+    lens = [300, 290, 300, 280]
+    q, k, v, cache, scales = large_row(d, Hq, Hkv, 300, lens, [0, 141, 299, 65], gap, nats, False)
+    scales[1] = (scales[1].int() - 93).clamp_min(10).to(torch.uint8)
+    v = v * 2.0 ** -93
+    check_dense(pisa, q, k, v, cache, scales, lens, 300)
+
+
 @pytest.mark.parametrize("d,Hq,Hkv", [(128, 8, 2), (64, 8, 1)])
 def test_a_large_row_in_a_cache_split_over_the_gpu(pisa, d, Hq, Hkv):
     lens = [9000, 8000]
