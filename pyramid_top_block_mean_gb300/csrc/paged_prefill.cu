@@ -1361,8 +1361,10 @@ size_t paged_prefill_ws_bytes(const Prob& pr, int64_t n) {
 // codes / expanded (us), one sequence behind 8192 (65536) cached tokens: 16 / 4
 // heads of 128 with 5 items a key head 52 / 56 (196 / 189), with 8 73 / 72 (323 /
 // 276), with 32 177 / 135 (1159 / 825); 32 / 8 heads of 64 with 8 86 / 87 (429 /
-// 415), with 16 122 / 113 (807 / 732).  Without a cached part it loses some 5
-// us up to 16 items.  Not beyond 4 GiB.
+// 415), with 16 122 / 113 (807 / 732).  Without a cached part, which only the
+// device knows of, it loses 5 to 9 us with few items: 16 / 4 heads of 128 with 8
+// 21 / 26, with 16 64 / 70, with 32 46 / 45; 8 / 8 of 128 with 8 71 / 80, with 16
+// 79 / 71; 32 / 8 of 64 with 16 25 / 31, with 32 38 / 43.  Not beyond 4 GiB.
 size_t paged_prefill_scratch_bytes(const Prob& pr, int64_t n) {
   if (make_plan(pr, n).tiles < (pr.d == 128 ? 8 : 16) || pr.Hkv > 65535) return 0;  // (a grid's third dimension)
   const size_t pages = (size_t)pr.B * (size_t)ceil_div64(pr.N, kPage);
